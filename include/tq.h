@@ -51,7 +51,9 @@ typedef enum {
 typedef enum { TQ_MSE = 0, TQ_PROD = 1, TQ_MIXED = 2 } tq_mode;
 typedef enum { TQ_ROT_DENSE = 0, TQ_ROT_HADAMARD = 1 } tq_rot_kind;
 typedef enum { TQ_DENS_BETA = 0, TQ_DENS_GAUSS = 1 } tq_density;
-typedef enum { TQ_F32 = 0, TQ_F16 = 1 } tq_dtype;
+/* TQ_BF16: tq_qk_norm_rope and tq_tree_attention only. */
+typedef enum { TQ_F32 = 0, TQ_F16 = 1, TQ_BF16 = 2 } tq_dtype;
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_style;
 typedef enum { TQ_LAYOUT_TOKEN = 0, TQ_LAYOUT_PAIR = 1 } tq_layout;
 
 /* Library version string, e.g. "tq 0.1 sm_103a". */
@@ -325,6 +327,136 @@ tq_status tq_decode_attention_noalloc(const tq_ctx* kctx, const tq_ctx* vctx, co
                                       int Hq, int Hkv, int64_t seq, int64_t cap, float scale,
                                       float* d_out, tq_stream stream);
 
+/* ------------------------------------------------------------------ serving
+ * What a continuously batched server with drafted tokens does around the
+ * packed cache.  The pages have no counterpart to these calls.  One step:
+ * tq_block_tables (pages for the step's tokens), tq_qk_norm_rope (norms and
+ * position rotation of q and k), tq_tree_attention (the step's tokens, drafted
+ * as a tree, a chain or one each, over the cache), and once it is known which
+ * tokens stay, tq_encode_slots (their k and v into their pages).
+ *
+ * Paged cache: a page holds `block` tokens of every KV head; vector index of
+ * place o of head h of page g is (g * Hkv + h) * block + o.  A token's slot is
+ * g * block + o.  `d_table` [B, max_blocks] int32 lists a request's pages in
+ * order of position.  Lengths, offsets and tables live on the device and are
+ * read by the kernels, so a call captured into a graph serves later lengths.
+ * None of these calls synchronises, allocates or keeps anything between calls.
+ */
+
+/* Block tables and slot maps of one step, from the requests' lengths.
+ *   need_b = ceil((len_b + new_b) / block); a request takes need_b - held_b
+ *   pages if that is positive and gives back held_b - need_b if it is not
+ *   (rejected drafts; an ended request has len = new = 0).
+ * d_len, d_new, d_held [B]: tokens that stay in the cache, tokens to append,
+ *           pages held (the first d_held[b] entries of the table's row b).
+ * d_ring    [ring] int32 page numbers, a ring of free pages; d_state {head,
+ *           tail}: entries head .. tail-1 (modulo ring) are free.  Pages are
+ *           taken from head on, in order of the requests; pages given back go
+ *           behind tail and can be taken from the next call on.  The ring holds
+ *           every page of the cache at most once, so ring = the cache's pages.
+ * d_table   in and out: entries [held_b, need_b) of a served request are set;
+ *           entries past need_b are left as they are.
+ * d_held_out, d_state_out: the new d_held and d_state; other buffers than the
+ *           inputs (the caller swaps them), so a call can be repeated.
+ * d_row_start [B + 1]: first row of each request among the step's token rows.
+ * d_slots, d_pos [rows]: slot and position of every row; rows past
+ *           d_row_start[B] get -1 and 0.  Rows past `rows` are not listed.
+ * A request is served if it takes no page or if the pages it and the requests
+ * before it take are all there.  One that is not served, or whose numbers are
+ * negative or exceed max_blocks, keeps its pages and gets no rows.
+ * Errors: INVALID_ARG; UNSUPPORTED for B > 4096 or B * max_blocks >= 2^31.  The
+ * rows of all requests together must stay below 2^31.
+ */
+tq_status tq_block_tables(const int32_t* d_len, const int32_t* d_new, const int32_t* d_held, int B, int block,
+                          int32_t* d_ring, int64_t ring, const int64_t* d_state, int32_t* d_table, int max_blocks,
+                          int32_t* d_held_out, int64_t* d_state_out, int32_t* d_row_start, int64_t* d_slots,
+                          int32_t* d_pos, int64_t rows, tq_stream stream);
+
+/* Angular frequencies (radians per position, fp64) as fractions of a turn:
+ * h_freq[i] = floor(frac(h_inv_freq[i] / 2π) · 2^64), so that the angle of any
+ * position is one wrapping 64-bit product.  Host only, synchronous; the caller
+ * copies h_freq to the device.  Errors: INVALID_ARG (NULL, n < 0, not finite). */
+tq_status tq_rope_frequencies(int n, const double* h_inv_freq, uint64_t* h_freq);
+
+/* Norms of queries and keys for each head and the position rotation, one pass:
+ *   y = x · w / sqrt(mean(x²) + eps) per head of d elements, then pairs (a, b)
+ *   of the first `rot` elements become (a cos φ - b sin φ, b cos φ + a sin φ),
+ *   φ = pos · f_j.  TQ_ROPE_HALF pairs elements j and j + rot/2,
+ *   TQ_ROPE_INTERLEAVED 2j and 2j + 1.
+ * d_q       [N, Hq, d], d_k [N, Hkv, d] of in_dtype (F32, F16, BF16); a token's
+ *           heads are contiguous, tokens q_stride / k_stride elements apart (a
+ *           slice of a joint projection will do).  Hq or Hkv may be 0.
+ * d_wq, d_wk [d] weights of in_dtype; NULL: ones.
+ * d_freq    [rot / 2] from tq_rope_frequencies, on the device; rot = 0: norms only.
+ * d_pos     [N] int32 positions (any value, negative ones turn backwards).
+ * d_q_out, d_k_out: out_dtype, strides as above; may be the inputs themselves
+ *           when types and strides agree.  Other overlaps are the caller's error.
+ * Arithmetic is fp32, rounded once at the end.  Pointers and strides in bytes
+ * must be multiples of 16.  Errors: INVALID_ARG; UNSUPPORTED for d not a
+ * multiple of 32 up to 256 or rot not a multiple of 16.
+ */
+tq_status tq_qk_norm_rope(const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride, int in_dtype,
+                          int64_t N, int Hq, int Hkv, int d, const void* d_wq, const void* d_wk, float eps,
+                          const uint64_t* d_freq, int rot, int style, const int32_t* d_pos, void* d_q_out,
+                          int64_t q_out_stride, void* d_k_out, int64_t k_out_stride, int out_dtype, tq_stream stream);
+
+/* tq_encode into a paged cache: row (token i, head h) of d_x [N, Hkv, d] goes
+ * to vector (g * Hkv + h) * block + o of `out`, g = d_slots[i] / block and
+ * o = d_slots[i] % block.  A token whose slot is negative, or whose page lies
+ * past the end of `out`, is not written.  Slots are distinct (which of two
+ * tokens of one slot is stored, or a mixture, is not defined).  Codes, norms
+ * and both layouts as tq_encode; in PAIR layout the other token of a block
+ * keeps its codes.  Calls that write the same PAIR block must be ordered on one
+ * stream.  d = 128, block even (TQ_ERR_UNSUPPORTED otherwise, and for a
+ * codebook that is not symmetric).
+ */
+tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64_t N, int Hkv,
+                          const int64_t* d_slots, int block, const tq_codes* out, tq_stream stream);
+
+/* Attention of drafted tokens over a packed cache.  Row i of a sequence (a
+ * drafted token) and query head h:
+ *   out = Σ_t p_t v̂_t + Σ_j p_j v_j over the sum of all p,
+ *   p = exp(scale · ⟨q, k⟩), t over the sequence's cached tokens (all of them),
+ *   j over the drafted tokens of the same sequence that the row's mask names.
+ * The drafted k and v enter as they are (they are not in the cache yet).  One
+ * drafted token per sequence is single-token decode; without d_mask the drafts
+ * are a chain (row i sees drafted tokens 0..i: a prompt's next piece).
+ * d_q       [rows, Hq, d], d_k_new, d_v_new [rows, Hkv, d], all of `dtype` (F32,
+ *           F16, BF16), a token's heads contiguous, tokens q_stride (k_stride,
+ *           v_stride) elements apart.  d_k_new and d_v_new may both be NULL: the
+ *           rows then see the cache alone.
+ * d_row_start [B + 1] int32, ascending from 0: rows of sequence b are
+ *           [d_row_start[b], d_row_start[b + 1]); offsets past `rows` are cut.
+ *           Rows past d_row_start[B] are neither read nor written.
+ * d_mask    [rows, mask_words] uint32: bit j of a row's words = it sees drafted
+ *           token j of its sequence; tokens past 32 * mask_words are not seen.
+ *           A row that sees nothing at all (no cached token either) is zero.
+ * K, V      as tq_decode_attention (TOKEN and PAIR layout, TQ_MSE, any bits each).
+ * d_len     [B] int32 cached tokens; cut to the capacity max_blocks * block.
+ * d_table   [B, max_blocks] int32 pages; a page outside the cache is left out of
+ *           the sums and reported by tq_status_poll(kctx) as
+ *           TQ_ERR_INVALID_ARG.  NULL: the contiguous cache of
+ *           tq_decode_attention with cap = block (vector (b * Hkv + h) * block
+ *           + t).
+ * Hq / Hkv any whole number.  block a multiple of 16.
+ * d_out     [rows, Hq, d] of `dtype`, contiguous.
+ * Accuracy: F32 inputs are computed in fp32 throughout.
+ * d_ws      workspace of tq_tree_attention_workspace_size bytes (16-byte
+ *           aligned; its contents do not matter).  Calls that share one must be
+ *           ordered on one stream; captured graphs that may run at the same time
+ *           need one each.
+ * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
+ * UNSUPPORTED for d != 128, Prod or b + 1/2-bit codes, a block that is not a
+ * multiple of 16, or rows * Hq, max_blocks * block >= 2^31.
+ */
+tq_status tq_tree_attention_workspace_size(const tq_ctx* kctx, int B, int Hq, int Hkv, int64_t rows, size_t* bytes);
+tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* d_q, int64_t q_stride,
+                            const void* d_k_new, int64_t k_stride, const void* d_v_new, int64_t v_stride, int dtype,
+                            int64_t rows, const int32_t* d_row_start, const uint32_t* d_mask, int mask_words,
+                            const tq_codes* K, const tq_codes* V, const int32_t* d_len, const int32_t* d_table,
+                            int max_blocks, int block, int B, int Hq, int Hkv, float scale, void* d_out, void* d_ws,
+                            size_t ws_bytes, tq_stream stream);
+
 /* ------------------------------------------------------------------ views
  * Canonical view of stored codes, for checking: copies vectors
  * [first, first + count) to the host and writes their coordinate indices
@@ -349,7 +481,8 @@ tq_status tq_ctx_set_wait_limit(tq_ctx* ctx, uint32_t polls);
 /* Reads and clears the context's device status word (synchronises `stream`).
  * Returns TQ_OK, or TQ_ERR_TIMEOUT if a bounded device wait of a kernel
  * launched with this context ran out since the last poll (that kernel's
- * outputs are then unspecified). */
+ * outputs are then unspecified), or TQ_ERR_INVALID_ARG if tq_tree_attention
+ * met a page outside its cache. */
 tq_status tq_status_poll(const tq_ctx* ctx, tq_stream stream);
 
 #ifdef __cplusplus

@@ -16,7 +16,8 @@ TQ_OK, TQ_ERR_INVALID_ARG, TQ_ERR_UNSUPPORTED, TQ_ERR_CUDA, TQ_ERR_ALLOC, TQ_ERR
 TQ_MSE, TQ_PROD, TQ_MIXED = 0, 1, 2
 TQ_ROT_DENSE, TQ_ROT_HADAMARD = 0, 1
 TQ_DENS_BETA, TQ_DENS_GAUSS = 0, 1
-TQ_F32, TQ_F16 = 0, 1
+TQ_F32, TQ_F16, TQ_BF16 = 0, 1, 2
+TQ_ROPE_HALF, TQ_ROPE_INTERLEAVED = 0, 1
 TQ_LAYOUT_TOKEN, TQ_LAYOUT_PAIR = 0, 1
 
 # every entry point of include/tq.h
@@ -25,7 +26,8 @@ EXPORTS = (
     "tq_rotation_haar", "tq_ctx_create", "tq_ctx_destroy", "tq_codes_layout", "tq_encode",
     "tq_scores_workspace_size", "tq_scores", "tq_decode_workspace_size",
     "tq_decode_attention", "tq_decode_step", "tq_decode_attention_noalloc", "tq_unpack_indices", "tq_status_poll",
-    "tq_ctx_set_wait_limit",
+    "tq_ctx_set_wait_limit", "tq_block_tables", "tq_rope_frequencies", "tq_qk_norm_rope", "tq_encode_slots",
+    "tq_tree_attention_workspace_size", "tq_tree_attention",
 )
 
 
@@ -92,6 +94,14 @@ def lib():
         "tq_unpack_indices": ([P(Codes), _i64, _i64, _vp, _vp], _i),
         "tq_status_poll": ([_vp, _vp], _i),
         "tq_ctx_set_wait_limit": ([_vp, ctypes.c_uint32], _i),
+        "tq_block_tables": ([_vp, _vp, _vp, _i, _i, _vp, _i64, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _i),
+        "tq_rope_frequencies": ([_i, _vp, _vp], _i),
+        "tq_qk_norm_rope": ([_vp, _i64, _vp, _i64, _i, _i64, _i, _i, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _i64,
+                             _vp, _i64, _i, _vp], _i),
+        "tq_encode_slots": ([_vp, _vp, _i, _i64, _i, _vp, _i, P(Codes), _vp], _i),
+        "tq_tree_attention_workspace_size": ([_vp, _i, _i, _i, _i64, P(_sz)], _i),
+        "tq_tree_attention": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i, _i64, _vp, _vp, _i, P(Codes), P(Codes),
+                               _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _sz, _vp], _i),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -272,6 +282,111 @@ def tq_decode_attention_noalloc(kctx, vctx, q, K, V, B, Hq, Hkv, seq, cap, scale
         kctx.handle, vctx.handle, ctypes.c_void_p(q.data_ptr()), dt, ctypes.byref(K.desc),
         ctypes.byref(V.desc), B, Hq, Hkv, seq, cap, float(scale), ctypes.c_void_p(out.data_ptr()),
         _stream(stream)))
+
+
+# ---------------------------------------------------------------- serving
+def _dtype(t):
+    import torch
+    return {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}[t.dtype]
+
+
+def _dev(t, dtype, n, what):
+    """Device address of a contiguous tensor of this type with n elements or more."""
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more is wanted")
+    return t.data_ptr()
+
+
+def _heads(t, n, h, d, what):
+    """Address and token stride of a [n, h, d] CUDA tensor whose heads are contiguous."""
+    if tuple(t.shape) != (n, h, d) or not t.is_cuda or t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{what}: a CUDA tensor [{n}, {h}, {d}] with contiguous heads is wanted")
+    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+
+
+def tq_block_tables(lens, new, held, ring, state, table, block, held_out, state_out, row_start, slots, pos,
+                    stream=None):
+    """Pages, slots and positions of one step's tokens (include/tq.h).  table [B, max_blocks], ring, lens, new, held,
+    held_out, row_start and pos are int32, state, state_out and slots int64; pos and slots have one entry per row."""
+    import torch
+    i32, i64, B = torch.int32, torch.int64, lens.numel()
+    _check("tq_block_tables", lib().tq_block_tables(
+        _dev(lens, i32, B, "lens"), _dev(new, i32, B, "new"), _dev(held, i32, B, "held"), B, block,
+        _dev(ring, i32, 1, "ring"), ring.numel(), _dev(state, i64, 2, "state"),
+        _dev(table, i32, B * table.shape[-1], "table"), table.shape[-1], _dev(held_out, i32, B, "held_out"),
+        _dev(state_out, i64, 2, "state_out"), _dev(row_start, i32, B + 1, "row_start"), _dev(slots, i64, 0, "slots"),
+        _dev(pos, i32, slots.numel(), "pos"), slots.numel(), _stream(stream)))
+
+
+def tq_rope_frequencies(inv_freq, device="cuda"):
+    """Frequencies (radians per position, fp64) as 64-bit fractions of a turn, on the device (int64 words)."""
+    import numpy as np
+    import torch
+    f = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    out = np.empty(f.size, dtype=np.uint64)
+    _check("tq_rope_frequencies", lib().tq_rope_frequencies(f.size, _ptr(f), _ptr(out)))
+    return torch.from_numpy(out.view(np.int64)).to(device)
+
+
+def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=None):
+    """Head norms and position rotation of q [N, Hq, d] and k [N, Hkv, d] into q_out and k_out (include/tq.h).
+    wq, wk: [d] of q's type or None; freq: tq_rope_frequencies or None (norms alone); outputs may be the inputs."""
+    import torch
+    (N, Hq, d), Hkv = q.shape, k.shape[1]
+    if k.dtype != q.dtype or k_out.dtype != q_out.dtype:
+        raise ValueError("q and k, and q_out and k_out, are of one type")
+    (qp, qs), (kp, ks) = _heads(q, N, Hq, d, "q"), _heads(k, N, Hkv, d, "k")
+    (qo, qos), (ko, kos) = _heads(q_out, N, Hq, d, "q_out"), _heads(k_out, N, Hkv, d, "k_out")
+    _check("tq_qk_norm_rope", lib().tq_qk_norm_rope(
+        qp, qs, kp, ks, _dtype(q), N, Hq, Hkv, d, None if wq is None else _dev(wq, q.dtype, d, "wq"),
+        None if wk is None else _dev(wk, q.dtype, d, "wk"), eps,
+        None if freq is None else _dev(freq, torch.int64, 0, "freq"), 0 if freq is None else 2 * freq.numel(), style,
+        _dev(pos, torch.int32, N, "pos"), qo, qos, ko, kos, _dtype(q_out), _stream(stream)))
+
+
+def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
+    """tq_encode of x [N, Hkv, d] into a paged cache, token i at slots[i] (include/tq.h)."""
+    import torch
+    N, Hkv, d = x.shape
+    if d != ctx.d:
+        raise ValueError(f"x: rows of {ctx.d} elements are wanted")
+    if x.dtype not in (torch.float32, torch.float16):
+        raise ValueError("x: float32 or float16 is wanted")
+    _check("tq_encode_slots", lib().tq_encode_slots(
+        ctx.handle, _dev(x, x.dtype, 0, "x"), _dtype(x), N, Hkv, _dev(slots, torch.int64, N, "slots"), block,
+        ctypes.byref(codes.desc), _stream(stream)))
+
+
+def tq_tree_attention_workspace_size(kctx, B, Hq, Hkv, rows):
+    n = ctypes.c_size_t()
+    _check("tq_tree_attention_workspace_size",
+           lib().tq_tree_attention_workspace_size(kctx.handle, B, Hq, Hkv, rows, ctypes.byref(n)))
+    return n.value
+
+
+def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, table, block, scale, out, ws,
+                      Hkv=None, stream=None):
+    """Attention of drafted tokens q [rows, Hq, d] over a packed cache and each other (include/tq.h).  k_new, v_new
+    [rows, Hkv, d] or None (Hkv is then given); mask [rows, words] int32 or None (a chain); table [B, max_blocks] or
+    None (contiguous, cap = block)."""
+    import torch
+    rows, Hq, d = q.shape
+    B, Hkv = lens.numel(), k_new.shape[1] if k_new is not None else Hkv
+    qp, qs = _heads(q, rows, Hq, d, "q")
+    kp = vp = None
+    ks = vs = 0
+    if k_new is not None:
+        if k_new.dtype != q.dtype or v_new.dtype != q.dtype:
+            raise ValueError("q, k_new and v_new are of one type")
+        (kp, ks), (vp, vs) = _heads(k_new, rows, Hkv, d, "k_new"), _heads(v_new, rows, Hkv, d, "v_new")
+    i32 = torch.int32
+    words, width = 0 if mask is None else mask.shape[1], 0 if table is None else table.shape[1]
+    _check("tq_tree_attention", lib().tq_tree_attention(
+        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, _dtype(q), rows, _dev(row_start, i32, B + 1, "row_start"),
+        None if mask is None else _dev(mask, i32, rows * words, "mask"), words, ctypes.byref(K.desc),
+        ctypes.byref(V.desc), _dev(lens, i32, B, "lens"),
+        None if table is None else _dev(table, i32, B * width, "table"), width, block, B, Hq, Hkv, scale,
+        _dev(out, q.dtype, rows * Hq * d, "out"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
 
 
 def tq_unpack_indices(codes, first=0, count=None, with_bits=False):

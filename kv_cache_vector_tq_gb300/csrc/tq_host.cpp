@@ -942,7 +942,148 @@ tq_status tq_status_poll(const tq_ctx* ctx, tq_stream stream) {
   if (e == cudaSuccess) e = cudaStreamSynchronize((cudaStream_t)stream);
   if (e == cudaSuccess && h != 0) e = cudaMemsetAsync(v.status, 0, sizeof(int), (cudaStream_t)stream);
   if (e != cudaSuccess) return set_cuda_error(e);
-  return h == 0 ? TQ_OK : TQ_ERR_TIMEOUT;
+  return h == 0 ? TQ_OK : (h & 1) ? TQ_ERR_TIMEOUT : TQ_ERR_INVALID_ARG;
+}
+
+// ------------------------------------------------------------------ serving
+tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64_t N, int Hkv,
+                          const int64_t* d_slots, int block, const tq_codes* out, tq_stream stream) {
+  if (!ctx || !out) return TQ_ERR_INVALID_ARG;
+  const DevCtx& v = reinterpret_cast<const Ctx*>(ctx)->dev;
+  if (x_dtype != TQ_F32 && x_dtype != TQ_F16) return TQ_ERR_INVALID_ARG;
+  if (N < 0 || Hkv <= 0 || block <= 0) return TQ_ERR_INVALID_ARG;
+  const tq_status st = check_codes(v, out);
+  if (st != TQ_OK) return st;
+  if (N == 0) return TQ_OK;
+  if (!d_x || !al16(d_x) || !d_slots || ((uintptr_t)d_slots & 7u)) return TQ_ERR_INVALID_ARG;
+  if (block & 1) return TQ_ERR_UNSUPPORTED;  // a PAIR block stays inside its page
+  if (v.d != kChunk || !enc128_supported(v)) return TQ_ERR_UNSUPPORTED;
+  if (out->n < (int64_t)Hkv * block) return TQ_ERR_INVALID_ARG;  // not one page
+  return launch_encode_slots(v, d_x, x_dtype, N, Hkv, d_slots, block, out, (cudaStream_t)stream);
+}
+
+tq_status tq_block_tables(const int32_t* d_len, const int32_t* d_new, const int32_t* d_held, int B, int block,
+                          int32_t* d_ring, int64_t ring, const int64_t* d_state, int32_t* d_table, int max_blocks,
+                          int32_t* d_held_out, int64_t* d_state_out, int32_t* d_row_start, int64_t* d_slots,
+                          int32_t* d_pos, int64_t rows, tq_stream stream) {
+  if (B <= 0 || block <= 0 || ring <= 0 || max_blocks <= 0 || rows < 0) return TQ_ERR_INVALID_ARG;
+  if (!d_len || !d_new || !d_held || !d_ring || !d_state || !d_table || !d_held_out || !d_state_out || !d_row_start)
+    return TQ_ERR_INVALID_ARG;
+  if (rows > 0 && (!d_slots || !d_pos)) return TQ_ERR_INVALID_ARG;
+  if (d_held == d_held_out || d_state == d_state_out) return TQ_ERR_INVALID_ARG;
+  if (((uintptr_t)d_state | (uintptr_t)d_state_out | (uintptr_t)d_slots) & 7u) return TQ_ERR_INVALID_ARG;
+  if (B > block_tables_max_batch() || (int64_t)B * max_blocks > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+  return launch_block_tables(d_len, d_new, d_held, B, block, d_ring, ring, d_state, d_table, max_blocks, d_held_out,
+                             d_state_out, d_row_start, d_slots, d_pos, rows, (cudaStream_t)stream);
+}
+
+tq_status tq_rope_frequencies(int n, const double* h_inv_freq, uint64_t* h_freq) {
+  if (n < 0 || (n > 0 && (!h_inv_freq || !h_freq))) return TQ_ERR_INVALID_ARG;
+  for (int i = 0; i < n; ++i)
+    if (!std::isfinite(h_inv_freq[i])) return TQ_ERR_INVALID_ARG;
+  const double two_pi = 6.283185307179586476925;
+  for (int i = 0; i < n; ++i) {
+    double turn = h_inv_freq[i] / two_pi;
+    turn -= std::floor(turn);
+    h_freq[i] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0u;
+  }
+  return TQ_OK;
+}
+
+static int dtype_size(int t) { return t == TQ_F32 ? 4 : (t == TQ_F16 || t == TQ_BF16) ? 2 : 0; }
+
+tq_status tq_qk_norm_rope(const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride, int in_dtype,
+                          int64_t N, int Hq, int Hkv, int d, const void* d_wq, const void* d_wk, float eps,
+                          const uint64_t* d_freq, int rot, int style, const int32_t* d_pos, void* d_q_out,
+                          int64_t q_out_stride, void* d_k_out, int64_t k_out_stride, int out_dtype, tq_stream stream) {
+  const int si = dtype_size(in_dtype), so = dtype_size(out_dtype);
+  if (!si || !so || N < 0 || Hq < 0 || Hkv < 0 || Hq + Hkv <= 0 || d <= 0 || rot < 0 || rot > d)
+    return TQ_ERR_INVALID_ARG;
+  if (style != TQ_ROPE_HALF && style != TQ_ROPE_INTERLEAVED) return TQ_ERR_INVALID_ARG;
+  if (!(eps > 0.f) || !std::isfinite(eps)) return TQ_ERR_INVALID_ARG;
+  if ((Hq > 0 && (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d)) ||
+      (Hkv > 0 && (k_stride < (int64_t)Hkv * d || k_out_stride < (int64_t)Hkv * d)))
+    return TQ_ERR_INVALID_ARG;
+  if (d % 32 != 0 || d > 256 || rot % 16 != 0) return TQ_ERR_UNSUPPORTED;
+  if (N == 0) return TQ_OK;
+  if ((Hq > 0 && (!d_q || !d_q_out)) || (Hkv > 0 && (!d_k || !d_k_out)) || !d_pos || (rot > 0 && !d_freq))
+    return TQ_ERR_INVALID_ARG;
+  if (!al16(d_q) || !al16(d_k) || !al16(d_q_out) || !al16(d_k_out) || !al16(d_wq) || !al16(d_wk) ||
+      ((uintptr_t)d_freq & 7u))
+    return TQ_ERR_INVALID_ARG;
+  if ((Hq > 0 && (q_stride * si % 16 || q_out_stride * so % 16)) ||
+      (Hkv > 0 && (k_stride * si % 16 || k_out_stride * so % 16)))
+    return TQ_ERR_INVALID_ARG;
+  return launch_norm_rope(d_q, d_k, in_dtype, N, Hq, Hkv, d, q_stride, k_stride, d_wq, d_wk, eps, d_freq, rot, style,
+                          d_pos, d_q_out, d_k_out, out_dtype, q_out_stride, k_out_stride, (cudaStream_t)stream);
+}
+
+tq_status tq_tree_attention_workspace_size(const tq_ctx* kctx, int B, int Hq, int Hkv, int64_t rows, size_t* bytes) {
+  if (!kctx || !bytes || B <= 0 || Hq <= 0 || Hkv <= 0 || rows < 0) return TQ_ERR_INVALID_ARG;
+  *bytes = tree_ws_bytes(B, Hq, Hkv, rows);
+  return TQ_OK;
+}
+
+tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* d_q, int64_t q_stride,
+                            const void* d_k_new, int64_t k_stride, const void* d_v_new, int64_t v_stride, int dtype,
+                            int64_t rows, const int32_t* d_row_start, const uint32_t* d_mask, int mask_words,
+                            const tq_codes* K, const tq_codes* V, const int32_t* d_len, const int32_t* d_table,
+                            int max_blocks, int block, int B, int Hq, int Hkv, float scale, void* d_out, void* d_ws,
+                            size_t ws_bytes, tq_stream stream) {
+  if (!kctx || !vctx || !K || !V) return TQ_ERR_INVALID_ARG;
+  const DevCtx& kc = reinterpret_cast<const Ctx*>(kctx)->dev;
+  const DevCtx& vc = reinterpret_cast<const Ctx*>(vctx)->dev;
+  if (kc.d != vc.d) return TQ_ERR_INVALID_ARG;
+  tq_status st = check_codes(kc, K);
+  if (st != TQ_OK) return st;
+  st = check_codes(vc, V);
+  if (st != TQ_OK) return st;
+  if (K->layout != TQ_LAYOUT_TOKEN || V->layout != TQ_LAYOUT_PAIR) return TQ_ERR_INVALID_ARG;
+  const int sz = dtype_size(dtype);
+  if (!sz || rows < 0 || rows > INT32_MAX || B <= 0 || Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || block <= 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+  if ((d_k_new == nullptr) != (d_v_new == nullptr)) return TQ_ERR_INVALID_ARG;
+  if (q_stride < (int64_t)Hq * kc.d || (d_k_new && (k_stride < (int64_t)Hkv * kc.d || v_stride < (int64_t)Hkv * kc.d)))
+    return TQ_ERR_INVALID_ARG;
+  if (q_stride * sz % 16 || (d_k_new && (k_stride * sz % 16 || v_stride * sz % 16))) return TQ_ERR_INVALID_ARG;
+  if (d_mask && mask_words <= 0) return TQ_ERR_INVALID_ARG;
+  if (d_table && max_blocks <= 0) return TQ_ERR_INVALID_ARG;
+  const int64_t need = d_table ? (int64_t)Hkv * block : (int64_t)B * Hkv * block;  // vectors the caches must hold
+  if (need > K->n || need > V->n) return TQ_ERR_INVALID_ARG;
+  if ((d_table && (int64_t)max_blocks * block > INT32_MAX) || (int64_t)rows * Hq > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+  if (kc.d != kChunk || kc.mode != TQ_MSE || vc.mode != TQ_MSE || block % 16 != 0) return TQ_ERR_UNSUPPORTED;
+  if (rows == 0) return TQ_OK;
+  if (!d_q || !d_out || !d_ws || !d_row_start || !d_len) return TQ_ERR_INVALID_ARG;
+  if (!al16(d_q) || !al16(d_k_new) || !al16(d_v_new) || !al16(d_out) || !al16(d_ws) || !al16(K->d_norm) ||
+      !al16(V->d_norm))
+    return TQ_ERR_INVALID_ARG;
+  if (ws_bytes < tree_ws_bytes(B, Hq, Hkv, rows)) return TQ_ERR_INVALID_ARG;
+  TreeArgs a;
+  a.q = d_q;
+  a.k_new = d_k_new;
+  a.v_new = d_v_new;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.R = rows;
+  a.dtype = dtype;
+  a.row_start = d_row_start;
+  a.len = d_len;
+  a.table = d_table;
+  a.mask = d_mask;
+  a.mask_words = d_mask ? mask_words : 0;
+  a.max_blocks = max_blocks;
+  a.block = block;
+  a.B = B;
+  a.Hq = Hq;
+  a.Hkv = Hkv;
+  a.K = K;
+  a.V = V;
+  a.scale = scale;
+  a.out = d_out;
+  a.ws = d_ws;
+  return launch_tree(kc, vc, a, (cudaStream_t)stream);
 }
 
 }  // extern "C"

@@ -114,6 +114,31 @@ tq_status launch_encode_umma(const DevCtx& c, const void* x, int x_dtype, int64_
                              int64_t offset, int64_t group_rows, int64_t group_stride, cudaStream_t stream);
 tq_status launch_encode_wht(const DevCtx& c, const void* x, int x_dtype, int64_t N, const tq_codes* out,
                             int64_t offset, int64_t group_rows, int64_t group_stride, cudaStream_t stream);
+tq_status launch_encode_slots(const DevCtx& c, const void* x, int x_dtype, int64_t N, int Hkv, const int64_t* slots,
+                              int block, const tq_codes* out, cudaStream_t stream);
+tq_status launch_block_tables(const int32_t* len, const int32_t* nnew, const int32_t* held, int B, int block,
+                              int32_t* ring, int64_t ring_size, const int64_t* state, int32_t* table, int max_blocks,
+                              int32_t* held_out, int64_t* state_out, int32_t* row_start, int64_t* slots, int32_t* pos,
+                              int64_t rows, cudaStream_t stream);
+int block_tables_max_batch();
+tq_status launch_norm_rope(const void* q, const void* k, int in_dtype, int64_t N, int Hq, int Hkv, int d, int64_t qs,
+                           int64_t ks, const void* wq, const void* wk, float eps, const uint64_t* freq, int rot,
+                           int style, const int32_t* pos, void* qo, void* ko, int out_dtype, int64_t qos, int64_t kos,
+                           cudaStream_t stream);
+struct TreeArgs {
+  const void *q, *k_new, *v_new;
+  int64_t q_stride, k_stride, v_stride, R;
+  int dtype;
+  const int32_t *row_start, *len, *table;
+  const uint32_t* mask;
+  int mask_words, max_blocks, block, B, Hq, Hkv;
+  const tq_codes *K, *V;
+  float scale;
+  void* out;
+  void* ws;
+};
+size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R);
+tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cudaStream_t stream);
 // SM count of the current device (cached per device).
 int num_sms();
 // Current device, or -1 if the runtime cannot tell.

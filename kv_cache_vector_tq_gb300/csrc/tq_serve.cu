@@ -1,0 +1,454 @@
+// What a serving loop does around the packed cache, beside encode and
+// attention: pages for the tokens of a step (tq_block_tables) and the norms
+// and position rotation of queries and keys (tq_qk_norm_rope).
+#include <algorithm>
+
+#include <cuda_bf16.h>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+namespace {
+
+// ------------------------------------------------------------------ block tables
+//   need_b = ceil((len_b + new_b) / P), take_b = max(need_b - held_b, 0),
+//   give_b = max(held_b - need_b, 0); request b is served iff take_b = 0 or
+//   take_0 + ... + take_b <= tail - head.
+// Three prefix sums over the requests (takes, gives, served tokens) place every
+// page and every token row, so no CTA depends on another: each one computes the
+// sums for itself (B <= 4096 entries of L2-resident input) and fills its share
+// of the rows.  Rows read pages they hold from the table and new pages from the
+// ring, never what another CTA writes.  Bound by launch latency at a step's
+// sizes; the rows of a long prompt are spread over the grid.
+constexpr int kBtThreads = 512;
+constexpr int kBtMaxB = 4096;
+constexpr int kBtRowsPerCta = 2048;  // token rows that make another CTA worth its own prefix sums
+
+struct BlockTableParams {
+  const int32_t *len, *nnew, *held, *ring_in;
+  const int64_t* state;
+  int32_t *ring, *table, *held_out, *row_start, *pos;
+  int64_t *state_out, *slots;
+  int64_t ring_size, rows;
+  int B, block, max_blocks;
+};
+
+// Inclusive sums of x and y over the CTA's threads, in place; returns the totals.
+__device__ __forceinline__ int2 cta_scan2(int& x, int& y, int2* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(kFull, x, o), b = __shfl_up_sync(kFull, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
+  }
+  __syncthreads();  // the sums of the last call have been read
+  if (lane == 31) warp_sums[warp] = make_int2(x, y);
+  __syncthreads();
+  int2 base = make_int2(0, 0), tot = make_int2(0, 0);
+#pragma unroll
+  for (int w = 0; w < kBtThreads / 32; ++w) {
+    const int2 s = warp_sums[w];
+    if (w < warp) {
+      base.x += s.x;
+      base.y += s.y;
+    }
+    tot.x += s.x;
+    tot.y += s.y;
+  }
+  x += base.x;
+  y += base.y;
+  return tot;
+}
+
+__global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTableParams p) {
+  extern __shared__ int bt_smem[];
+  int* s_start = bt_smem;             // [B] first row of request b
+  int* s_first = bt_smem + p.B;       // [B] its first new page, counted from the ring's head
+  __shared__ int2 warp_sums[kBtThreads / 32];
+  __shared__ int s_taken;
+  const int tid = threadIdx.x;
+  const int64_t head = p.state[0], tail = p.state[1];
+  const int64_t avail = tail > head ? tail - head : 0;
+  if (tid == 0) s_taken = 0;
+  int take0 = 0, give0 = 0, row0 = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kBtThreads) {
+    const int b = b0 + tid;
+    int len = 0, nn = 0, held = 0, need = 0, take = 0, give = 0;
+    bool ok = false;
+    if (b < p.B) {
+      len = p.len[b];
+      nn = p.nnew[b];
+      held = p.held[b];
+      const int64_t want = ((int64_t)len + nn + p.block - 1) / p.block;
+      ok = len >= 0 && nn >= 0 && held >= 0 && held <= p.max_blocks && want <= p.max_blocks;
+      need = ok ? (int)want : held;
+      take = max(need - held, 0);
+      give = max(held - need, 0);
+    }
+    int it = take, ig = give;
+    const int2 tg = cta_scan2(it, ig, warp_sums);
+    it += take0;
+    ig += give0;
+    const bool served = ok && (take == 0 || it <= avail);
+    int rows = served ? nn : 0, dummy = 0;
+    const int mine = rows;
+    const int2 rr = cta_scan2(rows, dummy, warp_sums);
+    if (b < p.B) {
+      s_start[b] = row0 + rows - mine;
+      s_first[b] = it - take;
+      if (served && take > 0) atomicMax(&s_taken, it);
+      if (blockIdx.x == 0) {
+        p.held_out[b] = served ? need : held;
+        p.row_start[b] = row0 + rows - mine;
+      }
+      if (blockIdx.x == b % gridDim.x) {
+        int32_t* row = p.table + (int64_t)b * p.max_blocks;
+        // few pages a request: its own thread moves them (a prompt's many are moved below)
+        if (served && take <= 32)
+          for (int j = 0; j < take; ++j)
+            row[held + j] = p.ring_in[(head + (it - take) + j) % p.ring_size];
+        if (served && give <= 32)
+          for (int j = 0; j < give; ++j) {
+            const int64_t at = tail + (ig - give) + j;
+            if (at < head + p.ring_size) p.ring[at % p.ring_size] = row[need + j];
+          }
+      }
+    }
+    // requests that take or give many pages, one warp each
+    unsigned many = __ballot_sync(kFull, b < p.B && served && (take > 32 || give > 32) &&
+                                             blockIdx.x == b % gridDim.x);
+    while (many) {
+      const int src = __ffs(many) - 1;
+      many &= many - 1;
+      const int bb = __shfl_sync(kFull, b, src), t = __shfl_sync(kFull, take, src), g = __shfl_sync(kFull, give, src);
+      const int h = __shfl_sync(kFull, held, src), nd = __shfl_sync(kFull, need, src);
+      const int t0 = __shfl_sync(kFull, it, src) - t, g0 = __shfl_sync(kFull, ig, src) - g;
+      int32_t* row = p.table + (int64_t)bb * p.max_blocks;
+      if (t > 32)
+        for (int j = tid & 31; j < t; j += 32) row[h + j] = p.ring_in[(head + t0 + j) % p.ring_size];
+      if (g > 32)
+        for (int j = tid & 31; j < g; j += 32) {
+          const int64_t at = tail + g0 + j;
+          if (at < head + p.ring_size) p.ring[at % p.ring_size] = row[nd + j];
+        }
+    }
+    take0 += tg.x;
+    give0 += tg.y;
+    row0 += rr.x;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    p.row_start[p.B] = row0;
+    p.state_out[0] = head + s_taken;
+    p.state_out[1] = tail + give0;
+  }
+  for (int64_t r = (int64_t)blockIdx.x * kBtThreads + tid; r < p.rows; r += (int64_t)gridDim.x * kBtThreads) {
+    int64_t slot = -1;
+    int pos = 0;
+    if (r < row0) {
+      int lo = 0, hi = p.B - 1;  // last request whose first row is <= r (requests without rows come before it)
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_start[mid] <= r)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      pos = p.len[lo] + (int)(r - s_start[lo]);
+      const int j = pos / p.block, held = p.held[lo];
+      const int32_t page = j < held ? p.table[(int64_t)lo * p.max_blocks + j]
+                                          : p.ring_in[(head + s_first[lo] + (j - held)) % p.ring_size];
+      slot = page >= 0 ? (int64_t)page * p.block + pos % p.block : -1;
+    }
+    p.slots[r] = slot;
+    p.pos[r] = pos;
+  }
+}
+
+// ------------------------------------------------------------------ norms and rotation
+//   y = x · w / sqrt(mean(x²) + eps);  pairs (a, b) of y turn by the angle
+//   pos·f_j:  (a cos - b sin, b cos + a sin).
+// Angles: f_j as a 64-bit fraction of a turn, so that pos·f_j modulo one turn
+// is one 64-bit integer product, exact to 2^-64 of a turn per position (a
+// 32-bit angle is off by whole degrees past 10^6 positions).  The fraction's
+// leading 32 bits, as a signed multiple of half a turn, go to sincospif; its
+// rounding to fp32 is at most 2^-25 half turns.
+// One pass: a row is d/8 lanes of 8 elements (one 16-byte load of a 16-bit
+// type), its sum of squares a shuffle tree in fp32; the half-split pairing
+// takes its partner elements from the lane rot/16 away.  A warp keeps one
+// token's sines for its share of the heads.  HBM-bound for prompts; a token or
+// a tree is one launch latency.
+constexpr int kNrThreads = 256;
+
+struct NormRopeParams {
+  const void *q, *k, *wq, *wk;
+  void *qo, *ko;
+  const uint64_t* freq;
+  const int32_t* pos;
+  int64_t N, qs, ks, qos, kos;  // strides between tokens in elements
+  int Hq, Hkv, d, rot, style;
+  int chunk, chunks;  // heads per warp, warps per token
+  float eps;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  } else {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float2 f;
+      if constexpr (std::is_same<T, __half>::value)
+        f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      else
+        f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
+      v[2 * i] = f.x;
+      v[2 * i + 1] = f.y;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        w[i] = h2_bits(__floats2half2_rn(v[2 * i], v[2 * i + 1]));
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// LPR lanes per row (the power of two at or above d/8), U rows per lane group in flight.
+template <typename TI, typename TO, int LPR>
+__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int RPW = 32 / LPR, U = 2;
+  const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
+  const int64_t job = (int64_t)blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
+  if (job >= p.N * p.chunks) return;  // whole warps
+  const int64_t n = job / p.chunks;
+  const int h0 = (int)(job % p.chunks) * p.chunk, h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
+  const bool in = 8 * l < p.d;
+  const int j0 = 8 * l, half = p.rot >> 1;
+  // sines of this lane's 8 elements (half-split: element j turns with frequency j mod rot/2;
+  // interleaved: j / 2)
+  float cs[8], sn[8];
+  const uint64_t pos = (uint64_t)(int64_t)p.pos[n];
+  const bool turns = j0 < p.rot;
+  const bool second = p.style == 0 && j0 >= half;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    cs[e] = 1.f;
+    sn[e] = 0.f;
+    if (p.style == 0 || (e & 1) == 0) {
+      if (turns) {
+        const int f = p.style == 0 ? (j0 + e) - (second ? half : 0) : (j0 + e) >> 1;
+        const uint64_t t = pos * p.freq[f];
+        sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn[e], &cs[e]);
+      }
+    } else {
+      cs[e] = cs[e - 1];
+      sn[e] = sn[e - 1];
+    }
+  }
+  if (second) {  // b cos + a sin: the partner a is added
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
+  }
+  // partner lane of the half-split pairing (inside the row's LPR lanes)
+  const int plane = sub * LPR + (second ? l - (half >> 3) : l + (half >> 3));
+  float wq[8], wk[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) wq[e] = wk[e] = 1.f;
+  if (in && p.wq) load8(static_cast<const TI*>(p.wq) + j0, wq);
+  if (in && p.wk) load8(static_cast<const TI*>(p.wk) + j0, wk);
+  const float inv_d = 1.f / (float)p.d;
+
+  for (int hb = h0; hb < h1; hb += RPW * U) {
+    float x[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hb + u * RPW + sub;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
+      if (in && h < h1) {
+        const TI* src = h < p.Hq ? static_cast<const TI*>(p.q) + n * p.qs + (int64_t)h * p.d
+                                 : static_cast<const TI*>(p.k) + n * p.ks + (int64_t)(h - p.Hq) * p.d;
+        load8(src + j0, x[u]);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hb + u * RPW + sub;
+      const bool isq = h < p.Hq;
+      float ss = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+      float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+      if (__any_sync(kFull, !(ss < 1e36f))) {
+        // squares past the fp32 range: once more with the row scaled by the
+        // power of two that brings its largest magnitude to [1, 2)
+        float m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[u][e]));
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        int ex = 1;
+        if (m > 0.f && m < INFINITY) frexpf(m, &ex);
+        const float sc = ldexpf(1.f, 1 - ex);
+        float s2 = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s2 = fmaf(x[u][e] * sc, x[u][e] * sc, s2);
+#pragma unroll
+        for (int o = LPR / 2; o; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
+        if (!(ss < 1e36f)) r = rsqrtf(fmaf(s2, inv_d, p.eps * sc * sc)) * sc;
+      }
+      float y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = x[u][e] * r * (isq ? wq[e] : wk[e]);
+      float z[8];
+      if (p.style == 0) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_sync(kFull, y[e], plane & 31);
+          z[e] = turns ? fmaf(y[e], cs[e], -o * sn[e]) : y[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) {
+          z[e] = fmaf(y[e], cs[e], -y[e + 1] * sn[e]);
+          z[e + 1] = fmaf(y[e + 1], cs[e], y[e] * sn[e]);
+        }
+      }
+      if (in && h < h1) {
+        TO* dst = isq ? static_cast<TO*>(p.qo) + n * p.qos + (int64_t)h * p.d
+                      : static_cast<TO*>(p.ko) + n * p.kos + (int64_t)(h - p.Hq) * p.d;
+        store8(dst + j0, z);
+      }
+    }
+  }
+}
+
+template <typename TI, typename TO>
+cudaError_t run_norm_rope(NormRopeParams p, cudaStream_t st) {
+  int lpr = 4;
+  while (8 * lpr < p.d) lpr <<= 1;
+  const int heads = p.Hq + p.Hkv, rows_per_trip = 2 * (32 / lpr);
+  // a whole token per warp once the tokens alone fill the GPU (its sines are
+  // then computed once); else as many warps per token as there are trips
+  const int64_t fill = (int64_t)num_sms() * 32;
+  int64_t per = (fill + p.N - 1) / p.N;
+  const int trips = (heads + rows_per_trip - 1) / rows_per_trip;
+  per = std::max<int64_t>(1, std::min<int64_t>(per, trips));
+  p.chunk = (int)((trips + per - 1) / per) * rows_per_trip;
+  p.chunks = (heads + p.chunk - 1) / p.chunk;
+  const int64_t jobs = p.N * p.chunks, grid = (jobs + kNrThreads / 32 - 1) / (kNrThreads / 32);
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  switch (lpr) {
+    case 4: norm_rope_kernel<TI, TO, 4><<<(int)grid, kNrThreads, 0, st>>>(p); break;
+    case 8: norm_rope_kernel<TI, TO, 8><<<(int)grid, kNrThreads, 0, st>>>(p); break;
+    case 16: norm_rope_kernel<TI, TO, 16><<<(int)grid, kNrThreads, 0, st>>>(p); break;
+    case 32: norm_rope_kernel<TI, TO, 32><<<(int)grid, kNrThreads, 0, st>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
+template <typename TI>
+cudaError_t run_norm_rope_o(const NormRopeParams& p, int out_dtype, cudaStream_t st) {
+  switch (out_dtype) {
+    case TQ_F32: return run_norm_rope<TI, float>(p, st);
+    case TQ_F16: return run_norm_rope<TI, __half>(p, st);
+    case TQ_BF16: return run_norm_rope<TI, __nv_bfloat16>(p, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+int block_tables_max_batch() { return kBtMaxB; }
+
+tq_status launch_block_tables(const int32_t* len, const int32_t* nnew, const int32_t* held, int B, int block,
+                              int32_t* ring, int64_t ring_size, const int64_t* state, int32_t* table, int max_blocks,
+                              int32_t* held_out, int64_t* state_out, int32_t* row_start, int64_t* slots, int32_t* pos,
+                              int64_t rows, cudaStream_t stream) {
+  BlockTableParams p;
+  p.len = len;
+  p.nnew = nnew;
+  p.held = held;
+  p.ring_in = ring;
+  p.ring = ring;
+  p.state = state;
+  p.table = table;
+  p.held_out = held_out;
+  p.row_start = row_start;
+  p.pos = pos;
+  p.state_out = state_out;
+  p.slots = slots;
+  p.ring_size = ring_size;
+  p.rows = rows;
+  p.B = B;
+  p.block = block;
+  p.max_blocks = max_blocks;
+  const int64_t ctas = std::max<int64_t>((rows + kBtRowsPerCta - 1) / kBtRowsPerCta, (B + 63) / 64);
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(ctas, num_sms()));
+  block_tables_kernel<<<grid, kBtThreads, 2 * B * (int)sizeof(int), stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
+}
+
+tq_status launch_norm_rope(const void* q, const void* k, int in_dtype, int64_t N, int Hq, int Hkv, int d, int64_t qs,
+                           int64_t ks, const void* wq, const void* wk, float eps, const uint64_t* freq, int rot,
+                           int style, const int32_t* pos, void* qo, void* ko, int out_dtype, int64_t qos, int64_t kos,
+                           cudaStream_t stream) {
+  NormRopeParams p;
+  p.q = q;
+  p.k = k;
+  p.wq = wq;
+  p.wk = wk;
+  p.qo = qo;
+  p.ko = ko;
+  p.freq = freq;
+  p.pos = pos;
+  p.N = N;
+  p.qs = qs;
+  p.ks = ks;
+  p.qos = qos;
+  p.kos = kos;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.d = d;
+  p.rot = rot;
+  p.style = style;
+  p.eps = eps;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (in_dtype) {
+    case TQ_F32: e = run_norm_rope_o<float>(p, out_dtype, stream); break;
+    case TQ_F16: e = run_norm_rope_o<__half>(p, out_dtype, stream); break;
+    case TQ_BF16: e = run_norm_rope_o<__nv_bfloat16>(p, out_dtype, stream); break;
+  }
+  return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
+}
+
+}  // namespace tq

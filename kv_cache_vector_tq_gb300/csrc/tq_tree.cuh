@@ -1,0 +1,100 @@
+#pragma once
+// Attention of drafted tokens over a packed cache: what the kernels share.
+//
+//   out_i = (Σ_t p_it v̂_t + Σ_j p_ij v_j) / (Σ_t p_it + Σ_j p_ij),
+//   p = exp(scale·⟨q_i, k⟩), t over the cached tokens of the row's sequence,
+//   j over the drafted tokens that the row's mask names.
+//
+// Everything runs in the rotated domain: q, the drafted k and the drafted v
+// are rotated once (⟨q, k⟩ = ⟨Πq, Πk⟩), the cached k̂ = s·ŷ/√d needs no rotation
+// there, and the sum of values is rotated back once per row.
+//
+// Work: a group is (sequence, KV head, tile of kRows rows), a row being one
+// (drafted token, query head of the KV head) pair; its units are 128 cached
+// tokens each, then 128 drafted tokens each.  The units of all groups, laid
+// end to end, are shared evenly among the CTAs of a grid that fits the GPU
+// once, whatever the lengths are: lengths live on the device, so a captured
+// call serves every later length.  A CTA that starts a group leaves the rows'
+// state (m, l, acc) in their own records, one that continues a group in the
+// CTA's; a last kernel joins them.
+#include <cuda_bf16.h>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr int kTreeTok = 128;       // tokens per unit
+constexpr int kTreeRec = 132;       // floats per record: m, l, 2 pad, acc[128]
+constexpr float kTreeLog2e = 1.4426950408889634f;
+
+struct TreeParams {
+  const void *q, *kn, *vn;
+  int64_t qs, ks, vs;  // strides between tokens in elements
+  int dtype;
+  const int32_t *row_start, *len, *table;
+  const uint32_t* mask;
+  int mask_words;
+  int B, Hq, Hkv, G, max_blocks, block;
+  int64_t R, pages;
+  const uint32_t *kcodes, *vcodes;
+  const float *knorm, *vnorm;
+  int kb, vb;           // bits of a code
+  const float4 *kslices, *vslices;  // Π of the K and V contexts in column slices
+  const float* vpi;     // Π of the V context, row-major
+  float kcen[16], vcen[16];
+  float zscale;         // scale·log2(e)
+  void* out;
+  int* status;
+  // workspace
+  int64_t* unit_start;  // [B + 1] first unit of a sequence
+  float *qrot, *krot, *vrot;  // rotated rows, fp32
+  float *kfac, *vfac;         // [R·Hkv] factor of a drafted row (NaN: see tree_prep_kernel)
+  float* rec;           // [R·Hq] records of the rows
+  float* crec;          // [ctas][kRows] records of continued groups
+  int ctas, rows;       // CTAs of the grid, rows per tile
+};
+
+// A sequence as the kernels see it: bad offsets and lengths are cut to what
+// the buffers hold.
+struct TreeSeq {
+  int start, T, len, rt, per;  // first row, drafted tokens, cached tokens, row tiles, units per group
+};
+__device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
+  TreeSeq s;
+  const int64_t lo = min(max((int64_t)p.row_start[b], (int64_t)0), p.R);
+  const int64_t hi = min(max((int64_t)p.row_start[b + 1], lo), p.R);
+  s.start = (int)lo;
+  s.T = (int)(hi - lo);
+  s.len = (int)min((int64_t)max(p.len[b], 0), (int64_t)p.max_blocks * p.block);
+  s.rt = (int)(((int64_t)s.T * p.G + p.rows - 1) / p.rows);
+  s.per = (s.len + kTreeTok - 1) / kTreeTok + (p.kn ? (s.T + kTreeTok - 1) / kTreeTok : 0);
+  if (s.per < 1) s.per = 1;
+  return s;
+}
+// First unit of CTA c of n.
+__device__ __forceinline__ int64_t tree_cut(int64_t c, int64_t units, int64_t n) { return c * units / n; }
+
+// Largest index i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+template <typename T>
+__device__ __forceinline__ int tree_find(const T* a, int n, T x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= x)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ float tree_load(const void* p, int64_t i, int dtype) {
+  if (dtype == TQ_F32) return static_cast<const float*>(p)[i];
+  if (dtype == TQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
+  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+}
+
+cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st);
+
+}  // namespace tq
