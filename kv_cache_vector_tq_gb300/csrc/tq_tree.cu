@@ -18,19 +18,26 @@ namespace {
 // not see it are not touched by a product 0 · NaN.
 constexpr int kPrepV = 8;
 
+// TC: rows for the tensor cores, scaled by a power of two into fp16's range,
+// the leading part and (q) the remainder; else fp32.
+template <bool TC>
 __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
   __shared__ __align__(16) float xs[kPrepV][128];
+  __shared__ float wmax[kPrepV][4];
   __shared__ int64_t wsum[8];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  griddep_wait();
+  griddep_launch();
   const int64_t nq = p.R * p.Hq, nk = p.kn ? p.R * p.Hkv : 0;
   const int64_t cq = (nq + kPrepV - 1) / kPrepV, ck = (nk + kPrepV - 1) / kPrepV;
   if (blockIdx.x == 0) {
     int64_t base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 256) {
-      const int b = b0 + tid, lane = tid & 31, warp = tid >> 5;
+      const int b = b0 + tid;
+      TreeSeq s;
       int64_t n = 0;
       if (b < p.B) {
-        const TreeSeq s = tree_seq(p, b);
+        s = tree_seq(p, b);
         n = (int64_t)s.rt * p.Hkv * s.per;
       }
       int64_t inc = n;
@@ -48,34 +55,54 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
         if (w < warp) before += wsum[w];
         tot += wsum[w];
       }
-      if (b < p.B) p.unit_start[b] = base + before + inc - n;
+      if (b < p.B) {
+        s.unit = base + before + inc - n;
+        p.seq[b] = s;
+      }
       base += tot;
     }
-    if (tid == 0) p.unit_start[p.B] = base;
+    if (tid == 0) p.seq[p.B].unit = base;
+    __syncthreads();
+    for (int c = tid; c < p.ctas; c += 256) {
+      const int64_t u = tree_cut(c, base, p.ctas);
+      int lo = 0, hi = p.B - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.seq[mid].unit <= u)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      p.cta_seq[c] = lo;
+    }
     return;
   }
   int64_t c = blockIdx.x - 1;
   const void* src = p.q;
-  float *dst = p.qrot, *fac = nullptr;
+  float *dst = p.qrot, *fac = p.qfac;
   const float4* mat = p.kslices;
   int64_t stride = p.qs, n = nq;
-  int heads = p.Hq;
+  int heads = p.Hq, kind = 0;
+  float one = 1.f;
   if (c >= cq) {
     c -= cq;
     n = nk;
     heads = p.Hkv;
+    kind = 1;
     if (c >= ck) {
       c -= ck;
       src = p.vn;
       dst = p.vrot;
-      fac = p.vfac;
       mat = p.vslices;
       stride = p.vs;
+      fac = p.vfac;
+      one = p.vone;
     } else {
       src = p.kn;
       dst = p.krot;
-      fac = p.kfac;
       stride = p.ks;
+      fac = p.kfac;
+      one = p.kone;
     }
   }
   const int64_t v0 = c * kPrepV;
@@ -83,7 +110,7 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
   if (v0 >= live) return;
   for (int e = tid; e < kPrepV * 128; e += 256) {
     const int64_t v = v0 + (e >> 7);
-    xs[e >> 7][e & 127] = v < n ? tree_load(src, (v / heads) * stride + (v % heads) * 128 + (e & 127), p.dtype) : 0.f;
+    xs[e >> 7][e & 127] = v < live ? tree_load(src, (v / heads) * stride + (v % heads) * 128 + (e & 127), p.dtype) : 0.f;
   }
   __syncthreads();
   const int j = tid & 127, h = tid >> 7;
@@ -99,28 +126,48 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
       acc[v] = fmaf(w.x, x.x, fmaf(w.y, x.y, fmaf(w.z, x.z, fmaf(w.w, x.w, acc[v]))));
     }
   }
-  if (fac) {
-    int bad = 0;
-#pragma unroll
-    for (int v = 0; v < kPrepV / 2; ++v) bad |= (fabsf(acc[v]) <= 3.4e38f ? 0 : 1) << (h * (kPrepV / 2) + v);
-    bad = __reduce_or_sync(kFull, bad);
-    __shared__ int wbad[8];
-    if ((tid & 31) == 0) wbad[tid >> 5] = bad;
-    __syncthreads();
-    bad = 0;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) bad |= wbad[w];
+  if (!TC && kind == 0) {  // fp32 rows of q are used as they are
 #pragma unroll
     for (int v = 0; v < kPrepV / 2; ++v) {
-      const bool b = (bad >> (h * (kPrepV / 2) + v)) & 1;
-      if (b) acc[v] = 0.f;
-      if (j == 0 && v0 + h * (kPrepV / 2) + v < n) fac[v0 + h * (kPrepV / 2) + v] = b ? NAN : 1.f;
+      const int64_t at = v0 + h * (kPrepV / 2) + v;
+      if (at < n) dst[at * 128 + j] = acc[v];
     }
+    return;
   }
+  // the largest magnitude of every row (+inf where one is not a number)
 #pragma unroll
   for (int v = 0; v < kPrepV / 2; ++v) {
-    const int64_t at = v0 + h * (kPrepV / 2) + v;
-    if (at < n) dst[at * 128 + j] = acc[v];
+    float m = fabsf(acc[v]) <= 3.4e38f ? fabsf(acc[v]) : INFINITY;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if (lane == 0) wmax[h * (kPrepV / 2) + v][warp & 3] = m;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int v = 0; v < kPrepV / 2; ++v) {
+    const int vi = h * (kPrepV / 2) + v;
+    const int64_t at = v0 + vi;
+    const float m = fmaxf(fmaxf(wmax[vi][0], wmax[vi][1]), fmaxf(wmax[vi][2], wmax[vi][3]));
+    if (at >= n) continue;
+    const bool bad = m == INFINITY;
+    float sc = 1.f;
+    if (TC && m > 0.f && !bad) {  // largest magnitude to [2^11, 2^12) for q, [8, 16) for drafted rows
+      const int ex = (int)(__float_as_uint(m) >> 23) - 127, up = (kind == 0 ? 11 : 3) - ex;
+      sc = __uint_as_float((uint32_t)(127 + min(max(up, -120), 120)) << 23);
+    }
+    const float y = bad ? 0.f : acc[v] * sc;
+    if (j == 0) {
+      const float f = bad ? NAN : one / sc;
+      fac[kind == 0 ? at : (at % heads) * p.R + at / heads] = f;
+    }
+    if constexpr (TC) {
+      __half* d = reinterpret_cast<__half*>(dst) + at * (kind == 0 ? 256 : 128) + j;
+      const __half hi = __float2half_rn(y);
+      d[0] = hi;
+      if (kind == 0) d[128] = __float2half_rn(y - __half2float(hi));
+    } else {
+      dst[at * 128 + j] = y;
+    }
   }
 }
 
@@ -160,18 +207,17 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
     cen[tid] = p.kcen[tid];
     cen[16 + tid] = p.vcen[tid];
   }
-  const int64_t units = p.unit_start[p.B];
+  griddep_wait();
+  griddep_launch();
+  const int64_t units = p.seq[p.B].unit;
   int64_t u = tree_cut(blockIdx.x, units, p.ctas);
   const int64_t u_end = tree_cut(blockIdx.x + 1, units, p.ctas);
+  int sb = u < u_end ? p.cta_seq[blockIdx.x] : 0;
   while (u < u_end) {
-    const int b = tree_find(p.unit_start, p.B, u);
-    const TreeSeq s = tree_seq(p, b);
-    const int64_t w = u - p.unit_start[b];
-    const int grp = (int)(w / s.per), first = (int)(w % s.per);
-    const int kvh = grp / s.rt, rt = grp % s.rt;
-    const int last = (int)min((int64_t)s.per, first + (u_end - u));
-    const int row0 = rt * kFRows, nrow = min(kFRows, s.T * p.G - row0);
-    const int ctiles = (s.len + kTreeTok - 1) / kTreeTok;
+    const TreeSeg g = tree_seg(p, u, u_end, sb);
+    sb = g.b;
+    const TreeSeq& s = g.s;
+    const int b = g.b, kvh = g.kvh, row0 = g.row0, nrow = g.nrow, first = g.first, last = g.last, ctiles = g.ctiles;
     __syncthreads();
     for (int e = tid; e < kFRows * 128; e += 256) {
       const int r = e >> 7, rho = row0 + r;
@@ -208,8 +254,8 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
             vd[k] = good ? *reinterpret_cast<const float4*>(p.vrot + at + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
           if (good) {
-            skn = p.kfac[at >> 7];
-            svn = p.vfac[at >> 7];
+            skn = p.kfac[(int64_t)kvh * p.R + s.start + t0 + tok];
+            svn = p.vfac[(int64_t)kvh * p.R + s.start + t0 + tok];
           }
         } else {
           int64_t vec = 0;
@@ -364,20 +410,22 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
 __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
   __shared__ __align__(16) float os[kPrepV][128];
   const int tid = threadIdx.x, j = tid & 127, h = tid >> 7;
+  griddep_wait();
+  griddep_launch();
   const int64_t v0 = (int64_t)blockIdx.x * kPrepV;
   const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * p.Hq;
   if (v0 >= live) return;
-  const int64_t units = p.unit_start[p.B];
+  const int64_t units = p.seq[p.B].unit;
   for (int v = h; v < kPrepV; v += 2) {
     const int64_t at = v0 + v;
     float val = 0.f;
     if (at < live) {
       const int r = (int)(at / p.Hq), head = (int)(at % p.Hq), kvh = head / p.G;
       const int b = tree_find(p.row_start, p.B, r);  // the last sequence that starts at or before r
-      const TreeSeq s = tree_seq(p, b);
+      const TreeSeq s = p.seq[b];
       const int rho = (r - s.start) * p.G + head % p.G;
       if (r >= s.start && r < s.start + s.T) {
-        const int64_t gs = p.unit_start[b] + (int64_t)(kvh * s.rt + rho / p.rows) * s.per, ge = gs + s.per;
+        const int64_t gs = s.unit + (int64_t)(kvh * s.rt + rho / p.rows) * s.per, ge = gs + s.per;
         const int64_t c0 = ((gs + 1) * p.ctas - 1) / units, c1 = (ge * p.ctas - 1) / units;
         const float* own = p.rec + at * kTreeRec;
         float M = own[0], L = own[1], A = own[4 + j];
@@ -394,7 +442,7 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
         val = L > 0.f ? A / L : (L == 0.f ? 0.f : A + L);  // a NaN stays one
       }
     }
-    os[v][j] = val;
+    os[v][j] = val * p.ofold;
   }
   __syncthreads();
   float acc[kPrepV / 2];
@@ -426,18 +474,21 @@ __global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 struct TreeWs {
-  size_t units, q, k, v, kf, vf, rec, crec, total;
+  size_t seq, cta, q, k, v, qf, kf, vf, rec, crec, total;
 };
 TreeWs tree_ws(int B, int Hq, int Hkv, int64_t R) {
   TreeWs w;
-  w.units = 0;
-  w.q = w.units + al256((size_t)(B + 1) * 8);
-  w.k = w.q + al256((size_t)R * Hq * 512);
-  w.v = w.k + al256((size_t)R * Hkv * 512);
-  w.kf = w.v + al256((size_t)R * Hkv * 512);
-  w.vf = w.kf + al256((size_t)R * Hkv * 4);
-  w.rec = w.vf + al256((size_t)R * Hkv * 4);
-  w.crec = w.rec + al256((size_t)R * Hq * kTreeRec * 4);
+  const size_t rq = (size_t)R * Hq, rk = (size_t)R * Hkv;
+  w.seq = 0;
+  w.cta = w.seq + al256((size_t)(B + 1) * sizeof(TreeSeq));
+  w.q = w.cta + al256((size_t)num_sms() * 4);
+  w.k = w.q + al256(rq * 512);
+  w.v = w.k + al256(rk * 512);
+  w.qf = w.v + al256(rk * 512);
+  w.kf = w.qf + al256(rq * 4);
+  w.vf = w.kf + al256(rk * 4);
+  w.rec = w.vf + al256(rk * 4);
+  w.crec = w.rec + al256(rq * kTreeRec * 4);
   w.total = w.crec + al256((size_t)num_sms() * 128 * kTreeRec * 4);
   return w;
 }
@@ -448,8 +499,7 @@ cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st) {
   static PerDeviceValue attr;
   const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_f32_kernel, kFSmem);
   if (e != cudaSuccess) return e;
-  tree_attend_f32_kernel<<<p.ctas, 256, kFSmem, st>>>(p);
-  return cudaGetLastError();
+  return tree_launch(tree_attend_f32_kernel, p.ctas, 256, kFSmem, p, st);
 }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R) { return tree_ws(B, Hq, Hkv, R).total; }
@@ -494,25 +544,38 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   p.status = kc.status;
   const TreeWs w = tree_ws(a.B, a.Hq, a.Hkv, a.R);
   unsigned char* base = static_cast<unsigned char*>(a.ws);
-  p.unit_start = reinterpret_cast<int64_t*>(base + w.units);
+  p.seq = reinterpret_cast<TreeSeq*>(base + w.seq);
+  p.cta_seq = reinterpret_cast<int*>(base + w.cta);
   p.qrot = reinterpret_cast<float*>(base + w.q);
   p.krot = reinterpret_cast<float*>(base + w.k);
   p.vrot = reinterpret_cast<float*>(base + w.v);
+  p.qfac = reinterpret_cast<float*>(base + w.qf);
   p.kfac = reinterpret_cast<float*>(base + w.kf);
   p.vfac = reinterpret_cast<float*>(base + w.vf);
   p.rec = reinterpret_cast<float*>(base + w.rec);
   p.crec = reinterpret_cast<float*>(base + w.crec);
   p.ctas = num_sms();
-  p.rows = kFRows;
+  // fp32 rows are computed in fp32; 16-bit types round coarser than the
+  // tensor-core kernel does
+  const bool tc = a.dtype != TQ_F32;
+  p.rows = tc ? 128 : kFRows;
+  p.klut = kc.lut;
+  p.vlut = vc.lut;
+  bool same = kc.b_mse == vc.b_mse && kc.alpha == vc.alpha;
+  for (int k = 0; same && k < (1 << kc.b_mse); ++k) same = kc.cen[k] == vc.cen[k];
+  p.same_lut = same;
+  p.kone = tc ? kc.sqrt_d * kc.alpha : 1.f;
+  p.vone = tc ? vc.sqrt_d * vc.alpha : 1.f;
+  p.zfold = p.zscale / p.kone;
+  p.ofold = 1.f / p.vone;
+  p.wait_limit = kc.wait_limit;
   const int64_t nq = (a.R * a.Hq + kPrepV - 1) / kPrepV, nk = a.k_new ? (a.R * a.Hkv + kPrepV - 1) / kPrepV : 0;
   if (1 + nq + 2 * nk > INT32_MAX) return TQ_ERR_UNSUPPORTED;
-  tree_prep_kernel<<<(int)(1 + nq + 2 * nk), 256, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e == cudaSuccess) e = tree_attend_f32(p, stream);
-  if (e == cudaSuccess) {
-    tree_join_kernel<<<(int)nq, 256, 0, stream>>>(p);
-    e = cudaGetLastError();
-  }
+  const int grid = (int)(1 + nq + 2 * nk);
+  cudaError_t e = tc ? tree_launch(tree_prep_kernel<true>, grid, 256, 0, p, stream)
+                     : tree_launch(tree_prep_kernel<false>, grid, 256, 0, p, stream);
+  if (e == cudaSuccess) e = tc ? tree_attend_umma(p, stream) : tree_attend_f32(p, stream);
+  if (e == cudaSuccess) e = tree_launch(tree_join_kernel, (int)nq, 256, 0, p, stream);
   return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
 }
 

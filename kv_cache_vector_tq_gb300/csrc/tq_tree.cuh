@@ -28,6 +28,14 @@ constexpr int kTreeTok = 128;       // tokens per unit
 constexpr int kTreeRec = 132;       // floats per record: m, l, 2 pad, acc[128]
 constexpr float kTreeLog2e = 1.4426950408889634f;
 
+// A sequence as the kernels see it: bad offsets and lengths are cut to what
+// the buffers hold.  unit: its first unit.
+struct TreeSeq {
+  int start, T, len, rt, per;  // first row, drafted tokens, cached tokens, row tiles, units per group
+  int pad;
+  int64_t unit;
+};
+
 struct TreeParams {
   const void *q, *kn, *vn;
   int64_t qs, ks, vs;  // strides between tokens in elements
@@ -44,22 +52,26 @@ struct TreeParams {
   const float* vpi;     // Π of the V context, row-major
   float kcen[16], vcen[16];
   float zscale;         // scale·log2(e)
+  // tensor-core path
+  const uint32_t *klut, *vlut;  // pair tables α·c
+  int same_lut;
+  float zfold;          // scale·log2(e)/(√d·α_K)
+  float kone, vone;     // factor of a drafted row of scale 1: √d·α (fp32 path: 1)
+  float ofold;          // 1/(√d·α_V) (fp32 path: 1)
+  uint32_t wait_limit;
   void* out;
   int* status;
   // workspace
-  int64_t* unit_start;  // [B + 1] first unit of a sequence
-  float *qrot, *krot, *vrot;  // rotated rows, fp32
-  float *kfac, *vfac;         // [R·Hkv] factor of a drafted row (NaN: see tree_prep_kernel)
+  TreeSeq* seq;         // [B + 1]; seq[B].unit: the number of units
+  int* cta_seq;         // [ctas] the sequence of a CTA's first unit
+  float *qrot, *krot, *vrot;  // rotated rows: fp32, or fp16 (q: 128 leading parts, 128 remainders)
+  float* qfac;          // [R·Hq] power of two that was divided out of a row of q (tensor-core path)
+  float *kfac, *vfac;   // [Hkv][R] the same of the drafted rows, times kone / vone
   float* rec;           // [R·Hq] records of the rows
-  float* crec;          // [ctas][kRows] records of continued groups
+  float* crec;          // [ctas][rows] records of continued groups
   int ctas, rows;       // CTAs of the grid, rows per tile
 };
 
-// A sequence as the kernels see it: bad offsets and lengths are cut to what
-// the buffers hold.
-struct TreeSeq {
-  int start, T, len, rt, per;  // first row, drafted tokens, cached tokens, row tiles, units per group
-};
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   TreeSeq s;
   const int64_t lo = min(max((int64_t)p.row_start[b], (int64_t)0), p.R);
@@ -70,6 +82,8 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.rt = (int)(((int64_t)s.T * p.G + p.rows - 1) / p.rows);
   s.per = (s.len + kTreeTok - 1) / kTreeTok + (p.kn ? (s.T + kTreeTok - 1) / kTreeTok : 0);
   if (s.per < 1) s.per = 1;
+  s.pad = 0;
+  s.unit = 0;
   return s;
 }
 // First unit of CTA c of n.
@@ -89,6 +103,28 @@ __device__ __forceinline__ int tree_find(const T* a, int n, T x) {
   return lo;
 }
 
+// A run of units of one group: units [first, last) of it, rows row0.. of the group.
+struct TreeSeg {
+  int b, kvh, row0, nrow, first, last, ctiles;
+  TreeSeq s;
+};
+// The segment that starts at unit u (b: a sequence at or before it).
+__device__ __forceinline__ TreeSeg tree_seg(const TreeParams& p, int64_t u, int64_t u_end, int b) {
+  TreeSeg g;
+  while (b + 1 < p.B && p.seq[b + 1].unit <= u) ++b;
+  g.b = b;
+  g.s = p.seq[b];
+  const int w = (int)(u - g.s.unit);  // fewer than 2^31 units in a sequence: rows and lengths are
+  const int grp = w / g.s.per;
+  g.first = w - grp * g.s.per;
+  g.kvh = grp / g.s.rt;
+  g.row0 = (grp - g.kvh * g.s.rt) * p.rows;
+  g.nrow = min(p.rows, g.s.T * p.G - g.row0);
+  g.last = (int)min((int64_t)g.s.per, g.first + (u_end - u));
+  g.ctiles = (g.s.len + kTreeTok - 1) / kTreeTok;
+  return g;
+}
+
 __device__ __forceinline__ float tree_load(const void* p, int64_t i, int dtype) {
   if (dtype == TQ_F32) return static_cast<const float*>(p)[i];
   if (dtype == TQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
@@ -96,5 +132,23 @@ __device__ __forceinline__ float tree_load(const void* p, int64_t i, int dtype) 
 }
 
 cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st);
+cudaError_t tree_attend_umma(const TreeParams& p, cudaStream_t st);
+
+// A launch that may begin while the kernel before it in the stream ends; every
+// kernel here waits for that one (griddep_wait) before it touches its data.
+template <typename K>
+inline cudaError_t tree_launch(K kernel, int grid, int threads, size_t smem, const TreeParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
 
 }  // namespace tq
