@@ -10,27 +10,33 @@ namespace tq {
 namespace {
 
 // ------------------------------------------------------------------ rotation of q, k, v
-// y = Π·x for kPrepV vectors per CTA: thread (coordinate, half of the vectors),
-// the matrix in column slices (coalesced, L2-resident), x broadcast from
-// shared memory, fp32 sums.  CTA 0 also lays out the units of the sequences.
+// y = Π·x for groups of kPrepV vectors.  Warp w of a CTA keeps columns
+// [16w, 16w + 16) of the matrix in registers (loaded once, before the wait for
+// the kernel ahead: the matrix is constant), every lane four rows of them, and
+// multiplies group after group; the eight partial sums meet in shared memory.
+// fp32 sums.  CTA 0 also lays out the units of the sequences.
 // A drafted row that holds an infinity or a NaN is stored as zeros with the
 // factor NaN: rows that see it become NaN through the factor, and rows that do
 // not see it are not touched by a product 0 · NaN.
 constexpr int kPrepV = 8;
 
+// part[w][v][j]: warp w's share of coordinate j of vector v.
+struct RotSmem {
+  float x[kPrepV][128];
+  float part[8][kPrepV][128];
+};
+
 // TC: rows for the tensor cores, scaled by a power of two into fp16's range,
 // the leading part and (q) the remainder; else fp32.
 template <bool TC>
-__global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
-  __shared__ __align__(16) float xs[kPrepV][128];
+__global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, const int per, const int nbq, const int nbk) {
+  __shared__ __align__(16) RotSmem sm;
   __shared__ float wmax[kPrepV][4];
   __shared__ int64_t wsum[8];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  griddep_wait();
-  griddep_launch();
-  const int64_t nq = p.R * p.Hq, nk = p.kn ? p.R * p.Hkv : 0;
-  const int64_t cq = (nq + kPrepV - 1) / kPrepV, ck = (nk + kPrepV - 1) / kPrepV;
   if (blockIdx.x == 0) {
+    griddep_wait();
+    griddep_launch();
     int64_t base = 0;
     for (int b0 = 0; b0 < p.B; b0 += 256) {
       const int b = b0 + tid;
@@ -77,20 +83,19 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
     }
     return;
   }
-  int64_t c = blockIdx.x - 1;
+  // this CTA's rows: q, drafted k or drafted v, `per` groups of kPrepV
+  int c = blockIdx.x - 1, kind = 0, heads = p.Hq;
   const void* src = p.q;
   float *dst = p.qrot, *fac = p.qfac;
   const float4* mat = p.kslices;
-  int64_t stride = p.qs, n = nq;
-  int heads = p.Hq, kind = 0;
+  int64_t stride = p.qs;
   float one = 1.f;
-  if (c >= cq) {
-    c -= cq;
-    n = nk;
+  if (c >= nbq) {
+    c -= nbq;
     heads = p.Hkv;
     kind = 1;
-    if (c >= ck) {
-      c -= ck;
+    if (c >= nbk) {
+      c -= nbk;
       src = p.vn;
       dst = p.vrot;
       mat = p.vslices;
@@ -105,68 +110,82 @@ __global__ void __launch_bounds__(256) tree_prep_kernel(const TreeParams p) {
       one = p.kone;
     }
   }
-  const int64_t v0 = c * kPrepV;
+  float4 w[4][4];  // Π[32b + lane][16·warp + 4a ..]
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) w[a][b] = __ldg(mat + (4 * warp + a) * 128 + 32 * b + lane);
+  griddep_wait();
+  griddep_launch();
   const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * heads;
-  if (v0 >= live) return;
-  for (int e = tid; e < kPrepV * 128; e += 256) {
-    const int64_t v = v0 + (e >> 7);
-    xs[e >> 7][e & 127] = v < live ? tree_load(src, (v / heads) * stride + (v % heads) * 128 + (e & 127), p.dtype) : 0.f;
-  }
-  __syncthreads();
-  const int j = tid & 127, h = tid >> 7;
-  float acc[kPrepV / 2];
+  for (int gi = 0; gi < per; ++gi) {
+    const int64_t v0 = ((int64_t)c * per + gi) * kPrepV;
+    if (v0 >= live) return;
+    {  // a warp per row, four elements a lane (rows of all kinds: fewer than 2^31)
+      const uint32_t v = (uint32_t)v0 + warp;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (v < (uint32_t)live) {
+        const uint32_t r = v / (uint32_t)heads;
+        x = tree_load4(src, (int64_t)r * stride + (v - r * heads) * 128 + 4 * lane, p.dtype);
+      }
+      *reinterpret_cast<float4*>(&sm.x[warp][4 * lane]) = x;
+    }
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < kPrepV / 2; ++v) acc[v] = 0.f;
-#pragma unroll 8
-  for (int i4 = 0; i4 < 32; ++i4) {
-    const float4 w = __ldg(mat + i4 * 128 + j);
+    for (int v = 0; v < kPrepV; ++v) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.x[v][16 * warp + 4 * a]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+          acc[b] = fmaf(w[a][b].x, x.x, fmaf(w[a][b].y, x.y, fmaf(w[a][b].z, x.z, fmaf(w[a][b].w, x.w, acc[b]))));
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b) sm.part[warp][v][32 * b + lane] = acc[b];
+    }
+    __syncthreads();
+    const int j = tid & 127, h = tid >> 7;
+    float y[kPrepV / 2];
 #pragma unroll
     for (int v = 0; v < kPrepV / 2; ++v) {
-      const float4 x = *reinterpret_cast<const float4*>(&xs[h * (kPrepV / 2) + v][4 * i4]);
-      acc[v] = fmaf(w.x, x.x, fmaf(w.y, x.y, fmaf(w.z, x.z, fmaf(w.w, x.w, acc[v]))));
+      const int vi = h * (kPrepV / 2) + v;
+      float s = 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += sm.part[k][vi][j];
+      y[v] = s;
+      // the row's largest magnitude (+inf where one is not a number)
+      float m = fabsf(s) <= 3.4e38f ? fabsf(s) : INFINITY;
+#pragma unroll
+      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      if (lane == 0) wmax[vi][warp & 3] = m;
     }
-  }
-  if (!TC && kind == 0) {  // fp32 rows of q are used as they are
+    __syncthreads();
 #pragma unroll
     for (int v = 0; v < kPrepV / 2; ++v) {
-      const int64_t at = v0 + h * (kPrepV / 2) + v;
-      if (at < n) dst[at * 128 + j] = acc[v];
-    }
-    return;
-  }
-  // the largest magnitude of every row (+inf where one is not a number)
-#pragma unroll
-  for (int v = 0; v < kPrepV / 2; ++v) {
-    float m = fabsf(acc[v]) <= 3.4e38f ? fabsf(acc[v]) : INFINITY;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if (lane == 0) wmax[h * (kPrepV / 2) + v][warp & 3] = m;
-  }
-  __syncthreads();
-#pragma unroll
-  for (int v = 0; v < kPrepV / 2; ++v) {
-    const int vi = h * (kPrepV / 2) + v;
-    const int64_t at = v0 + vi;
-    const float m = fmaxf(fmaxf(wmax[vi][0], wmax[vi][1]), fmaxf(wmax[vi][2], wmax[vi][3]));
-    if (at >= n) continue;
-    const bool bad = m == INFINITY;
-    float sc = 1.f;
-    if (TC && m > 0.f && !bad) {  // largest magnitude to [2^11, 2^12) for q, [8, 16) for drafted rows
-      const int ex = (int)(__float_as_uint(m) >> 23) - 127, up = (kind == 0 ? 11 : 3) - ex;
-      sc = __uint_as_float((uint32_t)(127 + min(max(up, -120), 120)) << 23);
-    }
-    const float y = bad ? 0.f : acc[v] * sc;
-    if (j == 0) {
-      const float f = bad ? NAN : one / sc;
-      fac[kind == 0 ? at : (at % heads) * p.R + at / heads] = f;
-    }
-    if constexpr (TC) {
-      __half* d = reinterpret_cast<__half*>(dst) + at * (kind == 0 ? 256 : 128) + j;
-      const __half hi = __float2half_rn(y);
-      d[0] = hi;
-      if (kind == 0) d[128] = __float2half_rn(y - __half2float(hi));
-    } else {
-      dst[at * 128 + j] = y;
+      const int vi = h * (kPrepV / 2) + v;
+      const int64_t at = v0 + vi;
+      const float m = fmaxf(fmaxf(wmax[vi][0], wmax[vi][1]), fmaxf(wmax[vi][2], wmax[vi][3]));
+      if (at >= live) continue;
+      const bool bad = m == INFINITY && (TC || kind != 0);  // fp32 rows of q are used as they are
+      float sc = 1.f;
+      if (TC && m > 0.f && !bad) {  // largest magnitude to [2^11, 2^12) for q, [8, 16) for drafted rows
+        const int ex = (int)(__float_as_uint(m) >> 23) - 127, up = (kind == 0 ? 11 : 3) - ex;
+        sc = __uint_as_float((uint32_t)(127 + min(max(up, -120), 120)) << 23);
+      }
+      const float z = bad ? 0.f : y[v] * sc;
+      if (j == 0) {
+        const uint32_t r = (uint32_t)at / (uint32_t)heads;
+        fac[kind == 0 ? at : (int64_t)((uint32_t)at - r * heads) * p.R + r] = bad ? NAN : one / sc;
+      }
+      if constexpr (TC) {
+        __half* d = reinterpret_cast<__half*>(dst) + at * (kind == 0 ? 256 : 128) + j;
+        const __half hi = __float2half_rn(z);
+        d[0] = hi;
+        if (kind == 0) d[128] = __float2half_rn(z - __half2float(hi));
+      } else {
+        dst[at * 128 + j] = z;
+      }
     }
   }
 }
@@ -404,70 +423,137 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
 }
 
 // ------------------------------------------------------------------ join and rotation back
-// kPrepV rows per CTA: each row's records (its own and those of the CTAs that
-// continued its group) under their common maximum, divided by the sum, then
-// out = Πᵀ·o.  A row that saw nothing is zero.
-__global__ void __launch_bounds__(256) tree_join_kernel(const TreeParams p) {
-  __shared__ __align__(16) float os[kPrepV][128];
-  const int tid = threadIdx.x, j = tid & 127, h = tid >> 7;
+// A warp per row: its records (its own and those of the CTAs that continued its
+// group) under their common maximum, divided by the sum of weights; then
+// out = Πᵀ·o for the CTA's kPrepV rows, the matrix in registers as in the
+// rotation.  A row that saw nothing is zero.
+__global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, const int per) {
+  __shared__ __align__(16) RotSmem sm;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float4 w[16];  // Π[16·warp + k][4·lane ..]
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = __ldg(reinterpret_cast<const float4*>(p.vpi + (16 * warp + k) * 128) + lane);
   griddep_wait();
   griddep_launch();
-  const int64_t v0 = (int64_t)blockIdx.x * kPrepV;
   const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * p.Hq;
-  if (v0 >= live) return;
   const int64_t units = p.seq[p.B].unit;
-  for (int v = h; v < kPrepV; v += 2) {
-    const int64_t at = v0 + v;
-    float val = 0.f;
+  for (int gi = 0; gi < per; ++gi) {
+    const int64_t v0 = ((int64_t)blockIdx.x * per + gi) * kPrepV;
+    if (v0 >= live) return;
+    const int64_t at = v0 + warp;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
     if (at < live) {
-      const int r = (int)(at / p.Hq), head = (int)(at % p.Hq), kvh = head / p.G;
+      const int r = (int)((uint32_t)at / (uint32_t)p.Hq), head = (int)at - r * p.Hq, kvh = head / p.G;
       const int b = tree_find(p.row_start, p.B, r);  // the last sequence that starts at or before r
       const TreeSeq s = p.seq[b];
-      const int rho = (r - s.start) * p.G + head % p.G;
       if (r >= s.start && r < s.start + s.T) {
-        const int64_t gs = s.unit + (int64_t)(kvh * s.rt + rho / p.rows) * s.per, ge = gs + s.per;
-        const int64_t c0 = ((gs + 1) * p.ctas - 1) / units, c1 = (ge * p.ctas - 1) / units;
+        const int rho = (r - s.start) * p.G + head - kvh * p.G;
+        const int rt = rho / p.rows;
+        const int64_t gs = s.unit + (int64_t)(kvh * s.rt + rt) * s.per, ge = gs + s.per;
+        const int64_t n0 = (gs + 1) * p.ctas - 1, n1 = ge * p.ctas - 1;  // 32-bit division where it will do
+        const bool small = n1 <= 0xFFFFFFFFll;
+        const int c0 = small ? (int)((uint32_t)n0 / (uint32_t)units) : (int)(n0 / units);
+        const int c1 = small ? (int)((uint32_t)n1 / (uint32_t)units) : (int)(n1 / units);
         const float* own = p.rec + at * kTreeRec;
-        float M = own[0], L = own[1], A = own[4 + j];
-        for (int64_t c = c0 + 1; c <= c1; ++c) {
-          if (tree_cut(c + 1, units, p.ctas) == tree_cut(c, units, p.ctas)) continue;  // no unit of its own
-          const float* rec = p.crec + (c * p.rows + rho % p.rows) * kTreeRec;
-          const float m = rec[0];
-          if (rec[1] == 0.f) continue;  // saw nothing (a NaN sum goes on)
-          const float nm = fmaxf(M, m), fa = M == -INFINITY ? 0.f : exp2f(M - nm), fb = exp2f(m - nm);
-          L = L * fa + rec[1] * fb;
-          A = A * fa + rec[4 + j] * fb;
+        const float* more = p.crec + (int64_t)(rho - rt * p.rows) * kTreeRec;
+        const int64_t step = (int64_t)p.rows * kTreeRec;
+        // records 0 (own) .. c1 - c0, 32 at a time; with fewer units than CTAs
+        // some of the CTAs between have none
+        float M = -INFINITY, L = 0.f;
+        for (int k0 = 0; k0 <= c1 - c0; k0 += 32) {
+          const int k = k0 + lane;
+          bool on = k <= c1 - c0;
+          if (on && k > 0 && units < p.ctas)
+            on = tree_cut(c0 + k + 1, units, p.ctas) != tree_cut(c0 + k, units, p.ctas);
+          float m = -INFINITY, l = 0.f;
+          if (on) {
+            const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
+            m = ml.x;
+            l = ml.y;
+          }
+          on = on && l != 0.f;  // saw nothing (a NaN sum goes on)
+          float top = on ? m : -INFINITY;
+#pragma unroll
+          for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+          const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
+          const float fa = M == -INFINITY ? 0.f : exp2f(M - use);
+          const float f = on ? exp2f(m - use) : 0.f;
+          float ls = on ? l * f : 0.f;
+#pragma unroll
+          for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
+          L = L * fa + ls;
+          o.x *= fa;
+          o.y *= fa;
+          o.z *= fa;
+          o.w *= fa;
+          uint32_t todo = __ballot_sync(kFull, on);
+          while (todo) {  // four records at a time, all their loads in flight
+            float4 a[4];
+            float fk[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              fk[q] = 0.f;
+              a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (todo) {
+                const int kk = __ffs(todo) - 1;
+                todo &= todo - 1;
+                fk[q] = __shfl_sync(kFull, f, kk);
+                a[q] = *(reinterpret_cast<const float4*>((k0 + kk == 0 ? own : more + (c0 + k0 + kk) * step) + 4) + lane);
+              }
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              o.x = fmaf(a[q].x, fk[q], o.x);
+              o.y = fmaf(a[q].y, fk[q], o.y);
+              o.z = fmaf(a[q].z, fk[q], o.z);
+              o.w = fmaf(a[q].w, fk[q], o.w);
+            }
+          }
           M = nm;
         }
-        val = L > 0.f ? A / L : (L == 0.f ? 0.f : A + L);  // a NaN stays one
+        const float inv = L == 0.f ? 0.f : p.ofold / L;  // a NaN stays one
+        o.x *= inv;
+        o.y *= inv;
+        o.z *= inv;
+        o.w *= inv;
       }
     }
-    os[v][j] = val * p.ofold;
-  }
-  __syncthreads();
-  float acc[kPrepV / 2];
+    *reinterpret_cast<float4*>(&sm.x[warp][4 * lane]) = o;
+    __syncthreads();
 #pragma unroll
-  for (int v = 0; v < kPrepV / 2; ++v) acc[v] = 0.f;
-#pragma unroll 4
-  for (int k4 = 0; k4 < 32; ++k4) {
-    const float w0 = __ldg(p.vpi + (4 * k4 + 0) * 128 + j), w1 = __ldg(p.vpi + (4 * k4 + 1) * 128 + j);
-    const float w2 = __ldg(p.vpi + (4 * k4 + 2) * 128 + j), w3 = __ldg(p.vpi + (4 * k4 + 3) * 128 + j);
+    for (int v = 0; v < kPrepV; ++v) {
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k4 = 0; k4 < 4; ++k4) {
+        const float4 x = *reinterpret_cast<const float4*>(&sm.x[v][16 * warp + 4 * k4]);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          acc.x = fmaf(w[4 * k4 + e].x, xs[e], acc.x);
+          acc.y = fmaf(w[4 * k4 + e].y, xs[e], acc.y);
+          acc.z = fmaf(w[4 * k4 + e].z, xs[e], acc.z);
+          acc.w = fmaf(w[4 * k4 + e].w, xs[e], acc.w);
+        }
+      }
+      *reinterpret_cast<float4*>(&sm.part[warp][v][4 * lane]) = acc;
+    }
+    __syncthreads();
+    const int j = tid & 127, h = tid >> 7;
 #pragma unroll
     for (int v = 0; v < kPrepV / 2; ++v) {
-      const float4 x = *reinterpret_cast<const float4*>(&os[h * (kPrepV / 2) + v][4 * k4]);
-      acc[v] = fmaf(w0, x.x, fmaf(w1, x.y, fmaf(w2, x.z, fmaf(w3, x.w, acc[v]))));
-    }
-  }
+      const int vi = h * (kPrepV / 2) + v;
+      if (v0 + vi >= live) continue;
+      float s = 0.f;
 #pragma unroll
-  for (int v = 0; v < kPrepV / 2; ++v) {
-    const int64_t at = v0 + h * (kPrepV / 2) + v;
-    if (at >= live) continue;
-    if (p.dtype == TQ_F32)
-      static_cast<float*>(p.out)[at * 128 + j] = acc[v];
-    else if (p.dtype == TQ_F16)
-      static_cast<__half*>(p.out)[at * 128 + j] = __float2half_rn(acc[v]);
-    else
-      static_cast<__nv_bfloat16*>(p.out)[at * 128 + j] = __float2bfloat16_rn(acc[v]);
+      for (int k = 0; k < 8; ++k) s += sm.part[k][vi][j];
+      const int64_t to = (v0 + vi) * 128 + j;
+      if (p.dtype == TQ_F32)
+        static_cast<float*>(p.out)[to] = s;
+      else if (p.dtype == TQ_F16)
+        static_cast<__half*>(p.out)[to] = __float2half_rn(s);
+      else
+        static_cast<__nv_bfloat16*>(p.out)[to] = __float2bfloat16_rn(s);
+    }
   }
 }
 
@@ -489,7 +575,7 @@ TreeWs tree_ws(int B, int Hq, int Hkv, int64_t R) {
   w.vf = w.kf + al256(rk * 4);
   w.rec = w.vf + al256(rk * 4);
   w.crec = w.rec + al256(rq * kTreeRec * 4);
-  w.total = w.crec + al256((size_t)num_sms() * 128 * kTreeRec * 4);
+  w.total = w.crec + al256((size_t)num_sms() * 64 * kTreeRec * 4);
   return w;
 }
 
@@ -499,7 +585,7 @@ cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st) {
   static PerDeviceValue attr;
   const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_f32_kernel, kFSmem);
   if (e != cudaSuccess) return e;
-  return tree_launch(tree_attend_f32_kernel, p.ctas, 256, kFSmem, p, st);
+  return tree_launch(tree_attend_f32_kernel, p.ctas, 256, kFSmem, st, p);
 }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R) { return tree_ws(B, Hq, Hkv, R).total; }
@@ -558,7 +644,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   // fp32 rows are computed in fp32; 16-bit types round coarser than the
   // tensor-core kernel does
   const bool tc = a.dtype != TQ_F32;
-  p.rows = tc ? 128 : kFRows;
+  p.rows = tc ? tree_umma_rows(a.R, a.B, p.G) : kFRows;
   p.klut = kc.lut;
   p.vlut = vc.lut;
   bool same = kc.b_mse == vc.b_mse && kc.alpha == vc.alpha;
@@ -569,13 +655,16 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   p.zfold = p.zscale / p.kone;
   p.ofold = 1.f / p.vone;
   p.wait_limit = kc.wait_limit;
+  // groups of kPrepV rows, as many to a CTA as leave two CTAs on every SM
   const int64_t nq = (a.R * a.Hq + kPrepV - 1) / kPrepV, nk = a.k_new ? (a.R * a.Hkv + kPrepV - 1) / kPrepV : 0;
-  if (1 + nq + 2 * nk > INT32_MAX) return TQ_ERR_UNSUPPORTED;
-  const int grid = (int)(1 + nq + 2 * nk);
-  cudaError_t e = tc ? tree_launch(tree_prep_kernel<true>, grid, 256, 0, p, stream)
-                     : tree_launch(tree_prep_kernel<false>, grid, 256, 0, p, stream);
+  const int64_t fill = 2 * (int64_t)num_sms();
+  const int per = (int)((nq + 2 * nk + fill - 1) / fill), perj = (int)((nq + fill - 1) / fill);
+  const int nbq = (int)((nq + per - 1) / per), nbk = (int)((nk + per - 1) / per);
+  const int grid = 1 + nbq + 2 * nbk;
+  cudaError_t e = tc ? tree_launch(tree_prep_kernel<true>, grid, 256, 0, stream, p, per, nbq, nbk)
+                     : tree_launch(tree_prep_kernel<false>, grid, 256, 0, stream, p, per, nbq, nbk);
   if (e == cudaSuccess) e = tc ? tree_attend_umma(p, stream) : tree_attend_f32(p, stream);
-  if (e == cudaSuccess) e = tree_launch(tree_join_kernel, (int)nq, 256, 0, p, stream);
+  if (e == cudaSuccess) e = tree_launch(tree_join_kernel, (int)((nq + perj - 1) / perj), 256, 0, stream, p, perj);
   return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
 }
 

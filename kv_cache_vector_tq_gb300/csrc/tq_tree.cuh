@@ -125,19 +125,29 @@ __device__ __forceinline__ TreeSeg tree_seg(const TreeParams& p, int64_t u, int6
   return g;
 }
 
-__device__ __forceinline__ float tree_load(const void* p, int64_t i, int dtype) {
-  if (dtype == TQ_F32) return static_cast<const float*>(p)[i];
-  if (dtype == TQ_F16) return __half2float(static_cast<const __half*>(p)[i]);
-  return __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]);
+// Four elements from element i on (a multiple of four) as fp32.
+__device__ __forceinline__ float4 tree_load4(const void* p, int64_t i, int dtype) {
+  if (dtype == TQ_F32) return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
+  float2 a, b;
+  if (dtype == TQ_F16) {
+    a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+    b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+  } else {
+    a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+    b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+  }
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st);
 cudaError_t tree_attend_umma(const TreeParams& p, cudaStream_t st);
+int tree_umma_rows(int64_t rows, int B, int G);
 
 // A launch that may begin while the kernel before it in the stream ends; every
 // kernel here waits for that one (griddep_wait) before it touches its data.
-template <typename K>
-inline cudaError_t tree_launch(K kernel, int grid, int threads, size_t smem, const TreeParams& p, cudaStream_t st) {
+template <typename... P, typename... A>
+inline cudaError_t tree_launch(void (*kernel)(P...), int grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -148,7 +158,7 @@ inline cudaError_t tree_launch(K kernel, int grid, int threads, size_t smem, con
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 }  // namespace tq

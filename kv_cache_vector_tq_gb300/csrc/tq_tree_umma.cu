@@ -2,81 +2,84 @@
 // tensor cores (fp16 and bf16 inputs).  tq_tree.cuh has the mathematics and
 // the division of the work into units of 128 tokens.
 //
-// A persistent CTA per SM; per unit, with 128 rows (drafted token x query
-// head) on the lanes of tensor memory:
-//     S[row][token] = Q̂·K̂ᵀ       A = Q̂ (tensor memory), B = K̂ (shared memory)
-//     P = 2^(S·s_k·c - M)·s_v     in fp16, over S's own columns
-//     O[row][coord] += P·V̂        A = P (tensor memory), B = V̂ᵀ (shared memory)
-// K̂ and V̂ are the codebook's fp16 pairs (α·c) in the 128-byte swizzle; the
-// norms are applied to the score and to the weight in fp32, so no rounding
-// depends on them.  M is the running maximum of log2 weight times s_v, raised
-// only when a weight would pass 2^14 (the sums are rescaled then, which is
-// rare); subtracting log2 of the tile's largest s_v keeps any magnitude of the
-// values inside fp16.
+// A persistent CTA per SM; per unit, with the 128 tokens on the lanes of
+// tensor memory and N rows (drafted token x query head) on its columns:
+//     Sᵀ[token][row] = K̂·Q̂ᵀ        A = K̂ (tensor memory), B = Q̂ (shared memory)
+//     P[token][row]  = 2^(Sᵀ·s_k·c - M)·s_v   in fp16, shared memory
+//     Oᵀ[coord][row] += V̂ᵀ·P       A = V̂ᵀ (tensor memory), B = P (row-contiguous)
+// Tokens on the lanes make the work on scores proportional to the rows there
+// are (a single token has four or eight of them), and a token's norms one
+// register each.  K̂ and V̂ᵀ are the codebook's fp16 pairs (α·c), written to
+// tensor memory by the threads that look them up: TOKEN rows hold pairs of
+// coordinates of a token, PAIR blocks pairs of tokens of a coordinate, which are
+// the pairs along K of the two products.  The norms act on scores and weights
+// in fp32, so no rounding depends on them.  M (per row) is a running maximum of
+// log2 of weight times s_v, raised only before a weight passes 2^14 (the sums
+// are then rescaled, which is rare); with s_v inside it, values of any
+// magnitude stay inside fp16.
 // Rounding of the operands: for fp16 outputs Q̂ and P are split into two fp16
 // terms each (two products), since one rounding of either costs as much as the
-// output's own; bf16 outputs round sixteen times coarser and take one term.
+// output's own; bf16 outputs round eight times coarser and take one term.
 //
-// Warps: 0-3 softmax (thread = row), 4-7 K̂ (thread = token: 64 table lookups
-// of two codes, 16 swizzled 16-byte stores), 8-11 V̂ᵀ (thread = 8 tokens x 16
-// coordinates; PAIR blocks hold two tokens of a coordinate side by side, which
-// is V̂ᵀ's order), 12 issues the products, 13 the bulk copies of the packed
-// tiles (per 16 tokens, so pages may end anywhere on a multiple of 16).
-// Lookup tables are replicated per lane (one bank each) and aligned so that an
-// address is one shift and one and-or.
+// Warps: 0-7 softmax (thread = token, half of the rows), 8-15 K̂ (thread = token,
+// half of the coordinates: 32 lookups of two codes), 16-23 V̂ᵀ (thread =
+// coordinate, half of the tokens: 32 lookups, one per PAIR block), 24 issues the
+// products, 25 the bulk copies of the packed tiles (per 16 tokens, so pages may
+// end anywhere on a multiple of 16); two more fill the warpgroup that hands its
+// registers to the softmax.  Lookup tables are replicated
+// per lane (one bank each) and aligned to their size, so an address is a shift
+// and an and-or.  Four roles run on each quarter of the SM, each through its own
+// code once per unit, so every role is a short rolled loop: unrolled over the
+// unit, instruction fetch bounded all of them (7000-11000 clocks a unit).
 #include "tq_tree.cuh"
 
 namespace tq {
 
 namespace {
 
-constexpr int kThreads = 14 * 32;
-constexpr int kOp = 128 * 256;            // bytes of one 128 x 128 fp16 operand
-constexpr int kNormSlots = 4;
-constexpr uint32_t kColS = 0, kColO = 256, kColQ = 384;  // tensor memory: S/P x 2, O, Q̂ (hi 64 | lo 64)
-constexpr float kLazyUp = 14.f;           // raise M before a weight passes 2^14
-constexpr float kShift = 6.f;             // a fresh maximum sits at weight 2^6: small weights keep their bits longer
+constexpr int kSoft = 8;                    // softmax warps: two per 32 tokens, half of the rows each
+constexpr int kMma = kSoft + 16, kCopy = kMma + 1;
+constexpr int kThreads = (kSoft + 20) * 32;
+constexpr int kRS = 5;                     // packed tiles in flight (3 where K and V have tables of their own)
+constexpr int kNormSlots = 8;
+// Tensor memory columns: Sᵀ x 2, Oᵀ, the rows' sums of weights per token lane, K̂ x 2, V̂ᵀ x 2
+constexpr uint32_t kColO = 128, kColL = 192, kColK = 256, kColV = 384;
+constexpr float kLazyUp = 14.f;            // raise M before a weight passes 2^14
+constexpr float kShift = 6.f;              // a fresh maximum sits at weight 2^6: small weights keep their bits longer
 
-// Shared memory by absolute address (dynamic shared memory starts at 1024, the
-// system's reserved bytes): raw tiles, [the K table], the V table (or both) at
-// 64 KB, the operands, norms and barriers.
-constexpr uint32_t kBase = 1024;
-constexpr uint32_t kLutV = 65536;
-constexpr uint32_t kOps = kLutV + 32768;  // K̂ x 2, V̂ x 2
-constexpr uint32_t kNorms = kOps + 4 * kOp;  // [slot][K | V][128] fp32
-constexpr uint32_t kBars = kNorms + 3072;     // three norm slots here, the fourth below the tables
-constexpr uint32_t kEnd = 1024 + 227 * 1024;
-constexpr uint32_t kRaw = kBase + 1024;       // the fourth norm slot comes first
+// Shared memory
+constexpr int kLutV = 0, kLutK = 32768;    // (one table for both: kLutV)
+constexpr int kQ = 65536;                  // Q̂: leading parts, remainders; 64 rows x 256 bytes each
+constexpr int kQPart = 64 * 256;
+constexpr int kP = kQ + 2 * kQPart;        // P x 2: leading parts, remainders; 128 tokens x 128 bytes each
+constexpr int kPPart = 128 * 128;
+constexpr int kRaw = kP + 4 * kPPart;      // packed tiles: K codes, V codes
+constexpr int kRawStage = 2 * 128 * 64;
+// packed tile s: three stages of their own, two in the place of the second table
+__device__ __forceinline__ int raw_at(uint32_t s) { return s < 3 ? kRaw + (int)s * kRawStage : kLutK + (int)(s - 3) * kRawStage; }
+static_assert(kLutK + 2 * kRawStage <= kQ, "shared memory");
+constexpr int kNorms = kRaw + 3 * kRawStage;  // [slot][K | V][128] fp32
+constexpr int kMisc = kNorms + kNormSlots * 1024;
 
-__host__ __device__ constexpr uint32_t lut_bytes(int b) { return (1u << (2 * b)) * 128u; }
-__host__ __device__ constexpr uint32_t raw_v_off(int kb) { return 2048u * kb; }
-__host__ __device__ constexpr uint32_t raw_bytes(int kb, int vb) { return 2048u * kb + 16u * (128u * vb + 16u); }
-
-struct Bars {
-  uint64_t raw_full[3], raw_empty[3];
+struct Misc {
+  float c[64];       // factors of the rows' scores
+  float nm[64];      // -M
+  float f[64];       // rescale factors of a raise
+  float red[4][64];
+  int vec[64];       // record of a row; -1: no such row
+  int ti[64];        // its drafted token
+  uint64_t raw_full[kRS], raw_empty[kRS];
   uint64_t kh_full[2], kh_empty[2], vh_full[2], vh_empty[2];
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t n_full[kNormSlots], n_empty[kNormSlots];
   uint64_t q_full, drain;
-  uint32_t valid[kNormSlots];  // 16-token chunks of the tile that are there
+  uint32_t valid[kNormSlots];  // bit 4c: the tile's 16-token chunk c is there
   uint32_t tmem;
   int abort;
 };
-static_assert(kBars + sizeof(Bars) <= kEnd, "shared memory");
+constexpr int kSmem = kMisc + (int)sizeof(Misc);
+static_assert(kSmem <= 227 * 1024, "shared memory");
 
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
-  uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(v) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
-}
 // Two fp32 values in one 64-bit register: one instruction per pair.
 __device__ __forceinline__ uint64_t pk2(float a, float b) {
   uint64_t r;
@@ -101,7 +104,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
-
 // Tensor-memory loads complete; the loaded registers pass through, so that
 // nothing that uses them moves ahead of the wait.
 template <int N>
@@ -110,147 +112,215 @@ __device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
-
-// Table entry of the 2B-bit field at bit `off` (a constant once unrolled) of
-// w: the field moved to bits 7.., then one and-or with the lane's table base.
-template <int B, int N>
-__device__ __forceinline__ uint32_t look(const uint32_t (&w)[N], int off, uint32_t base) {
-  constexpr uint32_t m = ((1u << (2 * B)) - 1u) << 7;
-  const int i = off >> 5, s = off & 31;
-  uint32_t x;
-  if (s + 2 * B > 32)
-    x = __funnelshift_r(w[i], w[i + 1 < N ? i + 1 : i], s) << 7;
-  else if (s >= 7)
-    x = w[i] >> (s - 7);
-  else
-    x = w[i] << (7 - s);
-  return lds32((x & m) | base);
+__device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[32]) {
+  uint32_t a[16], b[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    a[i] = v[i];
+    b[i] = v[16 + i];
+  }
+  tmem_st16(at, a);
+  tmem_st16(at + 16, b);
+}
+__device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[32]) { tmem_ld32_nw(at, v); }
+__device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[16]) { tmem_ld16_nw(at, v); }
+__device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[8]) { tmem_ld8_nw(at, v); }
+__device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[16]) { tmem_st16(at, v); }
+__device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[8]) { tmem_st8(at, v); }
+// bar_wait with a suspension of up to a few microseconds per poll: 25 warps that
+// poll as fast as they can take issue slots from those that work.
+__device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
+                                         uint32_t limit) {
+  for (uint32_t n = 0;; ++n) {
+    if (n >= limit) {
+      *abort_flag = 1;
+      atomicOr(status, 1);
+      return false;
+    }
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+        " selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
+        : "memory");
+    if (ok) return true;
+    if ((n & 15u) == 15u && *abort_flag) return false;
+  }
+}
+// One lane of a converged warp, by the instruction made for it: the products
+// inside a branch on it issue every 31 clocks (N = 64, the tensor cores' rate),
+// on `lane == 0` every 54, predicated every 70 (descriptors are then moved to
+// uniform registers for each of them).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+__device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
+// Barrier of the softmax warps that tells whether any thread asked.
+__device__ __forceinline__ bool bar_any(bool ask) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)ask)
+      : "memory");
+  return r != 0;
 }
 
-// K̂ row of token t: 16 chunks of 8 coordinates.
-template <int B>
-__device__ __forceinline__ void dequant_k(uint32_t raw, uint32_t op, uint32_t lut, int t) {
-  const uint32_t row = op + t * 128, sw = (uint32_t)(t & 7) << 4;
-  if constexpr (B == 4) {
-    // 16-byte pieces in an order that differs between lanes: rows are 64 bytes,
-    // eight lanes reading the same piece would meet in two banks of eight
+// Lane l gets the result of column l over the warp's lanes (v: a lane's 32 columns).
+template <bool SUM>
+__device__ __forceinline__ float reduce_columns(float (&v)[32], int lane) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int x = (i + (t >> 1)) & 3;  // coordinates 32x..
-      const uint4 u = lds128(raw + t * 64 + 16 * x);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      const uint32_t at = row + ((x >> 1) << 14);
+  for (int w = 16; w >= 1; w >>= 1) {
+    const bool up = (lane & w) != 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t c = (uint32_t)(4 * (x & 1) + e) << 4;
-        const uint32_t v0 = look<4>(w, 32 * e, lut), v1 = look<4>(w, 32 * e + 8, lut);
-        const uint32_t v2 = look<4>(w, 32 * e + 16, lut), v3 = look<4>(w, 32 * e + 24, lut);
-        sts128(at + (c ^ sw), v0, v1, v2, v3);
-      }
+    for (int i = 0; i < w; ++i) {
+      const float send = up ? v[i] : v[i + w], keep = up ? v[i + w] : v[i];
+      const float got = __shfl_xor_sync(kFull, send, w);
+      v[i] = SUM ? keep + got : fmaxf(keep, got);
     }
+  }
+  return v[0];
+}
+
+__device__ __forceinline__ uint32_t lds_u32(const unsigned char* p) { return *reinterpret_cast<const uint32_t*>(p); }
+
+// Half of the K̂ row of token t (tensor-memory lane t): 32 columns of coordinate
+// pairs, 16 at a time: 32 coordinates are B whole words of the row.
+template <int B>
+__device__ __forceinline__ void dequant_k(const unsigned char* smem, int raw, uint32_t tmem, uint32_t lut, int t, int half) {
+  constexpr uint32_t m = ((1u << (2 * B)) - 1u) << 7;
+  const unsigned char* row = smem + raw + t * (16 * B) + half * (8 * B);
+  uint32_t all[2 * B];
+  if constexpr (B == 4) {
+    // rows of 64 bytes: eight lanes reading the same 16-byte piece would meet in
+    // two of eight bank groups; lanes in two orders meet in four
+    const bool r = (t >> 1) & 1;
+    const uint4 x = *reinterpret_cast<const uint4*>(row + (r ? 16 : 0)), y = *reinterpret_cast<const uint4*>(row + (r ? 0 : 16));
+    all[0] = r ? y.x : x.x;
+    all[1] = r ? y.y : x.y;
+    all[2] = r ? y.z : x.z;
+    all[3] = r ? y.w : x.w;
+    all[4] = r ? x.x : y.x;
+    all[5] = r ? x.y : y.y;
+    all[6] = r ? x.z : y.z;
+    all[7] = r ? x.w : y.w;
+  } else if constexpr (B == 2) {
+    const uint4 x = *reinterpret_cast<const uint4*>(row);
+    all[0] = x.x;
+    all[1] = x.y;
+    all[2] = x.z;
+    all[3] = x.w;
   } else {
-    uint32_t w[4 * B];
 #pragma unroll
     for (int i = 0; i < B; ++i) {
-      const uint4 u = lds128(raw + t * (16 * B) + 16 * i);
-      w[4 * i] = u.x;
-      w[4 * i + 1] = u.y;
-      w[4 * i + 2] = u.z;
-      w[4 * i + 3] = u.w;
+      const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * i);
+      all[2 * i] = x.x;
+      all[2 * i + 1] = x.y;
     }
+  }
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[16];
 #pragma unroll
-    for (int c = 0; c < 16; ++c) {
-      uint32_t v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = look<B>(w, (8 * c + 2 * e) * B, lut);
-      sts128(row + ((c >> 3) << 14) + (((c & 7) << 4) ^ sw), v[0], v[1], v[2], v[3]);
+    for (int e = 0; e < 16; ++e) {
+      const int i = (2 * B * e) >> 5, s = (2 * B * e) & 31;
+      uint32_t x;  // the field to bits 7..
+      if (s + 2 * B > 32)
+        x = __funnelshift_r(all[i], all[i + 1 < B ? i + 1 : i], s) << 7;
+      else
+        x = s >= 7 ? all[i] >> (s - 7) : all[i] << (7 - s);
+      v[e] = lds_u32(smem + ((x & m) | lut));
     }
+    tmem_st16(tmem + 16 * c, v);
+#pragma unroll
+    for (int i = 0; i < B; ++i) all[i] = all[i + B];
   }
 }
 
-// V̂ᵀ: 8 tokens (group c8 of block blk) of coordinates 16·cg..+15.
+// Half of the V̂ᵀ row of coordinate d (tensor-memory lane d): column i holds PAIR
+// block i's two tokens, the 2B bits at bit 2B·d of the block.
 template <int B>
-__device__ __forceinline__ void dequant_v(uint32_t raw, uint32_t op, uint32_t lut, int c8, int cg, int blk) {
-  uint32_t w[4][B];
-  const uint32_t src = raw + (blk * 8 + c8) * (128 * B + 16) + cg * (4 * B);
+__device__ __forceinline__ void dequant_v(const unsigned char* smem, int raw, uint32_t tmem, uint32_t lut, int d, int half) {
+  constexpr uint32_t m = ((1u << (2 * B)) - 1u) << 7;
+  const unsigned char* src = smem + raw + half * (32 * 32 * B) + ((2 * B * d) >> 3);
+  const int up = B == 4 ? 7 : 7 - ((2 * B * d) & 7);  // the field to bits 7..
+#pragma unroll 1
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[16];
 #pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    if constexpr (B == 4) {
-      const uint4 u = lds128(src + p * 128);
-      w[p][0] = u.x;
-      w[p][1] = u.y;
-      w[p][2] = u.z;
-      w[p][3] = u.w;
-    } else {
-#pragma unroll
-      for (int i = 0; i < B; ++i) w[p][i] = lds32(src + p * (32 * B) + 4 * i);
+    for (int e = 0; e < 16; ++e) {
+      const unsigned char* at = src + e * (32 * B);
+      v[e] = at[0];
+      if constexpr (B == 3) v[e] |= (uint32_t)at[1] << 8;  // six bits may end in the next byte
     }
-  }
-  const uint32_t at = op + (blk << 14) + cg * (16 * 128);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    uint32_t v[4];
-#pragma unroll
-    for (int p = 0; p < 4; ++p) v[p] = look<B>(w[p], 2 * B * k, lut);
-    sts128(at + k * 128 + ((uint32_t)(c8 ^ (k & 7)) << 4), v[0], v[1], v[2], v[3]);
+    for (int e = 0; e < 16; ++e) v[e] = lds_u32(smem + (B == 4 ? lut + v[e] * 128u : (((v[e] << up) & m) | lut)));
+    tmem_st16(tmem + 16 * c, v);
+    src += 16 * 32 * B;
   }
 }
 
-template <bool SPLIT>
+template <int N, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreeParams p) {
+  static_assert(N == 16 || N == 32 || N == 64, "rows per tile");
+  constexpr int PC = N < 32 ? N / 2 : 16;  // columns of a piece
   extern __shared__ __align__(1024) unsigned char smem[];
-  if (smem_u32(smem) != kBase) {  // the layout below is absolute
+  Misc& ms = *reinterpret_cast<Misc*>(smem + kMisc);
+  if ((smem_u32(smem) & 1023u) != 0u) {  // the swizzled operands need it
     if (threadIdx.x == 0) atomicOr(p.status, 1);
     return;
   }
-  Bars& bar = *reinterpret_cast<Bars*>(smem + (kBars - kBase));
-  volatile int* abort_flag = &bar.abort;
+  volatile int* abort_flag = &ms.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t lim = p.wait_limit;
-  const uint32_t lut_k = p.same_lut ? kLutV : kLutV - lut_bytes(p.kb);
-  const uint32_t stage = raw_bytes(p.kb, p.vb);
-  const int RS = min(3, (int)((lut_k - kRaw) / stage));  // raw stages that fit below the tables
-  auto norm_slot = [&](uint32_t i) -> uint32_t {
-    const uint32_t s = i % kNormSlots;
-    return s == 3 ? kBase : kNorms + s * 1024u;
-  };
+  const int lut_k = p.same_lut ? kLutV : kLutK;
+  const uint32_t RS = p.same_lut ? kRS : 3;
 
   if (tid == 0) {
-    for (int i = 0; i < 3; ++i) {
-      mbar_init(&bar.raw_full[i], 1);
-      mbar_init(&bar.raw_empty[i], 8);
+    for (int i = 0; i < kRS; ++i) {
+      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_empty[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.kh_full[i], 4);
-      mbar_init(&bar.kh_empty[i], 1);
-      mbar_init(&bar.vh_full[i], 4);
-      mbar_init(&bar.vh_empty[i], 1);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 4);
-      mbar_init(&bar.pv_done[i], 1);
+      mbar_init(&ms.kh_full[i], 8);
+      mbar_init(&ms.kh_empty[i], 1);
+      mbar_init(&ms.vh_full[i], 8);
+      mbar_init(&ms.vh_empty[i], 1);
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], kSoft);
+      mbar_init(&ms.pv_done[i], 1);
     }
     for (int i = 0; i < kNormSlots; ++i) {
-      mbar_init(&bar.n_full[i], 1);
-      mbar_init(&bar.n_empty[i], 4);
+      mbar_init(&ms.n_full[i], 1);
+      mbar_init(&ms.n_empty[i], kSoft);
     }
-    mbar_init(&bar.q_full, 4);
-    mbar_init(&bar.drain, 1);
-    bar.abort = 0;
+    mbar_init(&ms.q_full, kSoft);
+    mbar_init(&ms.drain, 1);
+    ms.abort = 0;
     fence_mbar_init();
   }
   {
-    uint32_t* lv = reinterpret_cast<uint32_t*>(smem + (kLutV - kBase));
-    for (int i = tid; i < (32 << (2 * p.vb)); i += kThreads) lv[i] = __ldg(p.vlut + (i >> 5));
+    uint4* lv = reinterpret_cast<uint4*>(smem + kLutV);
+    for (int i = tid; i < (8 << (2 * p.vb)); i += kThreads) {
+      const uint32_t x = __ldg(p.vlut + (i >> 3));
+      lv[i] = make_uint4(x, x, x, x);
+    }
     if (!p.same_lut) {
-      uint32_t* lk = reinterpret_cast<uint32_t*>(smem + (lut_k - kBase));
-      for (int i = tid; i < (32 << (2 * p.kb)); i += kThreads) lk[i] = __ldg(p.klut + (i >> 5));
+      uint4* lk = reinterpret_cast<uint4*>(smem + kLutK);
+      for (int i = tid; i < (8 << (2 * p.kb)); i += kThreads) {
+        const uint32_t x = __ldg(p.klut + (i >> 3));
+        lk[i] = make_uint4(x, x, x, x);
+      }
     }
   }
-  if (warp == 12) tmem_alloc(&bar.tmem, 512);
+  if (warp == kMma) tmem_alloc(&ms.tmem, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = bar.tmem;
+  constexpr uint32_t tmem = 0;  // 512 columns are all there are: they start at 0
   griddep_wait();
   griddep_launch();
 
@@ -259,275 +329,303 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   const int64_t u_end = tree_cut(blockIdx.x + 1, units, p.ctas);
   int b = u < u_end ? p.cta_seq[blockIdx.x] : 0;
 
-  if (warp < 4) {
-    // ---------------- softmax: thread = row
-    const uint32_t lane_base = (uint32_t)(32 * warp) << 16;
-    const uint32_t tO = tmem + lane_base + kColO, tQ = tmem + lane_base + kColQ;
+  if (warp < kSoft) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    // ---------------- softmax: thread = token tok (its tensor-memory lane) and
+    // rows n0 .. n0 + HN - 1; in the epilogue coordinate tok
+    constexpr int HN = N / 2;  // rows of a thread
+    const int n0 = (warp >> 2) * HN, quad = warp & 3, tok = tid & 127;
+    const uint32_t lane_base = ((uint32_t)(32 * quad) << 16) + n0;
+    const uint32_t tO = tmem + lane_base + kColO, tL = tmem + lane_base + kColL;
+    const int sw = tok & 7;
     uint32_t i = 0;
     bool ok = true;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
       b = g.b;
-      const int r = 32 * warp + lane, rho = g.row0 + r;
-      const bool live = r < g.nrow, active = 32 * warp < g.nrow;
-      const int ti = live ? rho / p.G : 0;
-      const int64_t vec = live ? (int64_t)(g.s.start + ti) * p.Hq + g.kvh * p.G + (rho - ti * p.G) : 0;
-      // Q̂ into tensor memory (every product of the last segment with the old
-      // one has completed: its last S was read here)
-      if (active) {
-        const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.qrot) + vec * 256);
-#pragma unroll
-        for (int c = 0; c < (SPLIT ? 8 : 4); ++c) {
-          uint32_t v[16];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 x = live ? src[4 * c + e] : make_uint4(0u, 0u, 0u, 0u);
-            v[4 * e] = x.x;
-            v[4 * e + 1] = x.y;
-            v[4 * e + 2] = x.z;
-            v[4 * e + 3] = x.w;
-          }
-          tmem_st16(tQ + 16 * c, v);
+      // the rows: Q̂ into shared memory (every product with the last segment's
+      // has completed: its last Sᵀ was read here), their factors and records
+      if (tid < N) {
+        int vec = -1, ti = 0;
+        float c = 0.f, m = INFINITY;  // no such row: weights 0 (M = inf)
+        if (tid < g.nrow) {
+          const int rho = g.row0 + tid;
+          ti = rho / p.G;
+          vec = (g.s.start + ti) * p.Hq + g.kvh * p.G + (rho - ti * p.G);
+          c = p.qfac[vec] * p.zfold;
+          m = -INFINITY;
         }
+        // a row that is not a number: every weight that it has is none either
+        ms.c[tid] = c == c ? c : 0.f;
+        ms.nm[tid] = c == c ? -m : c;
+        ms.vec[tid] = vec;
+        ms.ti[tid] = ti;
+      }
+      bar_softmax();
+      // One factor for all rows of the tile: the largest; the rows are scaled down
+      // to it by powers of two.  (Absolute errors of scores stay below 2^-36 of
+      // the tile's largest, however far the rows are apart.)
+      float ct = fmaxf(ms.c[lane & (N - 1)], ms.c[(lane + 32) & (N - 1)]);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) ct = fmaxf(ct, __shfl_xor_sync(kFull, ct, o));
+      const float inv_ct = ct > 0.f ? 1.f / ct : 0.f;
+      // 16-byte pieces: 16 of the leading part and 16 of the remainder per row
+#pragma unroll 4
+      for (int e = tid; e < N * (SPLIT ? 32 : 16); e += 32 * kSoft) {
+        const int n = SPLIT ? e >> 5 : e >> 4, k = SPLIT ? e & 31 : e & 15, c = k & 15, part = k >> 4;
+        const int vec = ms.vec[n];
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (vec >= 0) x = *(reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.qrot) + (int64_t)vec * 256) + k);
+        const __half2 sc = __float2half2_rn(ms.c[n] * inv_ct);  // a power of two up to rounding: made one by fp16's
+        __half2* h = reinterpret_cast<__half2*>(&x);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = __hmul2(h[q], sc);
+        *reinterpret_cast<uint4*>(smem + kQ + part * kQPart + (c >> 3) * (N * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) = x;
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.q_full);
+      {
+        const uint32_t zero[PC] = {};
+#pragma unroll 1
+        for (int c = 0; c < HN / PC; ++c) tmem_st_n(tL + PC * c, zero);
         tmem_wait_st();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar.q_full);
-      const float rs = live ? p.qfac[vec] * p.zfold : 0.f;
-      float M = -INFINITY, l = 0.f;
-      for (int t = g.first; ok && t < g.last; ++t, ++i) {
+
+      for (int t = g.first; t < g.last; ++t, ++i) {
         const uint32_t sb = i & 1u, ns = i % kNormSlots;
-        ok = __all_sync(kFull, bar_wait(&bar.s_full[sb], (i >> 1) & 1u, abort_flag, p.status, lim) &&
-                                   bar_wait(&bar.n_full[ns], (i / kNormSlots) & 1u, abort_flag, p.status, lim));
-        if (!ok) break;
-        tc_fence_after();
-        if (active) {
-          const uint32_t tS = tmem + lane_base + kColS + sb * 128;
-          const uint32_t kn = norm_slot(i), vn = kn + 512;
-          // Tokens of the tile that this row sees: all of them (whole), or the
-          // bits of see(c) for tokens 32c..
-          const bool draft = t >= g.ctiles;
-          const int t0 = draft ? (t - g.ctiles) * kTreeTok : t * kTreeTok;
-          const int nt = min(kTreeTok, (draft ? g.s.T : g.s.len) - t0);
-          const uint32_t chunks = bar.valid[ns];
-          const bool whole = nt == kTreeTok && chunks == 0xFFu && !draft;
-          auto see = [&](int c) -> uint32_t {
-            const int n = nt - 32 * c;
-            const uint32_t m = n >= 32 ? 0xFFFFFFFFu : (n > 0 ? (1u << n) - 1u : 0u);
-            if (!draft)
-              return m & (((chunks >> (2 * c)) & 1u ? 0xFFFFu : 0u) | ((chunks >> (2 * c + 1)) & 1u ? 0xFFFF0000u : 0u));
-            if (p.mask) {
-              const int at = (t0 >> 5) + c;
-              return m & (live && at < p.mask_words ? p.mask[(int64_t)(g.s.start + ti) * p.mask_words + at] : 0u);
-            }
-            const int k = ti - t0 - 32 * c + 1;  // a chain: tokens 0..ti
-            return m & (k >= 32 ? 0xFFFFFFFFu : (k > 0 ? (1u << k) - 1u : 0u));
-          };
-          // largest s_v of the tile (of the tokens that are there), as a power
-          // of two's exponent
-          float vmax = 0.f;
-          {
-            const uint4 x = lds128(vn + 16 * lane);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-            const uint32_t here = whole ? 0xFu : (nt > 4 * lane ? 0xFu >> max(0, 4 * lane + 4 - nt) : 0u) *
-                                                     (draft ? 1u : ((chunks >> (lane >> 2)) & 1u));
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((here >> e) & 1u) vmax = fmaxf(vmax, __uint_as_float(w[e]));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) vmax = fmaxf(vmax, __shfl_xor_sync(kFull, vmax, o));
+        ok = __all_sync(kFull, bar_rest(&ms.s_full[sb], (i >> 1) & 1u, abort_flag, p.status, lim) &&
+                                   bar_rest(&ms.n_full[ns], (i / kNormSlots) & 1u, abort_flag, p.status, lim));
+        tc_fence_after();  // (a wait that gave up: what follows is garbage and dropped below)
+        const uint32_t tS = tmem + lane_base + sb * 64;
+        const float* nrm = reinterpret_cast<const float*>(smem + kNorms + ns * 1024);
+        const bool draft = t >= g.ctiles;
+        const int t0 = draft ? (t - g.ctiles) * kTreeTok : t * kTreeTok;
+        const int nt = min(kTreeTok, (draft ? g.s.T : g.s.len) - t0);
+        const uint32_t chunks = ms.valid[ns];
+        const bool here = tok < nt && ((chunks >> (4 * (tok >> 4))) & 1u);  // this token is there
+        const bool whole = nt == kTreeTok && chunks == 0x11111111u && !draft;
+        const float kn = nrm[tok], vn = nrm[128 + tok];
+        // 2^lv > vn, kept within 2^±100
+        const float lv = fminf(fmaxf((float)((int)((__float_as_uint(vn) >> 23) & 255u) - 126), -100.f), 100.f);
+        const float ck = ct * kn;
+        const uint64_t ck2 = pk2(ck, ck);
+        const bool odd = vn != vn;
+        // drafted tokens: bit `lane` of a row's mask word for this warp's 32
+        // tokens; lane n holds the word of row n0 + n
+        uint32_t mw = 0u;
+        if (draft && lane < HN && ms.vec[n0 + lane] >= 0) {
+          const int ti = ms.ti[n0 + lane], at = (t0 >> 5) + quad;
+          if (p.mask) {
+            if (at < p.mask_words) mw = __ldg(p.mask + (int64_t)(g.s.start + ti) * p.mask_words + at);
+          } else {  // a chain: tokens 0..ti
+            const int k = ti - 32 * at + 1;
+            mw = k >= 32 ? 0xFFFFFFFFu : (k > 0 ? (1u << k) - 1u : 0u);
           }
-          // 2^lv >= vmax, kept within 2^±100
-          const float lv = fminf(fmaxf((float)((int)(__float_as_uint(vmax) >> 23) - 126), -100.f), 100.f);
-          // pass 1: the row's largest S·s_k
-          float mx = -INFINITY;
-          if (whole) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32_nw(tS + 32 * c, s);
-              wait_ld(s);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint4 k4 = lds128(kn + 128 * c + 16 * e);
-                float a0, a1, a2, a3;
-                up2(mul2(pk2(__uint_as_float(s[4 * e]), __uint_as_float(s[4 * e + 1])),
-                         pk2(__uint_as_float(k4.x), __uint_as_float(k4.y))), a0, a1);
-                up2(mul2(pk2(__uint_as_float(s[4 * e + 2]), __uint_as_float(s[4 * e + 3])),
-                         pk2(__uint_as_float(k4.z), __uint_as_float(k4.w))), a2, a3);
-                mx = fmaxf(fmaxf(mx, fmaxf(a0, a1)), fmaxf(a2, a3));
-              }
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t sw = see(c);
-              uint32_t s[32];
-              tmem_ld32_nw(tS + 32 * c, s);
-              wait_ld(s);
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if ((sw >> e) & 1u) mx = fmaxf(mx, __uint_as_float(s[e]) * __uint_as_float(lds32(kn + 128 * c + 4 * e)));
-            }
-          }
-          // a weight is 2^(z - M)·s_v <= 2^(cand - M): raise M before one passes 2^14
-          const float cand = mx == -INFINITY ? -INFINITY : fmaf(mx, rs, lv);
-          const bool raise = live && cand > M + kLazyUp;
-          if (__any_sync(kFull, raise)) {
-            const float nm = raise ? cand - kShift : M;
-            const float f = raise ? (M == -INFINITY ? 0.f : ex2(M - nm)) : 1.f;
-            if (t > g.first) {  // the sums so far, once the last product into them is done
-              ok = __all_sync(kFull, bar_wait(&bar.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, abort_flag, p.status, lim));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < 8; ++c) {
-                uint32_t o[16];
-                tmem_ld16_nw(tO + 16 * c, o);
-                wait_ld(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tO + 16 * c, o);
-              }
-            }
-            l *= f;
-            M = nm;
-          }
-          const float use = M == -INFINITY ? 0.f : M;
-          // pass 2: weights and their sum; the weights of 32 tokens over the 32
-          // columns their scores were in (16 of leading parts, 16 of remainders)
-          if (whole) {
-            const uint64_t rs2 = pk2(rs, rs), nm2 = pk2(-use, -use);
-            uint64_t l2 = pk2(0.f, 0.f);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t s[32];
-              tmem_ld32_nw(tS + 32 * c, s);
-              wait_ld(s);
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const uint4 k4 = lds128(kn + 128 * c + 16 * e), v4 = lds128(vn + 128 * c + 16 * e);
-                const uint32_t kw[4] = {k4.x, k4.y, k4.z, k4.w}, vw[4] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  float a, d, w0, w1;
-                  const uint64_t z = mul2(pk2(__uint_as_float(s[4 * e + 2 * q]), __uint_as_float(s[4 * e + 2 * q + 1])),
-                                          pk2(__uint_as_float(kw[2 * q]), __uint_as_float(kw[2 * q + 1])));
-                  up2(fma2(z, rs2, nm2), a, d);
-                  const uint64_t pp = pk2(ex2(a), ex2(d));
-                  l2 = add2(l2, pp);
-                  up2(mul2(pp, pk2(__uint_as_float(vw[2 * q]), __uint_as_float(vw[2 * q + 1]))), w0, w1);
-                  const __half2 h = __floats2half2_rn(w0, w1);
-                  hi[2 * e + q] = h2_bits(h);
-                  if constexpr (SPLIT)
-                    lo[2 * e + q] = h2_bits(__floats2half2_rn(w0 - __low2float(h), w1 - __high2float(h)));
-                }
-              }
-              tmem_st16(tS + 32 * c, hi);
-              if constexpr (SPLIT) tmem_st16(tS + 32 * c + 16, lo);
-            }
-            float la, lb;
-            up2(l2, la, lb);
-            l += la + lb;
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              const uint32_t sw = see(c);
-              uint32_t s[32];
-              tmem_ld32_nw(tS + 32 * c, s);
-              wait_ld(s);
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                float w[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const uint32_t at = 128 * c + 8 * e + 4 * q;
-                  const bool on = (sw >> (2 * e + q)) & 1u;
-                  const float z = __uint_as_float(s[2 * e + q]) * __uint_as_float(lds32(kn + at));
-                  const float pr = on ? ex2(fmaf(z, rs, -use)) : 0.f;
-                  l += pr;
-                  w[q] = on ? pr * __uint_as_float(lds32(vn + at)) : 0.f;
-                }
-                const __half2 h = __floats2half2_rn(w[0], w[1]);
-                hi[e] = h2_bits(h);
-                if constexpr (SPLIT) lo[e] = h2_bits(__floats2half2_rn(w[0] - __low2float(h), w[1] - __high2float(h)));
-              }
-              tmem_st16(tS + 32 * c, hi);
-              if constexpr (SPLIT) tmem_st16(tS + 32 * c + 16, lo);
-            }
-          }
-          tmem_wait_st();
         }
+        auto sees = [&](int n) -> bool {  // this token is seen by row n0 + n
+          const bool named = !draft || ((__shfl_sync(kFull, mw, n) >> lane) & 1u);
+          return here && named;
+        };
+        // weights with the M there is; should one pass the limit (M = -inf, a
+        // row's first token, does), M is raised and they are computed again
+        float pr[HN];
+        for (int tries = 0;; ++tries) {
+          float top = -INFINITY;
+          {
+            uint32_t s[HN];
+            tmem_ld_n(tS, s);
+            wait_ld(s);
+#pragma unroll
+            for (int e = 0; e < HN; e += 4) {
+              const float4 m4 = *reinterpret_cast<const float4*>(ms.nm + n0 + e);
+              up2(fma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ck2, pk2(m4.x, m4.y)), pr[e], pr[e + 1]);
+              up2(fma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), ck2, pk2(m4.z, m4.w)), pr[e + 2], pr[e + 3]);
+            }
+          }
+          if (!whole) {
+#pragma unroll
+            for (int e = 0; e < HN; ++e)
+              if (!sees(e)) pr[e] = -INFINITY;
+          }
+#pragma unroll
+          for (int e = 0; e < HN; e += 4) top = fmaxf(top, fmaxf(fmaxf(pr[e], pr[e + 1]), fmaxf(pr[e + 2], pr[e + 3])));
+#pragma unroll
+          for (int e = 0; e < HN; ++e) pr[e] = ex2(pr[e]);
+          if (!bar_any(!ok || (top + lv > kLazyUp && tries < 2))) break;
+          if (bar_any(!ok)) {  // the four warps stop together
+            ok = false;
+            break;
+          }
+          // the rows' maxima over the tile, then new M where one is passed
+          {
+            uint32_t s[HN];
+            tmem_ld_n(tS, s);
+            wait_ld(s);
+            float v[32];
+#pragma unroll
+            for (int n = 0; n < 32; ++n) {
+              v[n] = -INFINITY;
+              if (n < HN) {
+                const bool on = sees(n);
+                if (on) v[n] = fmaf(__uint_as_float(s[n < HN ? n : 0]), ck, lv);
+              }
+            }
+            const float r = reduce_columns<false>(v, lane);
+            if (lane < HN) ms.red[quad][n0 + lane] = r;
+          }
+          bar_softmax();
+          if (tid < N) {
+            const float m = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
+            const float old = -ms.nm[tid];
+            const bool up = m > old + kShift;
+            ms.f[tid] = up ? (old == -INFINITY ? 0.f : ex2(old - (m - kShift))) : 1.f;
+            if (up) ms.nm[tid] = kShift - m;
+          }
+          if (t > g.first)  // the sums so far, once the last product into them is done
+            ok = __all_sync(kFull, bar_rest(&ms.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, abort_flag, p.status, lim));
+          if (bar_any(!ok)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          if (t > g.first) {
+#pragma unroll 1
+            for (int c = 0; c < 2 * (HN / PC); ++c) {  // Oᵀ, then the sums
+              const uint32_t at = (c & 1 ? tL : tO) + PC * (c >> 1);
+              uint32_t o[PC];
+              tmem_ld_n(at, o);
+              wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < PC; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * ms.f[n0 + PC * (c >> 1) + e]);
+              tmem_st_n(at, o);
+            }
+            tmem_wait_st();
+          }
+        }
+        if (!ok) break;
+        // the rows' sums; P of a token: N values, 16-byte pieces in the 128-byte swizzle
+        unsigned char* prow = smem + kP + sb * (2 * kPPart) + tok * 128;
+        const float vs = here ? vn : 0.f;  // the factors of a token that is not there may be anything
+        const uint64_t vs2 = pk2(vs, vs);
+        uint32_t l[HN];
+        tmem_ld_n(tL, l);
+        wait_ld(l);
+#pragma unroll
+        for (int c = 0; c < HN / 8; ++c) {
+          uint32_t hi[4], lo[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int n = 8 * c + 2 * e;
+            const uint64_t pp = pk2(pr[n], pr[n + 1]);
+            float l0, l1, w0, w1;
+            up2(add2(pk2(__uint_as_float(l[n]), __uint_as_float(l[n + 1])), pp), l0, l1);
+            l[n] = __float_as_uint(l0);
+            l[n + 1] = __float_as_uint(l1);
+            up2(mul2(pp, vs2), w0, w1);
+            if (odd) {  // a drafted row that is not a number has the factor NaN: only for rows that see it
+              w0 = pr[n] == 0.f ? 0.f : w0;
+              w1 = pr[n + 1] == 0.f ? 0.f : w1;
+            }
+            const __half2 h = __floats2half2_rn(w0, w1);
+            hi[e] = h2_bits(h);
+            if constexpr (SPLIT) lo[e] = h2_bits(__floats2half2_rn(w0 - __low2float(h), w1 - __high2float(h)));
+          }
+          unsigned char* at = prow + (((n0 / 8 + c) ^ sw) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          if constexpr (SPLIT) *reinterpret_cast<uint4*>(at + kPPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        }
+        tmem_st_n(tL, l);
+        tmem_wait_st();
+        fence_proxy_async();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(&bar.p_full[sb]);
-          mbar_arrive(&bar.n_empty[ns]);
+          mbar_arrive(&ms.p_full[sb]);
+          mbar_arrive(&ms.n_empty[ns]);
         }
       }
-      // the segment's sums, once its last product is done
       if (!ok) break;
-      ok = __all_sync(kFull, bar_wait(&bar.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, abort_flag, p.status, lim));
-      if (!ok) break;
-      tc_fence_after();
-      if (active) {
-        float* rec = g.first == 0 ? p.rec + vec * kTreeRec : p.crec + ((int64_t)blockIdx.x * 128 + r) * kTreeRec;
-        if (live) *reinterpret_cast<float2*>(rec) = make_float2(M, l);
-#pragma unroll 1
-        for (int c = 0; c < 4; ++c) {
-          uint32_t o[32];
-          tmem_ld32_nw(tO + 32 * c, o);
-          wait_ld(o);
-          if (live)
+      // the rows' records, once the segment's last product is done
+      {
+        float v[32];
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-              *reinterpret_cast<uint4*>(rec + 4 + 32 * c + 4 * e) = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        for (int c = 0; c < 32 / PC; ++c) {
+          uint32_t x[PC];
+          if (c < HN / PC) {
+            tmem_ld_n(tL + PC * c, x);
+            wait_ld(x);
+          }
+#pragma unroll
+          for (int e = 0; e < PC; ++e) v[PC * c + e] = PC * c + e < HN ? __uint_as_float(x[e]) : 0.f;
+        }
+        const float r = reduce_columns<true>(v, lane);
+        if (lane < HN) ms.red[quad][n0 + lane] = r;
+      }
+      ok = __all_sync(kFull, bar_rest(&ms.pv_done[(i - 1) & 1u], ((i - 1) >> 1) & 1u, abort_flag, p.status, lim));
+      if (bar_any(!ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float* base = g.first == 0 ? p.rec : p.crec + (int64_t)blockIdx.x * N * kTreeRec;
+      if (tid < g.nrow)
+        *reinterpret_cast<float2*>(base + (int64_t)(g.first == 0 ? ms.vec[tid] : tid) * kTreeRec) =
+            make_float2(-ms.nm[tid], (ms.red[0][tid] + ms.red[1][tid]) + (ms.red[2][tid] + ms.red[3][tid]));
+#pragma unroll 1
+      for (int c = 0; c < HN / PC; ++c) {
+        if (n0 + PC * c >= g.nrow) break;
+        uint32_t o[PC];
+        tmem_ld_n(tO + PC * c, o);
+        wait_ld(o);
+#pragma unroll
+        for (int e = 0; e < PC; ++e) {
+          const int n = n0 + PC * c + e;
+          if (n < g.nrow) base[(int64_t)(g.first == 0 ? ms.vec[n] : n) * kTreeRec + 4 + tok] = __uint_as_float(o[e]);
         }
       }
       tc_fence_before();
+      bar_softmax();  // the rows' tables are rewritten next
       u += g.last - g.first;
     }
-  } else if (warp < 12) {
-    // ---------------- K̂ (warps 4-7) and V̂ᵀ (8-11) operands
-    const bool is_v = warp >= 8;
-    const int v = tid - (is_v ? 256 : 128);  // thread of the role
-    uint64_t* full = is_v ? bar.vh_full : bar.kh_full;
-    uint64_t* empty = is_v ? bar.vh_empty : bar.kh_empty;
-    const uint32_t ops = kOps + (is_v ? 2u * kOp : 0u);
-    const uint32_t lut = (is_v ? kLutV : lut_k) | (uint32_t)(lane * 4);
-    const int c8 = v & 7, cg = (v >> 3) & 7, blk = v >> 6;  // V̂ᵀ: tokens 64·blk + 8·c8.., coordinates 16·cg..
-    uint32_t i = 0, rc = 0;
+  } else if (warp < kSoft + 16) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    // ---------------- K̂ (thread = token v) and V̂ᵀ (thread = coordinate v), half of the columns each
+    const bool is_v = warp >= kSoft + 8;
+    const int v = tid & 127, half = (warp >> 2) & 1;
+    uint64_t* full = is_v ? ms.vh_full : ms.kh_full;
+    uint64_t* empty = is_v ? ms.vh_empty : ms.kh_empty;
+    const uint32_t dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (is_v ? kColV : kColK) + 32 * half;
+    const uint32_t lut = (uint32_t)((is_v ? kLutV : lut_k) + lane * 4);
+    uint32_t i = 0, st = 0, rph = 0;  // tile, raw stage and its phase
     bool ok = true;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
       b = g.b;
       for (int t = g.first; t < g.last; ++t, ++i) {
-        const uint32_t sb = i & 1u, op = ops + sb * kOp;
+        const uint32_t sb = i & 1u, op = dst + sb * 64;
         const bool draft = t >= g.ctiles;
-        const uint32_t st = rc % RS;
-        ok = bar_wait(&empty[sb], ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, lim) &&
-             (draft || bar_wait(&bar.raw_full[st], (rc / RS) & 1u, abort_flag, p.status, lim));
+        ok = bar_rest(&empty[sb], ((i >> 1) & 1u) ^ 1u, abort_flag, p.status, lim) &&
+             (draft || bar_rest(&ms.raw_full[st], rph, abort_flag, p.status, lim));
         ok = __all_sync(kFull, ok);
         if (!ok) break;
+        tc_fence_after();
         if (!draft) {
-          const uint32_t raw = kRaw + st * stage;
+          const int raw = raw_at(st);
           if (!is_v) {
             switch (p.kb) {
-              case 1: dequant_k<1>(raw, op, lut, v); break;
-              case 2: dequant_k<2>(raw, op, lut, v); break;
-              case 3: dequant_k<3>(raw, op, lut, v); break;
-              default: dequant_k<4>(raw, op, lut, v); break;
+              case 1: dequant_k<1>(smem, raw, op, lut, v, half); break;
+              case 2: dequant_k<2>(smem, raw, op, lut, v, half); break;
+              case 3: dequant_k<3>(smem, raw, op, lut, v, half); break;
+              default: dequant_k<4>(smem, raw, op, lut, v, half); break;
             }
           } else {
-            const uint32_t rv = raw + raw_v_off(p.kb);
+            const int rv = raw + 2048 * p.kb;
             switch (p.vb) {
-              case 1: dequant_v<1>(rv, op, lut, c8, cg, blk); break;
-              case 2: dequant_v<2>(rv, op, lut, c8, cg, blk); break;
-              case 3: dequant_v<3>(rv, op, lut, c8, cg, blk); break;
-              default: dequant_v<4>(rv, op, lut, c8, cg, blk); break;
+              case 1: dequant_v<1>(smem, rv, op, lut, v, half); break;
+              case 2: dequant_v<2>(smem, rv, op, lut, v, half); break;
+              case 3: dequant_v<3>(smem, rv, op, lut, v, half); break;
+              default: dequant_v<4>(smem, rv, op, lut, v, half); break;
             }
           }
         } else {
@@ -536,213 +634,260 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           const int64_t tok = g.s.start + t0;
           if (!is_v) {
             const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.krot) +
-                                                              ((tok + v) * p.Hkv + g.kvh) * 128);
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c) {
-              const uint4 x = v < nt ? src[c] : make_uint4(0u, 0u, 0u, 0u);
-              sts128(op + ((c >> 3) << 14) + v * 128 + ((uint32_t)((c & 7) ^ (v & 7)) << 4), x.x, x.y, x.z, x.w);
+                                                              ((tok + v) * p.Hkv + g.kvh) * 128) + 8 * half;
+#pragma unroll 1
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[16];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint4 x = v < nt ? src[4 * c + e] : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * e] = x.x;
+                w[4 * e + 1] = x.y;
+                w[4 * e + 2] = x.z;
+                w[4 * e + 3] = x.w;
+              }
+              tmem_st16(op + 16 * c, w);
             }
           } else {
-            const int first = 64 * blk + 8 * c8;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.vrot) + (tok * p.Hkv + g.kvh) * 128 + v;
+            const int64_t step = (int64_t)p.Hkv * 128;
 #pragma unroll 1
-            for (int half = 0; half < 2; ++half) {  // 8 coordinates of 8 tokens
-              uint32_t w[8][4];
+            for (int c = 0; c < 2; ++c) {
+              uint32_t w[16];
 #pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint4 x = first + k < nt
-                                    ? *(reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.vrot) +
-                                                                       ((tok + first + k) * p.Hkv + g.kvh) * 128 + 16 * cg) + half)
-                                    : make_uint4(0u, 0u, 0u, 0u);
-                w[k][0] = x.x;
-                w[k][1] = x.y;
-                w[k][2] = x.z;
-                w[k][3] = x.w;
+              for (int e = 0; e < 16; ++e) {
+                const int k = 64 * half + 32 * c + 2 * e;
+                const uint32_t x = k < nt ? src[k * step] : 0u, y = k + 1 < nt ? src[(k + 1) * step] : 0u;
+                w[e] = x | (y << 16);
               }
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {  // coordinate 16·cg + 8·half + k
-                uint32_t q[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  q[e] = __byte_perm(w[2 * e][k >> 1], w[2 * e + 1][k >> 1], (k & 1) ? 0x7632 : 0x5410);
-                sts128(op + (blk << 14) + (16 * cg + 8 * half + k) * 128 + ((uint32_t)(c8 ^ k) << 4), q[0], q[1], q[2], q[3]);
-              }
+              tmem_st16(op + 16 * c, w);
             }
           }
         }
-        fence_proxy_async();  // generic-proxy stores, read next by the tensor cores
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(&full[sb]);
-          if (!draft) mbar_arrive(&bar.raw_empty[st]);
+          if (!draft) mbar_arrive(&ms.raw_empty[st]);
         }
-        if (!draft) ++rc;
+        if (!draft && ++st == RS) {
+          st = 0;
+          rph ^= 1u;
+        }
       }
       u += g.last - g.first;
     }
-  } else if (warp == 12) {
-    // ---------------- the products: S of tile j goes before P·V̂ of tile j - 1,
-    // except where a new group's Q̂ has to wait for the last group's end
-    if (lane == 0) {
-      const uint32_t idesc = umma_idesc_f16(128, 128);
-      const int64_t n = u_end - u;
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    if (warp == kMma) {
+    // ---------------- the products: Sᵀ of tile j goes before V̂ᵀ·P of tile j - 1,
+    // except where a new group's Q̂ has to wait for the last group's end.  The
+    // whole warp walks through it, an elected lane issues
+      constexpr uint32_t idesc = umma_idesc_f16(128, N);
+      constexpr uint32_t idesc_p = idesc | (1u << 16);  // B contiguous along N
+      const uint64_t dq = umma_desc_sw128(smem_u32(smem + kQ));
+      // P: 64 rows of a token in 128 bytes, swizzled; 8-token groups 1024 bytes apart
+      constexpr uint64_t kPDesc = ((uint64_t)(1024 >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) |
+                                  ((uint64_t)2 << 61);
+      const uint64_t dp = kPDesc | (uint64_t)((smem_u32(smem + kP) >> 4) & 0x3FFF);
+      const int n = (int)(u_end - u);  // a CTA's share: fewer than 2^31
       int left = 0;
       uint32_t qn = 0;
       bool ok = true, fresh = false, fresh_prev = false;
-      auto product = [&](int64_t j, bool first) -> bool {  // P·V̂ of tile j
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(kFull, bar_rest(bar, parity, abort_flag, p.status, lim));
+      };
+      auto product = [&](int j, bool first) -> bool {  // V̂ᵀ·P of tile j
         const uint32_t sb = (uint32_t)j & 1u, ph = (uint32_t)(j >> 1) & 1u;
-        if (!bar_wait(&bar.p_full[sb], ph, abort_flag, p.status, lim) ||
-            !bar_wait(&bar.vh_full[sb], ph, abort_flag, p.status, lim))
-          return false;
+        if (!wait(&ms.p_full[sb], ph) || !wait(&ms.vh_full[sb], ph)) return false;
         tc_fence_after();
-        const uint32_t a = tmem + kColS + sb * 128, op = kOps + (2 + sb) * kOp;
+        const uint64_t bd = dp + (uint64_t)(sb * (2 * kPPart / 16));
+        const uint32_t a = tmem + kColV + sb * 64;
+        if (elect_one()) {
+          if constexpr (SPLIT) {  // remainders first: not truncated against a large sum
+            umma_f16_ts(tmem + kColO, a, bd + kPPart / 16, idesc_p, first ? 0u : 1u);
 #pragma unroll
-        for (int pass = SPLIT ? 0 : 1; pass < 2; ++pass)  // remainders first: not truncated against a large sum
+            for (int ks = 1; ks < 8; ++ks) umma_f16_ts(tmem + kColO, a + 8 * ks, bd + kPPart / 16 + ks * 128, idesc_p, 1u);
+          }
+          umma_f16_ts(tmem + kColO, a, bd, idesc_p, SPLIT || !first ? 1u : 0u);
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            umma_f16_ts(tmem + kColO, a + 32 * (ks >> 1) + 8 * (ks & 1) + (pass == 0 ? 16 : 0),
-                        umma_desc_sw128(op + (ks >> 2) * 16384 + (ks & 3) * 32), idesc,
-                        (first && ks == 0 && pass == (SPLIT ? 0 : 1)) ? 0u : 1u);
-        umma_commit(&bar.vh_empty[sb]);
-        umma_commit(&bar.pv_done[sb]);
+          for (int ks = 1; ks < 8; ++ks) umma_f16_ts(tmem + kColO, a + 8 * ks, bd + ks * 128, idesc_p, 1u);
+          umma_commit(&ms.vh_empty[sb]);
+          umma_commit(&ms.pv_done[sb]);
+        }
+        __syncwarp();
         return true;
       };
-      for (int64_t j = 0; ok && j <= n; ++j) {
+      for (int j = 0; ok && j <= n; ++j) {
         if (j < n) {
           fresh_prev = fresh;
           fresh = left == 0;
           if (left == 0) {
             const TreeSeg g = tree_seg(p, u + j, u_end, b);
             b = g.b;
-            left = g.last - g.first;
+            left = __shfl_sync(kFull, g.last - g.first, 0);
           }
           --left;
           if (fresh && j > 0 && !(ok = product(j - 1, fresh_prev))) break;
-          if (fresh && !(ok = bar_wait(&bar.q_full, qn++ & 1u, abort_flag, p.status, lim))) break;
+          if (fresh && !(ok = wait(&ms.q_full, qn++ & 1u))) break;
           const uint32_t sb = (uint32_t)j & 1u;
-          if (!(ok = bar_wait(&bar.kh_full[sb], (uint32_t)(j >> 1) & 1u, abort_flag, p.status, lim))) break;
+          if (!(ok = wait(&ms.kh_full[sb], (uint32_t)(j >> 1) & 1u))) break;
           tc_fence_after();
-          const uint32_t op = kOps + sb * kOp;
+          const uint32_t d = tmem + sb * 64, a = tmem + kColK + sb * 64;
+          if (elect_one()) {
 #pragma unroll
-          for (int pass = SPLIT ? 0 : 1; pass < 2; ++pass)
+            for (int pass = SPLIT ? 0 : 1; pass < 2; ++pass)
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-              umma_f16_ts(tmem + kColS + sb * 128, tmem + kColQ + 8 * ks + (pass == 0 ? 64 : 0),
-                          umma_desc_sw128(op + (ks >> 2) * 16384 + (ks & 3) * 32), idesc,
-                          (ks == 0 && pass == (SPLIT ? 0 : 1)) ? 0u : 1u);
-          umma_commit(&bar.kh_empty[sb]);
-          umma_commit(&bar.s_full[sb]);
+              for (int ks = 0; ks < 8; ++ks)
+                umma_f16_ts(d, a + 8 * ks, dq + ((pass == 0 ? kQPart : 0) + (ks >> 2) * (N * 128) + (ks & 3) * 32) / 16, idesc,
+                            (ks == 0 && pass == (SPLIT ? 0 : 1)) ? 0u : 1u);
+            umma_commit(&ms.kh_empty[sb]);
+            umma_commit(&ms.s_full[sb]);
+          }
+          __syncwarp();
           if (!fresh && !(ok = product(j - 1, fresh_prev))) break;
         } else if (j > 0 && !(ok = product(j - 1, fresh))) {
           break;
         }
       }
-      umma_commit(&bar.drain);  // every product issued completes before tensor memory is released
-      for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&bar.drain, 0u); ++k) {
+      if (elect_one()) umma_commit(&ms.drain);  // every product issued completes before tensor memory is released
+      for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
       }
-    }
-  } else {
-    // ---------------- copies of the packed tiles: lane = (16-token chunk, part)
+    } else if (warp == kCopy) {
+    // ---------------- copies of the packed tiles: lane = (16-token chunk, part);
+    // the first chunk of a run inside one page copies the run
     const int c = lane >> 2, part = lane & 3;
-    uint32_t i = 0, rc = 0;
+    uint32_t i = 0, rc = 0, st = 0, rph = 1;  // tile, cached tile, its stage and phase
     bool ok = true;
+    // pages and places advance by a tile without a division
+    const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
       b = g.b;
+      // this lane's chunk of tile t: token, page number within the sequence and
+      // place in the page; the vector there (-1: no such token, -2: no such page)
+      int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
+      const int32_t* pages = p.table ? p.table + (int64_t)g.b * p.max_blocks : nullptr;
+      auto vector_here = [&](int t) -> int64_t {
+        if (t >= g.ctiles || at >= g.s.len) return -1;
+        const int64_t page = pages ? (int64_t)__ldg(pages + j) : g.b;
+        return page >= 0 && page < p.pages ? (page * p.Hkv + g.kvh) * p.block + o : -2;
+      };
+      int64_t next = vector_here(g.first);
       for (int t = g.first; t < g.last; ++t, ++i) {
-        const uint32_t ns = i % kNormSlots, nb = norm_slot(i);
+        const uint32_t ns = i % kNormSlots;
+        unsigned char* nb = smem + kNorms + ns * 1024;
         const bool draft = t >= g.ctiles;
-        const uint32_t st = rc % RS;
-        ok = bar_wait(&bar.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
-             (draft || bar_wait(&bar.raw_empty[st], ((rc / RS) & 1u) ^ 1u, abort_flag, p.status, lim));
+        const int64_t vec = next;
+        at += kTreeTok;
+        j += jt;
+        o += ot;
+        if (o >= p.block) {
+          o -= p.block;
+          ++j;
+        }
+        next = vector_here(t + 1);  // its table entry is read while this tile waits for room
+        ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
+             (draft || bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim));
         ok = __all_sync(kFull, ok);
         if (!ok) break;
         if (draft) {
           const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+          float* nf = reinterpret_cast<float*>(nb);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int k = 4 * lane + e;
+            const int k = 32 * e + lane;
             const int64_t at = (int64_t)g.kvh * p.R + g.s.start + t0 + k;
-            const float fk = k < nt ? p.kfac[at] : 0.f, fv = k < nt ? p.vfac[at] : 0.f;
-            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(nb + 4 * k), "f"(fk) : "memory");
-            asm volatile("st.shared.f32 [%0], %1;\n" ::"r"(nb + 512 + 4 * k), "f"(fv) : "memory");
+            nf[k] = k < nt ? p.kfac[at] : 0.f;
+            nf[128 + k] = k < nt ? p.vfac[at] : 0.f;
           }
-          if (lane == 0) bar.valid[ns] = 0xFFu;
+          if (lane == 0) ms.valid[ns] = 0x11111111u;
           __syncwarp();
-          if (lane == 0) mbar_arrive(&bar.n_full[ns]);
+          if (lane == 0) mbar_arrive(&ms.n_full[ns]);
           continue;
         }
-        const int tok = t * kTreeTok + 16 * c;
-        int64_t vec = -1;
-        if (tok < g.s.len) {
-          const int j = tok / p.block;
-          const int64_t page = p.table ? (int64_t)__ldg(p.table + (int64_t)g.b * p.max_blocks + j) : g.b;
-          if (page >= 0 && page < p.pages)
-            vec = (page * p.Hkv + g.kvh) * p.block + (tok - j * p.block);
-          else if (part == 0)
-            atomicOr(p.status, 2);
-        }
+        if (vec == -2 && part == 0) atomicOr(p.status, 2);
         const uint32_t there = __ballot_sync(kFull, vec >= 0 && part == 0);
-        const uint32_t n = __popc(there);
-        const uint32_t raw = kRaw + st * stage;
+        const int64_t before = __shfl_up_sync(kFull, vec, 4);
+        const bool leads = vec >= 0 && (c == 0 || before < 0 || vec != before + 16);
+        const uint32_t starts = __ballot_sync(kFull, (leads || vec < 0) && part == 0);
         if (lane == 0) {
-          uint32_t m = 0;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) m |= ((there >> (4 * k)) & 1u) << k;
-          bar.valid[ns] = m;
-          mbar_arrive_expect_tx(&bar.raw_full[st], n * 256u * (uint32_t)(p.kb + p.vb));
-          mbar_arrive_expect_tx(&bar.n_full[ns], n * 128u);
+          ms.valid[ns] = there;
+          const uint32_t n = __popc(there);
+          mbar_arrive_expect_tx(&ms.raw_full[st], n * 256u * (uint32_t)(p.kb + p.vb));
+          mbar_arrive_expect_tx(&ms.n_full[ns], n * 128u);
         }
         __syncwarp();
-        if (vec >= 0) {
-          unsigned char* base = smem + (raw - kBase);
-          if (part == 0) {
-            bulk_g2s(base + c * 256 * p.kb, p.kcodes + vec * (4 * p.kb), 256 * p.kb, &bar.raw_full[st]);
-          } else if (part < 3) {  // 8 tokens, four PAIR blocks
-            const int h = part - 1;
-            bulk_g2s(base + raw_v_off(p.kb) + (2 * c + h) * (128 * p.vb + 16),
-                     p.vcodes + ((vec >> 1) + 4 * h) * (8 * p.vb), 128 * p.vb, &bar.raw_full[st]);
-          } else {
-            unsigned char* nd = smem + (nb - kBase) + 64 * c;
-            bulk_g2s(nd, p.knorm + vec, 64, &bar.n_full[ns]);
-            bulk_g2s(nd + 512, p.vnorm + vec, 64, &bar.n_full[ns]);
-          }
+        if (leads) {
+          // up to the next start (or the tile's end)
+          const uint32_t later = c < 7 ? starts >> (4 * (c + 1)) : 0u;
+          const uint32_t run = later ? (uint32_t)(__ffs(later) - 1) / 4 + 1 : (uint32_t)(8 - c);
+          unsigned char* raw = smem + raw_at(st);
+          if (part == 0)
+            bulk_g2s(raw + c * 256 * p.kb, p.kcodes + vec * (4 * p.kb), 256 * p.kb * run, &ms.raw_full[st]);
+          else if (part == 1)  // eight PAIR blocks a chunk
+            bulk_g2s(raw + 2048 * p.kb + c * 256 * p.vb, p.vcodes + (vec >> 1) * (8 * p.vb), 256 * p.vb * run, &ms.raw_full[st]);
+          else
+            bulk_g2s(nb + 512 * (part - 2) + 64 * c, (part == 2 ? p.knorm : p.vnorm) + vec, 64 * run, &ms.n_full[ns]);
         }
         ++rc;
+        if (++st == RS) {
+          st = 0;
+          rph ^= 1u;
+        }
       }
       u += g.last - g.first;
     }
     if (lane == 0) {
       // every copy issued lands before the CTA may exit (bounded)
-      for (uint32_t j = rc > (uint32_t)RS ? rc - RS : 0u; j < rc; ++j)
-        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&bar.raw_full[j % RS], (j / RS) & 1u); ++k) {
+      for (uint32_t j = rc > RS ? rc - RS : 0u; j < rc; ++j)
+        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.raw_full[j % RS], (j / RS) & 1u); ++k) {
         }
       for (uint32_t j = i > kNormSlots ? i - kNormSlots : 0u; j < i; ++j)
-        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&bar.n_full[j % kNormSlots], (j / kNormSlots) & 1u); ++k) {
+        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.n_full[j % kNormSlots], (j / kNormSlots) & 1u); ++k) {
         }
     }
+  }
   }
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 12) {
+  if (warp == kMma) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(ms.tmem, 512);
   }
 }
 
-template <bool SPLIT>
+template <int N, bool SPLIT>
 cudaError_t run(const TreeParams& p, cudaStream_t st) {
   static PerDeviceValue attr;
-  constexpr int bytes = (int)(kBars + sizeof(Bars) - kBase);
-  const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_kernel<SPLIT>, bytes);
+  const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_kernel<N, SPLIT>, kSmem);
   if (e != cudaSuccess) return e;
-  return tree_launch(tree_attend_kernel<SPLIT>, p.ctas, kThreads, bytes, p, st);
+  return tree_launch(tree_attend_kernel<N, SPLIT>, p.ctas, kThreads, kSmem, st, p);
+}
+
+template <bool SPLIT>
+cudaError_t run_n(const TreeParams& p, cudaStream_t st) {
+  switch (p.rows) {
+    case 16: return run<16, SPLIT>(p, st);
+    case 32: return run<32, SPLIT>(p, st);
+    case 64: return run<64, SPLIT>(p, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
+// Rows of a tile: enough for the mean sequence (its drafted tokens times the
+// query heads of a KV head), at most 64.  A longer one takes several tiles.
+int tree_umma_rows(int64_t rows, int B, int G) {
+  const int64_t mean = (rows + B - 1) / B * G;
+  return mean <= 16 ? 16 : mean <= 32 ? 32 : 64;
+}
+
 cudaError_t tree_attend_umma(const TreeParams& p, cudaStream_t st) {
-  return p.dtype == TQ_F16 ? run<true>(p, st) : run<false>(p, st);
+  return p.dtype == TQ_F16 ? run_n<true>(p, st) : run_n<false>(p, st);
 }
 
 }  // namespace tq
