@@ -285,37 +285,55 @@ def tq_decode_attention_noalloc(kctx, vctx, q, K, V, B, Hq, Hkv, seq, cap, scale
 
 
 # ---------------------------------------------------------------- serving
-def _dtype(t):
-    import torch
-    return {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}[t.dtype]
+# These calls are a few microseconds of GPU time each, so the binding looks at
+# every tensor once and asks the runtime for as little as it can.
+_T = None
+
+
+def _types():
+    """(torch, its type -> tq type, the raw current stream of a device), once torch is wanted."""
+    global _T
+    if _T is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = (lambda: raw(torch.cuda.current_device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        _T = torch, {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}, stream
+    return _T
+
+
+def _raw_stream(stream):
+    if stream is None:
+        return _types()[2]()
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dev(t, dtype, n, what):
     """Device address of a contiguous tensor of this type with n elements or more."""
-    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more is wanted")
     return t.data_ptr()
 
 
 def _heads(t, n, h, d, what):
     """Address and token stride of a [n, h, d] CUDA tensor whose heads are contiguous."""
-    if tuple(t.shape) != (n, h, d) or not t.is_cuda or t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    a, b, c = t.stride()
+    if t.shape != (n, h, d) or c != 1 or (b != d and h > 1) or not t.is_cuda:
         raise ValueError(f"{what}: a CUDA tensor [{n}, {h}, {d}] with contiguous heads is wanted")
-    return t.data_ptr(), t.stride(0) if n > 1 else h * d
+    return t.data_ptr(), a if n > 1 else h * d
 
 
 def tq_block_tables(lens, new, held, ring, state, table, block, held_out, state_out, row_start, slots, pos,
                     stream=None):
     """Pages, slots and positions of one step's tokens (include/tq.h).  table [B, max_blocks], ring, lens, new, held,
     held_out, row_start and pos are int32, state, state_out and slots int64; pos and slots have one entry per row."""
-    import torch
+    torch = _types()[0]
     i32, i64, B = torch.int32, torch.int64, lens.numel()
     _check("tq_block_tables", lib().tq_block_tables(
         _dev(lens, i32, B, "lens"), _dev(new, i32, B, "new"), _dev(held, i32, B, "held"), B, block,
         _dev(ring, i32, 1, "ring"), ring.numel(), _dev(state, i64, 2, "state"),
         _dev(table, i32, B * table.shape[-1], "table"), table.shape[-1], _dev(held_out, i32, B, "held_out"),
         _dev(state_out, i64, 2, "state_out"), _dev(row_start, i32, B + 1, "row_start"), _dev(slots, i64, 0, "slots"),
-        _dev(pos, i32, slots.numel(), "pos"), slots.numel(), _stream(stream)))
+        _dev(pos, i32, slots.numel(), "pos"), slots.numel(), _raw_stream(stream)))
 
 
 def tq_rope_frequencies(inv_freq, device="cuda"):
@@ -331,30 +349,31 @@ def tq_rope_frequencies(inv_freq, device="cuda"):
 def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=None):
     """Head norms and position rotation of q [N, Hq, d] and k [N, Hkv, d] into q_out and k_out (include/tq.h).
     wq, wk: [d] of q's type or None; freq: tq_rope_frequencies or None (norms alone); outputs may be the inputs."""
-    import torch
-    (N, Hq, d), Hkv = q.shape, k.shape[1]
-    if k.dtype != q.dtype or k_out.dtype != q_out.dtype:
+    torch, types, _ = _types()
+    (N, Hq, d), Hkv, ti, to = q.shape, k.shape[1], q.dtype, q_out.dtype
+    if k.dtype is not ti or k_out.dtype is not to:
         raise ValueError("q and k, and q_out and k_out, are of one type")
     (qp, qs), (kp, ks) = _heads(q, N, Hq, d, "q"), _heads(k, N, Hkv, d, "k")
     (qo, qos), (ko, kos) = _heads(q_out, N, Hq, d, "q_out"), _heads(k_out, N, Hkv, d, "k_out")
     _check("tq_qk_norm_rope", lib().tq_qk_norm_rope(
-        qp, qs, kp, ks, _dtype(q), N, Hq, Hkv, d, None if wq is None else _dev(wq, q.dtype, d, "wq"),
-        None if wk is None else _dev(wk, q.dtype, d, "wk"), eps,
+        qp, qs, kp, ks, types[ti], N, Hq, Hkv, d, None if wq is None else _dev(wq, ti, d, "wq"),
+        None if wk is None else _dev(wk, ti, d, "wk"), eps,
         None if freq is None else _dev(freq, torch.int64, 0, "freq"), 0 if freq is None else 2 * freq.numel(), style,
-        _dev(pos, torch.int32, N, "pos"), qo, qos, ko, kos, _dtype(q_out), _stream(stream)))
+        _dev(pos, torch.int32, N, "pos"), qo, qos, ko, kos, types[to], _raw_stream(stream)))
 
 
 def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
     """tq_encode of x [N, Hkv, d] into a paged cache, token i at slots[i] (include/tq.h)."""
-    import torch
+    torch, types, _ = _types()
     N, Hkv, d = x.shape
     if d != ctx.d:
         raise ValueError(f"x: rows of {ctx.d} elements are wanted")
-    if x.dtype not in (torch.float32, torch.float16):
+    ti = x.dtype
+    if ti is not torch.float32 and ti is not torch.float16:
         raise ValueError("x: float32 or float16 is wanted")
     _check("tq_encode_slots", lib().tq_encode_slots(
-        ctx.handle, _dev(x, x.dtype, 0, "x"), _dtype(x), N, Hkv, _dev(slots, torch.int64, N, "slots"), block,
-        ctypes.byref(codes.desc), _stream(stream)))
+        ctx.handle, _dev(x, ti, 0, "x"), types[ti], N, Hkv, _dev(slots, torch.int64, N, "slots"), block,
+        ctypes.byref(codes.desc), _raw_stream(stream)))
 
 
 def tq_tree_attention_workspace_size(kctx, B, Hq, Hkv, rows):
@@ -369,24 +388,25 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     """Attention of drafted tokens q [rows, Hq, d] over a packed cache and each other (include/tq.h).  k_new, v_new
     [rows, Hkv, d] or None (Hkv is then given); mask [rows, words] int32 or None (a chain); table [B, max_blocks] or
     None (contiguous, cap = block)."""
-    import torch
+    torch, types, _ = _types()
     rows, Hq, d = q.shape
+    ti = q.dtype
     B, Hkv = lens.numel(), k_new.shape[1] if k_new is not None else Hkv
     qp, qs = _heads(q, rows, Hq, d, "q")
     kp = vp = None
     ks = vs = 0
     if k_new is not None:
-        if k_new.dtype != q.dtype or v_new.dtype != q.dtype:
+        if k_new.dtype is not ti or v_new.dtype is not ti:
             raise ValueError("q, k_new and v_new are of one type")
         (kp, ks), (vp, vs) = _heads(k_new, rows, Hkv, d, "k_new"), _heads(v_new, rows, Hkv, d, "v_new")
     i32 = torch.int32
     words, width = 0 if mask is None else mask.shape[1], 0 if table is None else table.shape[1]
     _check("tq_tree_attention", lib().tq_tree_attention(
-        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, _dtype(q), rows, _dev(row_start, i32, B + 1, "row_start"),
+        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, types[ti], rows, _dev(row_start, i32, B + 1, "row_start"),
         None if mask is None else _dev(mask, i32, rows * words, "mask"), words, ctypes.byref(K.desc),
         ctypes.byref(V.desc), _dev(lens, i32, B, "lens"),
         None if table is None else _dev(table, i32, B * width, "table"), width, block, B, Hq, Hkv, scale,
-        _dev(out, q.dtype, rows * Hq * d, "out"), ws.data_ptr(), ws.numel() * ws.element_size(), _stream(stream)))
+        _dev(out, ti, rows * Hq * d, "out"), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)))
 
 
 def tq_unpack_indices(codes, first=0, count=None, with_bits=False):

@@ -582,6 +582,12 @@ __global__ void __launch_bounds__(kEncThreads, 1) encode128_kernel(const Enc128P
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if constexpr (SL) {
+    // a step appends few rows: the prologue and the matrix's copy overlap the
+    // kernel before (the matrix is constant); rows, slots and caches are touched
+    // after it
+    if (warp != 0) griddep_wait();
+  }
 
   if (warp == 0) {
     // ---------------- producer
@@ -590,6 +596,10 @@ __global__ void __launch_bounds__(kEncThreads, 1) encode128_kernel(const Enc128P
       mbar_arrive_expect_tx(tab_full, (uint32_t)(kTab * (PROD ? 2 : 1)));
       bulk_g2s(sPi, p.tab_pi, kTab, tab_full);
       if (PROD) bulk_g2s(sM, p.tab_m, kTab, tab_full);
+    }
+    if constexpr (SL) {
+      griddep_wait();
+      griddep_launch();
     }
     for (; (int)i < nloc; ++i) {
       const int64_t t = blockIdx.x + (int64_t)i * gridDim.x;
@@ -1228,6 +1238,19 @@ cudaError_t launch_t(const Enc128Params& p, const CUtensorMap& xmap, cudaStream_
   if (e != cudaSuccess) return e;
   const int64_t tiles = (p.N + kRows - 1) / kRows;
   const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)num_sms()));
+  if constexpr (SL) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kEncThreads);
+    cfg.dynamicSmemBytes = Lay<F16, PROD>::SmemAlloc;
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k, p, xmap);
+  }
   k<<<grid, kEncThreads, Lay<F16, PROD>::SmemAlloc, st>>>(p, xmap);
   return cudaGetLastError();
 }

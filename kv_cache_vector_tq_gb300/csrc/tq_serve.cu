@@ -74,6 +74,13 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
   const int tid = threadIdx.x;
   const int64_t head = p.state[0], tail = p.state[1];
   const int64_t avail = tail > head ? tail - head : 0;
+  // places in the ring: one remainder each, then offsets below the ring's size
+  const int64_t head_at = head % p.ring_size, tail_at = tail % p.ring_size;
+  auto place = [&](int64_t base, int64_t k) -> int64_t {  // k: fewer than the ring holds, but for broken states
+    int64_t at = base + k;
+    if (at >= p.ring_size) at -= p.ring_size;
+    return at < p.ring_size && at >= 0 ? at : ((at % p.ring_size) + p.ring_size) % p.ring_size;
+  };
   if (tid == 0) s_taken = 0;
   int take0 = 0, give0 = 0, row0 = 0;
   for (int b0 = 0; b0 < p.B; b0 += kBtThreads) {
@@ -111,11 +118,11 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
         // few pages a request: its own thread moves them (a prompt's many are moved below)
         if (served && take <= 32)
           for (int j = 0; j < take; ++j)
-            row[held + j] = p.ring_in[(head + (it - take) + j) % p.ring_size];
+            row[held + j] = p.ring_in[place(head_at, it - take + j)];
         if (served && give <= 32)
           for (int j = 0; j < give; ++j) {
-            const int64_t at = tail + (ig - give) + j;
-            if (at < head + p.ring_size) p.ring[at % p.ring_size] = row[need + j];
+            const int64_t k = (int64_t)(ig - give) + j;
+            if (tail + k < head + p.ring_size) p.ring[place(tail_at, k)] = row[need + j];
           }
       }
     }
@@ -130,11 +137,11 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
       const int t0 = __shfl_sync(kFull, it, src) - t, g0 = __shfl_sync(kFull, ig, src) - g;
       int32_t* row = p.table + (int64_t)bb * p.max_blocks;
       if (t > 32)
-        for (int j = tid & 31; j < t; j += 32) row[h + j] = p.ring_in[(head + t0 + j) % p.ring_size];
+        for (int j = tid & 31; j < t; j += 32) row[h + j] = p.ring_in[place(head_at, t0 + j)];
       if (g > 32)
         for (int j = tid & 31; j < g; j += 32) {
-          const int64_t at = tail + g0 + j;
-          if (at < head + p.ring_size) p.ring[at % p.ring_size] = row[nd + j];
+          const int64_t k = (int64_t)g0 + j;
+          if (tail + k < head + p.ring_size) p.ring[place(tail_at, k)] = row[nd + j];
         }
     }
     take0 += tg.x;
@@ -162,7 +169,7 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
       pos = p.len[lo] + (int)(r - s_start[lo]);
       const int j = pos / p.block, held = p.held[lo];
       const int32_t page = j < held ? p.table[(int64_t)lo * p.max_blocks + j]
-                                          : p.ring_in[(head + s_first[lo] + (j - held)) % p.ring_size];
+                                          : p.ring_in[place(head_at, s_first[lo] + (j - held))];
       slot = page >= 0 ? (int64_t)page * p.block + pos % p.block : -1;
     }
     p.slots[r] = slot;
@@ -196,15 +203,26 @@ struct NormRopeParams {
   float eps;
 };
 
+// Eight elements as they lie in memory, and as fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ Raw8<T> raw8(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
   if constexpr (sizeof(T) == 4) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   } else {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 f;
@@ -238,17 +256,42 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
-// LPR lanes per row (the power of two at or above d/8), U rows per lane group in flight.
+// LPR lanes per row (the power of two at or above d/8).  U rows per lane group
+// are loaded before the first is used: 24 warps with 4 rows of 256 bytes each
+// keep the 45 KB per SM in flight that the memory's latency asks for (2 rows and
+// 16 warps: 2.3 TB/s).
+template <typename TI>
+constexpr int kNrU = sizeof(TI) == 4 ? 2 : 4;
+
 template <typename TI, typename TO, int LPR>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int RPW = 32 / LPR, U = 2;
+__global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int RPW = 32 / LPR, U = kNrU<TI>;
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t job = (int64_t)blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
   if (job >= p.N * p.chunks) return;  // whole warps
-  const int64_t n = job / p.chunks;
-  const int h0 = (int)(job % p.chunks) * p.chunk, h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
+  int64_t n = job;
+  int h0 = 0;
+  if (p.chunks > 1) {
+    n = job <= 0xFFFFFFFFll ? (int64_t)((uint32_t)job / (uint32_t)p.chunks) : job / p.chunks;
+    h0 = (int)(job - n * p.chunks) * p.chunk;
+  }
+  const int h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
   const bool in = 8 * l < p.d;
   const int j0 = 8 * l, half = p.rot >> 1;
+  auto load = [&](int hb, Raw8<TI> (&x)[U]) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int h = hb + u * RPW + sub;
+      x[u] = Raw8<TI>{};
+      if (in && h < h1) {
+        const TI* src = h < p.Hq ? static_cast<const TI*>(p.q) + n * p.qs + (int64_t)h * p.d
+                                 : static_cast<const TI*>(p.k) + n * p.ks + (int64_t)(h - p.Hq) * p.d;
+        x[u] = raw8(src + j0);
+      }
+    }
+  };
+  Raw8<TI> x[U];
+  load(h0, x);
   // sines of this lane's 8 elements (half-split: element j turns with frequency j mod rot/2;
   // interleaved: j / 2)
   float cs[8], sn[8];
@@ -276,33 +319,23 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
   }
   // partner lane of the half-split pairing (inside the row's LPR lanes)
   const int plane = sub * LPR + (second ? l - (half >> 3) : l + (half >> 3));
-  float wq[8], wk[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) wq[e] = wk[e] = 1.f;
-  if (in && p.wq) load8(static_cast<const TI*>(p.wq) + j0, wq);
-  if (in && p.wk) load8(static_cast<const TI*>(p.wk) + j0, wk);
+  Raw8<TI> wq{}, wk{};
+  if (in && p.wq) wq = raw8(static_cast<const TI*>(p.wq) + j0);
+  if (in && p.wk) wk = raw8(static_cast<const TI*>(p.wk) + j0);
   const float inv_d = 1.f / (float)p.d;
 
   for (int hb = h0; hb < h1; hb += RPW * U) {
-    float x[U][8];
+    if (hb > h0) load(hb, x);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int h = hb + u * RPW + sub;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[u][e] = 0.f;
-      if (in && h < h1) {
-        const TI* src = h < p.Hq ? static_cast<const TI*>(p.q) + n * p.qs + (int64_t)h * p.d
-                                 : static_cast<const TI*>(p.k) + n * p.ks + (int64_t)(h - p.Hq) * p.d;
-        load8(src + j0, x[u]);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
+      if (hb + u * RPW >= h1) break;  // the same for the whole warp
       const int h = hb + u * RPW + sub;
       const bool isq = h < p.Hq;
+      float y[8];
+      widen8<TI>(x[u], y);
       float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[u][e], x[u][e], ss);
+      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
 #pragma unroll
       for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
       float r = rsqrtf(fmaf(ss, inv_d, p.eps));
@@ -311,7 +344,7 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
         // power of two that brings its largest magnitude to [1, 2)
         float m = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[u][e]));
+        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
 #pragma unroll
         for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
         int ex = 1;
@@ -319,14 +352,20 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const NormRopePar
         const float sc = ldexpf(1.f, 1 - ex);
         float s2 = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s2 = fmaf(x[u][e] * sc, x[u][e] * sc, s2);
+        for (int e = 0; e < 8; ++e) s2 = fmaf(y[e] * sc, y[e] * sc, s2);
 #pragma unroll
         for (int o = LPR / 2; o; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
         if (!(ss < 1e36f)) r = rsqrtf(fmaf(s2, inv_d, p.eps * sc * sc)) * sc;
       }
-      float y[8];
+      if (isq ? p.wq != nullptr : p.wk != nullptr) {
+        float w[8];
+        widen8<TI>(isq ? wq : wk, w);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[u][e] * r * (isq ? wq[e] : wk[e]);
+        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] *= r;
+      }
       float z[8];
       if (p.style == 0) {
 #pragma unroll
@@ -354,7 +393,7 @@ template <typename TI, typename TO>
 cudaError_t run_norm_rope(NormRopeParams p, cudaStream_t st) {
   int lpr = 4;
   while (8 * lpr < p.d) lpr <<= 1;
-  const int heads = p.Hq + p.Hkv, rows_per_trip = 2 * (32 / lpr);
+  const int heads = p.Hq + p.Hkv, rows_per_trip = kNrU<TI> * (32 / lpr);
   // a whole token per warp once the tokens alone fill the GPU (its sines are
   // then computed once); else as many warps per token as there are trips
   const int64_t fill = (int64_t)num_sms() * 32;

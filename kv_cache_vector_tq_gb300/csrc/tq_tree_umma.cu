@@ -24,9 +24,10 @@
 // Warps: 0-7 softmax (thread = token, half of the rows), 8-15 K̂ (thread = token,
 // half of the coordinates: 32 lookups of two codes), 16-23 V̂ᵀ (thread =
 // coordinate, half of the tokens: 32 lookups, one per PAIR block), 24 issues the
-// products, 25 the bulk copies of the packed tiles (per 16 tokens, so pages may
-// end anywhere on a multiple of 16); two more fill the warpgroup that hands its
-// registers to the softmax.  Lookup tables are replicated
+// products, 25-27 copy the packed tiles (K codes, V codes, norms) by 16-byte
+// asynchronous copies, each lane from the page of its own 16 tokens, so pages may
+// end anywhere on a multiple of 16 (bulk copies, one per run of a page, took 150
+// to 240 clocks each to issue: up to 32 a tile).  Lookup tables are replicated
 // per lane (one bank each) and aligned to their size, so an address is a shift
 // and an and-or.  Four roles run on each quarter of the SM, each through its own
 // code once per unit, so every role is a short rolled loop: unrolled over the
@@ -146,6 +147,24 @@ __device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatil
         : "memory");
     if (ok) return true;
     if ((n & 15u) == 15u && *abort_flag) return false;
+  }
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+// This lane's arrival on `bar` once its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
+}
+// B·16-byte-per-token codes of a tile: 16 tokens of a lane group's page (vec: the
+// vector of chunk lane / 4, or negative) are 16·B pieces in a row.
+template <int B>
+__device__ __forceinline__ void copy_codes(unsigned char* dst, const uint32_t* codes, int64_t vec, int lane) {
+#pragma unroll 4
+  for (int i = 0; i < 4 * B; ++i) {
+    const int e = 32 * i + lane, c = e / (16 * B);
+    const int64_t v = __shfl_sync(kFull, vec, 4 * c);
+    if (v >= 0) copy16(dst + 16 * e, reinterpret_cast<const unsigned char*>(codes) + v * (16 * B) + (e - c * (16 * B)) * 16);
   }
 }
 // One lane of a converged warp, by the instruction made for it: the products
@@ -281,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 
   if (tid == 0) {
     for (int i = 0; i < kRS; ++i) {
-      mbar_init(&ms.raw_full[i], 1);
+      mbar_init(&ms.raw_full[i], 64);  // every lane of two copy warps
       mbar_init(&ms.raw_empty[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
@@ -294,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       mbar_init(&ms.pv_done[i], 1);
     }
     for (int i = 0; i < kNormSlots; ++i) {
-      mbar_init(&ms.n_full[i], 1);
+      mbar_init(&ms.n_full[i], 33);  // every lane of the third, and the chunk bits
       mbar_init(&ms.n_empty[i], kSoft);
     }
     mbar_init(&ms.q_full, kSoft);
@@ -754,32 +773,26 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       if (elect_one()) umma_commit(&ms.drain);  // every product issued completes before tensor memory is released
       for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
       }
-    } else if (warp == kCopy) {
-    // ---------------- copies of the packed tiles: lane = (16-token chunk, part);
-    // the first chunk of a run inside one page copies the run
-    const int c = lane >> 2, part = lane & 3;
-    uint32_t i = 0, rc = 0, st = 0, rph = 1;  // tile, cached tile, its stage and phase
+    } else {
+    // ---------------- copies of the packed tiles: K codes, V codes, norms (and
+    // the factors of drafted rows)
+    const int what = warp - kCopy, c = lane >> 2;
+    uint32_t i = 0, st = 0, rph = 1;  // tile, stage of the cached tile and its phase
     bool ok = true;
     // pages and places advance by a tile without a division
     const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
       b = g.b;
-      // this lane's chunk of tile t: token, page number within the sequence and
-      // place in the page; the vector there (-1: no such token, -2: no such page)
+      // this lane's chunk of tile t: first token, page number within the sequence
+      // and place in the page; the vector there (-1: no such token, -2: no such page)
       int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
       const int32_t* pages = p.table ? p.table + (int64_t)g.b * p.max_blocks : nullptr;
-      auto vector_here = [&](int t) -> int64_t {
-        if (t >= g.ctiles || at >= g.s.len) return -1;
-        const int64_t page = pages ? (int64_t)__ldg(pages + j) : g.b;
-        return page >= 0 && page < p.pages ? (page * p.Hkv + g.kvh) * p.block + o : -2;
-      };
-      int64_t next = vector_here(g.first);
+      auto page_here = [&](int t) -> int { return t < g.ctiles && at < g.s.len ? (pages ? __ldg(pages + j) : g.b) : 0; };
+      int page = page_here(g.first);
       for (int t = g.first; t < g.last; ++t, ++i) {
-        const uint32_t ns = i % kNormSlots;
-        unsigned char* nb = smem + kNorms + ns * 1024;
         const bool draft = t >= g.ctiles;
-        const int64_t vec = next;
+        const int64_t vec = at >= g.s.len ? -1 : page >= 0 && page < p.pages ? ((int64_t)page * p.Hkv + g.kvh) * p.block + o : -2;
         at += kTreeTok;
         j += jt;
         o += ot;
@@ -787,51 +800,53 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           o -= p.block;
           ++j;
         }
-        next = vector_here(t + 1);  // its table entry is read while this tile waits for room
-        ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
-             (draft || bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim));
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        if (draft) {
-          const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
-          float* nf = reinterpret_cast<float*>(nb);
+        page = page_here(t + 1);  // read while this tile waits for room, used with the next
+        if (what == 2) {
+          const uint32_t ns = i % kNormSlots;
+          unsigned char* nb = smem + kNorms + ns * 1024;
+          ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          uint32_t there = 0x11111111u;
+          if (draft) {
+            const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+            float* nf = reinterpret_cast<float*>(nb);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 32 * e + lane;
-            const int64_t at = (int64_t)g.kvh * p.R + g.s.start + t0 + k;
-            nf[k] = k < nt ? p.kfac[at] : 0.f;
-            nf[128 + k] = k < nt ? p.vfac[at] : 0.f;
+            for (int e = 0; e < 4; ++e) {
+              const int k = 32 * e + lane;
+              const int64_t row = (int64_t)g.kvh * p.R + g.s.start + t0 + k;
+              nf[k] = k < nt ? p.kfac[row] : 0.f;
+              nf[128 + k] = k < nt ? p.vfac[row] : 0.f;
+            }
+            mbar_arrive(&ms.n_full[ns]);
+          } else {
+            if (vec == -2 && (lane & 3) == 0) atomicOr(p.status, 2);
+            there = __ballot_sync(kFull, vec >= 0 && (lane & 3) == 0);
+            if (vec >= 0) {  // four tokens a lane
+              copy16(nb + 16 * lane, p.knorm + vec + 4 * (lane & 3));
+              copy16(nb + 512 + 16 * lane, p.vnorm + vec + 4 * (lane & 3));
+            }
+            copies_arrive(&ms.n_full[ns]);
           }
-          if (lane == 0) ms.valid[ns] = 0x11111111u;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.n_full[ns]);
+          if (lane == 0) {
+            ms.valid[ns] = there;
+            mbar_arrive(&ms.n_full[ns]);
+          }
           continue;
         }
-        if (vec == -2 && part == 0) atomicOr(p.status, 2);
-        const uint32_t there = __ballot_sync(kFull, vec >= 0 && part == 0);
-        const int64_t before = __shfl_up_sync(kFull, vec, 4);
-        const bool leads = vec >= 0 && (c == 0 || before < 0 || vec != before + 16);
-        const uint32_t starts = __ballot_sync(kFull, (leads || vec < 0) && part == 0);
-        if (lane == 0) {
-          ms.valid[ns] = there;
-          const uint32_t n = __popc(there);
-          mbar_arrive_expect_tx(&ms.raw_full[st], n * 256u * (uint32_t)(p.kb + p.vb));
-          mbar_arrive_expect_tx(&ms.n_full[ns], n * 128u);
+        if (draft) continue;
+        ok = bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim);
+        ok = __all_sync(kFull, ok);
+        if (!ok) break;
+        unsigned char* raw = smem + raw_at(st) + (what == 1 ? 2048 * p.kb : 0);
+        const uint32_t* codes = what == 1 ? p.vcodes : p.kcodes;  // a PAIR block holds as much as its two vectors
+        switch (what == 1 ? p.vb : p.kb) {
+          case 1: copy_codes<1>(raw, codes, vec, lane); break;
+          case 2: copy_codes<2>(raw, codes, vec, lane); break;
+          case 3: copy_codes<3>(raw, codes, vec, lane); break;
+          default: copy_codes<4>(raw, codes, vec, lane); break;
         }
-        __syncwarp();
-        if (leads) {
-          // up to the next start (or the tile's end)
-          const uint32_t later = c < 7 ? starts >> (4 * (c + 1)) : 0u;
-          const uint32_t run = later ? (uint32_t)(__ffs(later) - 1) / 4 + 1 : (uint32_t)(8 - c);
-          unsigned char* raw = smem + raw_at(st);
-          if (part == 0)
-            bulk_g2s(raw + c * 256 * p.kb, p.kcodes + vec * (4 * p.kb), 256 * p.kb * run, &ms.raw_full[st]);
-          else if (part == 1)  // eight PAIR blocks a chunk
-            bulk_g2s(raw + 2048 * p.kb + c * 256 * p.vb, p.vcodes + (vec >> 1) * (8 * p.vb), 256 * p.vb * run, &ms.raw_full[st]);
-          else
-            bulk_g2s(nb + 512 * (part - 2) + 64 * c, (part == 2 ? p.knorm : p.vnorm) + vec, 64 * run, &ms.n_full[ns]);
-        }
-        ++rc;
+        copies_arrive(&ms.raw_full[st]);
         if (++st == RS) {
           st = 0;
           rph ^= 1u;
@@ -839,16 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       }
       u += g.last - g.first;
     }
-    if (lane == 0) {
-      // every copy issued lands before the CTA may exit (bounded)
-      for (uint32_t j = rc > RS ? rc - RS : 0u; j < rc; ++j)
-        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.raw_full[j % RS], (j / RS) & 1u); ++k) {
-        }
-      for (uint32_t j = i > kNormSlots ? i - kNormSlots : 0u; j < i; ++j)
-        for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.n_full[j % kNormSlots], (j / kNormSlots) & 1u); ++k) {
-        }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");  // every copy lands before the CTA may exit
     }
-  }
   }
 
   tc_fence_before();
