@@ -24,10 +24,9 @@
 // Warps: 0-7 softmax (thread = token, half of the rows), 8-15 K̂ (thread = token,
 // half of the coordinates: 32 lookups of two codes), 16-23 V̂ᵀ (thread =
 // coordinate, half of the tokens: 32 lookups, one per PAIR block), 24 issues the
-// products, 25-27 copy the packed tiles (K codes, V codes, norms) by 16-byte
-// asynchronous copies, each lane from the page of its own 16 tokens, so pages may
-// end anywhere on a multiple of 16 (bulk copies, one per run of a page, took 150
-// to 240 clocks each to issue: up to 32 a tile).  Lookup tables are replicated
+// products, 25 and 26 the bulk copies of the packed tiles (K and V, one per run of
+// 16-token chunks inside a page, so pages may end anywhere on a multiple of 16;
+// one warp for both kept the others waiting).  Lookup tables are replicated
 // per lane (one bank each) and aligned to their size, so an address is a shift
 // and an and-or.  Four roles run on each quarter of the SM, each through its own
 // code once per unit, so every role is a short rolled loop: unrolled over the
@@ -40,9 +39,12 @@ namespace {
 
 constexpr int kSoft = 8;                    // softmax warps: two per 32 tokens, half of the rows each
 constexpr int kMma = kSoft + 16, kCopy = kMma + 1;
-constexpr int kThreads = (kSoft + 20) * 32;
+constexpr int kThreads = (kSoft + 20) * 32;  // 28 warps of 72 registers; one fills the last warpgroup
+constexpr int kRegSoft = 96, kRegOps = 64, kRegRest = 56;  // 8·96 + 16·64 + 4·56 = 28·72
+static_assert(8 * kRegSoft + 16 * kRegOps + 4 * kRegRest <= 28 * 72, "registers that the launch does not have would be waited for");
 constexpr int kRS = 5;                     // packed tiles in flight (3 where K and V have tables of their own)
 constexpr int kNormSlots = 8;
+constexpr uint32_t kLandPolls = 1u << 14;  // a millisecond or more for copies under way
 // Tensor memory columns: Sᵀ x 2, Oᵀ, the rows' sums of weights per token lane, K̂ x 2, V̂ᵀ x 2
 constexpr uint32_t kColO = 128, kColL = 192, kColK = 256, kColV = 384;
 constexpr float kLazyUp = 14.f;            // raise M before a weight passes 2^14
@@ -74,35 +76,16 @@ struct Misc {
   uint64_t s_full[2], p_full[2], pv_done[2];
   uint64_t n_full[kNormSlots], n_empty[kNormSlots];
   uint64_t q_full, drain;
-  uint32_t valid[kNormSlots];  // bit 4c: the tile's 16-token chunk c is there
+  uint32_t valid[kNormSlots];  // bit c: the tile's 16-token chunk c is there
   uint32_t tmem;
   int abort;
 };
 constexpr int kSmem = kMisc + (int)sizeof(Misc);
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
-// Two fp32 values in one 64-bit register: one instruction per pair.
-__device__ __forceinline__ uint64_t pk2(float a, float b) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void up2(uint64_t r, float& a, float& b) {
-  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(a), "=f"(b) : "l"(r));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 // Tensor-memory loads complete; the loaded registers pass through, so that
@@ -147,24 +130,6 @@ __device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatil
         : "memory");
     if (ok) return true;
     if ((n & 15u) == 15u && *abort_flag) return false;
-  }
-}
-__device__ __forceinline__ void copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-// This lane's arrival on `bar` once its copies so far have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t* bar) {
-  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(smem_u32(bar)) : "memory");
-}
-// B·16-byte-per-token codes of a tile: 16 tokens of a lane group's page (vec: the
-// vector of chunk lane / 4, or negative) are 16·B pieces in a row.
-template <int B>
-__device__ __forceinline__ void copy_codes(unsigned char* dst, const uint32_t* codes, int64_t vec, int lane) {
-#pragma unroll 4
-  for (int i = 0; i < 4 * B; ++i) {
-    const int e = 32 * i + lane, c = e / (16 * B);
-    const int64_t v = __shfl_sync(kFull, vec, 4 * c);
-    if (v >= 0) copy16(dst + 16 * e, reinterpret_cast<const unsigned char*>(codes) + v * (16 * B) + (e - c * (16 * B)) * 16);
   }
 }
 // One lane of a converged warp, by the instruction made for it: the products
@@ -300,7 +265,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 
   if (tid == 0) {
     for (int i = 0; i < kRS; ++i) {
-      mbar_init(&ms.raw_full[i], 64);  // every lane of two copy warps
+      mbar_init(&ms.raw_full[i], 2);  // K and V
       mbar_init(&ms.raw_empty[i], 16);
     }
     for (int i = 0; i < 2; ++i) {
@@ -313,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       mbar_init(&ms.pv_done[i], 1);
     }
     for (int i = 0; i < kNormSlots; ++i) {
-      mbar_init(&ms.n_full[i], 33);  // every lane of the third, and the chunk bits
+      mbar_init(&ms.n_full[i], 2);
       mbar_init(&ms.n_empty[i], kSoft);
     }
     mbar_init(&ms.q_full, kSoft);
@@ -349,7 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   int b = u < u_end ? p.cta_seq[blockIdx.x] : 0;
 
   if (warp < kSoft) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegSoft));
     // ---------------- softmax: thread = token tok (its tensor-memory lane) and
     // rows n0 .. n0 + HN - 1; in the epilogue coordinate tok
     constexpr int HN = N / 2;  // rows of a thread
@@ -422,14 +387,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         const int t0 = draft ? (t - g.ctiles) * kTreeTok : t * kTreeTok;
         const int nt = min(kTreeTok, (draft ? g.s.T : g.s.len) - t0);
         const uint32_t chunks = ms.valid[ns];
-        const bool here = tok < nt && ((chunks >> (4 * (tok >> 4))) & 1u);  // this token is there
-        const bool whole = nt == kTreeTok && chunks == 0x11111111u && !draft;
+        const bool here = tok < nt && ((chunks >> (tok >> 4)) & 1u);  // this token is there
+        const bool whole = nt == kTreeTok && chunks == 0xFFu && !draft;
         const float kn = nrm[tok], vn = nrm[128 + tok];
         // 2^lv > vn, kept within 2^±100
         const float lv = fminf(fmaxf((float)((int)((__float_as_uint(vn) >> 23) & 255u) - 126), -100.f), 100.f);
         const float ck = ct * kn;
-        const uint64_t ck2 = pk2(ck, ck);
-        const bool odd = vn != vn;
         // drafted tokens: bit `lane` of a row's mask word for this warp's 32
         // tokens; lane n holds the word of row n0 + n
         uint32_t mw = 0u;
@@ -458,8 +421,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 #pragma unroll
             for (int e = 0; e < HN; e += 4) {
               const float4 m4 = *reinterpret_cast<const float4*>(ms.nm + n0 + e);
-              up2(fma2(pk2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), ck2, pk2(m4.x, m4.y)), pr[e], pr[e + 1]);
-              up2(fma2(pk2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), ck2, pk2(m4.z, m4.w)), pr[e + 2], pr[e + 3]);
+              pr[e] = fmaf(__uint_as_float(s[e]), ck, m4.x);
+              pr[e + 1] = fmaf(__uint_as_float(s[e + 1]), ck, m4.y);
+              pr[e + 2] = fmaf(__uint_as_float(s[e + 2]), ck, m4.z);
+              pr[e + 3] = fmaf(__uint_as_float(s[e + 3]), ck, m4.w);
             }
           }
           if (!whole) {
@@ -468,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
               if (!sees(e)) pr[e] = -INFINITY;
           }
 #pragma unroll
-          for (int e = 0; e < HN; e += 4) top = fmaxf(top, fmaxf(fmaxf(pr[e], pr[e + 1]), fmaxf(pr[e + 2], pr[e + 3])));
+          for (int e = 0; e < HN; e += 2) top = max3(top, pr[e], pr[e + 1]);
 #pragma unroll
           for (int e = 0; e < HN; ++e) pr[e] = ex2(pr[e]);
           if (!bar_any(!ok || (top + lv > kLazyUp && tries < 2))) break;
@@ -525,8 +490,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         if (!ok) break;
         // the rows' sums; P of a token: N values, 16-byte pieces in the 128-byte swizzle
         unsigned char* prow = smem + kP + sb * (2 * kPPart) + tok * 128;
-        const float vs = here ? vn : 0.f;  // the factors of a token that is not there may be anything
-        const uint64_t vs2 = pk2(vs, vs);
+        float vs = here ? vn : 0.f;  // the factors of a token that is not there may be anything
+        if (draft && vs != vs) {  // a drafted row that is not a number: neither are the rows that see it
+          vs = 0.f;
+#pragma unroll
+          for (int e = 0; e < HN; ++e) pr[e] = pr[e] == 0.f ? 0.f : NAN;
+        }
         uint32_t l[HN];
         tmem_ld_n(tL, l);
         wait_ld(l);
@@ -536,16 +505,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int n = 8 * c + 2 * e;
-            const uint64_t pp = pk2(pr[n], pr[n + 1]);
-            float l0, l1, w0, w1;
-            up2(add2(pk2(__uint_as_float(l[n]), __uint_as_float(l[n + 1])), pp), l0, l1);
-            l[n] = __float_as_uint(l0);
-            l[n + 1] = __float_as_uint(l1);
-            up2(mul2(pp, vs2), w0, w1);
-            if (odd) {  // a drafted row that is not a number has the factor NaN: only for rows that see it
-              w0 = pr[n] == 0.f ? 0.f : w0;
-              w1 = pr[n + 1] == 0.f ? 0.f : w1;
-            }
+            l[n] = __float_as_uint(__uint_as_float(l[n]) + pr[n]);
+            l[n + 1] = __float_as_uint(__uint_as_float(l[n + 1]) + pr[n + 1]);
+            const float w0 = pr[n] * vs, w1 = pr[n + 1] * vs;
             const __half2 h = __floats2half2_rn(w0, w1);
             hi[e] = h2_bits(h);
             if constexpr (SPLIT) lo[e] = h2_bits(__floats2half2_rn(w0 - __low2float(h), w1 - __high2float(h)));
@@ -608,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       u += g.last - g.first;
     }
   } else if (warp < kSoft + 16) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegOps));
     // ---------------- K̂ (thread = token v) and V̂ᵀ (thread = coordinate v), half of the columns each
     const bool is_v = warp >= kSoft + 8;
     const int v = tid & 127, half = (warp >> 2) & 1;
@@ -698,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       u += g.last - g.first;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegRest));
     if (warp == kMma) {
     // ---------------- the products: Sᵀ of tile j goes before V̂ᵀ·P of tile j - 1,
     // except where a new group's Q̂ has to wait for the last group's end.  The
@@ -773,26 +735,36 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       if (elect_one()) umma_commit(&ms.drain);  // every product issued completes before tensor memory is released
       for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
       }
-    } else {
-    // ---------------- copies of the packed tiles: K codes, V codes, norms (and
-    // the factors of drafted rows)
-    const int what = warp - kCopy, c = lane >> 2;
-    uint32_t i = 0, st = 0, rph = 1;  // tile, stage of the cached tile and its phase
+    } else if (warp <= kCopy + 1) {
+    // ---------------- copies of the packed tiles, K by one warp and V by the
+    // other: lane = 16-token chunk (codes: lanes 0-7, norms: 8-15); the first
+    // chunk of a run inside one page copies the run
+    const bool is_v = warp != kCopy;
+    const int c = lane & 7, bits = is_v ? p.vb : p.kb;
+    const unsigned char* codes = reinterpret_cast<const unsigned char*>(is_v ? p.vcodes : p.kcodes);
+    const float* norms = is_v ? p.vnorm : p.knorm;
+    const float* fac = is_v ? p.vfac : p.kfac;
+    const int raw_off = is_v ? 2048 * p.kb : 0, norm_off = is_v ? 512 : 0;
+    uint32_t i = 0, rc = 0, st = 0, rph = 1;  // tile, cached tile, its stage and phase
     bool ok = true;
     // pages and places advance by a tile without a division
     const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
       b = g.b;
-      // this lane's chunk of tile t: first token, page number within the sequence
-      // and place in the page; the vector there (-1: no such token, -2: no such page)
+      // this lane's chunk of tile t: token, page number within the sequence and
+      // place in the page
       int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
       const int32_t* pages = p.table ? p.table + (int64_t)g.b * p.max_blocks : nullptr;
       auto page_here = [&](int t) -> int { return t < g.ctiles && at < g.s.len ? (pages ? __ldg(pages + j) : g.b) : 0; };
       int page = page_here(g.first);
       for (int t = g.first; t < g.last; ++t, ++i) {
+        const uint32_t ns = i % kNormSlots;
+        unsigned char* nb = smem + kNorms + ns * 1024 + norm_off;
         const bool draft = t >= g.ctiles;
-        const int64_t vec = at >= g.s.len ? -1 : page >= 0 && page < p.pages ? ((int64_t)page * p.Hkv + g.kvh) * p.block + o : -2;
+        // the vector of the chunk (-1: no such token, -2: no such page)
+        const int64_t vec = draft || at >= g.s.len ? -1
+                            : page >= 0 && page < p.pages ? ((int64_t)page * p.Hkv + g.kvh) * p.block + o : -2;
         at += kTreeTok;
         j += jt;
         o += ot;
@@ -801,52 +773,43 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           ++j;
         }
         page = page_here(t + 1);  // read while this tile waits for room, used with the next
-        if (what == 2) {
-          const uint32_t ns = i % kNormSlots;
-          unsigned char* nb = smem + kNorms + ns * 1024;
-          ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim);
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
-          uint32_t there = 0x11111111u;
-          if (draft) {
-            const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
-            float* nf = reinterpret_cast<float*>(nb);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 32 * e + lane;
-              const int64_t row = (int64_t)g.kvh * p.R + g.s.start + t0 + k;
-              nf[k] = k < nt ? p.kfac[row] : 0.f;
-              nf[128 + k] = k < nt ? p.vfac[row] : 0.f;
-            }
-            mbar_arrive(&ms.n_full[ns]);
-          } else {
-            if (vec == -2 && (lane & 3) == 0) atomicOr(p.status, 2);
-            there = __ballot_sync(kFull, vec >= 0 && (lane & 3) == 0);
-            if (vec >= 0) {  // four tokens a lane
-              copy16(nb + 16 * lane, p.knorm + vec + 4 * (lane & 3));
-              copy16(nb + 512 + 16 * lane, p.vnorm + vec + 4 * (lane & 3));
-            }
-            copies_arrive(&ms.n_full[ns]);
-          }
-          if (lane == 0) {
-            ms.valid[ns] = there;
-            mbar_arrive(&ms.n_full[ns]);
-          }
-          continue;
-        }
-        if (draft) continue;
-        ok = bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim);
+        ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
+             (draft || bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim));
         ok = __all_sync(kFull, ok);
         if (!ok) break;
-        unsigned char* raw = smem + raw_at(st) + (what == 1 ? 2048 * p.kb : 0);
-        const uint32_t* codes = what == 1 ? p.vcodes : p.kcodes;  // a PAIR block holds as much as its two vectors
-        switch (what == 1 ? p.vb : p.kb) {
-          case 1: copy_codes<1>(raw, codes, vec, lane); break;
-          case 2: copy_codes<2>(raw, codes, vec, lane); break;
-          case 3: copy_codes<3>(raw, codes, vec, lane); break;
-          default: copy_codes<4>(raw, codes, vec, lane); break;
+        if (draft) {
+          const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int k = 32 * e + lane;
+            reinterpret_cast<float*>(nb)[k] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
+          }
+          if (lane == 0 && !is_v) ms.valid[ns] = 0xFFu;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.n_full[ns]);
+          continue;
         }
-        copies_arrive(&ms.raw_full[st]);
+        const uint32_t there = __ballot_sync(kFull, vec >= 0) & 0xFFu;
+        const int64_t before = __shfl_up_sync(kFull, vec, 1);
+        const bool leads = vec >= 0 && (c == 0 || before < 0 || vec != before + 16);
+        const uint32_t starts = __ballot_sync(kFull, leads || vec < 0) & 0xFFu;
+        if (lane == 0) {
+          if (!is_v) ms.valid[ns] = there;
+          const uint32_t n = __popc(there);
+          mbar_arrive_expect_tx(&ms.raw_full[st], n * 256u * (uint32_t)bits);
+          mbar_arrive_expect_tx(&ms.n_full[ns], n * 64u);
+        }
+        if (vec == -2 && lane < 8 && !is_v) atomicOr(p.status, 2);
+        __syncwarp();
+        if (leads && lane < 16) {
+          const uint32_t later = starts >> (c + 1);  // up to the next start (or the tile's end)
+          const uint32_t run = later ? (uint32_t)__ffs(later) : (uint32_t)(8 - c);
+          const bool nrm = lane >= 8;
+          bulk_g2s(nrm ? nb + 64 * c : smem + raw_at(st) + raw_off + c * 256 * bits,
+                   nrm ? (const void*)(norms + vec) : (const void*)(codes + vec * (16 * bits)),
+                   run * (nrm ? 64u : 256u * bits), nrm ? &ms.n_full[ns] : &ms.raw_full[st]);
+        }
+        ++rc;
         if (++st == RS) {
           st = 0;
           rph ^= 1u;
@@ -854,7 +817,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       }
       u += g.last - g.first;
     }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");  // every copy lands before the CTA may exit
+    // Every copy issued lands before the CTA may exit.  A walk to the end has had
+    // all of them consumed; one that a wait cut short leaves some under way, on
+    // barriers that nobody arms any more: each stage's and slot's last phase
+    // (bounded, and short: a barrier that only the other warp armed stays as it is).
+    if (lane == 0 && *abort_flag) {
+      for (uint32_t q = rc > RS ? rc - RS : 0u; q < rc; ++q)
+        for (uint32_t k = 0; k < kLandPolls && !mbar_try_wait(&ms.raw_full[q % RS], (q / RS) & 1u); ++k) {
+        }
+      for (uint32_t q = i > kNormSlots ? i - kNormSlots : 0u; q < i; ++q)
+        for (uint32_t k = 0; k < kLandPolls && !mbar_try_wait(&ms.n_full[q % kNormSlots], (q / kNormSlots) & 1u); ++k) {
+        }
+    }
     }
   }
 

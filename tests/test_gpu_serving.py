@@ -428,6 +428,13 @@ def test_tree_many_splits(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_tree_many_tiles_with_two_codebooks(dtype):
+    """Many tiles for every CTA, K and V of different widths (a table each), pages of one chunk; wide and narrow tiles."""
+    tree_case(dtype, 4, 2, 32, 8, 16, [6000, 5000, 7011, 4090], [16, 9, 12, 10], "tree")
+    tree_case(dtype, 3, 4, 8, 8, 48, [30011, 9000], [9, 5], "tree")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_tree_masks_and_empty_rows(dtype):
     """Random masks, rows that see nothing, drafted tokens past the mask's words."""
     tree_case(dtype, 4, 4, 8, 2, 16, [40, 0], [50, 33], "random")
