@@ -256,16 +256,22 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
   }
 }
 
-// LPR lanes per row (the power of two at or above d/8).  U rows per lane group
-// are loaded before the first is used: 24 warps with 4 rows of 256 bytes each
-// keep the 45 KB per SM in flight that the memory's latency asks for (2 rows and
-// 16 warps: 2.3 TB/s).
+// LPR lanes per row (the power of two at or above d/8).  Rows come by 16-byte
+// asynchronous copies into slots of shared memory that are each lane's own (no
+// barrier), kNrAhead lane groups of rows ahead of the one in use: 32 warps with
+// eight times 512 bytes each cover the memory's latency several times over.
+// (Four rows ahead in registers, 24 warps: 3.6 TB/s; two and 16 warps: 2.3 TB/s.)
 template <typename TI>
-constexpr int kNrU = sizeof(TI) == 4 ? 2 : 4;
+constexpr int kNrAhead = sizeof(TI) == 4 ? 4 : 8;
+
+__device__ __forceinline__ void nr_copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
 
 template <typename TI, typename TO, int LPR>
-__global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int RPW = 32 / LPR, U = kNrU<TI>;
+__global__ void __launch_bounds__(kNrThreads, 4) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int RPW = 32 / LPR, A = kNrAhead<TI>;
+  __shared__ __align__(16) Raw8<TI> ring[A][kNrThreads];
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t job = (int64_t)blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
   if (job >= p.N * p.chunks) return;  // whole warps
@@ -278,20 +284,19 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
   const int h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
   const bool in = 8 * l < p.d;
   const int j0 = 8 * l, half = p.rot >> 1;
-  auto load = [&](int hb, Raw8<TI> (&x)[U]) {
+  const TI* qrow = static_cast<const TI*>(p.q) + n * p.qs + j0;
+  const TI* krow = static_cast<const TI*>(p.k) + n * p.ks + j0;
+  auto fetch = [&](int h, int slot) {  // this lane's piece of head h
+    if (in && h < h1) {
+      const TI* src = h < p.Hq ? qrow + (int64_t)h * p.d : krow + (int64_t)(h - p.Hq) * p.d;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int h = hb + u * RPW + sub;
-      x[u] = Raw8<TI>{};
-      if (in && h < h1) {
-        const TI* src = h < p.Hq ? static_cast<const TI*>(p.q) + n * p.qs + (int64_t)h * p.d
-                                 : static_cast<const TI*>(p.k) + n * p.ks + (int64_t)(h - p.Hq) * p.d;
-        x[u] = raw8(src + j0);
-      }
+      for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
+        nr_copy16(&ring[slot][threadIdx.x].w[i], reinterpret_cast<const uint4*>(src) + i);
     }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");  // always, so that the groups count the heads
   };
-  Raw8<TI> x[U];
-  load(h0, x);
+#pragma unroll
+  for (int a = 0; a < A; ++a) fetch(h0 + a * RPW + sub, a);
   // sines of this lane's 8 elements (half-split: element j turns with frequency j mod rot/2;
   // interleaved: j / 2)
   float cs[8], sn[8];
@@ -324,15 +329,18 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
   if (in && p.wk) wk = raw8(static_cast<const TI*>(p.wk) + j0);
   const float inv_d = 1.f / (float)p.d;
 
-  for (int hb = h0; hb < h1; hb += RPW * U) {
-    if (hb > h0) load(hb, x);
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      if (hb + u * RPW >= h1) break;  // the same for the whole warp
-      const int h = hb + u * RPW + sub;
+  int slot = 0;
+#pragma unroll 1
+  for (int hb = h0; hb < h1; hb += RPW) {
+      const int h = hb + sub;
       const bool isq = h < p.Hq;
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(A - 1) : "memory");
+      Raw8<TI> x{};
+      if (in && h < h1) x = ring[slot][threadIdx.x];
+      fetch(h + A * RPW, slot);  // the slot's words are in registers
+      if (++slot == A) slot = 0;
       float y[8];
-      widen8<TI>(x[u], y);
+      widen8<TI>(x, y);
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
@@ -385,15 +393,15 @@ __global__ void __launch_bounds__(kNrThreads, 3) norm_rope_kernel(const NormRope
                       : static_cast<TO*>(p.ko) + n * p.kos + (int64_t)(h - p.Hq) * p.d;
         store8(dst + j0, z);
       }
-    }
   }
+  asm volatile("cp.async.wait_all;\n" ::: "memory");
 }
 
 template <typename TI, typename TO>
 cudaError_t run_norm_rope(NormRopeParams p, cudaStream_t st) {
   int lpr = 4;
   while (8 * lpr < p.d) lpr <<= 1;
-  const int heads = p.Hq + p.Hkv, rows_per_trip = kNrU<TI> * (32 / lpr);
+  const int heads = p.Hq + p.Hkv, rows_per_trip = 32 / lpr;
   // a whole token per warp once the tokens alone fill the GPU (its sines are
   // then computed once); else as many warps per token as there are trips
   const int64_t fill = (int64_t)num_sms() * 32;

@@ -487,11 +487,11 @@ __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, c
           o.z *= fa;
           o.w *= fa;
           uint32_t todo = __ballot_sync(kFull, on);
-          while (todo) {  // four records at a time, all their loads in flight
-            float4 a[4];
-            float fk[4];
+          while (todo) {  // eight records at a time, all their loads in flight
+            float4 a[8];
+            float fk[8];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 8; ++q) {
               fk[q] = 0.f;
               a[q] = make_float4(0.f, 0.f, 0.f, 0.f);
               if (todo) {
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, c
               }
             }
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < 8; ++q) {
               o.x = fmaf(a[q].x, fk[q], o.x);
               o.y = fmaf(a[q].y, fk[q], o.y);
               o.z = fmaf(a[q].z, fk[q], o.z);

@@ -111,24 +111,31 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[16]) { tmem
 __device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[8]) { tmem_ld8_nw(at, v); }
 __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[16]) { tmem_st16(at, v); }
 __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[8]) { tmem_st8(at, v); }
-// bar_wait with a suspension of up to a few microseconds per poll: 25 warps that
-// poll as fast as they can take issue slots from those that work.
+// One poll of a phase, suspended for up to a few microseconds: 25 warps that poll
+// as fast as they can take issue slots from those that work.
+__device__ __forceinline__ bool poll_rest(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
+      : "memory");
+  return ok != 0;
+}
+// bar_wait with such polls; the first one, which mostly does, takes five
+// instructions (a third of all instructions here once were waits).
 __device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
                                          uint32_t limit) {
-  for (uint32_t n = 0;; ++n) {
+  if (limit != 0u && poll_rest(bar, parity)) return true;
+#pragma unroll 1
+  for (uint32_t n = 1;; ++n) {
     if (n >= limit) {
       *abort_flag = 1;
       atomicOr(status, 1);
       return false;
     }
-    uint32_t ok;
-    asm volatile(
-        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-        " selp.u32 %0, 1, 0, p;\n}\n"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
-        : "memory");
-    if (ok) return true;
+    if (poll_rest(bar, parity)) return true;
     if ((n & 15u) == 15u && *abort_flag) return false;
   }
 }
@@ -213,7 +220,7 @@ __device__ __forceinline__ void dequant_k(const unsigned char* smem, int raw, ui
       const int i = (2 * B * e) >> 5, s = (2 * B * e) & 31;
       uint32_t x;  // the field to bits 7..
       if (s + 2 * B > 32)
-        x = __funnelshift_r(all[i], all[i + 1 < B ? i + 1 : i], s) << 7;
+        x = __funnelshift_r(all[i], all[i + 1 < B ? i + 1 : i], s - 7);
       else
         x = s >= 7 ? all[i] >> (s - 7) : all[i] << (7 - s);
       v[e] = lds_u32(smem + ((x & m) | lut));
