@@ -231,26 +231,68 @@ __device__ __forceinline__ void dequant_k(const unsigned char* smem, int raw, ui
   }
 }
 
-// Half of the V̂ᵀ row of coordinate d (tensor-memory lane d): column i holds PAIR
+// Coordinate of lane l of V̂ᵀ and Oᵀ.  With 3-bit codes a pair field is six bits,
+// and those of coordinates 5 and 10 of every 16 cross a 32-bit word: they are
+// gathered in the last lanes, so that the other warps take one load per field
+// instead of two bytes (349 -> 332 us for 32 tokens of 64 heads over 131072; with
+// split operands, whose other roles are longer, two bytes are the faster way, 295
+// against 310 us for 252 rows over 48K: there lanes keep their coordinates).
+template <bool WORDS>
+__device__ __forceinline__ int lane_coord(int l, int vb) {
+  if (!WORDS || vb != 3) return l;
+  const int q = l < 112 ? l / 14 : (l - 112) >> 1, r = l - 14 * q;
+  return 16 * q + (l < 112 ? r + (r >= 5) + (r >= 9) : ((l & 1) ? 10 : 5));
+}
+
+// Half of the V̂ᵀ row of coordinate d (tensor-memory lane l): column i holds PAIR
 // block i's two tokens, the 2B bits at bit 2B·d of the block.
-template <int B>
-__device__ __forceinline__ void dequant_v(const unsigned char* smem, int raw, uint32_t tmem, uint32_t lut, int d, int half) {
+template <int B, bool WORDS>
+__device__ __forceinline__ void dequant_v(const unsigned char* smem, int raw, uint32_t tmem, uint32_t lut, int d, int l, int half) {
   constexpr uint32_t m = ((1u << (2 * B)) - 1u) << 7;
-  const unsigned char* src = smem + raw + half * (32 * 32 * B) + ((2 * B * d) >> 3);
-  const int up = B == 4 ? 7 : 7 - ((2 * B * d) & 7);  // the field to bits 7..
+  if constexpr (B == 3 && WORDS) {
+    const unsigned char* src = smem + raw + half * (32 * 32 * B) + ((6 * d) >> 5) * 4;
+    const uint32_t s = (6 * d) & 31;
+    if (l < 96) {  // whole warps: the field inside one word, turned to bits 7..
+      const uint32_t turn = (39u - s) & 31u;
 #pragma unroll 1
-  for (int c = 0; c < 2; ++c) {
-    uint32_t v[16];
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const unsigned char* at = src + e * (32 * B);
-      v[e] = at[0];
-      if constexpr (B == 3) v[e] |= (uint32_t)at[1] << 8;  // six bits may end in the next byte
+        for (int e = 0; e < 16; ++e) v[e] = lds_u32(src + e * 96);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = lds_u32(smem + ((__funnelshift_l(v[e], v[e], turn) & m) | lut));
+        tmem_st16(tmem + 16 * c, v);
+        src += 16 * 96;
+      }
+    } else {  // the field across this word and the next (one word past the last block stays in the tile's buffer)
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t v[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          v[e] = __funnelshift_r(lds_u32(src + e * 96), lds_u32(src + e * 96 + 4), s);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = lds_u32(smem + (((v[e] << 7) & m) | lut));
+        tmem_st16(tmem + 16 * c, v);
+        src += 16 * 96;
+      }
     }
+  } else {
+    const unsigned char* src = smem + raw + half * (32 * 32 * B) + ((2 * B * d) >> 3);
+    const int up = B == 4 ? 7 : 7 - ((2 * B * d) & 7);  // the field to bits 7..
+#pragma unroll 1
+    for (int c = 0; c < 2; ++c) {
+      uint32_t v[16];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = lds_u32(smem + (B == 4 ? lut + v[e] * 128u : (((v[e] << up) & m) | lut)));
-    tmem_st16(tmem + 16 * c, v);
-    src += 16 * 32 * B;
+      for (int e = 0; e < 16; ++e) {
+        v[e] = src[e * (32 * B)];
+        if constexpr (B == 3) v[e] |= (uint32_t)src[e * (32 * B) + 1] << 8;  // six bits may end in the next byte
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) v[e] = lds_u32(smem + (B == 4 ? lut + v[e] * 128u : (((v[e] << up) & m) | lut)));
+      tmem_st16(tmem + 16 * c, v);
+      src += 16 * 32 * B;
+    }
   }
 }
 
@@ -323,9 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   if (warp < kSoft) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegSoft));
     // ---------------- softmax: thread = token tok (its tensor-memory lane) and
-    // rows n0 .. n0 + HN - 1; in the epilogue coordinate tok
+    // rows n0 .. n0 + HN - 1; in the epilogue coordinate `coord`
     constexpr int HN = N / 2;  // rows of a thread
-    const int n0 = (warp >> 2) * HN, quad = warp & 3, tok = tid & 127;
+    const int n0 = (warp >> 2) * HN, quad = warp & 3, tok = tid & 127, coord = lane_coord<!SPLIT>(tok, p.vb);
     const uint32_t lane_base = ((uint32_t)(32 * quad) << 16) + n0;
     const uint32_t tO = tmem + lane_base + kColO, tL = tmem + lane_base + kColL;
     const int sw = tok & 7;
@@ -569,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 #pragma unroll
         for (int e = 0; e < PC; ++e) {
           const int n = n0 + PC * c + e;
-          if (n < g.nrow) base[(int64_t)(g.first == 0 ? ms.vec[n] : n) * kTreeRec + 4 + tok] = __uint_as_float(o[e]);
+          if (n < g.nrow) base[(int64_t)(g.first == 0 ? ms.vec[n] : n) * kTreeRec + 4 + coord] = __uint_as_float(o[e]);
         }
       }
       tc_fence_before();
@@ -580,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegOps));
     // ---------------- K̂ (thread = token v) and V̂ᵀ (thread = coordinate v), half of the columns each
     const bool is_v = warp >= kSoft + 8;
-    const int v = tid & 127, half = (warp >> 2) & 1;
+    const int v = tid & 127, half = (warp >> 2) & 1, vd = lane_coord<!SPLIT>(v, p.vb);
     uint64_t* full = is_v ? ms.vh_full : ms.kh_full;
     uint64_t* empty = is_v ? ms.vh_empty : ms.kh_empty;
     const uint32_t dst = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + (is_v ? kColV : kColK) + 32 * half;
@@ -610,10 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           } else {
             const int rv = raw + 2048 * p.kb;
             switch (p.vb) {
-              case 1: dequant_v<1>(smem, rv, op, lut, v, half); break;
-              case 2: dequant_v<2>(smem, rv, op, lut, v, half); break;
-              case 3: dequant_v<3>(smem, rv, op, lut, v, half); break;
-              default: dequant_v<4>(smem, rv, op, lut, v, half); break;
+              case 1: dequant_v<1, !SPLIT>(smem, rv, op, lut, vd, v, half); break;
+              case 2: dequant_v<2, !SPLIT>(smem, rv, op, lut, vd, v, half); break;
+              case 3: dequant_v<3, !SPLIT>(smem, rv, op, lut, vd, v, half); break;
+              default: dequant_v<4, !SPLIT>(smem, rv, op, lut, vd, v, half); break;
             }
           }
         } else {
@@ -637,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
               tmem_st16(op + 16 * c, w);
             }
           } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.vrot) + (tok * p.Hkv + g.kvh) * 128 + v;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.vrot) + (tok * p.Hkv + g.kvh) * 128 + vd;
             const int64_t step = (int64_t)p.Hkv * 128;
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
