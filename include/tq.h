@@ -440,14 +440,19 @@ tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64
  *           + t).
  * Hq / Hkv any whole number.  block a multiple of 16.
  * d_out     [rows, Hq, d] of `dtype`, contiguous.
- * Accuracy: F32 inputs are computed in fp32 throughout.
+ * Accuracy: F32 inputs are computed in fp32 throughout (CUDA cores).  F16 and
+ * BF16 inputs take the tensor cores: cached values are the codebook's α·c
+ * rounded to fp16, the drafted rows Πk, Πv one fp16 each, q and the weights two
+ * fp16 terms (F16) or one (BF16), sums in fp32; the error is then of the size of
+ * the output type's own rounding.
  * d_ws      workspace of tq_tree_attention_workspace_size bytes (16-byte
  *           aligned; its contents do not matter).  Calls that share one must be
  *           ordered on one stream; captured graphs that may run at the same time
  *           need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
  * UNSUPPORTED for d != 128, Prod or b + 1/2-bit codes, a block that is not a
- * multiple of 16, or rows * Hq, max_blocks * block >= 2^31.
+ * multiple of 16, or rows * Hq, max_blocks * block >= 2^31, or so many rows over so
+ * large a capacity (rows * Hq / 16 times (capacity + rows) / 128) as to pass 2^31.
  */
 tq_status tq_tree_attention_workspace_size(const tq_ctx* kctx, int B, int Hq, int Hkv, int64_t rows, size_t* bytes);
 tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* d_q, int64_t q_stride,

@@ -9,7 +9,7 @@ namespace tq {
 
 tq_status launch_encode_slots(const DevCtx& c, const void* x, int x_dtype, int64_t N, int Hkv, const int64_t* slots,
                               int block, const tq_codes* out, cudaStream_t stream) {
-  if (!enc128_supported(c) || N * Hkv > INT32_MAX) return TQ_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit
+  if (!enc128_supported(c) || N > INT32_MAX / Hkv) return TQ_ERR_UNSUPPORTED;  // TMA row coordinates are 32-bit
   Enc128Params p = enc128_params(c, x, N * Hkv, out);
   p.slots = slots;
   p.hkv = Hkv;

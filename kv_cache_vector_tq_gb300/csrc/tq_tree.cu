@@ -655,6 +655,10 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   p.zfold = p.zscale / p.kone;
   p.ofold = 1.f / p.vone;
   p.wait_limit = kc.wait_limit;
+  // the units of a sequence, whatever it turns out to be, are counted in 32 bits
+  const int64_t most_rt = (a.R * p.G + p.rows - 1) / p.rows;
+  const int64_t most_per = (int64_t)p.max_blocks * p.block / kTreeTok + a.R / kTreeTok + 2;
+  if (most_rt > 0 && most_per > (int64_t)INT32_MAX / (most_rt * a.Hkv)) return TQ_ERR_UNSUPPORTED;
   // groups of kPrepV rows, as many to a CTA as leave two CTAs on every SM
   const int64_t nq = (a.R * a.Hq + kPrepV - 1) / kPrepV, nk = a.k_new ? (a.R * a.Hkv + kPrepV - 1) / kPrepV : 0;
   const int64_t fill = 2 * (int64_t)num_sms();

@@ -540,6 +540,48 @@ def test_tree_captured_serves_later_lengths():
     assert torch.equal(other[:10], out)
 
 
+def test_tree_waits_are_bounded():
+    """With a wait limit of 0 every pipeline wait gives up before its first poll: the call returns, the status says so
+    once, and the next call is right again."""
+    c = tq.Context(D, 4, tq.TQ_MSE, tq.TQ_ROT_DENSE, tq.tq_rotation_haar(synth.gaussian_matrix(0, D)))
+    for dtype, new in ((torch.bfloat16, [3, 2]), (torch.float16, [20, 9])):
+        s = make_tree(dtype, 4, 4, 8, 2, 16, [700, 3000], new)
+        ws = torch.zeros(tq.tq_tree_attention_workspace_size(c, 2, 8, 2, sum(new)) // 4 + 4, device="cuda")
+        out = torch.zeros(sum(new), 8, D, dtype=dtype, device="cuda")
+
+        def call():
+            tq.tq_tree_attention(c, c, s["q"], s["k"], s["v"], s["start"], None, s["K"], s["V"], s["lens"], s["table"], 16,
+                                 1 / math.sqrt(D), out, ws)
+
+        c.set_wait_limit(0)
+        call()
+        assert c.poll() == tq.TQ_ERR_TIMEOUT and c.poll() == tq.TQ_OK
+        c.set_wait_limit(1 << 22)
+        call()
+        assert c.poll() == tq.TQ_OK
+        assert torch.equal(out, run_tree(s, 4, 4, 16))
+
+
+def test_tree_over_hadamard_rotated_caches():
+    """A context with the randomized Hadamard rotation: the same answer as the decode call's over the same cache."""
+    c = tq.Context(D, 4, tq.TQ_MSE, tq.TQ_ROT_HADAMARD, synth.hadamard_signs(3, D))
+    g, B, Hq, Hkv, cap = gen(8), 2, 8, 2, 1008
+    K, V = tq.CodeSet(c, B * Hkv * cap), tq.CodeSet(c, B * Hkv * cap, tq.TQ_LAYOUT_PAIR)
+    for cs in (K, V):
+        tq.tq_encode(c, torch.randn(B * Hkv * cap, D, device="cuda", generator=g), cs)
+    q = torch.randn(B, Hq, D, device="cuda", generator=g)
+    want = torch.empty(B, Hq, D, device="cuda")
+    ws = torch.zeros(tq.tq_decode_workspace_size(c, B, Hq, Hkv, cap) // 4 + 4, device="cuda")
+    tq.tq_decode_attention(c, c, q, K, V, B, Hq, Hkv, cap, cap, 1 / math.sqrt(D), want, ws)
+    for dtype in TYPES:
+        out = torch.empty(B, Hq, D, dtype=dtype, device="cuda")
+        ws = torch.zeros(tq.tq_tree_attention_workspace_size(c, B, Hq, Hkv, B) // 4 + 4, device="cuda")
+        tq.tq_tree_attention(c, c, q.to(dtype), None, None, i32([0, 1, 2]), None, K, V, i32([cap, cap]), None, cap,
+                             1 / math.sqrt(D), out, ws, Hkv=Hkv)
+        # the library's bound for attention on both sides, the roundings of q and of the output
+        assert (out.float() - want).norm() <= (4e-3 + 2 * torch.finfo(dtype).eps) * want.norm()
+
+
 def test_tree_is_deterministic():
     s = make_tree(torch.float16, 4, 4, 32, 8, 16, [3000, 100, 2500], [16, 3, 9])
     first = run_tree(s, 4, 4, 16)
