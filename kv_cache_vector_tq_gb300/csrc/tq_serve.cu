@@ -3,6 +3,8 @@
 // and position rotation of queries and keys (tq_qk_norm_rope).
 #include <algorithm>
 
+#include <type_traits>
+
 #include <cuda_bf16.h>
 
 #include "tq_device.cuh"
@@ -185,11 +187,12 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
 // 32-bit angle is off by whole degrees past 10^6 positions).  The fraction's
 // leading 32 bits, as a signed multiple of half a turn, go to sincospif; its
 // rounding to fp32 is at most 2^-25 half turns.
-// One pass: a row is d/8 lanes of 8 elements (one 16-byte load of a 16-bit
-// type), its sum of squares a shuffle tree in fp32; the half-split pairing
-// takes its partner elements from the lane rot/16 away.  A warp keeps one
-// token's sines for its share of the heads.  HBM-bound for prompts; a token or
-// a tree is one launch latency.
+// One pass: a row is d/8 lanes of 8 elements, its sum of squares a shuffle tree in
+// fp32.  With the half-split pairing a lane holds 4 elements and their 4 partners,
+// so no value changes lanes; cosines and sines are multiplied by the weights once
+// per token, so that a row is 16 products, 8 of them the norm's.  Prompts: bound
+// by instructions before (218 for two rows, 76 us for 16384 tokens of 40 heads),
+// by HBM now; a token or a tree is one launch latency.
 constexpr int kNrThreads = 256;
 
 struct NormRopeParams {
@@ -203,28 +206,21 @@ struct NormRopeParams {
   float eps;
 };
 
-// Eight elements as they lie in memory, and as fp32.
+// Four elements as they lie in memory, and as fp32.
 template <typename T>
-struct Raw8 {
-  uint4 w[sizeof(T) / 2];
-};
+using Raw4 = typename std::conditional<sizeof(T) == 4, uint4, uint2>::type;
+
 template <typename T>
-__device__ __forceinline__ Raw8<T> raw8(const T* p) {
-  Raw8<T> r;
-#pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.w[i] = reinterpret_cast<const uint4*>(p)[i];
-  return r;
-}
-template <typename T>
-__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
+__device__ __forceinline__ void widen4(const Raw4<T>& r, float* v) {
   if constexpr (sizeof(T) == 4) {
-    const uint32_t w[8] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w, r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+    v[0] = __uint_as_float(r.x);
+    v[1] = __uint_as_float(r.y);
+    v[2] = __uint_as_float(r.z);
+    v[3] = __uint_as_float(r.w);
   } else {
-    const uint32_t w[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+    const uint32_t w[2] = {r.x, r.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       float2 f;
       if constexpr (std::is_same<T, __half>::value)
         f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
@@ -237,14 +233,13 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&v)[8]) {
 }
 
 template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+__device__ __forceinline__ void store4(T* p, const float* v) {
   if constexpr (sizeof(T) == 4) {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
   } else {
-    uint32_t w[4];
+    uint32_t w[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       if constexpr (std::is_same<T, __half>::value) {
         w[i] = h2_bits(__floats2half2_rn(v[2 * i], v[2 * i + 1]));
       } else {
@@ -252,26 +247,30 @@ __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
         w[i] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
   }
 }
 
-// LPR lanes per row (the power of two at or above d/8).  Rows come by 16-byte
-// asynchronous copies into slots of shared memory that are each lane's own (no
-// barrier), kNrAhead lane groups of rows ahead of the one in use: 32 warps with
-// eight times 512 bytes each cover the memory's latency several times over.
-// (Four rows ahead in registers, 24 warps: 3.6 TB/s; two and 16 warps: 2.3 TB/s.)
+// LPR lanes per row (the power of two at or above d/8).  Rows come by asynchronous
+// copies into slots of shared memory that are each lane's own (no barrier),
+// kNrAhead lane groups of rows ahead of the one in use: 32 warps with eight times
+// 512 bytes each cover the memory's latency several times over.
 template <typename TI>
 constexpr int kNrAhead = sizeof(TI) == 4 ? 4 : 8;
 
-__device__ __forceinline__ void nr_copy16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+template <int BYTES>
+__device__ __forceinline__ void nr_copy(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES) : "memory");
 }
 
-template <typename TI, typename TO, int LPR>
+template <typename TI, typename TO, int LPR, bool HALF>
 __global__ void __launch_bounds__(kNrThreads, 4) norm_rope_kernel(const NormRopeParams p) {
   constexpr int RPW = 32 / LPR, A = kNrAhead<TI>;
-  __shared__ __align__(16) Raw8<TI> ring[A][kNrThreads];
+  using Raw = Raw4<TI>;
+  struct Slot {
+    Raw a, b;
+  };
+  __shared__ __align__(16) Slot ring[A][kNrThreads];
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
   const int64_t job = (int64_t)blockIdx.x * (kNrThreads / 32) + (threadIdx.x >> 5);
   if (job >= p.N * p.chunks) return;  // whole warps
@@ -282,117 +281,116 @@ __global__ void __launch_bounds__(kNrThreads, 4) norm_rope_kernel(const NormRope
     h0 = (int)(job - n * p.chunks) * p.chunk;
   }
   const int h1 = min(h0 + p.chunk, p.Hq + p.Hkv);
-  const bool in = 8 * l < p.d;
-  const int j0 = 8 * l, half = p.rot >> 1;
-  const TI* qrow = static_cast<const TI*>(p.q) + n * p.qs + j0;
-  const TI* krow = static_cast<const TI*>(p.k) + n * p.ks + j0;
+  const bool in = 8 * l < p.d, turns = 8 * l < p.rot;
+  // this lane's elements: ja.., jb.. (four each); half-split: partners of one another
+  const int ja = HALF && turns ? 4 * l : 8 * l, jb = HALF && turns ? (p.rot >> 1) + 4 * l : 8 * l + 4;
+  const TI* qrow = static_cast<const TI*>(p.q) + n * p.qs;
+  const TI* krow = static_cast<const TI*>(p.k) + n * p.ks;
   auto fetch = [&](int h, int slot) {  // this lane's piece of head h
     if (in && h < h1) {
       const TI* src = h < p.Hq ? qrow + (int64_t)h * p.d : krow + (int64_t)(h - p.Hq) * p.d;
-#pragma unroll
-      for (int i = 0; i < (int)sizeof(TI) / 2; ++i)
-        nr_copy16(&ring[slot][threadIdx.x].w[i], reinterpret_cast<const uint4*>(src) + i);
+      Slot& s = ring[slot][threadIdx.x];
+      nr_copy<(int)sizeof(Raw)>(&s.a, src + ja);
+      nr_copy<(int)sizeof(Raw)>(&s.b, src + jb);
     }
     asm volatile("cp.async.commit_group;\n" ::: "memory");  // always, so that the groups count the heads
   };
 #pragma unroll
   for (int a = 0; a < A; ++a) fetch(h0 + a * RPW + sub, a);
-  // sines of this lane's 8 elements (half-split: element j turns with frequency j mod rot/2;
-  // interleaved: j / 2)
-  float cs[8], sn[8];
+  // cosines and sines of the lane's four pairs
+  float cs[4], sn[4];
   const uint64_t pos = (uint64_t)(int64_t)p.pos[n];
-  const bool turns = j0 < p.rot;
-  const bool second = p.style == 0 && j0 >= half;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 4; ++e) {
     cs[e] = 1.f;
     sn[e] = 0.f;
-    if (p.style == 0 || (e & 1) == 0) {
-      if (turns) {
-        const int f = p.style == 0 ? (j0 + e) - (second ? half : 0) : (j0 + e) >> 1;
-        const uint64_t t = pos * p.freq[f];
-        sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn[e], &cs[e]);
-      }
-    } else {
-      cs[e] = cs[e - 1];
-      sn[e] = sn[e - 1];
+    if (turns) {
+      const uint64_t t = pos * p.freq[4 * l + e];
+      sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f /* 2^-31 */, &sn[e], &cs[e]);
     }
   }
-  if (second) {  // b cos + a sin: the partner a is added
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sn[e] = -sn[e];
-  }
-  // partner lane of the half-split pairing (inside the row's LPR lanes)
-  const int plane = sub * LPR + (second ? l - (half >> 3) : l + (half >> 3));
-  Raw8<TI> wq{}, wk{};
-  if (in && p.wq) wq = raw8(static_cast<const TI*>(p.wq) + j0);
-  if (in && p.wk) wk = raw8(static_cast<const TI*>(p.wk) + j0);
   const float inv_d = 1.f / (float)p.d;
+  // z_a = r·(x_a·ca - x_b·sb), z_b = r·(x_b·cb + x_a·sa) with the weights inside
+  float ca[4], sa[4], cb[4], sb[4];
+  int of = -1;  // whose weights they hold: 1 q, 0 k
 
   int slot = 0;
 #pragma unroll 1
   for (int hb = h0; hb < h1; hb += RPW) {
-      const int h = hb + sub;
-      const bool isq = h < p.Hq;
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(A - 1) : "memory");
-      Raw8<TI> x{};
-      if (in && h < h1) x = ring[slot][threadIdx.x];
-      fetch(h + A * RPW, slot);  // the slot's words are in registers
-      if (++slot == A) slot = 0;
-      float y[8];
-      widen8<TI>(x, y);
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-#pragma unroll
-      for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
-      float r = rsqrtf(fmaf(ss, inv_d, p.eps));
-      if (__any_sync(kFull, !(ss < 1e36f))) {
-        // squares past the fp32 range: once more with the row scaled by the
-        // power of two that brings its largest magnitude to [1, 2)
-        float m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(y[e]));
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-        int ex = 1;
-        if (m > 0.f && m < INFINITY) frexpf(m, &ex);
-        const float sc = ldexpf(1.f, 1 - ex);
-        float s2 = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s2 = fmaf(y[e] * sc, y[e] * sc, s2);
-#pragma unroll
-        for (int o = LPR / 2; o; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
-        if (!(ss < 1e36f)) r = rsqrtf(fmaf(s2, inv_d, p.eps * sc * sc)) * sc;
+    const int h = hb + sub;
+    const bool isq = h < p.Hq;
+    if (of != (int)isq) {
+      of = isq;
+      const TI* w = static_cast<const TI*>(isq ? p.wq : p.wk);
+      float wv[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      if (in && w) {
+        widen4<TI>(*reinterpret_cast<const Raw*>(w + ja), wv);
+        widen4<TI>(*reinterpret_cast<const Raw*>(w + jb), wv + 4);
       }
-      if (isq ? p.wq != nullptr : p.wk != nullptr) {
-        float w[8];
-        widen8<TI>(isq ? wq : wk, w);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] *= r;
+      for (int e = 0; e < 4; ++e) {
+        const float wa = HALF ? wv[e] : wv[2 * e], wb = HALF ? wv[4 + e] : wv[2 * e + 1];
+        ca[e] = wa * cs[e];
+        sa[e] = wa * sn[e];
+        cb[e] = wb * cs[e];
+        sb[e] = wb * sn[e];
       }
-      float z[8];
-      if (p.style == 0) {
+    }
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(A - 1) : "memory");
+    float x[8];
+    {
+      Slot s{};
+      if (in && h < h1) s = ring[slot][threadIdx.x];
+      widen4<TI>(s.a, x);
+      widen4<TI>(s.b, x + 4);
+    }
+    fetch(h + A * RPW, slot);  // the slot's words are in registers
+    if (++slot == A) slot = 0;
+    float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_sync(kFull, y[e], plane & 31);
-          z[e] = turns ? fmaf(y[e], cs[e], -o * sn[e]) : y[e];
-        }
-      } else {
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          z[e] = fmaf(y[e], cs[e], -y[e + 1] * sn[e]);
-          z[e + 1] = fmaf(y[e + 1], cs[e], y[e] * sn[e]);
-        }
+    for (int o = LPR / 2; o; o >>= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    float r = rsqrtf(fmaf(ss, inv_d, p.eps));
+    if (__any_sync(kFull, !(ss < 1e36f))) {
+      // squares past the fp32 range (or not numbers): once more with the row
+      // scaled by the power of two that brings its largest magnitude to [1, 2)
+      float m = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(x[e]));
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+      int ex = 1;
+      if (m > 0.f && m < INFINITY) frexpf(m, &ex);
+      const float sc = ldexpf(1.f, 1 - ex);
+      float s2 = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s2 = fmaf(x[e] * sc, x[e] * sc, s2);
+#pragma unroll
+      for (int o = LPR / 2; o; o >>= 1) s2 += __shfl_xor_sync(kFull, s2, o);
+      if (!(ss < 1e36f)) {  // x·r without the large x meeting the weights first
+        r = rsqrtf(fmaf(s2, inv_d, p.eps * sc * sc)) * sc;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] *= r;
+        r = 1.f;
       }
-      if (in && h < h1) {
-        TO* dst = isq ? static_cast<TO*>(p.qo) + n * p.qos + (int64_t)h * p.d
-                      : static_cast<TO*>(p.ko) + n * p.kos + (int64_t)(h - p.Hq) * p.d;
-        store8(dst + j0, z);
-      }
+    }
+    float z[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = HALF ? e : 2 * e, k = HALF ? 4 + e : 2 * e + 1;
+      // a lane past `rot` has sines 0, and no product with them
+      const float a = turns ? fmaf(x[i], ca[e], -x[k] * sb[e]) : x[i] * ca[e];
+      const float b = turns ? fmaf(x[k], cb[e], x[i] * sa[e]) : x[k] * cb[e];
+      z[i] = a * r;
+      z[k] = b * r;
+    }
+    if (in && h < h1) {
+      TO* dst = isq ? static_cast<TO*>(p.qo) + n * p.qos + (int64_t)h * p.d
+                    : static_cast<TO*>(p.ko) + n * p.kos + (int64_t)(h - p.Hq) * p.d;
+      store4(dst + ja, z);
+      store4(dst + jb, z + 4);
+    }
   }
   asm volatile("cp.async.wait_all;\n" ::: "memory");
 }
@@ -413,10 +411,30 @@ cudaError_t run_norm_rope(NormRopeParams p, cudaStream_t st) {
   const int64_t jobs = p.N * p.chunks, grid = (jobs + kNrThreads / 32 - 1) / (kNrThreads / 32);
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
   switch (lpr) {
-    case 4: norm_rope_kernel<TI, TO, 4><<<(int)grid, kNrThreads, 0, st>>>(p); break;
-    case 8: norm_rope_kernel<TI, TO, 8><<<(int)grid, kNrThreads, 0, st>>>(p); break;
-    case 16: norm_rope_kernel<TI, TO, 16><<<(int)grid, kNrThreads, 0, st>>>(p); break;
-    case 32: norm_rope_kernel<TI, TO, 32><<<(int)grid, kNrThreads, 0, st>>>(p); break;
+    case 4:
+      if (p.style == TQ_ROPE_HALF)
+        norm_rope_kernel<TI, TO, 4, true><<<(int)grid, kNrThreads, 0, st>>>(p);
+      else
+        norm_rope_kernel<TI, TO, 4, false><<<(int)grid, kNrThreads, 0, st>>>(p);
+      break;
+    case 8:
+      if (p.style == TQ_ROPE_HALF)
+        norm_rope_kernel<TI, TO, 8, true><<<(int)grid, kNrThreads, 0, st>>>(p);
+      else
+        norm_rope_kernel<TI, TO, 8, false><<<(int)grid, kNrThreads, 0, st>>>(p);
+      break;
+    case 16:
+      if (p.style == TQ_ROPE_HALF)
+        norm_rope_kernel<TI, TO, 16, true><<<(int)grid, kNrThreads, 0, st>>>(p);
+      else
+        norm_rope_kernel<TI, TO, 16, false><<<(int)grid, kNrThreads, 0, st>>>(p);
+      break;
+    case 32:
+      if (p.style == TQ_ROPE_HALF)
+        norm_rope_kernel<TI, TO, 32, true><<<(int)grid, kNrThreads, 0, st>>>(p);
+      else
+        norm_rope_kernel<TI, TO, 32, false><<<(int)grid, kNrThreads, 0, st>>>(p);
+      break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
