@@ -77,6 +77,7 @@ struct Misc {
   uint64_t n_full[kNormSlots], n_empty[kNormSlots];
   uint64_t q_full, drain;
   uint32_t valid[kNormSlots];  // bit c: the tile's 16-token chunk c is there
+  uint32_t sent[2][2];  // cached tiles and tiles that the copy warps have issued
   uint32_t tmem;
   int abort;
 };
@@ -711,9 +712,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegRest));
     if (warp == kMma) {
-    // ---------------- the products: Sᵀ of tile j goes before V̂ᵀ·P of tile j - 1,
-    // except where a new group's Q̂ has to wait for the last group's end.  The
-    // whole warp walks through it, an elected lane issues
+      // ---------------- the products: Sᵀ of tile j goes before V̂ᵀ·P of tile j - 1,
+      // except where a new group's Q̂ has to wait for the last group's end.  The
+      // whole warp walks through it, an elected lane issues
       constexpr uint32_t idesc = umma_idesc_f16(128, N);
       constexpr uint32_t idesc_p = idesc | (1u << 16);  // B contiguous along N
       const uint64_t dq = umma_desc_sw128(smem_u32(smem + kQ));
@@ -785,92 +786,103 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
       }
     } else if (warp <= kCopy + 1) {
-    // ---------------- copies of the packed tiles, K by one warp and V by the
-    // other: lane = 16-token chunk (codes: lanes 0-7, norms: 8-15); the first
-    // chunk of a run inside one page copies the run
-    const bool is_v = warp != kCopy;
-    const int c = lane & 7, bits = is_v ? p.vb : p.kb;
-    const unsigned char* codes = reinterpret_cast<const unsigned char*>(is_v ? p.vcodes : p.kcodes);
-    const float* norms = is_v ? p.vnorm : p.knorm;
-    const float* fac = is_v ? p.vfac : p.kfac;
-    const int raw_off = is_v ? 2048 * p.kb : 0, norm_off = is_v ? 512 : 0;
-    uint32_t i = 0, rc = 0, st = 0, rph = 1;  // tile, cached tile, its stage and phase
-    bool ok = true;
-    // pages and places advance by a tile without a division
-    const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
-    while (ok && u < u_end) {
-      const TreeSeg g = tree_seg(p, u, u_end, b);
-      b = g.b;
-      // this lane's chunk of tile t: token, page number within the sequence and
-      // place in the page
-      int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
-      const int32_t* pages = p.table ? p.table + (int64_t)g.b * p.max_blocks : nullptr;
-      auto page_here = [&](int t) -> int { return t < g.ctiles && at < g.s.len ? (pages ? __ldg(pages + j) : g.b) : 0; };
-      int page = page_here(g.first);
-      for (int t = g.first; t < g.last; ++t, ++i) {
-        const uint32_t ns = i % kNormSlots;
-        unsigned char* nb = smem + kNorms + ns * 1024 + norm_off;
-        const bool draft = t >= g.ctiles;
-        // the vector of the chunk (-1: no such token, -2: no such page)
-        const int64_t vec = draft || at >= g.s.len ? -1
-                            : page >= 0 && page < p.pages ? ((int64_t)page * p.Hkv + g.kvh) * p.block + o : -2;
-        at += kTreeTok;
-        j += jt;
-        o += ot;
-        if (o >= p.block) {
-          o -= p.block;
-          ++j;
-        }
-        page = page_here(t + 1);  // read while this tile waits for room, used with the next
-        ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
-             (draft || bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim));
-        ok = __all_sync(kFull, ok);
-        if (!ok) break;
-        if (draft) {
-          const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int k = 32 * e + lane;
-            reinterpret_cast<float*>(nb)[k] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
+      // ---------------- copies of the packed tiles, K by one warp and V by the
+      // other: lane = 16-token chunk (codes: lanes 0-7, norms: 8-15); the first
+      // chunk of a run inside one page copies the run
+      const bool is_v = warp != kCopy;
+      const int c = lane & 7, bits = is_v ? p.vb : p.kb;
+      const unsigned char* codes = reinterpret_cast<const unsigned char*>(is_v ? p.vcodes : p.kcodes);
+      const float* norms = is_v ? p.vnorm : p.knorm;
+      const float* fac = is_v ? p.vfac : p.kfac;
+      const int raw_off = is_v ? 2048 * p.kb : 0, norm_off = is_v ? 512 : 0;
+      uint32_t i = 0, rc = 0, st = 0, rph = 1;  // tile, cached tile, its stage and phase
+      bool ok = true;
+      // pages and places advance by a tile without a division
+      const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
+      while (ok && u < u_end) {
+        const TreeSeg g = tree_seg(p, u, u_end, b);
+        b = g.b;
+        // this lane's chunk of tile t: token, page number within the sequence and
+        // place in the page
+        int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
+        const int32_t* pages = p.table ? p.table + (int64_t)g.b * p.max_blocks : nullptr;
+        auto page_here = [&](int t) -> int { return t < g.ctiles && at < g.s.len ? (pages ? __ldg(pages + j) : g.b) : 0; };
+        int page = page_here(g.first);
+        for (int t = g.first; t < g.last; ++t, ++i) {
+          const uint32_t ns = i % kNormSlots;
+          unsigned char* nb = smem + kNorms + ns * 1024 + norm_off;
+          const bool draft = t >= g.ctiles;
+          // the vector of the chunk (-1: no such token, -2: no such page)
+          const int64_t vec = draft || at >= g.s.len ? -1
+                              : page >= 0 && page < p.pages ? ((int64_t)page * p.Hkv + g.kvh) * p.block + o : -2;
+          at += kTreeTok;
+          j += jt;
+          o += ot;
+          if (o >= p.block) {
+            o -= p.block;
+            ++j;
           }
-          if (lane == 0 && !is_v) ms.valid[ns] = 0xFFu;
+          page = page_here(t + 1);  // read while this tile waits for room, used with the next
+          ok = bar_rest(&ms.n_empty[ns], ((i / kNormSlots) & 1u) ^ 1u, abort_flag, p.status, lim) &&
+               (draft || bar_rest(&ms.raw_empty[st], rph, abort_flag, p.status, lim));
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+          if (draft) {
+            const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+  #pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = 32 * e + lane;
+              reinterpret_cast<float*>(nb)[k] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
+            }
+            if (lane == 0 && !is_v) ms.valid[ns] = 0xFFu;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.n_full[ns]);
+            continue;
+          }
+          const uint32_t there = __ballot_sync(kFull, vec >= 0) & 0xFFu;
+          const int64_t before = __shfl_up_sync(kFull, vec, 1);
+          const bool leads = vec >= 0 && (c == 0 || before < 0 || vec != before + 16);
+          const uint32_t starts = __ballot_sync(kFull, leads || vec < 0) & 0xFFu;
+          if (lane == 0) {
+            if (!is_v) ms.valid[ns] = there;
+            const uint32_t n = __popc(there);
+            mbar_arrive_expect_tx(&ms.raw_full[st], n * 256u * (uint32_t)bits);
+            mbar_arrive_expect_tx(&ms.n_full[ns], n * 64u);
+          }
+          if (vec == -2 && lane < 8 && !is_v) atomicOr(p.status, 2);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.n_full[ns]);
-          continue;
+          if (leads && lane < 16) {
+            const uint32_t later = starts >> (c + 1);  // up to the next start (or the tile's end)
+            const uint32_t run = later ? (uint32_t)__ffs(later) : (uint32_t)(8 - c);
+            const bool nrm = lane >= 8;
+            bulk_g2s(nrm ? nb + 64 * c : smem + raw_at(st) + raw_off + c * 256 * bits,
+                     nrm ? (const void*)(norms + vec) : (const void*)(codes + vec * (16 * bits)),
+                     run * (nrm ? 64u : 256u * bits), nrm ? &ms.n_full[ns] : &ms.raw_full[st]);
+          }
+          ++rc;
+          if (++st == RS) {
+            st = 0;
+            rph ^= 1u;
+          }
         }
-        const uint32_t there = __ballot_sync(kFull, vec >= 0) & 0xFFu;
-        const int64_t before = __shfl_up_sync(kFull, vec, 1);
-        const bool leads = vec >= 0 && (c == 0 || before < 0 || vec != before + 16);
-        const uint32_t starts = __ballot_sync(kFull, leads || vec < 0) & 0xFFu;
-        if (lane == 0) {
-          if (!is_v) ms.valid[ns] = there;
-          const uint32_t n = __popc(there);
-          mbar_arrive_expect_tx(&ms.raw_full[st], n * 256u * (uint32_t)bits);
-          mbar_arrive_expect_tx(&ms.n_full[ns], n * 64u);
-        }
-        if (vec == -2 && lane < 8 && !is_v) atomicOr(p.status, 2);
-        __syncwarp();
-        if (leads && lane < 16) {
-          const uint32_t later = starts >> (c + 1);  // up to the next start (or the tile's end)
-          const uint32_t run = later ? (uint32_t)__ffs(later) : (uint32_t)(8 - c);
-          const bool nrm = lane >= 8;
-          bulk_g2s(nrm ? nb + 64 * c : smem + raw_at(st) + raw_off + c * 256 * bits,
-                   nrm ? (const void*)(norms + vec) : (const void*)(codes + vec * (16 * bits)),
-                   run * (nrm ? 64u : 256u * bits), nrm ? &ms.n_full[ns] : &ms.raw_full[st]);
-        }
-        ++rc;
-        if (++st == RS) {
-          st = 0;
-          rph ^= 1u;
-        }
+        u += g.last - g.first;
       }
-      u += g.last - g.first;
+      if (lane == 0) {
+        ms.sent[warp - kCopy][0] = rc;
+        ms.sent[warp - kCopy][1] = i;
+      }
     }
-    // Every copy issued lands before the CTA may exit.  A walk to the end has had
-    // all of them consumed; one that a wait cut short leaves some under way, on
-    // barriers that nobody arms any more: each stage's and slot's last phase
-    // (bounded, and short: a barrier that only the other warp armed stays as it is).
-    if (lane == 0 && *abort_flag) {
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag) {
+    // Every copy issued lands before the CTA exits.  A walk to the end has had all
+    // of them consumed; one that a wait cut short, in whichever warp, leaves some
+    // under way: each stage's and slot's last phase (bounded, and short: a barrier
+    // that only one of the two warps armed stays as it is).
+    if ((warp == kCopy || warp == kCopy + 1) && lane == 0) {
+      const uint32_t rc = ms.sent[warp - kCopy][0], i = ms.sent[warp - kCopy][1];
       for (uint32_t q = rc > RS ? rc - RS : 0u; q < rc; ++q)
         for (uint32_t k = 0; k < kLandPolls && !mbar_try_wait(&ms.raw_full[q % RS], (q / RS) & 1u); ++k) {
         }
@@ -878,11 +890,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         for (uint32_t k = 0; k < kLandPolls && !mbar_try_wait(&ms.n_full[q % kNormSlots], (q / kNormSlots) & 1u); ++k) {
         }
     }
-    }
+    __syncthreads();
   }
-
-  tc_fence_before();
-  __syncthreads();
   if (warp == kMma) {
     tc_fence_after();
     tmem_dealloc(ms.tmem, 512);
