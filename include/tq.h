@@ -363,7 +363,8 @@ tq_status tq_decode_attention_noalloc(const tq_ctx* kctx, const tq_ctx* vctx, co
  *           d_row_start[B] get -1 and 0.  Rows past `rows` are not listed.
  * A request is served if it takes no page or if the pages it and the requests
  * before it take are all there.  One that is not served, or whose numbers are
- * negative or exceed max_blocks, keeps its pages and gets no rows.
+ * negative or exceed max_blocks or 2^31 - 1 tokens, keeps its pages and gets no
+ * rows.
  * Errors: INVALID_ARG; UNSUPPORTED for B > 4096 or B * max_blocks >= 2^31.  The
  * rows of all requests together must stay below 2^31.
  */
@@ -451,7 +452,7 @@ tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64
  *           need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
  * UNSUPPORTED for d != 128, Prod or b + 1/2-bit codes, a block that is not a
- * multiple of 16, or rows * Hq, max_blocks * block >= 2^31, or so many rows over so
+ * multiple of 16, rows * Hq or max_blocks * block past 2^31 - 256, or so many rows over so
  * large a capacity (rows * Hq / 16 times (capacity + rows) / 128) as to pass 2^31.
  */
 tq_status tq_tree_attention_workspace_size(const tq_ctx* kctx, int B, int Hq, int Hkv, int64_t rows, size_t* bytes);

@@ -291,13 +291,14 @@ _T = None
 
 
 def _types():
-    """(torch, its type -> tq type, the raw current stream of a device), once torch is wanted."""
+    """(torch, its type -> tq type, the raw current stream, the current device), once torch is wanted."""
     global _T
     if _T is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = (lambda: raw(torch.cuda.current_device())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
-        _T = torch, {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}, stream
+        dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        stream = (lambda: raw(dev())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
+        _T = torch, {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}, stream, dev
     return _T
 
 
@@ -308,17 +309,18 @@ def _raw_stream(stream):
 
 
 def _dev(t, dtype, n, what):
-    """Device address of a contiguous tensor of this type with n elements or more."""
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more is wanted")
+    """Device address of a contiguous tensor of this type with n elements or more, on the current device."""
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda or t.get_device() != _T[3]():
+        raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more, on the current "
+                         f"device, is wanted")
     return t.data_ptr()
 
 
 def _heads(t, n, h, d, what):
     """Address and token stride of a [n, h, d] CUDA tensor whose heads are contiguous."""
     a, b, c = t.stride()
-    if t.shape != (n, h, d) or c != 1 or (b != d and h > 1) or not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA tensor [{n}, {h}, {d}] with contiguous heads is wanted")
+    if t.shape != (n, h, d) or c != 1 or (b != d and h > 1) or not t.is_cuda or t.get_device() != _T[3]():
+        raise ValueError(f"{what}: a CUDA tensor [{n}, {h}, {d}] with contiguous heads, on the current device, is wanted")
     return t.data_ptr(), a if n > 1 else h * d
 
 
@@ -349,7 +351,7 @@ def tq_rope_frequencies(inv_freq, device="cuda"):
 def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=None):
     """Head norms and position rotation of q [N, Hq, d] and k [N, Hkv, d] into q_out and k_out (include/tq.h).
     wq, wk: [d] of q's type or None; freq: tq_rope_frequencies or None (norms alone); outputs may be the inputs."""
-    torch, types, _ = _types()
+    torch, types = _types()[:2]
     (N, Hq, d), Hkv, ti, to = q.shape, k.shape[1], q.dtype, q_out.dtype
     if k.dtype is not ti or k_out.dtype is not to:
         raise ValueError("q and k, and q_out and k_out, are of one type")
@@ -364,7 +366,7 @@ def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=No
 
 def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
     """tq_encode of x [N, Hkv, d] into a paged cache, token i at slots[i] (include/tq.h)."""
-    torch, types, _ = _types()
+    torch, types = _types()[:2]
     N, Hkv, d = x.shape
     if d != ctx.d:
         raise ValueError(f"x: rows of {ctx.d} elements are wanted")
@@ -388,7 +390,7 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     """Attention of drafted tokens q [rows, Hq, d] over a packed cache and each other (include/tq.h).  k_new, v_new
     [rows, Hkv, d] or None (Hkv is then given); mask [rows, words] int32 or None (a chain); table [B, max_blocks] or
     None (contiguous, cap = block)."""
-    torch, types, _ = _types()
+    torch, types = _types()[:2]
     rows, Hq, d = q.shape
     ti = q.dtype
     B, Hkv = lens.numel(), k_new.shape[1] if k_new is not None else Hkv
@@ -406,7 +408,8 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
         None if mask is None else _dev(mask, i32, rows * words, "mask"), words, ctypes.byref(K.desc),
         ctypes.byref(V.desc), _dev(lens, i32, B, "lens"),
         None if table is None else _dev(table, i32, B * width, "table"), width, block, B, Hq, Hkv, scale,
-        _dev(out, ti, rows * Hq * d, "out"), ws.data_ptr(), ws.numel() * ws.element_size(), _raw_stream(stream)))
+        _dev(out, ti, rows * Hq * d, "out"), _dev(ws, ws.dtype, 0, "ws"), ws.numel() * ws.element_size(),
+        _raw_stream(stream)))
 
 
 def tq_unpack_indices(codes, first=0, count=None, with_bits=False):

@@ -1051,7 +1051,9 @@ tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* 
   if (d_table && max_blocks <= 0) return TQ_ERR_INVALID_ARG;
   const int64_t need = d_table ? (int64_t)Hkv * block : (int64_t)B * Hkv * block;  // vectors the caches must hold
   if (need > K->n || need > V->n) return TQ_ERR_INVALID_ARG;
-  if ((d_table && (int64_t)max_blocks * block > INT32_MAX) || (int64_t)rows * Hq > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+  // places and rows are counted in 32 bits, to the end of the last tile of 128
+  const int64_t capacity = (int64_t)(d_table ? max_blocks : 1) * block;
+  if (capacity > INT32_MAX - 255 || rows * Hq > INT32_MAX - 255) return TQ_ERR_UNSUPPORTED;
   if (kc.d != kChunk || kc.mode != TQ_MSE || vc.mode != TQ_MSE || block % 16 != 0) return TQ_ERR_UNSUPPORTED;
   if (rows == 0) return TQ_OK;
   if (!d_q || !d_out || !d_ws || !d_row_start || !d_len) return TQ_ERR_INVALID_ARG;

@@ -95,8 +95,8 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
       len = p.len[b];
       nn = p.nnew[b];
       held = p.held[b];
-      const int64_t want = ((int64_t)len + nn + p.block - 1) / p.block;
-      ok = len >= 0 && nn >= 0 && held >= 0 && held <= p.max_blocks && want <= p.max_blocks;
+      const int64_t all = (int64_t)len + nn, want = (all + p.block - 1) / p.block;
+      ok = len >= 0 && nn >= 0 && held >= 0 && held <= p.max_blocks && want <= p.max_blocks && all <= INT32_MAX;
       need = ok ? (int)want : held;
       take = max(need - held, 0);
       give = max(held - need, 0);

@@ -122,6 +122,21 @@ def test_block_tables_odd_requests():
     assert got[2] == [1, 1, 1, 0, 3] and got[4] == [0, 0, 0, 0, 0, 1]
 
 
+def test_block_tables_lengths_past_32_bits():
+    """A request that would pass 2^31 - 1 tokens keeps its pages and gets no rows, however many a table row holds."""
+    big, block, width = 2 ** 31 - 1, 1 << 20, 2060
+    held = [2048, 1, 2048]  # pages of big tokens; of one
+    table = [[b * width + j for j in range(width)] for b in range(3)]
+    args = ([big - 3, 5, big], [4, 2, 0], held, list(range(9000, 9008)), 0, 8, table, block)
+    got = run_tables(*args, 4)
+    assert got[2] == held and got[3] == [0, 8] and got[4] == [0, 0, 2, 2]
+    assert got[5] == [width * block + 5, width * block + 6, -1, -1] and got[6] == [5, 6, 0, 0]
+    args[1][0] = 3  # as many as there may be
+    got = run_tables(*args, 4)
+    assert got[4] == [0, 3, 5, 5] and got[6] == [big - 3, big - 2, big - 1, 5]
+    assert got[5][2] == 2047 * block + (big - 1) % block
+
+
 # ------------------------------------------------------------------ norms and rotation
 def norm_rope_plain(x, w, eps, inv, style, pos):
     """In 64 bits: the rows, and the size of what each value was made from."""
@@ -628,8 +643,10 @@ def test_refusals():
     status(-2, kc=prod, K=tq.CodeSet(prod, 1024))
     status(-2, kc=mixed, K=tq.CodeSet(mixed, 1024))
     status(-1, kc=ctx(3))
-    with pytest.raises(ValueError):
-        call(q=s["q"].transpose(0, 1))
+    status(-2, table=torch.empty(1, 2 ** 27 - 1, dtype=torch.int32, device="cuda"))  # 16 short of 2^31 places
+    for kw in (dict(q=s["q"].transpose(0, 1)), dict(ws=ws.cpu()), dict(ws=ws[::2]), dict(q=s["q"].cpu())):
+        with pytest.raises(ValueError):
+            call(**kw)
     x = torch.randn(4, 2, D, device="cuda", dtype=torch.float16)
     slots = torch.arange(4, device="cuda")
     for st, kw in ((-2, dict(block=15)), (-1, dict(block=0)), (-1, dict(block=1 << 20))):
@@ -642,6 +659,17 @@ def test_refusals():
     with pytest.raises(tq.TqError) as e:
         tq.tq_encode_slots(wide, torch.randn(4, 2, 256, device="cuda"), slots, 16, tq.CodeSet(wide, 64))
     assert e.value.status == -2
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    x, pos = torch.ones(2, 1, D, device="cuda"), i32([0, 1])
+    args = (x, x, None, None, 1e-6, None, 0, pos, torch.empty_like(x), torch.empty_like(x))
+    tq.tq_qk_norm_rope(*args)
+    monkeypatch.setattr(tq, "_T", tq._types()[:3] + (lambda: 1 + x.get_device(),))  # as if another were current
+    with pytest.raises(ValueError, match="current device"):
+        tq.tq_qk_norm_rope(*args)
+    with pytest.raises(ValueError, match="current device"):
+        tq._dev(pos, torch.int32, 1, "pos")
 
 
 # ------------------------------------------------------------------ together
