@@ -32,7 +32,7 @@ template <bool TC>
 __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, const int per, const int nbq, const int nbk) {
   __shared__ __align__(16) RotSmem sm;
   __shared__ float wmax[kPrepV][4];
-  __shared__ int64_t wsum[8];
+  __shared__ int64_t wsum[8], first_unit[256];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (blockIdx.x == 0) {
     griddep_wait();
@@ -64,22 +64,27 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
       if (b < p.B) {
         s.unit = base + before + inc - n;
         p.seq[b] = s;
+        if (p.B <= 256) first_unit[b] = s.unit;
       }
       base += tot;
     }
     if (tid == 0) p.seq[p.B].unit = base;
     __syncthreads();
     for (int c = tid; c < p.ctas; c += 256) {
-      const int64_t u = tree_cut(c, base, p.ctas);
+      TreeCta share;
+      share.u = tree_cut(c, base, p.ctas);
+      share.end = tree_cut(c + 1, base, p.ctas);
       int lo = 0, hi = p.B - 1;
       while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (p.seq[mid].unit <= u)
+        if ((p.B <= 256 ? first_unit[mid] : p.seq[mid].unit) <= share.u)
           lo = mid;
         else
           hi = mid - 1;
       }
-      p.cta_seq[c] = lo;
+      share.b = ~lo;
+      share.s = p.seq[lo];
+      p.cta[c] = share;
     }
     return;
   }
@@ -228,15 +233,14 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
   }
   griddep_wait();
   griddep_launch();
-  const int64_t units = p.seq[p.B].unit;
-  int64_t u = tree_cut(blockIdx.x, units, p.ctas);
-  const int64_t u_end = tree_cut(blockIdx.x + 1, units, p.ctas);
-  int sb = u < u_end ? p.cta_seq[blockIdx.x] : 0;
+  const TreeCta& share = p.cta[blockIdx.x];
+  int64_t u = share.u;
+  const int64_t u_end = share.end;
+  int b = share.b;
   while (u < u_end) {
-    const TreeSeg g = tree_seg(p, u, u_end, sb);
-    sb = g.b;
+    const TreeSeg g = tree_seg(p, u, u_end, b);
     const TreeSeq& s = g.s;
-    const int b = g.b, kvh = g.kvh, row0 = g.row0, nrow = g.nrow, first = g.first, last = g.last, ctiles = g.ctiles;
+    const int kvh = g.kvh, row0 = g.row0, nrow = g.nrow, first = g.first, last = g.last, ctiles = g.ctiles;
     __syncthreads();
     for (int e = tid; e < kFRows * 128; e += 256) {
       const int r = e >> 7, rho = row0 + r;
@@ -280,7 +284,7 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
           int64_t vec = 0;
           if (good) {
             const int t = t0 + tok, j = t / p.block;
-            const int64_t page = p.table ? (int64_t)p.table[(int64_t)b * p.max_blocks + j] : b;
+            const int64_t page = p.table ? (int64_t)p.table[(int64_t)g.b * p.max_blocks + j] : g.b;
             good = page >= 0 && page < p.pages;
             if (!good) atomicOr(p.status, 2);
             vec = good ? (page * p.Hkv + kvh) * p.block + (t - j * p.block) : 0;
@@ -419,6 +423,7 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
       }
     }
     u += last - first;
+    if (u < u_end) b = tree_next(p, u, b);
   }
 }
 
@@ -433,30 +438,51 @@ __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, c
   float4 w[16];  // Π[16·warp + k][4·lane ..]
 #pragma unroll
   for (int k = 0; k < 16; ++k) w[k] = __ldg(reinterpret_cast<const float4*>(p.vpi + (16 * warp + k) * 128) + lane);
+  // Where a row's records are, from what was laid out before the attention kernel
+  // could begin: found before the wait for it.  (All its CTAs had waited for the
+  // rotation's end when this kernel was let in.)
+  const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * p.Hq;
+  const int64_t units = __ldcg(&p.seq[p.B].unit);
+  const int64_t step = (int64_t)p.rows * kTreeRec;
+  struct Row {
+    const float *own, *more;
+    int c0, c1;  // CTAs that have records of it (c1 < c0: none)
+  };
+  auto row_at = [&](int64_t at) -> Row {
+    Row w{nullptr, nullptr, 0, -1};
+    if (at >= live) return w;
+    const int r = (int)((uint32_t)at / (uint32_t)p.Hq), head = (int)at - r * p.Hq, kvh = head / p.G;
+    const int4* sp = reinterpret_cast<const int4*>(p.seq + tree_find(p.row_start, p.B, r));  // the last sequence that starts at or before r
+    const int4 s0 = __ldcg(sp), s1 = __ldcg(sp + 1);
+    TreeSeq s;
+    s.start = s0.x;
+    s.T = s0.y;
+    s.rt = s0.w;
+    s.per = s1.x;
+    s.unit = (int64_t)((uint64_t)(uint32_t)s1.z | ((uint64_t)(uint32_t)s1.w << 32));
+    if (r < s.start || r >= s.start + s.T) return w;
+    const int rho = (r - s.start) * p.G + head - kvh * p.G;
+    const int rt = rho / p.rows;
+    const int64_t gs = s.unit + (int64_t)(kvh * s.rt + rt) * s.per, ge = gs + s.per;
+    const int64_t n0 = (gs + 1) * p.ctas - 1, n1 = ge * p.ctas - 1;  // 32-bit division where it will do
+    const bool small = n1 <= 0xFFFFFFFFll;
+    w.c0 = small ? (int)((uint32_t)n0 / (uint32_t)units) : (int)(n0 / units);
+    w.c1 = small ? (int)((uint32_t)n1 / (uint32_t)units) : (int)(n1 / units);
+    w.own = p.rec + at * kTreeRec;
+    w.more = p.crec + (int64_t)(rho - rt * p.rows) * kTreeRec;
+    return w;
+  };
+  Row row = row_at((int64_t)blockIdx.x * per * kPrepV + warp);
   griddep_wait();
   griddep_launch();
-  const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * p.Hq;
-  const int64_t units = p.seq[p.B].unit;
   for (int gi = 0; gi < per; ++gi) {
     const int64_t v0 = ((int64_t)blockIdx.x * per + gi) * kPrepV;
     if (v0 >= live) return;
-    const int64_t at = v0 + warp;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (at < live) {
-      const int r = (int)((uint32_t)at / (uint32_t)p.Hq), head = (int)at - r * p.Hq, kvh = head / p.G;
-      const int b = tree_find(p.row_start, p.B, r);  // the last sequence that starts at or before r
-      const TreeSeq s = p.seq[b];
-      if (r >= s.start && r < s.start + s.T) {
-        const int rho = (r - s.start) * p.G + head - kvh * p.G;
-        const int rt = rho / p.rows;
-        const int64_t gs = s.unit + (int64_t)(kvh * s.rt + rt) * s.per, ge = gs + s.per;
-        const int64_t n0 = (gs + 1) * p.ctas - 1, n1 = ge * p.ctas - 1;  // 32-bit division where it will do
-        const bool small = n1 <= 0xFFFFFFFFll;
-        const int c0 = small ? (int)((uint32_t)n0 / (uint32_t)units) : (int)(n0 / units);
-        const int c1 = small ? (int)((uint32_t)n1 / (uint32_t)units) : (int)(n1 / units);
-        const float* own = p.rec + at * kTreeRec;
-        const float* more = p.crec + (int64_t)(rho - rt * p.rows) * kTreeRec;
-        const int64_t step = (int64_t)p.rows * kTreeRec;
+    {
+      if (row.c1 >= row.c0) {
+        const int c0 = row.c0, c1 = row.c1;
+        const float *own = row.own, *more = row.more;
         // records 0 (own) .. c1 - c0, 32 at a time; with fewer units than CTAs
         // some of the CTAs between have none
         float M = -INFINITY, L = 0.f;
@@ -519,6 +545,7 @@ __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, c
       }
     }
     *reinterpret_cast<float4*>(&sm.x[warp][4 * lane]) = o;
+    if (gi + 1 < per) row = row_at(v0 + kPrepV + warp);
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < kPrepV; ++v) {
@@ -567,7 +594,7 @@ TreeWs tree_ws(int B, int Hq, int Hkv, int64_t R) {
   const size_t rq = (size_t)R * Hq, rk = (size_t)R * Hkv;
   w.seq = 0;
   w.cta = w.seq + al256((size_t)(B + 1) * sizeof(TreeSeq));
-  w.q = w.cta + al256((size_t)num_sms() * 4);
+  w.q = w.cta + al256((size_t)num_sms() * sizeof(TreeCta));
   w.k = w.q + al256(rq * 512);
   w.v = w.k + al256(rk * 512);
   w.qf = w.v + al256(rk * 512);
@@ -631,7 +658,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   const TreeWs w = tree_ws(a.B, a.Hq, a.Hkv, a.R);
   unsigned char* base = static_cast<unsigned char*>(a.ws);
   p.seq = reinterpret_cast<TreeSeq*>(base + w.seq);
-  p.cta_seq = reinterpret_cast<int*>(base + w.cta);
+  p.cta = reinterpret_cast<TreeCta*>(base + w.cta);
   p.qrot = reinterpret_cast<float*>(base + w.q);
   p.krot = reinterpret_cast<float*>(base + w.k);
   p.vrot = reinterpret_cast<float*>(base + w.v);

@@ -36,6 +36,14 @@ struct TreeSeq {
   int64_t unit;
 };
 
+// A CTA's share of the units, and the sequence of its first unit: all that it
+// needs to begin, in one read.
+struct __align__(16) TreeCta {
+  TreeSeq s;
+  int64_t u, end;
+  int b, pad[3];  // b: ~ of its number
+};
+
 struct TreeParams {
   const void *q, *kn, *vn;
   int64_t qs, ks, vs;  // strides between tokens in elements
@@ -63,7 +71,7 @@ struct TreeParams {
   int* status;
   // workspace
   TreeSeq* seq;         // [B + 1]; seq[B].unit: the number of units
-  int* cta_seq;         // [ctas] the sequence of a CTA's first unit
+  TreeCta* cta;         // [ctas]
   float *qrot, *krot, *vrot;  // rotated rows: fp32, or fp16 (q: 128 leading parts, 128 remainders)
   float* qfac;          // [R·Hq] power of two that was divided out of a row of q (tensor-core path)
   float *kfac, *vfac;   // [Hkv][R] the same of the drafted rows, times kone / vone
@@ -108,21 +116,27 @@ struct TreeSeg {
   int b, kvh, row0, nrow, first, last, ctiles;
   TreeSeq s;
 };
-// The segment that starts at unit u (b: a sequence at or before it).
+// The segment that starts at unit u of sequence b (~b: the CTA's first).
 __device__ __forceinline__ TreeSeg tree_seg(const TreeParams& p, int64_t u, int64_t u_end, int b) {
   TreeSeg g;
-  while (b + 1 < p.B && p.seq[b + 1].unit <= u) ++b;
-  g.b = b;
-  g.s = p.seq[b];
-  const int w = (int)(u - g.s.unit);  // fewer than 2^31 units in a sequence: rows and lengths are
-  const int grp = w / g.s.per;
-  g.first = w - grp * g.s.per;
-  g.kvh = grp / g.s.rt;
-  g.row0 = (grp - g.kvh * g.s.rt) * p.rows;
-  g.nrow = min(p.rows, g.s.T * p.G - g.row0);
-  g.last = (int)min((int64_t)g.s.per, g.first + (u_end - u));
-  g.ctiles = (g.s.len + kTreeTok - 1) / kTreeTok;
+  g.b = b < 0 ? ~b : b;
+  g.s = *(b < 0 ? &p.cta[blockIdx.x].s : p.seq + b);
+  const TreeSeq& s = g.s;
+  const int w = (int)(u - s.unit);  // fewer than 2^31 units in a sequence: rows and lengths are
+  const int grp = w / s.per;
+  g.first = w - grp * s.per;
+  g.kvh = grp / s.rt;
+  g.row0 = (grp - g.kvh * s.rt) * p.rows;
+  g.nrow = min(p.rows, s.T * p.G - g.row0);
+  g.last = (int)min((int64_t)s.per, g.first + (u_end - u));
+  g.ctiles = (s.len + kTreeTok - 1) / kTreeTok;
   return g;
+}
+// The sequence of unit u, b being it or one before it.
+__device__ __forceinline__ int tree_next(const TreeParams& p, int64_t u, int b) {
+  if (b < 0) b = ~b;
+  while (b + 1 < p.B && p.seq[b + 1].unit <= u) ++b;
+  return b;
 }
 
 // Four elements from element i on (a multiple of four) as fp32.

@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   extern __shared__ __align__(1024) unsigned char smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + kMisc);
   if ((smem_u32(smem) & 1023u) != 0u) {  // the swizzled operands need it
+    griddep_wait();  // as every CTA, before it ends: the join is let in by that
     if (threadIdx.x == 0) atomicOr(p.status, 1);
     return;
   }
@@ -358,10 +359,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
   griddep_wait();
   griddep_launch();
 
-  const int64_t units = p.seq[p.B].unit;
-  int64_t u = tree_cut(blockIdx.x, units, p.ctas);
-  const int64_t u_end = tree_cut(blockIdx.x + 1, units, p.ctas);
-  int b = u < u_end ? p.cta_seq[blockIdx.x] : 0;
+  const TreeCta& share = p.cta[blockIdx.x];
+  int64_t u = share.u;
+  const int64_t u_end = share.end;
+  int b = share.b;
 
   if (warp < kSoft) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kRegSoft));
@@ -376,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
     bool ok = true;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
-      b = g.b;
       // the rows: Q̂ into shared memory (every product with the last segment's
       // has completed: its last Sᵀ was read here), their factors and records
       if (tid < N) {
@@ -618,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       tc_fence_before();
       bar_softmax();  // the rows' tables are rewritten next
       u += g.last - g.first;
+      if (u < u_end) b = tree_next(p, u, b);
     }
   } else if (warp < kSoft + 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegOps));
@@ -632,7 +633,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
     bool ok = true;
     while (ok && u < u_end) {
       const TreeSeg g = tree_seg(p, u, u_end, b);
-      b = g.b;
       for (int t = g.first; t < g.last; ++t, ++i) {
         const uint32_t sb = i & 1u, op = dst + sb * 64;
         const bool draft = t >= g.ctiles;
@@ -708,6 +708,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         }
       }
       u += g.last - g.first;
+      if (u < u_end) b = tree_next(p, u, b);
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kRegRest));
@@ -755,8 +756,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           fresh_prev = fresh;
           fresh = left == 0;
           if (left == 0) {
+            if (j > 0) b = tree_next(p, u + j, b);
             const TreeSeg g = tree_seg(p, u + j, u_end, b);
-            b = g.b;
             left = __shfl_sync(kFull, g.last - g.first, 0);
           }
           --left;
@@ -801,7 +802,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       const int jt = kTreeTok / p.block, ot = kTreeTok - jt * p.block;
       while (ok && u < u_end) {
         const TreeSeg g = tree_seg(p, u, u_end, b);
-        b = g.b;
         // this lane's chunk of tile t: token, page number within the sequence and
         // place in the page
         int at = g.first * kTreeTok + 16 * c, j = at / p.block, o = at - j * p.block;
@@ -866,6 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           }
         }
         u += g.last - g.first;
+        if (u < u_end) b = tree_next(p, u, b);
       }
       if (lane == 0) {
         ms.sent[warp - kCopy][0] = rc;
