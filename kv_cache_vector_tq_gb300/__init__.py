@@ -291,35 +291,35 @@ _T = None
 
 
 def _types():
-    """(torch, its type -> tq type, the raw current stream, the current device), once torch is wanted."""
+    """(torch, its type -> tq type, the raw current stream of a device, the current device), once torch is wanted."""
     global _T
     if _T is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = raw if raw else (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         dev = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-        stream = (lambda: raw(dev())) if raw else (lambda: torch.cuda.current_stream().cuda_stream)
         _T = torch, {torch.float32: TQ_F32, torch.float16: TQ_F16, torch.bfloat16: TQ_BF16}, stream, dev
     return _T
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, dev):
     if stream is None:
-        return _types()[2]()
+        return _T[2](dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _dev(t, dtype, n, what):
-    """Device address of a contiguous tensor of this type with n elements or more, on the current device."""
-    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or not t.is_cuda or t.get_device() != _T[3]():
+def _dev(t, dtype, n, what, dev):
+    """Device address of a contiguous tensor of this type with n elements or more, on this device."""
+    if t.dtype is not dtype or t.get_device() != dev or t.numel() < n or not t.is_contiguous():
         raise ValueError(f"{what}: a contiguous CUDA tensor of {dtype} with {n} elements or more, on the current "
                          f"device, is wanted")
     return t.data_ptr()
 
 
-def _heads(t, n, h, d, what):
-    """Address and token stride of a [n, h, d] CUDA tensor whose heads are contiguous."""
+def _heads(t, n, h, d, what, dev):
+    """Address and token stride of a [n, h, d] tensor on this device whose heads are contiguous."""
     a, b, c = t.stride()
-    if t.shape != (n, h, d) or c != 1 or (b != d and h > 1) or not t.is_cuda or t.get_device() != _T[3]():
+    if t.get_device() != dev or t.shape != (n, h, d) or c != 1 or (b != d and h > 1):
         raise ValueError(f"{what}: a CUDA tensor [{n}, {h}, {d}] with contiguous heads, on the current device, is wanted")
     return t.data_ptr(), a if n > 1 else h * d
 
@@ -328,14 +328,15 @@ def tq_block_tables(lens, new, held, ring, state, table, block, held_out, state_
                     stream=None):
     """Pages, slots and positions of one step's tokens (include/tq.h).  table [B, max_blocks], ring, lens, new, held,
     held_out, row_start and pos are int32, state, state_out and slots int64; pos and slots have one entry per row."""
-    torch = _types()[0]
+    torch, _, _, cur = _types()
+    dev = cur()
     i32, i64, B = torch.int32, torch.int64, lens.numel()
     _check("tq_block_tables", lib().tq_block_tables(
-        _dev(lens, i32, B, "lens"), _dev(new, i32, B, "new"), _dev(held, i32, B, "held"), B, block,
-        _dev(ring, i32, 1, "ring"), ring.numel(), _dev(state, i64, 2, "state"),
-        _dev(table, i32, B * table.shape[-1], "table"), table.shape[-1], _dev(held_out, i32, B, "held_out"),
-        _dev(state_out, i64, 2, "state_out"), _dev(row_start, i32, B + 1, "row_start"), _dev(slots, i64, 0, "slots"),
-        _dev(pos, i32, slots.numel(), "pos"), slots.numel(), _raw_stream(stream)))
+        _dev(lens, i32, B, "lens", dev), _dev(new, i32, B, "new", dev), _dev(held, i32, B, "held", dev), B, block,
+        _dev(ring, i32, 1, "ring", dev), ring.numel(), _dev(state, i64, 2, "state", dev),
+        _dev(table, i32, B * table.shape[-1], "table", dev), table.shape[-1], _dev(held_out, i32, B, "held_out", dev),
+        _dev(state_out, i64, 2, "state_out", dev), _dev(row_start, i32, B + 1, "row_start", dev),
+        _dev(slots, i64, 0, "slots", dev), _dev(pos, i32, slots.numel(), "pos", dev), slots.numel(), _raw_stream(stream, dev)))
 
 
 def tq_rope_frequencies(inv_freq, device="cuda"):
@@ -351,22 +352,24 @@ def tq_rope_frequencies(inv_freq, device="cuda"):
 def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=None):
     """Head norms and position rotation of q [N, Hq, d] and k [N, Hkv, d] into q_out and k_out (include/tq.h).
     wq, wk: [d] of q's type or None; freq: tq_rope_frequencies or None (norms alone); outputs may be the inputs."""
-    torch, types = _types()[:2]
+    torch, types, _, cur = _types()
+    dev = cur()
     (N, Hq, d), Hkv, ti, to = q.shape, k.shape[1], q.dtype, q_out.dtype
     if k.dtype is not ti or k_out.dtype is not to:
         raise ValueError("q and k, and q_out and k_out, are of one type")
-    (qp, qs), (kp, ks) = _heads(q, N, Hq, d, "q"), _heads(k, N, Hkv, d, "k")
-    (qo, qos), (ko, kos) = _heads(q_out, N, Hq, d, "q_out"), _heads(k_out, N, Hkv, d, "k_out")
+    (qp, qs), (kp, ks) = _heads(q, N, Hq, d, "q", dev), _heads(k, N, Hkv, d, "k", dev)
+    (qo, qos), (ko, kos) = _heads(q_out, N, Hq, d, "q_out", dev), _heads(k_out, N, Hkv, d, "k_out", dev)
     _check("tq_qk_norm_rope", lib().tq_qk_norm_rope(
-        qp, qs, kp, ks, types[ti], N, Hq, Hkv, d, None if wq is None else _dev(wq, ti, d, "wq"),
-        None if wk is None else _dev(wk, ti, d, "wk"), eps,
-        None if freq is None else _dev(freq, torch.int64, 0, "freq"), 0 if freq is None else 2 * freq.numel(), style,
-        _dev(pos, torch.int32, N, "pos"), qo, qos, ko, kos, types[to], _raw_stream(stream)))
+        qp, qs, kp, ks, types[ti], N, Hq, Hkv, d, None if wq is None else _dev(wq, ti, d, "wq", dev),
+        None if wk is None else _dev(wk, ti, d, "wk", dev), eps,
+        None if freq is None else _dev(freq, torch.int64, 0, "freq", dev), 0 if freq is None else 2 * freq.numel(), style,
+        _dev(pos, torch.int32, N, "pos", dev), qo, qos, ko, kos, types[to], _raw_stream(stream, dev)))
 
 
 def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
     """tq_encode of x [N, Hkv, d] into a paged cache, token i at slots[i] (include/tq.h)."""
-    torch, types = _types()[:2]
+    torch, types, _, cur = _types()
+    dev = cur()
     N, Hkv, d = x.shape
     if d != ctx.d:
         raise ValueError(f"x: rows of {ctx.d} elements are wanted")
@@ -374,8 +377,8 @@ def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
     if ti is not torch.float32 and ti is not torch.float16:
         raise ValueError("x: float32 or float16 is wanted")
     _check("tq_encode_slots", lib().tq_encode_slots(
-        ctx.handle, _dev(x, ti, 0, "x"), types[ti], N, Hkv, _dev(slots, torch.int64, N, "slots"), block,
-        ctypes.byref(codes.desc), _raw_stream(stream)))
+        ctx.handle, _dev(x, ti, 0, "x", dev), types[ti], N, Hkv, _dev(slots, torch.int64, N, "slots", dev), block,
+        ctypes.byref(codes.desc), _raw_stream(stream, dev)))
 
 
 def tq_tree_attention_workspace_size(kctx, B, Hq, Hkv, rows):
@@ -390,26 +393,29 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     """Attention of drafted tokens q [rows, Hq, d] over a packed cache and each other (include/tq.h).  k_new, v_new
     [rows, Hkv, d] or None (Hkv is then given); mask [rows, words] int32 or None (a chain); table [B, max_blocks] or
     None (contiguous, cap = block)."""
-    torch, types = _types()[:2]
+    torch, types, _, cur = _types()
+    dev = cur()
     rows, Hq, d = q.shape
+    if d != kctx.d:
+        raise ValueError(f"q: rows of {kctx.d} elements are wanted")
     ti = q.dtype
     B, Hkv = lens.numel(), k_new.shape[1] if k_new is not None else Hkv
-    qp, qs = _heads(q, rows, Hq, d, "q")
+    qp, qs = _heads(q, rows, Hq, d, "q", dev)
     kp = vp = None
     ks = vs = 0
     if k_new is not None:
         if k_new.dtype is not ti or v_new.dtype is not ti:
             raise ValueError("q, k_new and v_new are of one type")
-        (kp, ks), (vp, vs) = _heads(k_new, rows, Hkv, d, "k_new"), _heads(v_new, rows, Hkv, d, "v_new")
+        (kp, ks), (vp, vs) = _heads(k_new, rows, Hkv, d, "k_new", dev), _heads(v_new, rows, Hkv, d, "v_new", dev)
     i32 = torch.int32
     words, width = 0 if mask is None else mask.shape[1], 0 if table is None else table.shape[1]
     _check("tq_tree_attention", lib().tq_tree_attention(
-        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, types[ti], rows, _dev(row_start, i32, B + 1, "row_start"),
-        None if mask is None else _dev(mask, i32, rows * words, "mask"), words, ctypes.byref(K.desc),
-        ctypes.byref(V.desc), _dev(lens, i32, B, "lens"),
-        None if table is None else _dev(table, i32, B * width, "table"), width, block, B, Hq, Hkv, scale,
-        _dev(out, ti, rows * Hq * d, "out"), _dev(ws, ws.dtype, 0, "ws"), ws.numel() * ws.element_size(),
-        _raw_stream(stream)))
+        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, types[ti], rows, _dev(row_start, i32, B + 1, "row_start", dev),
+        None if mask is None else _dev(mask, i32, rows * words, "mask", dev), words, ctypes.byref(K.desc),
+        ctypes.byref(V.desc), _dev(lens, i32, B, "lens", dev),
+        None if table is None else _dev(table, i32, B * width, "table", dev), width, block, B, Hq, Hkv, scale,
+        _dev(out, ti, rows * Hq * d, "out", dev), _dev(ws, ws.dtype, 0, "ws", dev), ws.numel() * ws.element_size(),
+        _raw_stream(stream, dev)))
 
 
 def tq_unpack_indices(codes, first=0, count=None, with_bits=False):

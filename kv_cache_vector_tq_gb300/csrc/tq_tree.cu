@@ -14,7 +14,9 @@ namespace {
 // [16w, 16w + 16) of the matrix in registers (loaded once, before the wait for
 // the kernel ahead: the matrix is constant), every lane four rows of them, and
 // multiplies group after group; the eight partial sums meet in shared memory.
-// fp32 sums.  CTA 0 also lays out the units of the sequences.
+// fp32 sums.  CTA 0 also lays out the units of the sequences.  Bound by latency
+// for few rows (4.5 us for one token of 32 heads), by the FMA rate and its shared
+// reads for many (about 1.5 us for each eight rows that every CTA takes).
 // A drafted row that holds an infinity or a NaN is stored as zeros with the
 // factor NaN: rows that see it become NaN through the factor, and rows that do
 // not see it are not touched by a product 0 · NaN.
@@ -431,7 +433,9 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
 // A warp per row: its records (its own and those of the CTAs that continued its
 // group) under their common maximum, divided by the sum of weights; then
 // out = Πᵀ·o for the CTA's kPrepV rows, the matrix in registers as in the
-// rotation.  A row that saw nothing is zero.
+// rotation.  A row that saw nothing is zero.  Bound by latency, a record's two
+// reads after the attention kernel's end; where the records are is found before
+// it (25.4 -> 23.9 us for the three kernels on one token over 16384).
 __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, const int per) {
   __shared__ __align__(16) RotSmem sm;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;

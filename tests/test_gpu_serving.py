@@ -644,7 +644,8 @@ def test_refusals():
     status(-2, kc=mixed, K=tq.CodeSet(mixed, 1024))
     status(-1, kc=ctx(3))
     status(-2, table=torch.empty(1, 2 ** 27 - 1, dtype=torch.int32, device="cuda"))  # 16 short of 2^31 places
-    for kw in (dict(q=s["q"].transpose(0, 1)), dict(ws=ws.cpu()), dict(ws=ws[::2]), dict(q=s["q"].cpu())):
+    for kw in (dict(q=s["q"].transpose(0, 1)), dict(ws=ws.cpu()), dict(ws=ws[::2]), dict(q=s["q"].cpu()),
+               dict(q=s["q"][:, :1, :64])):  # half a row of one head, the stride of a whole one
         with pytest.raises(ValueError):
             call(**kw)
     x = torch.randn(4, 2, D, device="cuda", dtype=torch.float16)
@@ -668,8 +669,9 @@ def test_tensors_of_another_device_are_refused(monkeypatch):
     monkeypatch.setattr(tq, "_T", tq._types()[:3] + (lambda: 1 + x.get_device(),))  # as if another were current
     with pytest.raises(ValueError, match="current device"):
         tq.tq_qk_norm_rope(*args)
+    lens, n = i32([0]), torch.zeros(2, dtype=torch.int64, device="cuda")
     with pytest.raises(ValueError, match="current device"):
-        tq._dev(pos, torch.int32, 1, "pos")
+        tq.tq_block_tables(lens, lens, lens, pos, n, lens[None], 16, pos, n.clone(), pos, n, pos)
 
 
 # ------------------------------------------------------------------ together
