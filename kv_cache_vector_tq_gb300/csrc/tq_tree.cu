@@ -198,28 +198,49 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
 }
 
 // ------------------------------------------------------------------ attention, fp32
-// 64 rows against 64 tokens at a time on the CUDA cores: S = Q·K̂ᵀ with 4 x 4
-// values per thread, running maximum and sum per row, O += P·V̂ with 4 x 8.
-// Products and sums in fp32 throughout; bound by the FMA rate.
-constexpr int kFRows = 64, kFTok = 64, kFStride = 132, kFPStride = 68;
-constexpr int kFSmem = (2 * kFRows * kFStride + kFTok * 128 + kFRows * kFPStride + 3 * kFTok + 3 * kFRows + 32) * 4;
+// Rows against 64 tokens at a time on the CUDA cores: S = Q·K̂ᵀ with RT x 4
+// values per thread, running maximum and sum per row, O += P·V̂ with RT x 8.
+// Products and sums in fp32 throughout.  The next tile's packed words are loaded
+// into registers before this one's products; a thread unpacks 32 coordinates of
+// a token, whole words in both layouts, against 16 centroids in 16 banks.
+// 64 rows (RT = 4) are bound by the FMA rate and its shared reads; 16 (RT = 1,
+// where the mean sequence has no more, two CTAs an SM) by the shared reads of K̂
+// and V̂.
+constexpr int kFTok = 64, kFStride = 132, kFPStride = 68;
+template <int RT>
+constexpr int kFSmem = (16 * RT * kFStride + kFTok * kFStride + kFTok * 128 + 16 * RT * kFPStride + 3 * kFTok +
+                        3 * 16 * RT + 32) * 4;
 
-// Code j of a vector: b bits at bit j·b of its own stream, or (PAIR) at bit
-// (2j + slot)·b of the block it shares.
-__device__ __forceinline__ uint32_t tree_code(const uint32_t* w, int j, int b, bool pair, int slot) {
-  const int bit = pair ? (2 * j + slot) * b : j * b;
-  const int i = bit >> 5, sh = bit & 31;
-  uint32_t v = __ldg(w + i) >> sh;
-  if (sh + b > 32) v |= __ldg(w + i + 1) << (32 - sh);
-  return v & ((1u << b) - 1u);
+// 32 fields of B bits, S bits apart, of the words w: centroids as floats.
+template <int B, int S>
+__device__ __forceinline__ void tree_unpack(const uint32_t* w, const float* cen, float4* dst) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int bit = (4 * k + e) * S, i = bit >> 5, s = bit & 31;
+      const uint32_t x = s + B > 32 ? __funnelshift_r(w[i], w[i + 1], s) : w[i] >> s;
+      v[e] = cen[x & ((1u << B) - 1u)];
+    }
+    dst[k] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+template <int B>
+__device__ __forceinline__ void tree_unpack_pair(uint32_t* w, int slot, const float* cen, float4* dst) {
+#pragma unroll
+  for (int i = 0; i < 2 * B; ++i) w[i] = __funnelshift_r(w[i], i + 1 < 2 * B ? w[i + 1] : 0u, slot * B);
+  tree_unpack<B, 2 * B>(w, cen, dst);
 }
 
-__global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p) {
+template <int RT>
+__global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(const TreeParams p) {
+  constexpr int kFRows = 16 * RT;
   extern __shared__ __align__(16) float fsm[];
-  float* Qs = fsm;                              // [64][132]
+  float* Qs = fsm;                              // [rows][132]
   float* Ks = Qs + kFRows * kFStride;           // [64][132]
   float* Vs = Ks + kFTok * kFStride;            // [64][128]
-  float* Ps = Vs + kFTok * 128;                 // [64][68]
+  float* Ps = Vs + kFTok * 128;                 // [rows][68]
   float* kn = Ps + kFRows * kFPStride;          // [64] K norm / √d
   float* vn = kn + kFTok;                       // [64] V norm / √d
   float* ok = vn + kFTok;                       // [64] 1: a token of the sequence
@@ -253,12 +274,54 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
       rm[tid] = -INFINITY;
       rl[tid] = 0.f;
     }
-    float o[4][8];
+    float o[RT][8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[i][k] = 0.f;
 
+    // this thread's token of a tile and 32 of its coordinates: packed words and norms
+    const int tok0 = tid >> 2, quarter = tid & 3;
+    uint32_t kw[4], vw[8];
+    float skn = 0.f, svn = 0.f;
+    bool good = false;
+    int slot = 0;
+    auto fetch = [&](int t2) {
+      const int t = t2 * kFTok + tok0;
+      good = t < s.len;
+      skn = svn = 0.f;
+      slot = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) kw[i] = 0u;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) vw[i] = 0u;
+      if (!good) return;
+      const int j = t / p.block;
+      const int64_t page = p.table ? (int64_t)p.table[(int64_t)g.b * p.max_blocks + j] : g.b;
+      good = page >= 0 && page < p.pages;
+      if (!good) {
+        atomicOr(p.status, 2);
+        return;
+      }
+      const int64_t vec = (page * p.Hkv + kvh) * p.block + (t - j * p.block);
+      const uint32_t* ks = p.kcodes + vec * (4 * p.kb) + quarter * p.kb;
+      const uint2* vs = reinterpret_cast<const uint2*>(p.vcodes + (vec >> 1) * (8 * p.vb)) + quarter * p.vb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < p.kb) kw[i] = __ldg(ks + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < p.vb) {
+          const uint2 x = __ldg(vs + i);
+          vw[2 * i] = x.x;
+          vw[2 * i + 1] = x.y;
+        }
+      slot = (int)(vec & 1);
+      skn = p.knorm[vec];
+      svn = p.vnorm[vec];
+    };
+    const int cend = min(2 * last, (s.len + kFTok - 1) / kFTok);  // cached tiles of the segment end here
+    if (2 * first < cend) fetch(2 * first);
     for (int t2 = 2 * first; t2 < 2 * last; ++t2) {
       const bool draft = (t2 >> 1) >= ctiles;
       const int t0 = draft ? (t2 - 2 * ctiles) * kFTok : t2 * kFTok;  // first token of the tile
@@ -266,83 +329,69 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
       if (nt <= 0) continue;
       __syncthreads();  // the last tile's operands have been read
       {
-        const int tok = tid >> 2, c0 = (tid & 3) * 32;  // token and 32 coordinates of this thread
-        bool good = tok < nt;
-        float4* kd = reinterpret_cast<float4*>(Ks + tok * kFStride + c0);
-        float4* vd = reinterpret_cast<float4*>(Vs + tok * 128 + c0);
-        float skn = 0.f, svn = 0.f;
+        float4* kd = reinterpret_cast<float4*>(Ks + tok0 * kFStride + 32 * quarter);
+        float4* vd = reinterpret_cast<float4*>(Vs + tok0 * 128 + 32 * quarter);
         if (draft) {
-          const int64_t at = ((int64_t)(s.start + t0 + tok) * p.Hkv + kvh) * 128 + c0;
+          good = tok0 < nt;
+          skn = svn = 0.f;
+          const int64_t row = s.start + t0 + tok0, at = (row * p.Hkv + kvh) * 128 + 32 * quarter;
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             kd[k] = good ? *reinterpret_cast<const float4*>(p.krot + at + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
             vd[k] = good ? *reinterpret_cast<const float4*>(p.vrot + at + 4 * k) : make_float4(0.f, 0.f, 0.f, 0.f);
           }
           if (good) {
-            skn = p.kfac[(int64_t)kvh * p.R + s.start + t0 + tok];
-            svn = p.vfac[(int64_t)kvh * p.R + s.start + t0 + tok];
+            skn = p.kfac[(int64_t)kvh * p.R + row];
+            svn = p.vfac[(int64_t)kvh * p.R + row];
           }
         } else {
-          int64_t vec = 0;
-          if (good) {
-            const int t = t0 + tok, j = t / p.block;
-            const int64_t page = p.table ? (int64_t)p.table[(int64_t)g.b * p.max_blocks + j] : g.b;
-            good = page >= 0 && page < p.pages;
-            if (!good) atomicOr(p.status, 2);
-            vec = good ? (page * p.Hkv + kvh) * p.block + (t - j * p.block) : 0;
+          switch (p.kb) {
+            case 1: tree_unpack<1, 1>(kw, cen, kd); break;
+            case 2: tree_unpack<2, 2>(kw, cen, kd); break;
+            case 3: tree_unpack<3, 3>(kw, cen, kd); break;
+            default: tree_unpack<4, 4>(kw, cen, kd); break;
           }
-          const uint32_t* kw = p.kcodes + vec * (4 * p.kb);
-          const uint32_t* vw = p.vcodes + (vec >> 1) * (8 * p.vb);
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            float4 kv = make_float4(0.f, 0.f, 0.f, 0.f), vv = kv;
-            if (good) {
-              const int j = c0 + 4 * k, sl = (int)(vec & 1);
-              kv = make_float4(cen[tree_code(kw, j, p.kb, false, 0)], cen[tree_code(kw, j + 1, p.kb, false, 0)],
-                               cen[tree_code(kw, j + 2, p.kb, false, 0)], cen[tree_code(kw, j + 3, p.kb, false, 0)]);
-              vv = make_float4(cen[16 + tree_code(vw, j, p.vb, true, sl)], cen[16 + tree_code(vw, j + 1, p.vb, true, sl)],
-                               cen[16 + tree_code(vw, j + 2, p.vb, true, sl)],
-                               cen[16 + tree_code(vw, j + 3, p.vb, true, sl)]);
-            }
-            kd[k] = kv;
-            vd[k] = vv;
+          switch (p.vb) {
+            case 1: tree_unpack_pair<1>(vw, slot, cen + 16, vd); break;
+            case 2: tree_unpack_pair<2>(vw, slot, cen + 16, vd); break;
+            case 3: tree_unpack_pair<3>(vw, slot, cen + 16, vd); break;
+            default: tree_unpack_pair<4>(vw, slot, cen + 16, vd); break;
           }
-          if (good) {
-            skn = p.knorm[vec] * inv_sd;
-            svn = p.vnorm[vec] * inv_sd;
-          }
+          skn *= inv_sd;
+          svn *= inv_sd;
         }
-        if ((tid & 3) == 0) {
-          kn[tok] = skn;
-          vn[tok] = svn;
-          ok[tok] = good ? 1.f : 0.f;
+        if (quarter == 0) {
+          kn[tok0] = skn;
+          vn[tok0] = svn;
+          ok[tok0] = good ? 1.f : 0.f;
         }
       }
+      if (t2 + 1 < cend) fetch(t2 + 1);
       __syncthreads();
-      // S: rows 4·ty.., tokens tx + 16·k
-      float acc[4][4];
+      // S: rows RT·ty.., tokens tx + 16·k
+      float acc[RT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
 #pragma unroll 4
       for (int d4 = 0; d4 < 32; ++d4) {
-        float4 a[4], c[4];
+        float4 a[RT], c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (4 * ty + i) * kFStride + 4 * d4);
+        for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (RT * ty + i) * kFStride + 4 * d4);
 #pragma unroll
         for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * k) * kFStride + 4 * d4);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             acc[i][k] = fmaf(a[i].x, c[k].x, fmaf(a[i].y, c[k].y, fmaf(a[i].z, c[k].z, fmaf(a[i].w, c[k].w, acc[i][k]))));
       }
       // scores in base-2 units, masks, the tile's row maxima (16 threads share a row)
-      float f[4];
+      float f[RT];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 4 * ty + i, rho = row0 + r, ti = rho / p.G;
+      for (int i = 0; i < RT; ++i) {
+        const int r = RT * ty + i, rho = row0 + r, ti = rho / p.G;
         float m = -INFINITY;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -381,21 +430,21 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
         }
       }
       __syncthreads();
-      // O: rows 4·ty.., coordinates 8·tx..
+      // O: rows RT·ty.., coordinates 8·tx..
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < RT; ++i)
 #pragma unroll
         for (int k = 0; k < 8; ++k) o[i][k] *= f[i];
       for (int t4 = 0; t4 < kFTok / 4; ++t4) {
-        float4 pr[4];
+        float4 pr[RT];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(Ps + (4 * ty + i) * kFPStride + 4 * t4);
+        for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(Ps + (RT * ty + i) * kFPStride + 4 * t4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float4 v0 = *reinterpret_cast<const float4*>(Vs + (4 * t4 + e) * 128 + 8 * tx);
           const float4 v1 = *reinterpret_cast<const float4*>(Vs + (4 * t4 + e) * 128 + 8 * tx + 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
+          for (int i = 0; i < RT; ++i) {
             const float x = e == 0 ? pr[i].x : (e == 1 ? pr[i].y : (e == 2 ? pr[i].z : pr[i].w));
             o[i][0] = fmaf(x, v0.x, o[i][0]);
             o[i][1] = fmaf(x, v0.y, o[i][1]);
@@ -411,8 +460,8 @@ __global__ void __launch_bounds__(256) tree_attend_f32_kernel(const TreeParams p
     }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = 4 * ty + i, rho = row0 + r;
+    for (int i = 0; i < RT; ++i) {
+      const int r = RT * ty + i, rho = row0 + r;
       if (r < nrow) {
         float* rec = first == 0 ? p.rec + ((int64_t)(s.start + rho / p.G) * p.Hq + kvh * p.G + rho % p.G) * kTreeRec
                                 : p.crec + ((int64_t)blockIdx.x * p.rows + r) * kTreeRec;
@@ -598,7 +647,7 @@ TreeWs tree_ws(int B, int Hq, int Hkv, int64_t R) {
   const size_t rq = (size_t)R * Hq, rk = (size_t)R * Hkv;
   w.seq = 0;
   w.cta = w.seq + al256((size_t)(B + 1) * sizeof(TreeSeq));
-  w.q = w.cta + al256((size_t)num_sms() * sizeof(TreeCta));
+  w.q = w.cta + al256((size_t)num_sms() * 2 * sizeof(TreeCta));
   w.k = w.q + al256(rq * 512);
   w.v = w.k + al256(rk * 512);
   w.qf = w.v + al256(rk * 512);
@@ -612,11 +661,15 @@ TreeWs tree_ws(int B, int Hq, int Hkv, int64_t R) {
 
 }  // namespace
 
-cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st) {
+template <int RT>
+static cudaError_t attend_f32(const TreeParams& p, cudaStream_t st) {
   static PerDeviceValue attr;
-  const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_f32_kernel, kFSmem);
+  const cudaError_t e = smem_attr_once(attr, (const void*)tree_attend_f32_kernel<RT>, kFSmem<RT>);
   if (e != cudaSuccess) return e;
-  return tree_launch(tree_attend_f32_kernel, p.ctas, 256, kFSmem, st, p);
+  return tree_launch(tree_attend_f32_kernel<RT>, p.ctas, 256, kFSmem<RT>, st, p);
+}
+cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st) {
+  return p.rows == 16 ? attend_f32<1>(p, st) : attend_f32<4>(p, st);
 }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R) { return tree_ws(B, Hq, Hkv, R).total; }
@@ -671,11 +724,12 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   p.vfac = reinterpret_cast<float*>(base + w.vf);
   p.rec = reinterpret_cast<float*>(base + w.rec);
   p.crec = reinterpret_cast<float*>(base + w.crec);
-  p.ctas = num_sms();
   // fp32 rows are computed in fp32; 16-bit types round coarser than the
   // tensor-core kernel does
   const bool tc = a.dtype != TQ_F32;
-  p.rows = tc ? tree_umma_rows(a.R, a.B, p.G) : kFRows;
+  p.rows = tree_umma_rows(a.R, a.B, p.G);
+  if (!tc && p.rows > 16) p.rows = 64;
+  p.ctas = num_sms() * (!tc && p.rows == 16 ? 2 : 1);
   p.klut = kc.lut;
   p.vlut = vc.lut;
   bool same = kc.b_mse == vc.b_mse && kc.alpha == vc.alpha;
