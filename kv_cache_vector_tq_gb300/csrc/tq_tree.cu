@@ -206,10 +206,11 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
 // 64 rows (RT = 4) are bound by the FMA rate and its shared reads; 16 (RT = 1,
 // where the mean sequence has no more, two CTAs an SM) by the shared reads of K̂
 // and V̂.
-constexpr int kFTok = 64, kFStride = 132, kFPStride = 68;
+// A token's four runs of 32 coordinates lie 40 words apart and tokens 164, so that
+// the eight lanes of a store's quarter, two tokens by four runs, meet no bank twice.
+constexpr int kFTok = 64, kFStride = 132, kFPStride = 68, kFRun = 40, kFTokStride = 164;
 template <int RT>
-constexpr int kFSmem = (16 * RT * kFStride + kFTok * kFStride + kFTok * 128 + 16 * RT * kFPStride + 3 * kFTok +
-                        3 * 16 * RT + 32) * 4;
+constexpr int kFSmem = (16 * RT * kFStride + 2 * kFTok * kFTokStride + 16 * RT * kFPStride + 3 * kFTok + 3 * 16 * RT + 32) * 4;
 
 // 32 fields of B bits, S bits apart, of the words w: centroids as floats.
 template <int B, int S>
@@ -238,9 +239,9 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
   constexpr int kFRows = 16 * RT;
   extern __shared__ __align__(16) float fsm[];
   float* Qs = fsm;                              // [rows][132]
-  float* Ks = Qs + kFRows * kFStride;           // [64][132]
-  float* Vs = Ks + kFTok * kFStride;            // [64][128]
-  float* Ps = Vs + kFTok * 128;                 // [rows][68]
+  float* Ks = Qs + kFRows * kFStride;           // [64][164]
+  float* Vs = Ks + kFTok * kFTokStride;         // [64][164]
+  float* Ps = Vs + kFTok * kFTokStride;         // [rows][68]
   float* kn = Ps + kFRows * kFPStride;          // [64] K norm / √d
   float* vn = kn + kFTok;                       // [64] V norm / √d
   float* ok = vn + kFTok;                       // [64] 1: a token of the sequence
@@ -329,8 +330,8 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
       if (nt <= 0) continue;
       __syncthreads();  // the last tile's operands have been read
       {
-        float4* kd = reinterpret_cast<float4*>(Ks + tok0 * kFStride + 32 * quarter);
-        float4* vd = reinterpret_cast<float4*>(Vs + tok0 * 128 + 32 * quarter);
+        float4* kd = reinterpret_cast<float4*>(Ks + tok0 * kFTokStride + kFRun * quarter);
+        float4* vd = reinterpret_cast<float4*>(Vs + tok0 * kFTokStride + kFRun * quarter);
         if (draft) {
           good = tok0 < nt;
           skn = svn = 0.f;
@@ -380,7 +381,7 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
 #pragma unroll
         for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (RT * ty + i) * kFStride + 4 * d4);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * k) * kFStride + 4 * d4);
+        for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * k) * kFTokStride + 4 * d4 + (kFRun - 32) * (d4 >> 3));
 #pragma unroll
         for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
         }
       }
       __syncthreads();
-      // O: rows RT·ty.., coordinates 8·tx..
+      // O: rows RT·ty.., coordinates 4·tx.. and 64 + 4·tx..
+      const float* vrow = Vs + kFRun * (tx >> 3) + 4 * (tx & 7);
 #pragma unroll
       for (int i = 0; i < RT; ++i)
 #pragma unroll
@@ -441,8 +443,8 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
         for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(Ps + (RT * ty + i) * kFPStride + 4 * t4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float4 v0 = *reinterpret_cast<const float4*>(Vs + (4 * t4 + e) * 128 + 8 * tx);
-          const float4 v1 = *reinterpret_cast<const float4*>(Vs + (4 * t4 + e) * 128 + 8 * tx + 4);
+          const float4 v0 = *reinterpret_cast<const float4*>(vrow + (4 * t4 + e) * kFTokStride);
+          const float4 v1 = *reinterpret_cast<const float4*>(vrow + (4 * t4 + e) * kFTokStride + 2 * kFRun);
 #pragma unroll
           for (int i = 0; i < RT; ++i) {
             const float x = e == 0 ? pr[i].x : (e == 1 ? pr[i].y : (e == 2 ? pr[i].z : pr[i].w));
@@ -469,8 +471,8 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
           rec[0] = rm[r];
           rec[1] = rl[r];
         }
-        *reinterpret_cast<float4*>(rec + 4 + 8 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        *reinterpret_cast<float4*>(rec + 8 + 8 * tx) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        *reinterpret_cast<float4*>(rec + 4 + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        *reinterpret_cast<float4*>(rec + 68 + 4 * tx) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
       }
     }
     u += last - first;
