@@ -198,19 +198,23 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
 }
 
 // ------------------------------------------------------------------ attention, fp32
-// Rows against 64 tokens at a time on the CUDA cores: S = Q·K̂ᵀ with RT x 4
-// values per thread, running maximum and sum per row, O += P·V̂ with RT x 8.
-// Products and sums in fp32 throughout.  The next tile's packed words are loaded
-// into registers before this one's products; a thread unpacks 32 coordinates of
-// a token, whole words in both layouts, against 16 centroids in 16 banks.
-// 64 rows (RT = 4) are bound by the FMA rate and its shared reads; 16 (RT = 1,
-// where the mean sequence has no more, two CTAs an SM) by the shared reads of K̂
-// and V̂.
-// A token's four runs of 32 coordinates lie 40 words apart and tokens 164, so that
-// the eight lanes of a store's quarter, two tokens by four runs, meet no bank twice.
-constexpr int kFTok = 64, kFStride = 132, kFPStride = 68, kFRun = 40, kFTokStride = 164;
+// 16·RT rows against 64 tokens at a time on the CUDA cores, products and sums in
+// fp32 throughout.  What bounds such a kernel is its shared reads, so a thread's
+// tiles are as square as its registers allow and the long axis of either product
+// is split over threads:
+//   S = Q·K̂ᵀ  a warp takes 2·RT rows, a thread all of them by 8 tokens over a
+//              quarter of the coordinates; four lanes join (2·RT x 2 scores each);
+//   O += P·V̂  a thread takes kOR rows by 8 coordinates over a share of the tokens;
+//              the shares are joined once, at the segment's end.
+// The next tile's packed words are loaded into registers before this one's
+// products; a thread unpacks 32 coordinates of a token, whole words in both
+// layouts, against 16 centroids in 16 banks.  16 rows (RT = 1) where the mean
+// sequence has no more, then with two CTAs an SM; else 64 (RT = 4).
+// Runs of 32 coordinates lie 40 words apart and rows of Q, K̂, V̂ 164, so that the
+// eight lanes of a 16-byte access meet no bank twice.
+constexpr int kFTok = 64, kFStride = 164, kFPStride = 68, kFRun = 40;
 template <int RT>
-constexpr int kFSmem = (16 * RT * kFStride + 2 * kFTok * kFTokStride + 16 * RT * kFPStride + 3 * kFTok + 3 * 16 * RT + 32) * 4;
+constexpr int kFSmem = (16 * RT * kFStride + 2 * kFTok * kFStride + 16 * RT * kFPStride + 3 * kFTok + 3 * 16 * RT + 32) * 4;
 
 // 32 fields of B bits, S bits apart, of the words w: centroids as floats.
 template <int B, int S>
@@ -236,12 +240,12 @@ __device__ __forceinline__ void tree_unpack_pair(uint32_t* w, int slot, const fl
 
 template <int RT>
 __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(const TreeParams p) {
-  constexpr int kFRows = 16 * RT;
+  constexpr int kFRows = 16 * RT, kSR = 2 * RT, kOR = RT == 1 ? 4 : 8, kGroups = kFRows / kOR, kShares = 16 / kGroups;
   extern __shared__ __align__(16) float fsm[];
-  float* Qs = fsm;                              // [rows][132]
+  float* Qs = fsm;                              // [rows][164]
   float* Ks = Qs + kFRows * kFStride;           // [64][164]
-  float* Vs = Ks + kFTok * kFTokStride;         // [64][164]
-  float* Ps = Vs + kFTok * kFTokStride;         // [rows][68]
+  float* Vs = Ks + kFTok * kFStride;            // [64][164]
+  float* Ps = Vs + kFTok * kFStride;            // [rows][68]
   float* kn = Ps + kFRows * kFPStride;          // [64] K norm / √d
   float* vn = kn + kFTok;                       // [64] V norm / √d
   float* ok = vn + kFTok;                       // [64] 1: a token of the sequence
@@ -249,7 +253,9 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
   float* rl = rm + kFRows;                      // [64] row sum
   float* rf = rl + kFRows;                      // [64] rescale factor of the tile
   float* cen = rf + kFRows;                     // [2][16]
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int ds = lane & 3, tg = lane >> 2;  // S: quarter of the coordinates, tokens tg + 8k
+  const int cg = tid & 15, rg = (tid >> 4) % kGroups, sh = (tid >> 4) / kGroups;  // O: coordinates, rows, share of the tokens
   const float inv_sd = 0.08838834764831845f;  // 1/√128
   if (tid < 16) {
     cen[tid] = p.kcen[tid];
@@ -268,16 +274,16 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
     __syncthreads();
     for (int e = tid; e < kFRows * 128; e += 256) {
       const int r = e >> 7, rho = row0 + r;
-      Qs[r * kFStride + (e & 127)] =
+      Qs[r * kFStride + (e & 127) + (kFRun - 32) * ((e & 127) >> 5)] =
           r < nrow ? p.qrot[((int64_t)(s.start + rho / p.G) * p.Hq + kvh * p.G + rho % p.G) * 128 + (e & 127)] : 0.f;
     }
     if (tid < kFRows) {
       rm[tid] = -INFINITY;
       rl[tid] = 0.f;
     }
-    float o[RT][8];
+    float o[kOR][8];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
+    for (int i = 0; i < kOR; ++i)
 #pragma unroll
       for (int k = 0; k < 8; ++k) o[i][k] = 0.f;
 
@@ -330,8 +336,8 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
       if (nt <= 0) continue;
       __syncthreads();  // the last tile's operands have been read
       {
-        float4* kd = reinterpret_cast<float4*>(Ks + tok0 * kFTokStride + kFRun * quarter);
-        float4* vd = reinterpret_cast<float4*>(Vs + tok0 * kFTokStride + kFRun * quarter);
+        float4* kd = reinterpret_cast<float4*>(Ks + tok0 * kFStride + kFRun * quarter);
+        float4* vd = reinterpret_cast<float4*>(Vs + tok0 * kFStride + kFRun * quarter);
         if (draft) {
           good = tok0 < nt;
           skn = svn = 0.f;
@@ -369,84 +375,99 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
       }
       if (t2 + 1 < cend) fetch(t2 + 1);
       __syncthreads();
-      // S: rows RT·ty.., tokens tx + 16·k
-      float acc[RT][4];
+      float sc[kSR][2];  // the thread's scores: tokens tg + 8·(2·ds + e)
+      {
+        float acc[kSR][8];
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+        for (int i = 0; i < kSR; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][k] = 0.f;
-#pragma unroll 4
-      for (int d4 = 0; d4 < 32; ++d4) {
-        float4 a[RT], c[4];
+          for (int k = 0; k < 8; ++k) acc[i][k] = 0.f;
+        const float* qrow = Qs + kSR * warp * kFStride + kFRun * ds;
+        const float* krow = Ks + tg * kFStride + kFRun * ds;
+#pragma unroll 2
+        for (int d = 0; d < 32; d += 4) {
+          float4 a[kSR];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) a[i] = *reinterpret_cast<const float4*>(Qs + (RT * ty + i) * kFStride + 4 * d4);
+          for (int i = 0; i < kSR; ++i) a[i] = *reinterpret_cast<const float4*>(qrow + i * kFStride + d);
 #pragma unroll
-        for (int k = 0; k < 4; ++k) c[k] = *reinterpret_cast<const float4*>(Ks + (tx + 16 * k) * kFTokStride + 4 * d4 + (kFRun - 32) * (d4 >> 3));
+          for (int k = 0; k < 8; ++k) {
+            const float4 c = *reinterpret_cast<const float4*>(krow + 8 * k * kFStride + d);
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
+            for (int i = 0; i < kSR; ++i)
+              acc[i][k] = fmaf(a[i].x, c.x, fmaf(a[i].y, c.y, fmaf(a[i].z, c.z, fmaf(a[i].w, c.w, acc[i][k]))));
+          }
+        }
+        const bool up2 = (ds & 2) != 0, up1 = (ds & 1) != 0;
+#pragma unroll
+        for (int i = 0; i < kSR; ++i) {
+          float h[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            acc[i][k] = fmaf(a[i].x, c[k].x, fmaf(a[i].y, c[k].y, fmaf(a[i].z, c[k].z, fmaf(a[i].w, c[k].w, acc[i][k]))));
-      }
-      // scores in base-2 units, masks, the tile's row maxima (16 threads share a row)
-      float f[RT];
+            h[k] = (up2 ? acc[i][k + 4] : acc[i][k]) + __shfl_xor_sync(kFull, up2 ? acc[i][k] : acc[i][k + 4], 2);
 #pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        const int r = RT * ty + i, rho = row0 + r, ti = rho / p.G;
-        float m = -INFINITY;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tok = tx + 16 * k;
-          bool on = r < nrow && ok[tok] != 0.f;
-          if (draft && on) {
-            const int j = t0 + tok;
-            if (p.mask)
-              on = (j >> 5) < p.mask_words &&
-                   ((p.mask[(int64_t)(s.start + ti) * p.mask_words + (j >> 5)] >> (j & 31)) & 1u) != 0u;
-            else
-              on = j <= ti;
-          }
-          acc[i][k] = on ? acc[i][k] * kn[tok] * p.zscale : -INFINITY;
-          m = fmaxf(m, acc[i][k]);
+          for (int k = 0; k < 2; ++k)
+            sc[i][k] = (up1 ? h[k + 2] : h[k]) + __shfl_xor_sync(kFull, up1 ? h[k] : h[k + 2], 1);
         }
+      }
+      // scores in base-2 units, masks, the tile's row maxima and sums (a warp has all of a row)
+      const int tk = tg + 16 * ds;
+      const float k0 = kn[tk] * p.zscale, k1 = kn[tk + 8] * p.zscale, w0 = vn[tk], w1 = vn[tk + 8];
+      const bool on0 = ok[tk] != 0.f, on1 = ok[tk + 8] != 0.f;
 #pragma unroll
-        for (int off = 8; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
+      for (int i = 0; i < kSR; ++i) {
+        const int r = kSR * warp + i;
+        bool s0 = on0 && r < nrow, s1 = on1 && r < nrow;
+        if (draft && r < nrow) {
+          const int ti = (row0 + r) / p.G, j0 = t0 + tk, j1 = j0 + 8;
+          if (p.mask) {
+            const uint32_t* m = p.mask + (int64_t)(s.start + ti) * p.mask_words;
+            s0 = s0 && (j0 >> 5) < p.mask_words && ((m[j0 >> 5] >> (j0 & 31)) & 1u) != 0u;
+            s1 = s1 && (j1 >> 5) < p.mask_words && ((m[j1 >> 5] >> (j1 & 31)) & 1u) != 0u;
+          } else {
+            s0 = s0 && j0 <= ti;
+            s1 = s1 && j1 <= ti;
+          }
+        }
+        const float z0 = s0 ? sc[i][0] * k0 : -INFINITY, z1 = s1 ? sc[i][1] * k1 : -INFINITY;
+        float m = fmaxf(z0, z1);
+#pragma unroll
+        for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, off));
         const float old = rm[r];
         __syncwarp();
         const float nm = fmaxf(old, m), use = nm == -INFINITY ? 0.f : nm;
-        f[i] = old == -INFINITY ? 0.f : exp2f(old - use);
-        float l = 0.f;
+        const float f = old == -INFINITY ? 0.f : exp2f(old - use);
+        const float p0 = exp2f(z0 - use), p1 = exp2f(z1 - use);
+        Ps[r * kFPStride + tk] = p0 == 0.f ? 0.f : p0 * w0;
+        Ps[r * kFPStride + tk + 8] = p1 == 0.f ? 0.f : p1 * w1;
+        float l = p0 + p1;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float pr = exp2f(acc[i][k] - use);
-          l += pr;
-          const int tok = tx + 16 * k;
-          Ps[r * kFPStride + tok] = pr == 0.f ? 0.f : pr * vn[tok];
-        }
-#pragma unroll
-        for (int off = 8; off; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
-        if (tx == 0) {
+        for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(kFull, l, off);
+        if (lane == 0) {
           rm[r] = nm;
-          rl[r] = rl[r] * f[i] + l;
+          rl[r] = rl[r] * f + l;
+          rf[r] = f;
         }
       }
       __syncthreads();
-      // O: rows RT·ty.., coordinates 4·tx.. and 64 + 4·tx..
-      const float* vrow = Vs + kFRun * (tx >> 3) + 4 * (tx & 7);
+      // O: rows kOR·rg.., coordinates 4·cg.. and 64 + 4·cg.., a share of the tokens
+      const float* vrow = Vs + kFRun * (cg >> 3) + 4 * (cg & 7);
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int i = 0; i < kOR; ++i) {
+        const float f = rf[kOR * rg + i];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[i][k] *= f[i];
-      for (int t4 = 0; t4 < kFTok / 4; ++t4) {
-        float4 pr[RT];
+        for (int k = 0; k < 8; ++k) o[i][k] *= f;
+      }
+#pragma unroll 1
+      for (int t4 = sh * (kFTok / kShares); t4 < (sh + 1) * (kFTok / kShares); t4 += 4) {
+        float4 pr[kOR];
 #pragma unroll
-        for (int i = 0; i < RT; ++i) pr[i] = *reinterpret_cast<const float4*>(Ps + (RT * ty + i) * kFPStride + 4 * t4);
+        for (int i = 0; i < kOR; ++i) pr[i] = *reinterpret_cast<const float4*>(Ps + (kOR * rg + i) * kFPStride + t4);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float4 v0 = *reinterpret_cast<const float4*>(vrow + (4 * t4 + e) * kFTokStride);
-          const float4 v1 = *reinterpret_cast<const float4*>(vrow + (4 * t4 + e) * kFTokStride + 2 * kFRun);
+          const float4 v0 = *reinterpret_cast<const float4*>(vrow + (t4 + e) * kFStride);
+          const float4 v1 = *reinterpret_cast<const float4*>(vrow + (t4 + e) * kFStride + 2 * kFRun);
 #pragma unroll
-          for (int i = 0; i < RT; ++i) {
+          for (int i = 0; i < kOR; ++i) {
             const float x = e == 0 ? pr[i].x : (e == 1 ? pr[i].y : (e == 2 ? pr[i].z : pr[i].w));
             o[i][0] = fmaf(x, v0.x, o[i][0]);
             o[i][1] = fmaf(x, v0.y, o[i][1]);
@@ -460,19 +481,46 @@ __global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(c
         }
       }
     }
+    // the shares of the tokens meet in the place of K̂ and V̂, then the records
     __syncthreads();
+    float4* red = reinterpret_cast<float4*>(Ks);  // [shares - 1][rows][coordinates]
+    if (sh > 0) {
 #pragma unroll
-    for (int i = 0; i < RT; ++i) {
-      const int r = RT * ty + i, rho = row0 + r;
-      if (r < nrow) {
-        float* rec = first == 0 ? p.rec + ((int64_t)(s.start + rho / p.G) * p.Hq + kvh * p.G + rho % p.G) * kTreeRec
-                                : p.crec + ((int64_t)blockIdx.x * p.rows + r) * kTreeRec;
-        if (tx == 0) {
-          rec[0] = rm[r];
-          rec[1] = rl[r];
+      for (int i = 0; i < kOR; ++i) {
+        float4* at = red + ((sh - 1) * kFRows + kOR * rg + i) * 32 + cg;
+        at[0] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
+        at[16] = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+      }
+    }
+    __syncthreads();
+    if (sh == 0) {
+#pragma unroll
+      for (int i = 0; i < kOR; ++i) {
+        const int r = kOR * rg + i, rho = row0 + r;
+        if (r < nrow) {
+          float4 x = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]), y = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+#pragma unroll
+          for (int h = 1; h < kShares; ++h) {
+            const float4* at = red + ((h - 1) * kFRows + r) * 32 + cg;
+            const float4 u = at[0], v = at[16];
+            x.x += u.x;
+            x.y += u.y;
+            x.z += u.z;
+            x.w += u.w;
+            y.x += v.x;
+            y.y += v.y;
+            y.z += v.z;
+            y.w += v.w;
+          }
+          float* rec = first == 0 ? p.rec + ((int64_t)(s.start + rho / p.G) * p.Hq + kvh * p.G + rho % p.G) * kTreeRec
+                                  : p.crec + ((int64_t)blockIdx.x * p.rows + r) * kTreeRec;
+          if (cg == 0) {
+            rec[0] = rm[r];
+            rec[1] = rl[r];
+          }
+          *reinterpret_cast<float4*>(rec + 4 + 4 * cg) = x;
+          *reinterpret_cast<float4*>(rec + 68 + 4 * cg) = y;
         }
-        *reinterpret_cast<float4*>(rec + 4 + 4 * tx) = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        *reinterpret_cast<float4*>(rec + 68 + 4 * tx) = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
       }
     }
     u += last - first;
