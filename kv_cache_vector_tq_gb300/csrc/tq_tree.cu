@@ -208,8 +208,13 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
 //              the shares are joined once, at the segment's end.
 // The next tile's packed words are loaded into registers before this one's
 // products; a thread unpacks 32 coordinates of a token, whole words in both
-// layouts, against 16 centroids in 16 banks.  16 rows (RT = 1) where the mean
-// sequence has no more, then with two CTAs an SM; else 64 (RT = 4).
+// layouts, against 16 centroids in 16 banks.  16, 32 or 64 rows (RT = 1, 2, 4) by
+// the mean sequence, the smaller two with two CTAs an SM (32 rows for 256 of a
+// group: 4.76 ms against 4.26 with 64, the tiles being unpacked twice as often).
+// Calls: one token of 32 heads over 16384 cached (b = 4) 69 us; 8 requests of up to
+// 16 drafted over 8191 453 us; 32 drafted of 64 heads over 131072 (b = 3) 4.26 ms,
+// 32 TFLOP/s: bound by issue and shared reads about equally (0.58 a clock, reads
+// in two thirds of them).
 // Runs of 32 coordinates lie 40 words apart and rows of Q, K̂, V̂ 164, so that the
 // eight lanes of a 16-byte access meet no bank twice.
 constexpr int kFTok = 64, kFStride = 164, kFPStride = 68, kFRun = 40;
@@ -239,8 +244,8 @@ __device__ __forceinline__ void tree_unpack_pair(uint32_t* w, int slot, const fl
 }
 
 template <int RT>
-__global__ void __launch_bounds__(256, RT == 1 ? 2 : 1) tree_attend_f32_kernel(const TreeParams p) {
-  constexpr int kFRows = 16 * RT, kSR = 2 * RT, kOR = RT == 1 ? 4 : 8, kGroups = kFRows / kOR, kShares = 16 / kGroups;
+__global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(const TreeParams p) {
+  constexpr int kFRows = 16 * RT, kSR = 2 * RT, kOR = RT == 4 ? 8 : 4, kGroups = kFRows / kOR, kShares = 16 / kGroups;
   extern __shared__ __align__(16) float fsm[];
   float* Qs = fsm;                              // [rows][164]
   float* Ks = Qs + kFRows * kFStride;           // [64][164]
@@ -719,7 +724,7 @@ static cudaError_t attend_f32(const TreeParams& p, cudaStream_t st) {
   return tree_launch(tree_attend_f32_kernel<RT>, p.ctas, 256, kFSmem<RT>, st, p);
 }
 cudaError_t tree_attend_f32(const TreeParams& p, cudaStream_t st) {
-  return p.rows == 16 ? attend_f32<1>(p, st) : attend_f32<4>(p, st);
+  return p.rows == 16 ? attend_f32<1>(p, st) : p.rows == 32 ? attend_f32<2>(p, st) : attend_f32<4>(p, st);
 }
 
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R) { return tree_ws(B, Hq, Hkv, R).total; }
@@ -778,8 +783,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   // tensor-core kernel does
   const bool tc = a.dtype != TQ_F32;
   p.rows = tree_umma_rows(a.R, a.B, p.G);
-  if (!tc && p.rows > 16) p.rows = 64;
-  p.ctas = num_sms() * (!tc && p.rows == 16 ? 2 : 1);
+  p.ctas = num_sms() * (tc || p.rows == 64 ? 1 : 2);  // as many as fit at once
   p.klut = kc.lut;
   p.vlut = vc.lut;
   bool same = kc.b_mse == vc.b_mse && kc.alpha == vc.alpha;

@@ -450,6 +450,14 @@ def test_tree_many_tiles_with_two_codebooks(dtype):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("kb,vb", [(1, 3), (2, 4), (3, 2), (4, 1)])
+@pytest.mark.parametrize("new", [[4, 3, 1], [8, 5, 6], [16, 20, 9]])
+def test_tree_rows_of_a_tile(dtype, kb, vb, new):
+    """Tiles of 16, 32 and 64 rows (four query heads a KV head), each with every width of codes; sequences past one tile."""
+    tree_case(dtype, kb, vb, 8, 2, 16, [777, 64, 3001], new, "tree")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_tree_masks_and_empty_rows(dtype):
     """Random masks, rows that see nothing, drafted tokens past the mask's words."""
     tree_case(dtype, 4, 4, 8, 2, 16, [40, 0], [50, 33], "random")
