@@ -605,6 +605,34 @@ def test_tree_over_hadamard_rotated_caches():
         assert (out.float() - want).norm() <= (4e-3 + 2 * torch.finfo(dtype).eps) * want.norm()
 
 
+def test_calls_at_once_on_two_streams():
+    """Attention on two streams (a workspace each, one context pair) beside appends to a third cache: as one by one."""
+    a = make_tree(torch.bfloat16, 4, 4, 32, 8, 16, [3000, 517, 2048], [7, 16, 1], 3)
+    b = make_tree(torch.float16, 4, 4, 16, 2, 64, [9000, 33], [12, 30], 4)
+    x = torch.randn(500, 8, D, device="cuda", generator=gen(5)).half()
+    slots = torch.randperm(1024, device="cuda", generator=gen(6))[:500]
+    codes = [tq.CodeSet(ctx(4), 1024 * 8, tq.TQ_LAYOUT_PAIR) for _ in range(2)]
+    want = run_tree(a, 4, 4, 16), run_tree(b, 4, 4, 64)
+    tq.tq_encode_slots(ctx(4), x, slots, 16, codes[0])
+    ws = [torch.zeros(tq.tq_tree_attention_workspace_size(ctx(4), s["lens"].numel(), s["q"].shape[1], s["k"].shape[1], s["q"].shape[0]) // 4 + 4,
+                      device="cuda") for s in (a, b)]
+    outs = [[torch.zeros_like(w) for _ in range(8)] for w in want]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for k in range(8):
+        with torch.cuda.stream(streams[0]):
+            run_tree(a, 4, 4, 16, out=outs[0][k], ws=ws[0])
+        with torch.cuda.stream(streams[1]):
+            run_tree(b, 4, 4, 64, out=outs[1][k], ws=ws[1])
+        with torch.cuda.stream(streams[2]):
+            tq.tq_encode_slots(ctx(4), x, slots, 16, codes[1])
+    torch.cuda.synchronize()
+    for k in range(8):
+        assert torch.equal(outs[0][k], want[0]) and torch.equal(outs[1][k], want[1])
+    assert torch.equal(codes[0].codes, codes[1].codes) and torch.equal(codes[0].norm, codes[1].norm)
+    assert ctx(4).poll() == tq.TQ_OK
+
+
 def test_tree_is_deterministic():
     s = make_tree(torch.float16, 4, 4, 32, 8, 16, [3000, 100, 2500], [16, 3, 9])
     first = run_tree(s, 4, 4, 16)
