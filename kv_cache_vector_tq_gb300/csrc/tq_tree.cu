@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(256, 2) tree_join_kernel(const TreeParams p, c
   // Where a row's records are, from what was laid out before the attention kernel
   // could begin: found before the wait for it.  (All its CTAs had waited for the
   // rotation's end when this kernel was let in.)
-  const int64_t live = (int64_t)min(max((int64_t)p.row_start[p.B], (int64_t)0), p.R) * p.Hq;
+  const int64_t live = (int64_t)min(max((int64_t)__ldcg(p.row_start + p.B), (int64_t)0), p.R) * p.Hq;
   const int64_t units = __ldcg(&p.seq[p.B].unit);
   const int64_t step = (int64_t)p.rows * kTreeRec;
   struct Row {

@@ -97,13 +97,14 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
 // First unit of CTA c of n.
 __device__ __forceinline__ int64_t tree_cut(int64_t c, int64_t units, int64_t n) { return c * units / n; }
 
-// Largest index i in [0, n) with a[i] <= x (a ascending, a[0] <= x).
+// Largest index i in [0, n) with a[i] <= x (a ascending, a[0] <= x).  Past L1:
+// the join asks before it has waited for the kernel ahead.
 template <typename T>
 __device__ __forceinline__ int tree_find(const T* a, int n, T x) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a[mid] <= x)
+    if (__ldcg(a + mid) <= x)
       lo = mid;
     else
       hi = mid - 1;
