@@ -209,12 +209,13 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
 // The next tile's packed words are loaded into registers before this one's
 // products; a thread unpacks 32 coordinates of a token, whole words in both
 // layouts, against 16 centroids in 16 banks.  16, 32 or 64 rows (RT = 1, 2, 4) by
-// the mean sequence, the smaller two with two CTAs an SM (32 rows for 256 of a
-// group: 4.76 ms against 4.26 with 64, the tiles being unpacked twice as often).
+// the mean sequence, the smaller two with two CTAs an SM (32 rows for the 256
+// of a long group: 4.76 ms against 4.26, every tile being unpacked twice as often).
 // Calls: one token of 32 heads over 16384 cached (b = 4) 69 us; 8 requests of up to
-// 16 drafted over 8191 453 us; 32 drafted of 64 heads over 131072 (b = 3) 4.26 ms,
-// 32 TFLOP/s: bound by issue and shared reads about equally (0.58 a clock, reads
-// in two thirds of them).
+// 16 drafted over 8191 438 us; 32 drafted of 64 heads over 131072 (b = 3) 4.10 ms,
+// 34 TFLOP/s.  Bound by no one thing: issue 0.58 a clock and quarter, shared memory
+// two thirds busy; half the shared reads or twice the warps gained under 3%, pairs
+// of products in one instruction for O (fma2) 4%.
 // Runs of 32 coordinates lie 40 words apart and rows of Q, K̂, V̂ 164, so that the
 // eight lanes of a 16-byte access meet no bank twice.
 constexpr int kFTok = 64, kFStride = 164, kFPStride = 68, kFRun = 40;
@@ -241,6 +242,13 @@ __device__ __forceinline__ void tree_unpack_pair(uint32_t* w, int slot, const fl
 #pragma unroll
   for (int i = 0; i < 2 * B; ++i) w[i] = __funnelshift_r(w[i], i + 1 < 2 * B ? w[i + 1] : 0u, slot * B);
   tree_unpack<B, 2 * B>(w, cen, dst);
+}
+
+// Two fp32 products and sums in one instruction.
+__device__ __forceinline__ void fma2(float2& d, const float2& a, const float2& b) {
+  uint64_t x = *reinterpret_cast<uint64_t*>(&d);
+  asm("fma.rn.f32x2 %0, %1, %2, %0;\n" : "+l"(x) : "l"(*reinterpret_cast<const uint64_t*>(&a)), "l"(*reinterpret_cast<const uint64_t*>(&b)));
+  d = *reinterpret_cast<float2*>(&x);
 }
 
 template <int RT>
@@ -286,11 +294,11 @@ __global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(c
       rm[tid] = -INFINITY;
       rl[tid] = 0.f;
     }
-    float o[kOR][8];
+    float2 o[kOR][4];
 #pragma unroll
     for (int i = 0; i < kOR; ++i)
 #pragma unroll
-      for (int k = 0; k < 8; ++k) o[i][k] = 0.f;
+      for (int k = 0; k < 4; ++k) o[i][k] = make_float2(0.f, 0.f);
 
     // this thread's token of a tile and 32 of its coordinates: packed words and norms
     const int tok0 = tid >> 2, quarter = tid & 3;
@@ -460,7 +468,10 @@ __global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(c
       for (int i = 0; i < kOR; ++i) {
         const float f = rf[kOR * rg + i];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) o[i][k] *= f;
+        for (int k = 0; k < 4; ++k) {
+          o[i][k].x *= f;
+          o[i][k].y *= f;
+        }
       }
 #pragma unroll 1
       for (int t4 = sh * (kFTok / kShares); t4 < (sh + 1) * (kFTok / kShares); t4 += 4) {
@@ -474,14 +485,11 @@ __global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(c
 #pragma unroll
           for (int i = 0; i < kOR; ++i) {
             const float x = e == 0 ? pr[i].x : (e == 1 ? pr[i].y : (e == 2 ? pr[i].z : pr[i].w));
-            o[i][0] = fmaf(x, v0.x, o[i][0]);
-            o[i][1] = fmaf(x, v0.y, o[i][1]);
-            o[i][2] = fmaf(x, v0.z, o[i][2]);
-            o[i][3] = fmaf(x, v0.w, o[i][3]);
-            o[i][4] = fmaf(x, v1.x, o[i][4]);
-            o[i][5] = fmaf(x, v1.y, o[i][5]);
-            o[i][6] = fmaf(x, v1.z, o[i][6]);
-            o[i][7] = fmaf(x, v1.w, o[i][7]);
+            const float2 xx = make_float2(x, x);
+            fma2(o[i][0], xx, make_float2(v0.x, v0.y));
+            fma2(o[i][1], xx, make_float2(v0.z, v0.w));
+            fma2(o[i][2], xx, make_float2(v1.x, v1.y));
+            fma2(o[i][3], xx, make_float2(v1.z, v1.w));
           }
         }
       }
@@ -493,8 +501,8 @@ __global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(c
 #pragma unroll
       for (int i = 0; i < kOR; ++i) {
         float4* at = red + ((sh - 1) * kFRows + kOR * rg + i) * 32 + cg;
-        at[0] = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]);
-        at[16] = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+        at[0] = make_float4(o[i][0].x, o[i][0].y, o[i][1].x, o[i][1].y);
+        at[16] = make_float4(o[i][2].x, o[i][2].y, o[i][3].x, o[i][3].y);
       }
     }
     __syncthreads();
@@ -503,7 +511,7 @@ __global__ void __launch_bounds__(256, RT == 4 ? 1 : 2) tree_attend_f32_kernel(c
       for (int i = 0; i < kOR; ++i) {
         const int r = kOR * rg + i, rho = row0 + r;
         if (r < nrow) {
-          float4 x = make_float4(o[i][0], o[i][1], o[i][2], o[i][3]), y = make_float4(o[i][4], o[i][5], o[i][6], o[i][7]);
+          float4 x = make_float4(o[i][0].x, o[i][0].y, o[i][1].x, o[i][1].y), y = make_float4(o[i][2].x, o[i][2].y, o[i][3].x, o[i][3].y);
 #pragma unroll
           for (int h = 1; h < kShares; ++h) {
             const float4* at = red + ((h - 1) * kFRows + r) * 32 + cg;
