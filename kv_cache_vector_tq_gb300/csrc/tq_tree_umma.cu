@@ -834,12 +834,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           if (!ok) break;
           if (draft) {
             const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int k = 32 * e + lane;
               reinterpret_cast<float*>(nb)[k] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
             }
             if (lane == 0 && !is_v) ms.valid[ns] = 0xFFu;
+            fence_proxy_async();  // before the bulk copy that writes the slot next
             __syncwarp();
             if (lane == 0) mbar_arrive(&ms.n_full[ns]);
             continue;

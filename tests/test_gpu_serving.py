@@ -585,6 +585,12 @@ def test_tree_waits_are_bounded():
         assert torch.equal(out, run_tree(s, 4, 4, 16))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_tree_factors_of_drafted_tiles_before_copied_norms(dtype):
+    """A CTA's tiles of many short sequences: the place of a drafted tile's factors takes copied norms soon after."""
+    tree_case(dtype, 4, 4, 8, 8, 16, [130 + 2 * k for k in range(64)], [1 + k % 4 for k in range(64)], "tree")
+
+
 def test_tree_over_hadamard_rotated_caches():
     """A context with the randomized Hadamard rotation: the same answer as the decode call's over the same cache."""
     c = tq.Context(D, 4, tq.TQ_MSE, tq.TQ_ROT_HADAMARD, synth.hadamard_signs(3, D))
