@@ -224,9 +224,8 @@ def prepare(case, seed):
         s |= {"len": lens, "new": new, "held": held.int(), "table": table.int().contiguous(), "ring": ring, "rows": rows + rows // 8,
               "state": torch.tensor([0, total - used], dtype=torch.int64, device="cuda")}
         if own:
-            n = s["rows"]
-            z = lambda m, t: torch.empty(m, dtype=t, device="cuda")  # noqa: E731
-            s["o"] = (z(c["batch"], torch.int32), z(2, torch.int64), z(c["batch"] + 1, torch.int32), z(n, torch.int64), z(n, torch.int32))
+            import kv_cache_vector_tq_gb300 as tq
+            tq.lib()
         return s
     if c["op"] == "norm_rope":
         t, n, dim = TYPES[c["type"]], c["tokens"], c["dim"]
@@ -247,15 +246,16 @@ def prepare(case, seed):
     if own:
         import kv_cache_vector_tq_gb300 as tq
 
+        # what a model's loading makes once for each layer: the device tables of its rotation and codebooks (1 to 5 ms each,
+        # whatever is cached or asked later), nothing of a call's data; the rotation is the seed's here so that inputs differ
         def context(b):
-            cb = tq.tq_codebook_build(D, b)
-            for k in range(1 << b):
-                cb.centroid[k] = centroids(b)[k]
-            for k in range((1 << b) - 1):
-                cb.threshold[k] = thresholds(b)[k]
+            cb = tq.Codebook(d=D, b=b)
+            cb.centroid[:1 << b] = centroids(b).tolist()
+            cb.threshold[:(1 << b) - 1] = thresholds(b).tolist()
             return tq.Context(D, b, tq.TQ_MSE, tq.TQ_ROT_DENSE, pi, codebook=cb)
 
-        s["ctx"] = context(c["kbits"]), context(c["vbits"])
+        kctx = context(c["kbits"])
+        s["ctx"] = kctx, kctx if c["vbits"] == c["kbits"] else context(c["vbits"])
     lens = _lengths(c, g)
     if c["op"] == "append":
         t = TYPES[c["type"]]
@@ -306,9 +306,8 @@ def prepare(case, seed):
             s["c" + name] = cs
         else:
             s["c" + name] = codes, norm
-    if own:
-        s["out"] = torch.empty(rows, hq, D, device="cuda", dtype=t)
-        s["ws"] = torch.zeros(tq.tq_tree_attention_workspace_size(s["ctx"][0], c["batch"], hq, kv, rows) // 4 + 4, device="cuda")
+    if own:  # the workspace that a program keeps; its contents do not matter
+        s["ws"] = torch.empty(tq.tq_tree_attention_workspace_size(s["ctx"][0], c["batch"], hq, kv, rows) // 4 + 4, device="cuda")
     return s
 
 
@@ -432,8 +431,13 @@ def _tree(s):
 # ------------------------------------------------------------------ one pass
 def run(state):
     s, c = state, state["case"]
-    if own:
+    if own:  # outputs are allocated in the pass, as the plain form's are
         import kv_cache_vector_tq_gb300 as tq
+        if c["op"] == "tables":
+            n, i32, i64 = s["rows"], torch.int32, torch.int64
+            s = s | {"o": [torch.empty(m, dtype=t, device="cuda") for m, t in ((c["batch"], i32), (2, i64), (c["batch"] + 1, i32), (n, i64), (n, i32))]}
+        elif c["op"] == "tree":
+            s = s | {"out": torch.empty_like(s["q"])}
     if c["op"] == "tables":
         if not own:
             return _tables(s)
