@@ -526,6 +526,7 @@ tq_status tq_ctx_create(int d, int b, int mode, int rot_kind, const double* h_ro
         if (x == 0.0) continue;
         double r = std::fabs((double)h_val(h_bits((float)x)) - x) / std::fabs(x);
         worst = std::max(worst, r);
+        if (worst >= best) break;  // this a is not the best
       }
       if (worst < best) {
         best = worst;
