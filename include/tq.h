@@ -445,7 +445,9 @@ tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64
  * BF16 inputs take the tensor cores: cached values are the codebook's α·c
  * rounded to fp16, the drafted rows Πk, Πv one fp16 each, q and the weights two
  * fp16 terms (F16) or one (BF16), sums in fp32; the error is then of the size of
- * the output type's own rounding.
+ * the output type's own rounding.  Norms of values may be anything from 2^-80 (below it
+ * they lose bits, then count as zero) to the end of fp32's range; a drafted row
+ * whose norm passes that counts as one with a NaN in it.
  * d_ws      workspace of tq_tree_attention_workspace_size bytes (16-byte
  *           aligned; its contents do not matter).  Calls that share one must be
  *           ordered on one stream; captured graphs that may run at the same time

@@ -183,7 +183,8 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
       const float z = bad ? 0.f : y[v] * sc;
       if (j == 0) {
         const uint32_t r = (uint32_t)at / (uint32_t)heads;
-        fac[kind == 0 ? at : (int64_t)((uint32_t)at - r * heads) * p.R + r] = bad ? NAN : one / sc;
+        fac[kind == 0 ? at : (int64_t)((uint32_t)at - r * heads) * p.R + r] =
+            bad ? NAN : TC && m == 0.f ? 0.f : one / sc;  // zeros have no say in anyone's scaling
       }
       if constexpr (TC) {
         __half* d = reinterpret_cast<__half*>(dst) + at * (kind == 0 ? 256 : 128) + j;
@@ -798,7 +799,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   for (int k = 0; same && k < (1 << kc.b_mse); ++k) same = kc.cen[k] == vc.cen[k];
   p.same_lut = same;
   p.kone = tc ? kc.sqrt_d * kc.alpha : 1.f;
-  p.vone = tc ? vc.sqrt_d * vc.alpha : 1.f;
+  p.vone = tc ? vc.sqrt_d * vc.alpha * kTreeVDown : 1.f;
   p.zfold = p.zscale / p.kone;
   p.ofold = 1.f / p.vone;
   p.wait_limit = kc.wait_limit;

@@ -27,6 +27,9 @@ namespace tq {
 constexpr int kTreeTok = 128;       // tokens per unit
 constexpr int kTreeRec = 132;       // floats per record: m, l, 2 pad, acc[128]
 constexpr float kTreeLog2e = 1.4426950408889634f;
+// Tensor-core path: values are taken 2^20 smaller, so that weights, which hold the
+// inverse of a value's magnitude, leave fp32's range at neither end of it.
+constexpr float kTreeVDown = 9.5367431640625e-07f;
 
 // A sequence as the kernels see it: bad offsets and lengths are cut to what
 // the buffers hold.  unit: its first unit.
@@ -64,8 +67,8 @@ struct TreeParams {
   const uint32_t *klut, *vlut;  // pair tables α·c
   int same_lut;
   float zfold;          // scale·log2(e)/(√d·α_K)
-  float kone, vone;     // factor of a drafted row of scale 1: √d·α (fp32 path: 1)
-  float ofold;          // 1/(√d·α_V) (fp32 path: 1)
+  float kone, vone;     // factor of a drafted row of scale 1: √d·α, v's times kTreeVDown (fp32 path: 1)
+  float ofold;          // 1/vone
   uint32_t wait_limit;
   void* out;
   int* status;

@@ -15,8 +15,9 @@
 // the pairs along K of the two products.  The norms act on scores and weights
 // in fp32, so no rounding depends on them.  M (per row) is a running maximum of
 // log2 of weight times s_v, raised only before a weight passes 2^14 (the sums
-// are then rescaled, which is rare); with s_v inside it, values of any
-// magnitude stay inside fp16.
+// are then rescaled, which is rare); with s_v inside it, weights stay inside fp16
+// for norms from 2^-80 to the end of fp32's range.  The weights without s_v, of
+// which the sum is taken, are then between 2^-104 and 2^104 where they matter.
 // Rounding of the operands: for fp16 outputs Q̂ and P are split into two fp16
 // terms each (two products), since one rounding of either costs as much as the
 // output's own; bf16 outputs round eight times coarser and take one term.
@@ -53,6 +54,7 @@ constexpr uint32_t kLandPolls = 1u << 14;  // a millisecond or more for copies u
 // Tensor memory columns: Sᵀ x 2, Oᵀ, the rows' sums of weights per token lane, K̂ x 2, V̂ᵀ x 2
 constexpr uint32_t kColO = 128, kColL = 192, kColK = 256, kColV = 384;
 constexpr float kLazyUp = 14.f;            // raise M before a weight passes 2^14
+constexpr float kLogLo = -90.f, kLogHi = 110.f;  // log2 of s_v·2^-20 as M takes it
 constexpr float kShift = 6.f;              // a fresh maximum sits at weight 2^6: small weights keep their bits longer
 
 // Shared memory
@@ -444,9 +446,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         const uint32_t chunks = ms.valid[ns];
         const bool here = tok < nt && ((chunks >> (tok >> 4)) & 1u);  // this token is there
         const bool whole = nt == kTreeTok && chunks == 0xFFu && !draft;
-        const float kn = nrm[tok], vn = nrm[128 + tok];
-        // 2^lv > vn, kept within 2^±100
-        const float lv = fminf(fmaxf((float)((int)((__float_as_uint(vn) >> 23) & 255u) - 126), -100.f), 100.f);
+        const float kn = nrm[tok], vn = draft ? nrm[128 + tok] : nrm[128 + tok] * kTreeVDown;
+        // 2^lv > vn.  The upper end is past every finite value; below the lower one
+        // a weight is smaller than it might be, and the sum of weights has 2^23 tokens' room
+        const float lv = fminf(fmaxf((float)((int)((__float_as_uint(vn) >> 23) & 255u) - 126), kLogLo), kLogHi);
         const float ck = ct * kn;
         // drafted tokens: bit `lane` of a row's mask word for this warp's 32
         // tokens; lane n holds the word of row n0 + n

@@ -508,6 +508,24 @@ def test_tree_large_and_small_values(dtype):
         assert (off <= bound).all(), (scale, float((off / bound).max()))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("drafted,cached", [(1e36, 1.0), (1e33, 1.0), (1.0, 1e35), (1e36, 1e35), (1e-24, 1e-24), (1e-24, 1.0)])
+def test_tree_values_of_any_magnitude(dtype, drafted, cached):
+    """Drafted and cached values from 1e-24 to 1e36, together and apart; a drafted row of zeros among them."""
+    s = make_tree(dtype, 4, 4, 4, 2, 16, [300, 0, 40], [6, 5, 3], outliers=False)
+    s["v"] = (s["v"].clamp(-2, 2).double() * drafted).to(dtype)
+    s["v"][1] = 0
+    s["V"].norm *= cached
+    got = run_tree(s, 4, 4, 16)
+    want, size, top = tree_plain(s["q"], s["k"], s["v"], s["start"], None, s["K"], s["V"], s["lens"], s["table"], 16, 2, 1 / math.sqrt(D), 4, 4)
+    # as in check_tree, row by row
+    rel = 8 * 2.0 ** -11 * max(top, 1) / math.sqrt(D) + 2 * 2.0 ** -11 if dtype != torch.float32 else 8 * 2.0 ** -24 * 16 * max(top, 1)
+    fi = torch.finfo(dtype)
+    bound = rel * size + fi.eps / 2 * want.norm(dim=-1) + fi.tiny * fi.eps * math.sqrt(D)
+    off = (got.double() - want).norm(dim=-1)
+    assert (off <= bound).all(), float((off / bound).max())
+
+
 def test_tree_rows_past_the_end_and_strides():
     """Rows behind the last sequence are left; q, k, v may be slices of one projection; bad offsets are cut."""
     s = make_tree(torch.bfloat16, 4, 4, 8, 2, 16, [100, 50], [3, 4])
