@@ -403,13 +403,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         ms.ti[tid] = ti;
       }
       bar_softmax();
-      // One factor for all rows of the tile: the largest; the rows are scaled down
-      // to it by powers of two.  (Absolute errors of scores stay below 2^-36 of
-      // the tile's largest, however far the rows are apart.)
-      float ct = fmaxf(ms.c[lane & (N - 1)], ms.c[(lane + 32) & (N - 1)]);
+      // Rows within 2^13 of the tile's largest factor are scaled down to it by powers
+      // of two and share it: what fp16 drops is below 2^-22 of a row's largest
+      // entry.  Where one is further below (another row is huge, it is tiny), every
+      // row keeps its own, two instructions more a score (all tiles so: 338 -> 351 us
+      // for 32 tokens of 64 heads over 131072).  Factor 0: no row, a row of zeros or
+      // one that is not a number.
+      const float c0 = ms.c[lane & (N - 1)], c1 = ms.c[(lane + 32) & (N - 1)];
+      float ct = fmaxf(c0, c1);
 #pragma unroll
       for (int o = 16; o; o >>= 1) ct = fmaxf(ct, __shfl_xor_sync(kFull, ct, o));
-      const float inv_ct = ct > 0.f ? 1.f / ct : 0.f;
+      const float least = ct * 1.220703125e-4f;  // 2^-13
+      const bool shared_c = __all_sync(kFull, (c0 == 0.f || c0 >= least) && (c1 == 0.f || c1 >= least));
+      const float inv_ct = shared_c && ct > 0.f ? 1.f / ct : 0.f;
       // 16-byte pieces: 16 of the leading part and 16 of the remainder per row
 #pragma unroll 4
       for (int e = tid; e < N * (SPLIT ? 32 : 16); e += 32 * kSoft) {
@@ -417,10 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         const int vec = ms.vec[n];
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (vec >= 0) x = *(reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.qrot) + (int64_t)vec * 256) + k);
-        const __half2 sc = __float2half2_rn(ms.c[n] * inv_ct);  // a power of two up to rounding: made one by fp16's
-        __half2* h = reinterpret_cast<__half2*>(&x);
+        if (shared_c) {
+          const __half2 sc = __float2half2_rn(ms.c[n] * inv_ct);  // a power of two up to rounding: made one by fp16's
+          __half2* h = reinterpret_cast<__half2*>(&x);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) h[q] = __hmul2(h[q], sc);
+          for (int q = 0; q < 4; ++q) h[q] = __hmul2(h[q], sc);
+        }
         *reinterpret_cast<uint4*>(smem + kQ + part * kQPart + (c >> 3) * (N * 128) + n * 128 + (((c & 7) ^ (n & 7)) << 4)) = x;
       }
       fence_proxy_async();
@@ -450,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         // 2^lv > vn.  The upper end is past every finite value; below the lower one
         // a weight is smaller than it might be, and the sum of weights has 2^23 tokens' room
         const float lv = fminf(fmaxf((float)((int)((__float_as_uint(vn) >> 23) & 255u) - 126), kLogLo), kLogHi);
-        const float ck = ct * kn;
+        const float ck = shared_c ? ct * kn : kn;
         // drafted tokens: bit `lane` of a row's mask word for this warp's 32
         // tokens; lane n holds the word of row n0 + n
         uint32_t mw = 0u;
@@ -467,6 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           const bool named = !draft || ((__shfl_sync(kFull, mw, n) >> lane) & 1u);
           return here && named;
         };
+        auto scores = [&](uint32_t(&s)[HN]) {
+          tmem_ld_n(tS, s);
+          wait_ld(s);
+          if (!shared_c) {
+#pragma unroll
+            for (int e = 0; e < HN; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * ms.c[n0 + e]);
+          }
+        };
         // weights with the M there is; should one pass the limit (M = -inf, a
         // row's first token, does), M is raised and they are computed again
         float pr[HN];
@@ -474,8 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           float top = -INFINITY;
           {
             uint32_t s[HN];
-            tmem_ld_n(tS, s);
-            wait_ld(s);
+            scores(s);
 #pragma unroll
             for (int e = 0; e < HN; e += 4) {
               const float4 m4 = *reinterpret_cast<const float4*>(ms.nm + n0 + e);
@@ -502,8 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           // the rows' maxima over the tile, then new M where one is passed
           {
             uint32_t s[HN];
-            tmem_ld_n(tS, s);
-            wait_ld(s);
+            scores(s);
             float v[32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) {

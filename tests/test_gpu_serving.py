@@ -526,6 +526,39 @@ def test_tree_values_of_any_magnitude(dtype, drafted, cached):
     assert (off <= bound).all(), float((off / bound).max())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("factor", [0.0, 6e4, 1e30])
+def test_tree_rows_of_q_do_not_depend_on_each_other(dtype, factor):
+    """A row of zeros or of huge values in the same tile leaves small and ordinary rows what they are alone."""
+    if dtype == torch.float16 and factor > 6e4:
+        pytest.skip("past the type's range")
+    s = make_tree(dtype, 4, 4, 8, 2, 16, [3, 70], [5, 4], outliers=False)
+    # rows 0 and 6 stand apart; row 1 is small, with a key that is not; the others are ordinary
+    q = s["q"].double().clamp(-1, 1)
+    q[1] *= 1e-6 if dtype == torch.float16 else 1e-20
+    s["q"] = q.to(dtype)
+    big = torch.tensor([1], device="cuda")
+    scale, kf = (35.0, 3e3) if dtype == torch.float16 else (3.5, 1e19)  # row 1: a score of about one
+    s["k"][0] = (s["k"][0].double() * kf).to(dtype)
+    m = i32([[1], [3], [4], [8], [16], [1], [2], [4], [8]])  # rows 0 and 1 see it
+    t = dict(s, q=s["q"].clone())
+    for r in (0, 6):
+        t["q"][r] = (torch.sign(q[r]) * factor).to(dtype)
+    got = run_tree(t, 4, 4, 16, m, scale=scale)
+    rest = torch.tensor([1, 2, 3, 4, 5, 7, 8], device="cuda")
+    for rows in (rest[1:], big):  # the bound goes by the largest scores: row 1's are apart
+        keep = torch.zeros(9, 1, 1, dtype=torch.bool, device="cuda")
+        keep[rows] = True
+        want, size, top = tree_plain(torch.where(keep, t["q"], 0), s["k"], s["v"], s["start"], m, s["K"], s["V"], s["lens"], s["table"], 16, 2, scale, 4, 4)
+        if rows is big:  # its own largest score
+            top = float((s["q"][1].double().norm(dim=-1).max() * s["k"][0].double().norm(dim=-1).max()) * scale)
+        else:
+            top = float(q.norm(dim=-1).max() * max(values(s["K"], 4).norm(dim=-1).max(), s["k"][1:].double().norm(dim=-1).max()) * scale)
+        rel = 8 * 2.0 ** -11 * max(top, 1) / math.sqrt(D) + 2 * 2.0 ** -11 if dtype != torch.float32 else 8 * 2.0 ** -24 * 16 * max(top, 1)
+        off = (got.double() - want).norm(dim=-1)[rows]
+        assert (off <= rel * size[rows] + torch.finfo(dtype).eps / 2 * want.norm(dim=-1)[rows]).all(), float((off / size[rows]).max())
+
+
 def test_tree_rows_past_the_end_and_strides():
     """Rows behind the last sequence are left; q, k, v may be slices of one projection; bad offsets are cut."""
     s = make_tree(torch.bfloat16, 4, 4, 8, 2, 16, [100, 50], [3, 4])
