@@ -374,8 +374,8 @@ tq_status tq_block_tables(const int32_t* d_len, const int32_t* d_new, const int3
                           int32_t* d_pos, int64_t rows, tq_stream stream);
 
 /* Angular frequencies (radians per position, fp64) as fractions of a turn:
- * h_freq[i] = floor(frac(h_inv_freq[i] / 2π) · 2^64), so that the angle of any
- * position is one wrapping 64-bit product.  Host only, synchronous; the caller
+ * h_freq[i] = frac(h_inv_freq[i] / 2π) · 2^64 to within one (for magnitudes up to
+ * 2^40), so that the angle of any position is one wrapping 64-bit product.  Host only, synchronous; the caller
  * copies h_freq to the device.  Errors: INVALID_ARG (NULL, n < 0, not finite). */
 tq_status tq_rope_frequencies(int n, const double* h_inv_freq, uint64_t* h_freq);
 

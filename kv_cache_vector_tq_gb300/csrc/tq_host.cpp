@@ -982,11 +982,19 @@ tq_status tq_rope_frequencies(int n, const double* h_inv_freq, uint64_t* h_freq)
   if (n < 0 || (n > 0 && (!h_inv_freq || !h_freq))) return TQ_ERR_INVALID_ARG;
   for (int i = 0; i < n; ++i)
     if (!std::isfinite(h_inv_freq[i])) return TQ_ERR_INVALID_ARG;
-  const double two_pi = 6.283185307179586476925;
+  // f/2π as the sum of two doubles, product and remainder: one double alone is off
+  // by 2^-54 of itself, hundreds of the last place for a frequency of a radian
+  const double inv_hi = 0x1.45f306dc9c883p-3, inv_lo = -0x1.6b01ec5417056p-57;  // 1/2π
   for (int i = 0; i < n; ++i) {
-    double turn = h_inv_freq[i] / two_pi;
-    turn -= std::floor(turn);
-    h_freq[i] = turn < 1.0 ? (uint64_t)std::ldexp(turn, 64) : 0u;
+    const double f = std::fabs(h_inv_freq[i]);
+    const volatile double rounded = f * inv_hi;  // not fused into what is taken from it
+    const double turn = rounded;
+    double rest = std::fma(f, inv_hi, -turn) + f * inv_lo;
+    rest -= std::floor(rest + 0.5);
+    const double whole = std::ldexp(turn - std::floor(turn), 64);  // exact; fewer than 2^64
+    const uint64_t w = (uint64_t)whole;
+    const uint64_t q = w + (uint64_t)(int64_t)std::floor((whole - (double)w) + std::ldexp(rest, 64));
+    h_freq[i] = h_inv_freq[i] < 0 ? 0u - q : q;
   }
   return TQ_OK;
 }

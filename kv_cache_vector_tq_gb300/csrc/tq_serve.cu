@@ -188,10 +188,11 @@ __global__ void __launch_bounds__(kBtThreads) block_tables_kernel(const BlockTab
 //   y = x · w / sqrt(mean(x²) + eps);  pairs (a, b) of y turn by the angle
 //   pos·f_j:  (a cos - b sin, b cos + a sin).
 // Angles: f_j as a 64-bit fraction of a turn, so that pos·f_j modulo one turn
-// is one 64-bit integer product, exact to 2^-64 of a turn per position (a
-// 32-bit angle is off by whole degrees past 10^6 positions).  The fraction's
-// leading 32 bits, as a signed multiple of half a turn, go to sincospif; its
-// rounding to fp32 is at most 2^-25 half turns.
+// is one 64-bit integer product, right to 2^-64 of a turn per position (a
+// 32-bit angle is off by whole degrees past 10^6 positions), so to 2^-32 half
+// turns at any int32 position.  The fraction's leading 32 bits, as a signed
+// multiple of half a turn, go to sincospif; the rest is below 2^-31 half turns and
+// their rounding to fp32 at most 2^-25.
 // One pass: a row is d/8 lanes of 8 elements, its sum of squares a shuffle tree in
 // fp32.  With the half-split pairing a lane holds 4 elements and their 4 partners,
 // so no value changes lanes; cosines and sines are multiplied by the weights once

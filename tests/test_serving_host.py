@@ -78,6 +78,29 @@ def test_rope_frequencies_are_fractions_of_a_turn(L):
     assert L.tq_rope_frequencies(0, None, None) == tq.TQ_OK
 
 
+def test_rope_frequencies_to_the_last_place(L):
+    """Within one unit of frac(f/2π)·2^64, whose exact value is worked out in integers."""
+    bits = 1300  # the smallest double has its last place at 2^-1074
+
+    def arctan_of_inverse(n):  # the sum of (-1)^k / ((2k + 1) n^(2k + 1)), times 2^bits
+        total, term, k = 0, (1 << bits) // n, 0
+        while term:
+            total += -(term // (2 * k + 1)) if k % 2 else term // (2 * k + 1)
+            term, k = term // (n * n), k + 1
+        return total
+
+    pi = 16 * arctan_of_inverse(5) - 4 * arctan_of_inverse(239)
+    inv = np.concatenate([1e6 ** (-np.arange(0, 128, 2) / 128), -1e4 ** (-np.arange(0, 64, 2) / 64),
+                          [1.0, -1.0, 7.0, 0.0, 1e-30, -1e-30, 2 * np.pi, np.pi, 1000.5, 1e9, 1e12, 5e-324]])
+    out = np.empty(inv.size, dtype=np.uint64)
+    assert L.tq_rope_frequencies(inv.size, tq._ptr(inv), tq._ptr(out)) == tq.TQ_OK
+    for f, got in zip(inv.tolist(), out.tolist()):
+        n, d = f.as_integer_ratio()
+        exact = (n << (bits + 63 + 64)) // (d * pi)  # f/2π·2^64 with 64 places behind the point
+        off = ((got << 64) - exact) % (1 << 128)
+        assert min(off, (1 << 128) - off) <= 1 << 64, (f, got)
+
+
 def test_old_calls_keep_their_types(L):
     """bf16 is a type of the serving calls only; the encoder refuses it before it looks at anything else."""
     assert tq.TQ_BF16 == 2
