@@ -443,9 +443,10 @@ tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64
  * d_out     [rows, Hq, d] of `dtype`, contiguous.
  * Accuracy: F32 inputs are computed in fp32 throughout (CUDA cores).  F16 and
  * BF16 inputs take the tensor cores: cached values are the codebook's α·c
- * rounded to fp16, the drafted rows Πk, Πv one fp16 each, q and the weights two
- * fp16 terms (F16) or one (BF16), sums in fp32; the error is then of the size of
- * the output type's own rounding.  Norms of values may be anything from 2^-80 (below it
+ * rounded to fp16; q, the weights and the drafted rows Πk, Πv are two fp16 terms
+ * (F16) or one (BF16), sums in fp32.  The error is then of the size of the output
+ * type's own rounding (with 4-bit caches up to 1.8 times it
+ * for F16, from α·c); rows given as F32 are free of these roundings.  Norms of values may be anything from 2^-80 (below it
  * they lose bits, then count as zero) to the end of fp32's range; a drafted row
  * whose norm passes that counts as one with a NaN in it.
  * d_ws      workspace of tq_tree_attention_workspace_size bytes (16-byte
@@ -455,7 +456,7 @@ tq_status tq_encode_slots(const tq_ctx* ctx, const void* d_x, int x_dtype, int64
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
  * UNSUPPORTED for d != 128, Prod or b + 1/2-bit codes, a block that is not a
  * multiple of 16, rows * Hq or max_blocks * block past 2^31 - 256, or so many rows over so
- * large a capacity (rows * Hq / 16 times (capacity + rows) / 128) as to pass 2^31.
+ * large a capacity (rows * Hq / 16 times (capacity + 2 * rows) / 128) as to pass 2^31.
  */
 tq_status tq_tree_attention_workspace_size(const tq_ctx* kctx, int B, int Hq, int Hkv, int64_t rows, size_t* bytes);
 tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* d_q, int64_t q_stride,

@@ -29,7 +29,8 @@ struct RotSmem {
 };
 
 // TC: rows for the tensor cores, scaled by a power of two into fp16's range,
-// the leading part and (q) the remainder; else fp32.
+// the leading part and (q, and the drafted rows of an fp16 call) the remainder;
+// else fp32.
 template <bool TC>
 __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, const int per, const int nbq, const int nbk) {
   __shared__ __align__(16) RotSmem sm;
@@ -187,10 +188,11 @@ __global__ void __launch_bounds__(256, 2) tree_prep_kernel(const TreeParams p, c
             bad ? NAN : TC && m == 0.f ? 0.f : one / sc;  // zeros have no say in anyone's scaling
       }
       if constexpr (TC) {
-        __half* d = reinterpret_cast<__half*>(dst) + at * (kind == 0 ? 256 : 128) + j;
+        const bool two = kind == 0 || p.dtok < kTreeTok;
+        __half* d = reinterpret_cast<__half*>(dst) + at * (two ? 256 : 128) + j;
         const __half hi = __float2half_rn(z);
         d[0] = hi;
-        if (kind == 0) d[128] = __float2half_rn(z - __half2float(hi));
+        if (two) d[128] = __float2half_rn(z - __half2float(hi));
       } else {
         dst[at * 128 + j] = z;
       }
@@ -792,6 +794,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   // tensor-core kernel does
   const bool tc = a.dtype != TQ_F32;
   p.rows = tree_umma_rows(a.R, a.B, p.G);
+  p.dtok = a.dtype == TQ_F16 ? kTreeTok / 2 : kTreeTok;
   p.ctas = num_sms() * (tc || p.rows == 64 ? 1 : 2);  // as many as fit at once
   p.klut = kc.lut;
   p.vlut = vc.lut;
@@ -805,7 +808,7 @@ tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cud
   p.wait_limit = kc.wait_limit;
   // the units of a sequence, whatever it turns out to be, are counted in 32 bits
   const int64_t most_rt = (a.R * p.G + p.rows - 1) / p.rows;
-  const int64_t most_per = (int64_t)p.max_blocks * p.block / kTreeTok + a.R / kTreeTok + 2;
+  const int64_t most_per = (int64_t)p.max_blocks * p.block / kTreeTok + a.R / p.dtok + 2;
   if (most_rt > 0 && most_per > (int64_t)INT32_MAX / (most_rt * a.Hkv)) return TQ_ERR_UNSUPPORTED;
   // groups of kPrepV rows, as many to a CTA as leave two CTAs on every SM
   const int64_t nq = (a.R * a.Hq + kPrepV - 1) / kPrepV, nk = a.k_new ? (a.R * a.Hkv + kPrepV - 1) / kPrepV : 0;

@@ -11,7 +11,7 @@
 //
 // Work: a group is (sequence, KV head, tile of kRows rows), a row being one
 // (drafted token, query head of the KV head) pair; its units are 128 cached
-// tokens each, then 128 drafted tokens each.  The units of all groups, laid
+// tokens each, then 128 drafted tokens each (fp16 rows: 64, in two terms).  The units of all groups, laid
 // end to end, are shared evenly among the CTAs of a grid that fits the GPU
 // once, whatever the lengths are: lengths live on the device, so a captured
 // call serves every later length.  A CTA that starts a group leaves the rows'
@@ -75,12 +75,13 @@ struct TreeParams {
   // workspace
   TreeSeq* seq;         // [B + 1]; seq[B].unit: the number of units
   TreeCta* cta;         // [ctas]
-  float *qrot, *krot, *vrot;  // rotated rows: fp32, or fp16 (q: 128 leading parts, 128 remainders)
+  float *qrot, *krot, *vrot;  // rotated rows: fp32, or fp16 (q, and all of an fp16 call: 128 leading parts, 128 remainders)
   float* qfac;          // [R·Hq] power of two that was divided out of a row of q (tensor-core path)
   float *kfac, *vfac;   // [Hkv][R] the same of the drafted rows, times kone / vone
   float* rec;           // [R·Hq] records of the rows
   float* crec;          // [ctas][rows] records of continued groups
   int ctas, rows;       // CTAs of the grid, rows per tile
+  int dtok;             // drafted tokens per unit
 };
 
 __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
@@ -91,7 +92,7 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams& p, int b) {
   s.T = (int)(hi - lo);
   s.len = (int)min((int64_t)max(p.len[b], 0), (int64_t)p.max_blocks * p.block);
   s.rt = (int)(((int64_t)s.T * p.G + p.rows - 1) / p.rows);
-  s.per = (s.len + kTreeTok - 1) / kTreeTok + (p.kn ? (s.T + kTreeTok - 1) / kTreeTok : 0);
+  s.per = (s.len + kTreeTok - 1) / kTreeTok + (p.kn ? (s.T + p.dtok - 1) / p.dtok : 0);
   if (s.per < 1) s.per = 1;
   s.pad = 0;
   s.unit = 0;

@@ -20,7 +20,12 @@
 // which the sum is taken, are then between 2^-104 and 2^104 where they matter.
 // Rounding of the operands: for fp16 outputs Q̂ and P are split into two fp16
 // terms each (two products), since one rounding of either costs as much as the
-// output's own; bf16 outputs round eight times coarser and take one term.
+// output's own; bf16 outputs round eight times coarser and take one term.  The
+// drafted rows of fp16 calls are in two terms as well (in one, the error was up to
+// 1.9 times the output's own where they carry the weight): a unit is 64 of them,
+// the leading parts on lanes and columns 0-63, the remainders on 64-127.  The two
+// scores of a token are added before the softmax; its weight stands in both places
+// and is summed in the first.
 //
 // Warps: 0-7 softmax (thread = token, half of the rows), 8-15 K̂ (thread = token,
 // half of the coordinates: 32 lookups of two codes), 16-23 V̂ᵀ (thread =
@@ -50,6 +55,8 @@ constexpr int kRegSoft = 96, kRegOps = 64, kRegRest = 56;  // 8·96 + 16·64 + 4
 static_assert(8 * kRegSoft + 16 * kRegOps + 4 * kRegRest <= 28 * 72, "registers that the launch does not have would be waited for");
 constexpr int kRS = 5;                     // packed tiles in flight (3 where K and V have tables of their own)
 constexpr int kNormSlots = 8;
+template <bool SPLIT>
+constexpr int kDraft = SPLIT ? kTreeTok / 2 : kTreeTok;  // drafted tokens of a unit
 constexpr uint32_t kLandPolls = 1u << 14;  // a millisecond or more for copies under way
 // Tensor memory columns: Sᵀ x 2, Oᵀ, the rows' sums of weights per token lane, K̂ x 2, V̂ᵀ x 2
 constexpr uint32_t kColO = 128, kColL = 192, kColK = 256, kColV = 384;
@@ -304,6 +311,33 @@ __device__ __forceinline__ void dequant_v(const unsigned char* smem, int raw, ui
   }
 }
 
+// Adds the scores of the lane `to` bytes away, through a place [row][token] of
+// shared memory.  A call: inside the loop over tiles, most of which never come here,
+// it cost 2% (252 rows over 48K: 310 -> 303 us).
+template <int HN, int PC>
+__device__ __noinline__ void join_terms(uint32_t tS, unsigned char* at, int to) {
+#pragma unroll 1
+  for (int c = 0; c < HN / PC; ++c) {
+    uint32_t s[PC];
+    tmem_ld_n(tS + PC * c, s);
+    wait_ld(s);
+#pragma unroll
+    for (int e = 0; e < PC; ++e) *reinterpret_cast<uint32_t*>(at + (PC * c + e) * (4 * kTreeTok)) = s[e];
+  }
+  bar_softmax();
+  at += to;
+#pragma unroll 1
+  for (int c = 0; c < HN / PC; ++c) {
+    uint32_t s[PC];
+    tmem_ld_n(tS + PC * c, s);
+    wait_ld(s);
+#pragma unroll
+    for (int e = 0; e < PC; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) + *reinterpret_cast<const float*>(at + (PC * c + e) * (4 * kTreeTok)));
+    tmem_st_n(tS + PC * c, s);
+  }
+  tmem_wait_st();
+}
+
 template <int N, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreeParams p) {
   static_assert(N == 16 || N == 32 || N == 64, "rows per tile");
@@ -449,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         const uint32_t tS = tmem + lane_base + sb * 64;
         const float* nrm = reinterpret_cast<const float*>(smem + kNorms + ns * 1024);
         const bool draft = t >= g.ctiles;
-        const int t0 = draft ? (t - g.ctiles) * kTreeTok : t * kTreeTok;
+        const int t0 = draft ? (t - g.ctiles) * kDraft<SPLIT> : t * kTreeTok;
         const int nt = min(kTreeTok, (draft ? g.s.T : g.s.len) - t0);
         const uint32_t chunks = ms.valid[ns];
-        const bool here = tok < nt && ((chunks >> (tok >> 4)) & 1u);  // this token is there
+        const bool here = (tok & (SPLIT && draft ? 63 : 127)) < nt && ((chunks >> (tok >> 4)) & 1u);  // this token is there
         const bool whole = nt == kTreeTok && chunks == 0xFFu && !draft;
         const float kn = nrm[tok], vn = draft ? nrm[128 + tok] : nrm[128 + tok] * kTreeVDown;
         // 2^lv > vn.  The upper end is past every finite value; below the lower one
@@ -463,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
         // tokens; lane n holds the word of row n0 + n
         uint32_t mw = 0u;
         if (draft && lane < HN && ms.vec[n0 + lane] >= 0) {
-          const int ti = ms.ti[n0 + lane], at = (t0 >> 5) + quad;
+          const int ti = ms.ti[n0 + lane], at = (t0 >> 5) + (SPLIT ? quad & 1 : quad);
           if (p.mask) {
             if (at < p.mask_words) mw = __ldg(p.mask + (int64_t)(g.s.start + ti) * p.mask_words + at);
           } else {  // a chain: tokens 0..ti
@@ -483,6 +517,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
             for (int e = 0; e < HN; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * ms.c[n0 + e]);
           }
         };
+        if (SPLIT && draft) {  // a drafted token's two scores: each of its lanes gets the sum
+          // (where this tile's P will be, which is written behind the barrier that follows)
+          join_terms<HN, PC>(tS, smem + kP + sb * (2 * kPPart) + (n0 * kTreeTok + tok) * 4, quad >= 2 ? -256 : 256);
+        }
         // weights with the M there is; should one pass the limit (M = -inf, a
         // row's first token, does), M is raised and they are computed again
         float pr[HN];
@@ -588,7 +626,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
           if constexpr (SPLIT) *reinterpret_cast<uint4*>(at + kPPart) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
-        tmem_st_n(tL, l);
+        if (!(SPLIT && draft && quad >= 2)) tmem_st_n(tL, l);  // (lanes of remainders leave the sums)
         tmem_wait_st();
         fence_proxy_async();
         tc_fence_before();
@@ -683,17 +721,19 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           }
         } else {
           // drafted rows, rotated and rounded already; zeros past the last one
-          const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+          const int t0 = (t - g.ctiles) * kDraft<SPLIT>, nt = p.kn ? g.s.T - t0 : 0;
           const int64_t tok = g.s.start + t0;
+          constexpr int kRow = SPLIT ? 256 : 128;  // halves of a row
           if (!is_v) {
+            const int vt = SPLIT ? v & 63 : v;
             const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(p.krot) +
-                                                              ((tok + v) * p.Hkv + g.kvh) * 128) + 8 * half;
+                                                              ((tok + vt) * p.Hkv + g.kvh) * kRow + 128 * (SPLIT ? v >> 6 : 0)) + 8 * half;
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const uint4 x = v < nt ? src[4 * c + e] : make_uint4(0u, 0u, 0u, 0u);
+                const uint4 x = vt < nt ? src[4 * c + e] : make_uint4(0u, 0u, 0u, 0u);
                 w[4 * e] = x.x;
                 w[4 * e + 1] = x.y;
                 w[4 * e + 2] = x.z;
@@ -702,14 +742,14 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
               tmem_st16(op + 16 * c, w);
             }
           } else {
-            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.vrot) + (tok * p.Hkv + g.kvh) * 128 + vd;
-            const int64_t step = (int64_t)p.Hkv * 128;
+            const uint16_t* src = reinterpret_cast<const uint16_t*>(p.vrot) + (tok * p.Hkv + g.kvh) * kRow + vd + 128 * (SPLIT ? half : 0);
+            const int64_t step = (int64_t)p.Hkv * kRow;
 #pragma unroll 1
             for (int c = 0; c < 2; ++c) {
               uint32_t w[16];
 #pragma unroll
               for (int e = 0; e < 16; ++e) {
-                const int k = 64 * half + 32 * c + 2 * e;
+                const int k = (SPLIT ? 0 : 64 * half) + 32 * c + 2 * e;
                 const uint32_t x = k < nt ? src[k * step] : 0u, y = k + 1 < nt ? src[(k + 1) * step] : 0u;
                 w[e] = x | (y << 16);
               }
@@ -850,11 +890,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           ok = __all_sync(kFull, ok);
           if (!ok) break;
           if (draft) {
-            const int t0 = (t - g.ctiles) * kTreeTok, nt = p.kn ? g.s.T - t0 : 0;
+            const int t0 = (t - g.ctiles) * kDraft<SPLIT>, nt = p.kn ? g.s.T - t0 : 0;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int k = 32 * e + lane;
-              reinterpret_cast<float*>(nb)[k] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
+              const int k = (32 * e) % kDraft<SPLIT> + lane;
+              reinterpret_cast<float*>(nb)[32 * e + lane] = k < nt ? fac[(int64_t)g.kvh * p.R + g.s.start + t0 + k] : 0.f;
             }
             if (lane == 0 && !is_v) ms.valid[ns] = 0xFFu;
             fence_proxy_async();  // before the bulk copy that writes the slot next

@@ -559,6 +559,78 @@ def test_tree_rows_of_q_do_not_depend_on_each_other(dtype, factor):
         assert (off <= rel * size[rows] + torch.finfo(dtype).eps / 2 * want.norm(dim=-1)[rows]).all(), float((off / size[rows]).max())
 
 
+def one_term(x):
+    """Rows as one fp16 in the rotated domain would hold them."""
+    y = x.double() @ rotation().T
+    up = torch.exp2(11 - torch.floor(torch.log2(y.abs().amax(-1, keepdim=True))))
+    return (y * up).half().double() / up @ rotation()
+
+
+def test_tree_second_terms_of_fp16_scores():
+    """Large scores: q and the drafted keys count in two fp16 terms.  A score of up to `top` is off by 2^-23 of it for
+    each operand's terms and for each of two truncated sums, and weights by twice that: 2^-20·top, doubled once more.
+    One term of either breaks the bound."""
+    Hkv, scale = 2, 8.0
+    s = make_tree(torch.float16, 1, 1, 8, Hkv, 16, [40, 0, 9], [20, 64, 70], outliers=False)
+    m = tree_masks([20, 64, 70], "tree", torch.Generator().manual_seed(1), 3)
+
+    def plain(q, k):
+        return tree_plain(q, k, s["v"], s["start"], m, s["K"], s["V"], s["lens"], s["table"], 16, Hkv, scale, 1, 1)
+
+    want, size, top = plain(s["q"], s["k"])
+    bound = 2.0 ** -19 * top * size + 2.0 ** -11 * want.norm(dim=-1)
+    assert ((plain(one_term(s["q"]), s["k"])[0] - want).norm(dim=-1) > bound).any()
+    assert ((plain(s["q"], one_term(s["k"]))[0] - want).norm(dim=-1) > bound).any()
+    off = (run_tree(s, 1, 1, 16, m, scale=scale).double() - want).norm(dim=-1)
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+def test_tree_second_terms_of_fp16_weights():
+    """Two drafted tokens whose values cancel but for the difference of their weights: those count in two fp16 terms."""
+    n = 32
+    s = make_tree(torch.float16, 1, 1, 8, 2, 16, [0] * n, [2] * n, outliers=False)
+    s["v"][1::2] = -s["v"][::2]
+    m = i32([[3]] * (2 * n))
+    scale = 0.01 / math.sqrt(D)
+    got = run_tree(s, 1, 1, 16, m, scale=scale)
+    want, size, _ = tree_plain(s["q"], s["k"], s["v"], s["start"], m, s["K"], s["V"], s["lens"], s["table"], 16, 2, scale, 1, 1)
+    # sums and both terms are right to 2^-22 of Σ p‖v‖, eight of those; then the output's rounding
+    bound = 2.0 ** -19 * size + 2.0 ** -11 * want.norm(dim=-1)
+    z = (s["q"].double().view(n, 2, 2, 4, D)[:, :, :, :, None] * s["k"].double().view(n, 2, 2, D).transpose(1, 2)[:, None, :, None]).sum(-1) * scale
+    w = (z.softmax(-1) * 50).half().double()  # one term
+    one = ((w[..., :1] - w[..., 1:]) / w.sum(-1, keepdim=True) * s["v"][::2].double()[:, None, :, None]).reshape(2 * n, 8, D)
+    assert ((one - want).norm(dim=-1) > bound).any()
+    off = (got.double() - want).norm(dim=-1)
+    assert (off <= bound).all(), float((off / bound).max())
+
+
+@pytest.mark.parametrize("lens,new", [([0], [70]), ([0, 0, 0], [1, 64, 5]), ([0], [300])])
+def test_tree_a_row_that_sees_itself_alone_is_its_value(lens, new):
+    """fp16 rows: the value comes back but for 2^-20 of its norm (rotations in fp32, two fp16 terms) and one rounding."""
+    s = make_tree(torch.float16, 2, 2, 8, 2, 16, lens, new)
+    i = torch.cat([torch.arange(n) for n in new])
+    m = torch.zeros(len(i), (max(new) + 31) // 32, dtype=torch.int64)
+    m[torch.arange(len(i)), i // 32] = 1 << (i % 32)
+    m = torch.where(m >= 2 ** 31, m - 2 ** 32, m).int().cuda()
+    got = run_tree(s, 2, 2, 16, m).double().view(len(i), 2, 4, D)
+    v = s["v"].double()
+    bound = 2.0 ** -20 * v.norm(dim=-1, keepdim=True) + 2.0 ** -11 * v.abs()
+    assert ((one_term(s["v"]) - v).abs() > bound).any()
+    assert ((got - v[:, :, None]).abs() <= bound[:, :, None]).all()
+
+
+def test_tree_fp32_to_fp32_rounding():
+    """fp32 calls with moderate scores: sums of 128 and of all tokens in fp32.  A score is off by 8·2^-24·top (terms,
+    norm, scale, exponent), weights by twice that, the sums and rotations by 16·2^-24 of Σ p‖v‖."""
+    s = make_tree(torch.float32, 4, 4, 8, 2, 16, [700, 33, 0], [9, 30, 5], outliers=False)
+    m = tree_masks([9, 30, 5], "tree", torch.Generator().manual_seed(2), 1)
+    scale = 0.2 / math.sqrt(D)
+    got = run_tree(s, 4, 4, 16, m, scale=scale)
+    want, size, top = tree_plain(s["q"], s["k"], s["v"], s["start"], m, s["K"], s["V"], s["lens"], s["table"], 16, 2, scale, 4, 4)
+    off = (got.double() - want).norm(dim=-1)
+    assert (off <= 16 * 2.0 ** -24 * (1 + top) * size).all(), float((off / size).max())
+
+
 def test_tree_rows_past_the_end_and_strides():
     """Rows behind the last sequence are left; q, k, v may be slices of one projection; bad offsets are cut."""
     s = make_tree(torch.bfloat16, 4, 4, 8, 2, 16, [100, 50], [3, 4])
