@@ -324,6 +324,14 @@ def _heads(t, n, h, d, what, dev):
     return t.data_ptr(), a if n > 1 else h * d
 
 
+def _type(t, what):
+    """The tq type of a tensor."""
+    ty = _T[1].get(t.dtype)
+    if ty is None:
+        raise ValueError(f"{what}: float32, float16 or bfloat16 is wanted")
+    return ty
+
+
 def tq_block_tables(lens, new, held, ring, state, table, block, held_out, state_out, row_start, slots, pos,
                     stream=None):
     """Pages, slots and positions of one step's tokens (include/tq.h).  table [B, max_blocks], ring, lens, new, held,
@@ -352,7 +360,7 @@ def tq_rope_frequencies(inv_freq, device="cuda"):
 def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=None):
     """Head norms and position rotation of q [N, Hq, d] and k [N, Hkv, d] into q_out and k_out (include/tq.h).
     wq, wk: [d] of q's type or None; freq: tq_rope_frequencies or None (norms alone); outputs may be the inputs."""
-    torch, types, _, cur = _types()
+    torch, _, _, cur = _types()
     dev = cur()
     (N, Hq, d), Hkv, ti, to = q.shape, k.shape[1], q.dtype, q_out.dtype
     if k.dtype is not ti or k_out.dtype is not to:
@@ -360,10 +368,10 @@ def tq_qk_norm_rope(q, k, wq, wk, eps, freq, style, pos, q_out, k_out, stream=No
     (qp, qs), (kp, ks) = _heads(q, N, Hq, d, "q", dev), _heads(k, N, Hkv, d, "k", dev)
     (qo, qos), (ko, kos) = _heads(q_out, N, Hq, d, "q_out", dev), _heads(k_out, N, Hkv, d, "k_out", dev)
     _check("tq_qk_norm_rope", lib().tq_qk_norm_rope(
-        qp, qs, kp, ks, types[ti], N, Hq, Hkv, d, None if wq is None else _dev(wq, ti, d, "wq", dev),
+        qp, qs, kp, ks, _type(q, "q"), N, Hq, Hkv, d, None if wq is None else _dev(wq, ti, d, "wq", dev),
         None if wk is None else _dev(wk, ti, d, "wk", dev), eps,
         None if freq is None else _dev(freq, torch.int64, 0, "freq", dev), 0 if freq is None else 2 * freq.numel(), style,
-        _dev(pos, torch.int32, N, "pos", dev), qo, qos, ko, kos, types[to], _raw_stream(stream, dev)))
+        _dev(pos, torch.int32, N, "pos", dev), qo, qos, ko, kos, _type(q_out, "q_out"), _raw_stream(stream, dev)))
 
 
 def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
@@ -393,12 +401,14 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     """Attention of drafted tokens q [rows, Hq, d] over a packed cache and each other (include/tq.h).  k_new, v_new
     [rows, Hkv, d] or None (Hkv is then given); mask [rows, words] int32 or None (a chain); table [B, max_blocks] or
     None (contiguous, cap = block)."""
-    torch, types, _, cur = _types()
+    torch, _, _, cur = _types()
     dev = cur()
     rows, Hq, d = q.shape
     if d != kctx.d:
         raise ValueError(f"q: rows of {kctx.d} elements are wanted")
     ti = q.dtype
+    if (k_new is None) != (v_new is None) or (k_new is None and Hkv is None):
+        raise ValueError("k_new and v_new are given together, or neither of them and Hkv")
     B, Hkv = lens.numel(), k_new.shape[1] if k_new is not None else Hkv
     qp, qs = _heads(q, rows, Hq, d, "q", dev)
     kp = vp = None
@@ -410,7 +420,7 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     i32 = torch.int32
     words, width = 0 if mask is None else mask.shape[1], 0 if table is None else table.shape[1]
     _check("tq_tree_attention", lib().tq_tree_attention(
-        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, types[ti], rows, _dev(row_start, i32, B + 1, "row_start", dev),
+        kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, _type(q, "q"), rows, _dev(row_start, i32, B + 1, "row_start", dev),
         None if mask is None else _dev(mask, i32, rows * words, "mask", dev), words, ctypes.byref(K.desc),
         ctypes.byref(V.desc), _dev(lens, i32, B, "lens", dev),
         None if table is None else _dev(table, i32, B * width, "table", dev), width, block, B, Hq, Hkv, scale,

@@ -3,6 +3,7 @@ before anything is launched, so its device addresses are made up."""
 
 import ctypes
 import os
+import types
 
 import numpy as np
 import pytest
@@ -52,6 +53,34 @@ def test_qk_norm_rope_refusals(L, change, status):
 
 def test_nothing_to_do_is_fine(L):
     assert L.tq_qk_norm_rope(*{**NORM, "N": 0, "q": None, "k": None}.values()) == tq.TQ_OK
+
+
+@pytest.fixture
+def on_the_host(L, monkeypatch):
+    """The binding as if the host were the current device, so that what it refuses by itself is seen without a GPU."""
+    torch = pytest.importorskip("torch")
+    types = {torch.float32: tq.TQ_F32, torch.float16: tq.TQ_F16, torch.bfloat16: tq.TQ_BF16}
+    monkeypatch.setattr(tq, "_T", (torch, types, lambda dev: 0, lambda: -1))
+    return torch
+
+
+def test_binding_refuses_other_types_and_half_of_the_drafted_rows(on_the_host):
+    torch = on_the_host
+    x, pos = torch.zeros(2, 1, 128), torch.zeros(2, dtype=torch.int32)
+    for q, out in ((x.double(), x), (x, x.double()), (x.int(), x)):
+        with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
+            tq.tq_qk_norm_rope(q, q, None, None, 1e-6, None, 0, pos, out, out)
+    ctx = types.SimpleNamespace(d=128, handle=None)
+    code = types.SimpleNamespace(desc=tq.Codes())
+
+    def attend(q, k, v, **kw):
+        tq.tq_tree_attention(ctx, ctx, q, k, v, pos, None, code, code, pos[:1], None, 16, 1.0, q, x, **kw)
+
+    for k, v, kw in ((x, None, {}), (None, x, {}), (None, x, dict(Hkv=1)), (None, None, {})):
+        with pytest.raises(ValueError, match="together"):
+            attend(x, k, v, **kw)
+    with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
+        attend(x.double(), x.double(), x.double())
 
 
 def test_null_contexts_are_refused(L):
