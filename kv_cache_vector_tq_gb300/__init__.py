@@ -324,6 +324,13 @@ def _heads(t, n, h, d, what, dev):
     return t.data_ptr(), a if n > 1 else h * d
 
 
+def _codes(c, what, dev):
+    """Descriptor of a code set on this device."""
+    if c.norm.get_device() != dev:
+        raise ValueError(f"{what}: a code set on the current device is wanted")
+    return ctypes.byref(c.desc)
+
+
 def _type(t, what):
     """The tq type of a tensor."""
     ty = _T[1].get(t.dtype)
@@ -386,7 +393,7 @@ def tq_encode_slots(ctx, x, slots, block, codes, stream=None):
         raise ValueError("x: float32 or float16 is wanted")
     _check("tq_encode_slots", lib().tq_encode_slots(
         ctx.handle, _dev(x, ti, 0, "x", dev), types[ti], N, Hkv, _dev(slots, torch.int64, N, "slots", dev), block,
-        ctypes.byref(codes.desc), _raw_stream(stream, dev)))
+        _codes(codes, "codes", dev), _raw_stream(stream, dev)))
 
 
 def tq_tree_attention_workspace_size(kctx, B, Hq, Hkv, rows):
@@ -421,8 +428,8 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
     words, width = 0 if mask is None else mask.shape[1], 0 if table is None else table.shape[1]
     _check("tq_tree_attention", lib().tq_tree_attention(
         kctx.handle, vctx.handle, qp, qs, kp, ks, vp, vs, _type(q, "q"), rows, _dev(row_start, i32, B + 1, "row_start", dev),
-        None if mask is None else _dev(mask, i32, rows * words, "mask", dev), words, ctypes.byref(K.desc),
-        ctypes.byref(V.desc), _dev(lens, i32, B, "lens", dev),
+        None if mask is None else _dev(mask, i32, rows * words, "mask", dev), words, _codes(K, "K", dev),
+        _codes(V, "V", dev), _dev(lens, i32, B, "lens", dev),
         None if table is None else _dev(table, i32, B * width, "table", dev), width, block, B, Hq, Hkv, scale,
         _dev(out, ti, rows * Hq * d, "out", dev), _dev(ws, ws.dtype, 0, "ws", dev), ws.numel() * ws.element_size(),
         _raw_stream(stream, dev)))

@@ -71,7 +71,7 @@ def test_binding_refuses_other_types_and_half_of_the_drafted_rows(on_the_host):
         with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
             tq.tq_qk_norm_rope(q, q, None, None, 1e-6, None, 0, pos, out, out)
     ctx = types.SimpleNamespace(d=128, handle=None)
-    code = types.SimpleNamespace(desc=tq.Codes())
+    code = types.SimpleNamespace(desc=tq.Codes(), norm=x)
 
     def attend(q, k, v, **kw):
         tq.tq_tree_attention(ctx, ctx, q, k, v, pos, None, code, code, pos[:1], None, 16, 1.0, q, x, **kw)
@@ -81,6 +81,19 @@ def test_binding_refuses_other_types_and_half_of_the_drafted_rows(on_the_host):
             attend(x, k, v, **kw)
     with pytest.raises(ValueError, match="float32, float16 or bfloat16"):
         attend(x.double(), x.double(), x.double())
+
+
+def test_binding_refuses_code_sets_of_another_device(on_the_host):
+    torch = on_the_host
+    x, n = torch.zeros(2, 1, 128), torch.zeros(2, dtype=torch.int32)
+    ctx = types.SimpleNamespace(d=128, handle=None)
+    here = types.SimpleNamespace(desc=tq.Codes(), norm=torch.zeros(4))
+    there = types.SimpleNamespace(desc=tq.Codes(), norm=types.SimpleNamespace(get_device=lambda: 1))
+    for K, V, name in ((there, here, "K"), (here, there, "V")):
+        with pytest.raises(ValueError, match=name + ": a code set on the current device"):
+            tq.tq_tree_attention(ctx, ctx, x, x, x, n, None, K, V, n[:1], None, 16, 1.0, x, x)
+    with pytest.raises(ValueError, match="codes: a code set on the current device"):
+        tq.tq_encode_slots(ctx, x, n.long(), 16, there)
 
 
 def test_null_contexts_are_refused(L):
