@@ -357,7 +357,9 @@ tq_status tq_decode_attention_noalloc(const tq_ctx* kctx, const tq_ctx* vctx, co
  * d_table   in and out: entries [held_b, need_b) of a served request are set;
  *           entries past need_b are left as they are.
  * d_held_out, d_state_out: the new d_held and d_state; other buffers than the
- *           inputs (the caller swaps them), so a call can be repeated.
+ *           inputs, so a call can be repeated.  The caller swaps them; a step captured
+ *           into a graph copies them back (or two graphs, one for either direction,
+ *           take turns).
  * d_row_start [B + 1]: first row of each request among the step's token rows.
  * d_slots, d_pos [rows]: slot and position of every row; rows past
  *           d_row_start[B] get -1 and 0.  Rows past `rows` are not listed.
