@@ -137,6 +137,41 @@ def test_block_tables_lengths_past_32_bits():
     assert got[5][2] == 2047 * block + (big - 1) % block
 
 
+def test_block_tables_captured_serves_later_steps():
+    """One captured step, its new held counts and state copied back inside the graph: steps with other lengths, each
+    against the definition."""
+    r, B, block, width, rows = np.random.default_rng(9), 6, 16, 9, 90
+    pages = B * width
+    ring, state = i32(r.permutation(pages).tolist()), torch.tensor([0, pages], device="cuda")
+    table, held, lens, new = i32([[-1] * width] * B), i32([0] * B), i32([0] * B), i32([0] * B)
+    held2, state2, start = torch.empty_like(held), torch.empty_like(state), i32([0] * (B + 1))
+    slots, pos = torch.zeros(rows, dtype=torch.int64, device="cuda"), i32([0] * rows)
+
+    def step():
+        tq.tq_block_tables(lens, new, held, ring, state, table, block, held2, state2, start, slots, pos)
+        held.copy_(held2)
+        state.copy_(state2)
+
+    side = torch.cuda.Stream()  # a first call outside of the capture: nothing new, nothing held
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    now = [0] * B
+    for k in range(12):
+        now = [0 if r.random() < 0.15 else n for n in now]  # some have ended
+        add = [int(min(r.integers(0, 30), block * width - n)) for n in now]
+        lens.copy_(i32(now))
+        new.copy_(i32(add))
+        want = tables_plain(now, add, held.tolist(), ring.tolist(), *state.tolist(), table.tolist(), block, rows)
+        graph.replay()
+        assert [x.tolist() for x in (table, ring, held, state, start, slots, pos)] == list(want), k
+        now = [n + a for n, a in zip(now, add)]
+
+
 # ------------------------------------------------------------------ norms and rotation
 def norm_rope_plain(x, w, eps, inv, style, pos):
     """In 64 bits: the rows, and the size of what each value was made from."""
@@ -631,6 +666,20 @@ def test_tree_fp32_to_fp32_rounding():
     assert (off <= 16 * 2.0 ** -24 * (1 + top) * size).all(), float((off / size).max())
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("B", [257, 700])
+def test_tree_many_sequences(dtype, B):
+    """More sequences than a CTA lays out at once: short and ragged, many without rows (a run of them across the first
+    256), some with nothing cached."""
+    r = np.random.default_rng(B)
+    lens, new = r.integers(0, 300, B), r.integers(0, 4, B)
+    lens[r.random(B) < 0.3] = 0
+    new[200:256] = 0
+    new[B // 2 + 130:B // 2 + 200] = 0
+    new[-1] = 2
+    tree_case(dtype, 3, 2, 4, 2, 16, lens.tolist(), new.tolist(), "tree")
+
+
 def test_tree_rows_past_the_end_and_strides():
     """Rows behind the last sequence are left; q, k, v may be slices of one projection; bad offsets are cut."""
     s = make_tree(torch.bfloat16, 4, 4, 8, 2, 16, [100, 50], [3, 4])
@@ -825,6 +874,23 @@ def test_refusals():
     with pytest.raises(tq.TqError) as e:
         tq.tq_encode_slots(wide, torch.randn(4, 2, 256, device="cuda"), slots, 16, tq.CodeSet(wide, 64))
     assert e.value.status == -2
+
+
+def test_calls_that_take_no_bf16_refuse_it():
+    """TQ_BF16 belongs to tq_qk_norm_rope and tq_tree_attention; the other calls refuse it, whatever else is right."""
+    L, c, B, H, cap = tq.lib(), ctx(4), 1, 2, 64
+    K, V = tq.CodeSet(c, B * H * cap), tq.CodeSet(c, B * H * cap, tq.TQ_LAYOUT_PAIR)
+    x, out, slots = torch.zeros(B * H, D, device="cuda"), torch.empty(B, H, D, device="cuda"), torch.zeros(1, dtype=torch.int64, device="cuda")
+    ws = torch.zeros(tq.tq_decode_workspace_size(c, B, H, H, cap) // 4 + 4, device="cuda")
+    k, v, a, o = tq.ctypes.byref(K.desc), tq.ctypes.byref(V.desc), x.data_ptr(), out.data_ptr()
+    for dt, st in ((tq.TQ_BF16, tq.TQ_ERR_INVALID_ARG), (tq.TQ_F16, tq.TQ_OK)):
+        assert L.tq_encode(c.handle, a, dt, 1, k, 0, 1, 0, None) == st
+        assert L.tq_encode_slots(c.handle, a, dt, 1, H, slots.data_ptr(), 16, k, None) == st
+        assert L.tq_decode_attention(c.handle, c.handle, a, dt, k, v, B, H, H, cap, cap, 0.1, o, ws.data_ptr(), ws.numel() * 4, None) == st
+        assert L.tq_decode_step(c.handle, c.handle, a, dt, a, a, tq.TQ_F16, k, v, B, H, H, cap, cap, 0.1, o, ws.data_ptr(), ws.numel() * 4, None) == st
+        assert L.tq_decode_step(c.handle, c.handle, a, tq.TQ_F16, a, a, dt, k, v, B, H, H, cap, cap, 0.1, o, ws.data_ptr(), ws.numel() * 4, None) == st
+        assert L.tq_decode_attention_noalloc(c.handle, c.handle, a, dt, k, v, B, H, H, cap, cap, 0.1, o, None) == st
+    torch.cuda.synchronize()
 
 
 def test_tensors_of_another_device_are_refused(monkeypatch):
