@@ -338,6 +338,21 @@ __device__ __noinline__ void join_terms(uint32_t tS, unsigned char* at, int to) 
   tmem_wait_st();
 }
 
+// Scores times their rows' factors, in place: a call for the same reason.
+template <int HN, int PC>
+__device__ __noinline__ void scale_scores(uint32_t tS, const float* c) {
+#pragma unroll 1
+  for (int i = 0; i < HN; i += PC) {
+    uint32_t s[PC];
+    tmem_ld_n(tS + i, s);
+    wait_ld(s);
+#pragma unroll
+    for (int e = 0; e < PC; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * c[i + e]);
+    tmem_st_n(tS + i, s);
+  }
+  tmem_wait_st();
+}
+
 template <int N, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreeParams p) {
   static_assert(N == 16 || N == 32 || N == 64, "rows per tile");
@@ -440,8 +455,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
       // Rows within 2^13 of the tile's largest factor are scaled down to it by powers
       // of two and share it: what fp16 drops is below 2^-22 of a row's largest
       // entry.  Where one is further below (another row is huge, it is tiny), every
-      // row keeps its own, two instructions more a score (all tiles so: 338 -> 351 us
-      // for 32 tokens of 64 heads over 131072).  Factor 0: no row, a row of zeros or
+      // row keeps its own and the scores are multiplied in tensor memory first (in
+      // the softmax it cost all calls 4%).  Factor 0: no row, a row of zeros or
       // one that is not a number.
       const float c0 = ms.c[lane & (N - 1)], c1 = ms.c[(lane + 32) & (N - 1)];
       float ct = fmaxf(c0, c1);
@@ -509,18 +524,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           const bool named = !draft || ((__shfl_sync(kFull, mw, n) >> lane) & 1u);
           return here && named;
         };
-        auto scores = [&](uint32_t(&s)[HN]) {
-          tmem_ld_n(tS, s);
-          wait_ld(s);
-          if (!shared_c) {
-#pragma unroll
-            for (int e = 0; e < HN; ++e) s[e] = __float_as_uint(__uint_as_float(s[e]) * ms.c[n0 + e]);
-          }
-        };
         if (SPLIT && draft) {  // a drafted token's two scores: each of its lanes gets the sum
           // (where this tile's P will be, which is written behind the barrier that follows)
           join_terms<HN, PC>(tS, smem + kP + sb * (2 * kPPart) + (n0 * kTreeTok + tok) * 4, quad >= 2 ? -256 : 256);
         }
+        if (!shared_c) scale_scores<HN, PC>(tS, ms.c + n0);
         // weights with the M there is; should one pass the limit (M = -inf, a
         // row's first token, does), M is raised and they are computed again
         float pr[HN];
@@ -528,7 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
           float top = -INFINITY;
           {
             uint32_t s[HN];
-            scores(s);
+            tmem_ld_n(tS, s);
+            wait_ld(s);
 #pragma unroll
             for (int e = 0; e < HN; e += 4) {
               const float4 m4 = *reinterpret_cast<const float4*>(ms.nm + n0 + e);
@@ -548,14 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 #pragma unroll
           for (int e = 0; e < HN; ++e) pr[e] = ex2(pr[e]);
           if (!bar_any(!ok || (top + lv > kLazyUp && tries < 2))) break;
-          if (bar_any(!ok)) {  // the four warps stop together
+          if (bar_any(!ok)) {  // the eight warps stop together
             ok = false;
             break;
           }
           // the rows' maxima over the tile, then new M where one is passed
           {
             uint32_t s[HN];
-            scores(s);
+            tmem_ld_n(tS, s);
+            wait_ld(s);
             float v[32];
 #pragma unroll
             for (int n = 0; n < 32; ++n) {
