@@ -2,9 +2,13 @@
 // another destination rule, instantiated apart so that the plain encoder's
 // instances stay what they are.  Tokens of one head sit hkv rows apart, so the
 // two vectors of a PAIR block meet in one warp while hkv <= 16 and are then
-// written as whole words; the others are merged with atomics.  Bound by the
-// encoder's epilogue as tq_encode is: 16384 tokens of 8 heads, fp16, b = 3, K and
-// V: 49.6 us for 80.7 MB (1.6 TB/s); 3 tokens of 32 requests: 15 us for both.
+// written as whole words; the others are merged with atomics.  16384 tokens of 8
+// heads, fp16, b = 3, K and V: 49.8 us for 80.7 MB (1.6 TB/s, 5.3 G rows/s); 3 tokens
+// of 32 requests: 15 us for both.  tq_encode takes 21.5 us for as many rows of one of
+// them (24.9 here) and 114 us for a million (179 here, slots in random order): what
+// is more is the way to a row's destination, which each of a row's four epilogue
+// warps finds, with a load that a 64-bit division and the stores wait for (0.49
+// instructions a clock and quarter against 0.56).
 #include "tq_encode128_kernel.cuh"
 
 namespace tq {

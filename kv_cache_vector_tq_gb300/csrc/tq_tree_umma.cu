@@ -37,11 +37,12 @@
 // and an and-or.  Four roles run on each quarter of the SM, each through its own
 // code once per unit, so every role is a short rolled loop: unrolled over the
 // unit, instruction fetch bounded all of them (7000-11000 clocks a unit).
-// Bound by the lookups' and the softmax's instructions: about 8000 a unit of 64
-// rows, 0.5 to 0.72 a clock and quarter.  Whole calls, three kernels: 24 us for one
-// token of 32 heads over 16384 cached (b = 4, 0.11 of the copy bandwidth); 74 us
-// for 8 requests of up to 16 drafted over 8191 (42.9 MB, 9.7 GFLOP); 335 us for 32
-// drafted of 64 heads over 131072 (b = 3, 137 GFLOP, 410 TFLOP/s).
+// A long cache is bound by the lookups' and the softmax's instructions: about 8000
+// a unit of 64 rows, 0.73 a clock and quarter; a batch, at 0.50, by the pipeline's
+// beginnings and ends as well.  Whole calls, three kernels: 24 us for one
+// token of 32 heads over 16384 cached (b = 4, 0.11 of the copy bandwidth); 75 us
+// for 8 requests of up to 16 drafted over 8191 (42.9 MB, 9.7 GFLOP); 339 us for 32
+// drafted of 64 heads over 131072 (b = 3, 137 GFLOP, 404 TFLOP/s).
 #include "tq_tree.cuh"
 
 namespace tq {
