@@ -464,8 +464,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_attend_kernel(const TreePara
 #pragma unroll
       for (int o = 16; o; o >>= 1) ct = fmaxf(ct, __shfl_xor_sync(kFull, ct, o));
       const float least = ct * 1.220703125e-4f;  // 2^-13
-      const bool shared_c = __all_sync(kFull, (c0 == 0.f || c0 >= least) && (c1 == 0.f || c1 >= least));
-      const float inv_ct = shared_c && ct > 0.f ? 1.f / ct : 0.f;
+      // (a factor whose inverse is no number scales nothing)
+      const bool shared_c = __all_sync(kFull, ct >= 1e-30f && (c0 == 0.f || c0 >= least) && (c1 == 0.f || c1 >= least));
+      const float inv_ct = shared_c ? 1.f / ct : 0.f;
       // 16-byte pieces: 16 of the leading part and 16 of the remainder per row
 #pragma unroll 4
       for (int e = tid; e < N * (SPLIT ? 32 : 16); e += 32 * kSoft) {

@@ -594,6 +594,16 @@ def test_tree_rows_of_q_do_not_depend_on_each_other(dtype, factor):
         assert (off <= rel * size[rows] + torch.finfo(dtype).eps / 2 * want.norm(dim=-1)[rows]).all(), float((off / size[rows]).max())
 
 
+@pytest.mark.parametrize("dtype,q,scale", [(torch.float32, 1e-36, 1e-4), (torch.bfloat16, 1e-36, 1e-4), (torch.float16, 1e-6, 1e-30),
+                                           (torch.bfloat16, 1.0, 1e-36), (torch.float16, 1.0, 1e-38)])
+def test_tree_scores_near_zero(dtype, q, scale):
+    """Factors of q below the normal range: scores of zero, weights that are all one."""
+    s = make_tree(dtype, 4, 4, 4, 2, 16, [70], [3], outliers=False)
+    s["q"] = (s["q"].double() * q).to(dtype)
+    got = run_tree(s, 4, 4, 16, scale=scale)
+    check_tree(got, *tree_plain(s["q"], s["k"], s["v"], s["start"], None, s["K"], s["V"], s["lens"], s["table"], 16, 2, scale, 4, 4))
+
+
 def one_term(x):
     """Rows as one fp16 in the rotated domain would hold them."""
     y = x.double() @ rotation().T
