@@ -51,7 +51,7 @@ typedef enum {
 typedef enum { TQ_MSE = 0, TQ_PROD = 1, TQ_MIXED = 2 } tq_mode;
 typedef enum { TQ_ROT_DENSE = 0, TQ_ROT_HADAMARD = 1 } tq_rot_kind;
 typedef enum { TQ_DENS_BETA = 0, TQ_DENS_GAUSS = 1 } tq_density;
-/* TQ_BF16: tq_qk_norm_rope and tq_tree_attention only. */
+/* TQ_BF16: tq_qk_norm_rope, tq_tree_attention and the tq_cache8 calls only. */
 typedef enum { TQ_F32 = 0, TQ_F16 = 1, TQ_BF16 = 2 } tq_dtype;
 typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_style;
 typedef enum { TQ_LAYOUT_TOKEN = 0, TQ_LAYOUT_PAIR = 1 } tq_layout;
@@ -469,6 +469,91 @@ tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* 
                             const tq_codes* K, const tq_codes* V, const int32_t* d_len, const int32_t* d_table,
                             int max_blocks, int block, int B, int Hq, int Hkv, float scale, void* d_out, void* d_ws,
                             size_t ws_bytes, tq_stream stream);
+
+/* ------------------------------------------------------------------ serving, 8-bit cache
+ * A paged cache at 8 bits, for the layers that a server does not want at 4 bits
+ * or fewer (the first and last ones, layers with a sliding window whose caches
+ * are small anyway).  It shares lengths, row offsets and block tables with the
+ * calls above.  One step: tq_block_tables, tq_cache8_append (norms and position
+ * rotation of q and k, and the new tokens' k and v into their pages), then
+ * tq_cache8_attention, whose rows see the cache up to and with their own token.
+ * Drafted tokens go the same way, as a chain; those that are rejected are taken
+ * back by the next step's lengths (a draft's tree: tq_tree_attention).
+ *
+ *   d_k, d_v  [pages, Hkv, block, d] codes, e4m3 numbers (16-byte aligned).
+ *   d_kscale, d_vscale [pages, Hkv] fp32: a code stands for code · scale.
+ *   d_status  one word, or NULL: a call that meets a page outside the cache sets
+ *             bit 0 of it.  The caller clears and reads it.
+ * d = 64 or 128, block a multiple of 16 up to 1024 (TQ_ERR_UNSUPPORTED otherwise).
+ * Codes need no initial values; scales are written with the first token of a
+ * block.  The calls keep nothing else anywhere.
+ */
+typedef struct {
+  uint8_t *d_k, *d_v;
+  float *d_kscale, *d_vscale;
+  int32_t* d_status;
+  int64_t pages;
+  int Hkv, block, d;
+} tq_cache8;
+
+/* New tokens: q normed and turned into d_q_out, k normed, turned and stored, v
+ * stored.
+ * d_q       [rows, Hq, d], d_k, d_v [rows, Hkv, d], all of `dtype` (F32, F16, BF16),
+ *           a token's heads contiguous, tokens q_stride (k_stride, v_stride)
+ *           elements apart.  Hq may be 0.
+ * d_wq, d_wk, eps, d_freq, rot, style, d_pos: as tq_qk_norm_rope; eps = 0: no
+ *           norms (d_wq and d_wk are then NULL).
+ * d_row_start, d_len, d_table: as tq_tree_attention.  Row i of request b is stored
+ *           at position len_b + i, whatever d_pos says; d_len are the lengths
+ *           before the call.  Rows past d_row_start[B] are neither read nor written.
+ * d_q_out   [rows, Hq, d] of `dtype`; may be d_q itself with the same stride.
+ * A block's scale is the least power of two s with |x| <= 448 s for every x of the
+ * block's tokens of this call, and not below the scale it has where it holds
+ * earlier tokens (positions below len_b); if it grows, their codes are multiplied
+ * by the old scale over the new and rounded again.  Codes are x / s rounded to
+ * nearest even, from fp32 values.  Scales stay within 2^-60 and 2^40: larger
+ * values are stored as 448 · 2^40.  A block that is given an infinity or a NaN
+ * gets a NaN for its scale (its codes stay numbers), until it is begun anew: rows
+ * that see one of its tokens are NaN.
+ * A position past the table's capacity, or whose page lies outside the cache, is
+ * not stored (see d_status).  A block that is written belongs to one request; full
+ * blocks may be shared.  Calls on one cache must be ordered on one stream.
+ * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
+ * UNSUPPORTED for rot not a multiple of 16, rows or max_blocks * block past
+ * 2^31 - 256.
+ */
+tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride, const void* d_v,
+                           int64_t v_stride, int dtype, int64_t rows, int Hq, const void* d_wq, const void* d_wk,
+                           float eps, const uint64_t* d_freq, int rot, int style, const int32_t* d_pos,
+                           const int32_t* d_row_start, const int32_t* d_len, const int32_t* d_table, int max_blocks,
+                           int B, const tq_cache8* cache, void* d_q_out, int64_t q_out_stride, tq_stream stream);
+
+/* Attention over the cache.  Row i of request b stands at position p = len_b + i
+ * (d_len as the append before it had them) and sees the stored tokens t <= p, with
+ * window > 0 only t > p - window and t < sinks (a sliding window, and the first
+ * tokens); blocks that no row sees are not looked up, so a server may free them.
+ *   out = Σ_t e^(scale·⟨q, k_t⟩) v_t / Σ_t e^(scale·⟨q, k_t⟩)
+ * d_q       [rows, Hq, d] of dtype (F32, F16, BF16), tokens q_stride elements apart.
+ * d_out     [rows, Hq, d] of dtype, contiguous.  Rows past d_row_start[B] are
+ *           neither read nor written; a row that sees nothing is zero.
+ * A page outside the cache is left out of the sums (see d_status), as are positions
+ * past the table's capacity.  Hq / Hkv any whole number.
+ * Accuracy: codes enter the products whole, scores and sums are fp32.  q enters
+ * whole for F16 and BF16 (numbers 2^-24 and less of a row's largest may lose bits),
+ * as two fp16 terms for F32; weights as one fp16 term for BF16, two otherwise.
+ * V scales outside [2^-60, 2^40] count as the nearer end.
+ * d_ws      workspace of tq_cache8_attention_workspace_size bytes (16-byte aligned;
+ *           its contents do not matter).  Calls that share one must be ordered on
+ *           one stream; captured graphs that may run at the same time need one each.
+ * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
+ * UNSUPPORTED for rows * Hq or max_blocks * block past 2^31 - 256, or
+ * (max_blocks * block / 128 + 2) * Hkv past 2^31 - 1.
+ */
+tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int Hq, int64_t rows, size_t* bytes);
+tq_status tq_cache8_attention(const void* d_q, int64_t q_stride, int dtype, int64_t rows, const int32_t* d_row_start,
+                              const int32_t* d_len, const int32_t* d_table, int max_blocks, int B, int Hq,
+                              const tq_cache8* cache, float scale, int window, int sinks, void* d_out, void* d_ws,
+                              size_t ws_bytes, tq_stream stream);
 
 /* ------------------------------------------------------------------ views
  * Canonical view of stored codes, for checking: copies vectors

@@ -27,7 +27,8 @@ EXPORTS = (
     "tq_scores_workspace_size", "tq_scores", "tq_decode_workspace_size",
     "tq_decode_attention", "tq_decode_step", "tq_decode_attention_noalloc", "tq_unpack_indices", "tq_status_poll",
     "tq_ctx_set_wait_limit", "tq_block_tables", "tq_rope_frequencies", "tq_qk_norm_rope", "tq_encode_slots",
-    "tq_tree_attention_workspace_size", "tq_tree_attention",
+    "tq_tree_attention_workspace_size", "tq_tree_attention", "tq_cache8_append", "tq_cache8_attention_workspace_size",
+    "tq_cache8_attention",
 )
 
 
@@ -56,6 +57,14 @@ class Codes(ctypes.Structure):
         ("n", ctypes.c_int64), ("d", ctypes.c_int), ("b_mse", ctypes.c_int),
         ("mode", ctypes.c_int), ("layout", ctypes.c_int),
         ("words_per_vec", ctypes.c_int), ("qjl_words_per_vec", ctypes.c_int),
+    ]
+
+
+class Cache8Desc(ctypes.Structure):
+    _fields_ = [
+        ("d_k", ctypes.c_void_p), ("d_v", ctypes.c_void_p),
+        ("d_kscale", ctypes.c_void_p), ("d_vscale", ctypes.c_void_p), ("d_status", ctypes.c_void_p),
+        ("pages", ctypes.c_int64), ("Hkv", ctypes.c_int), ("block", ctypes.c_int), ("d", ctypes.c_int),
     ]
 
 
@@ -102,6 +111,11 @@ def lib():
         "tq_tree_attention_workspace_size": ([_vp, _i, _i, _i, _i64, P(_sz)], _i),
         "tq_tree_attention": ([_vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _i, _i64, _vp, _vp, _i, P(Codes), P(Codes),
                                _vp, _vp, _i, _i, _i, _i, _i, _f, _vp, _vp, _sz, _vp], _i),
+        "tq_cache8_append": ([_vp, _i64, _vp, _i64, _vp, _i64, _i, _i64, _i, _vp, _vp, _f, _vp, _i, _i, _vp, _vp, _vp,
+                              _vp, _i, _i, P(Cache8Desc), _vp, _i64, _vp], _i),
+        "tq_cache8_attention_workspace_size": ([P(Cache8Desc), _i, _i, _i64, P(_sz)], _i),
+        "tq_cache8_attention": ([_vp, _i64, _i, _i64, _vp, _vp, _vp, _i, _i, _i, P(Cache8Desc), _f, _i, _i, _vp, _vp,
+                                 _sz, _vp], _i),
     }
     for name, (args, res) in sig.items():
         fn = getattr(L, name)
@@ -431,6 +445,85 @@ def tq_tree_attention(kctx, vctx, q, k_new, v_new, row_start, mask, K, V, lens, 
         None if mask is None else _dev(mask, i32, rows * words, "mask", dev), words, _codes(K, "K", dev),
         _codes(V, "V", dev), _dev(lens, i32, B, "lens", dev),
         None if table is None else _dev(table, i32, B * width, "table", dev), width, block, B, Hq, Hkv, scale,
+        _dev(out, ti, rows * Hq * d, "out", dev), _dev(ws, ws.dtype, 0, "ws", dev), ws.numel() * ws.element_size(),
+        _raw_stream(stream, dev)))
+
+
+class Cache8:
+    """A paged cache at 8 bits (include/tq.h, tq_cache8): k, v [pages, Hkv, block, d] float8_e4m3fn, kscale, vscale
+    [pages, Hkv], status [1] int32 (set by a call that meets a page outside the cache)."""
+
+    def __init__(self, pages, Hkv, block, d=128, device="cuda"):
+        import torch
+        self.k, self.v = (torch.zeros((pages, Hkv, block, d), dtype=torch.uint8, device=device).view(torch.float8_e4m3fn)
+                          for _ in range(2))
+        self.kscale, self.vscale = (torch.zeros((pages, Hkv), dtype=torch.float32, device=device) for _ in range(2))
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self.pages, self.Hkv, self.block, self.d = pages, Hkv, block, d
+        self.desc = Cache8Desc(self.k.data_ptr(), self.v.data_ptr(), self.kscale.data_ptr(), self.vscale.data_ptr(),
+                               self.status.data_ptr(), pages, Hkv, block, d)
+
+
+def _cache8(c, dev):
+    """Descriptor of an 8-bit cache on this device."""
+    if c.k.get_device() != dev:
+        raise ValueError("cache: an 8-bit cache on the current device is wanted")
+    return ctypes.byref(c.desc)
+
+
+def _requests(row_start, lens, table, dev):
+    """Addresses of row_start [B + 1], lens [B] and table [B, max_blocks], max_blocks and B."""
+    i32, B = _T[0].int32, lens.numel()
+    if table.dim() != 2:
+        raise ValueError("table: [B, max_blocks] is wanted")
+    width = table.shape[1]
+    return (_dev(row_start, i32, B + 1, "row_start", dev), _dev(lens, i32, B, "lens", dev),
+            _dev(table, i32, B * width, "table", dev), width, B)
+
+
+def tq_cache8_append(q, k, v, wq, wk, eps, freq, style, pos, row_start, lens, table, cache, q_out, stream=None):
+    """New tokens into an 8-bit paged cache, norms and position rotation on the way (include/tq.h).  q [rows, Hq, d] or
+    None, k, v [rows, Hkv, d]; wq, wk: [d] of q's type or None; eps = 0: no norms; freq: tq_rope_frequencies or None."""
+    torch, _, _, cur = _types()
+    dev = cur()
+    (rows, Hkv, d), ti, i32 = k.shape, k.dtype, torch.int32
+    if (Hkv, d) != (cache.Hkv, cache.d):
+        raise ValueError(f"k: rows of {cache.Hkv} heads of {cache.d} elements are wanted")
+    if v.dtype is not ti or (q is not None and (q.dtype is not ti or q_out.dtype is not ti)):
+        raise ValueError("q, k, v and q_out are of one type")
+    Hq, qp, qs, qo, qos = 0, None, 0, None, 0
+    if q is not None and q.shape[1]:
+        Hq = q.shape[1]
+        (qp, qs), (qo, qos) = _heads(q, rows, Hq, d, "q", dev), _heads(q_out, rows, Hq, d, "q_out", dev)
+    (kp, ks), (vp, vs) = _heads(k, rows, Hkv, d, "k", dev), _heads(v, rows, Hkv, d, "v", dev)
+    start, ln, tab, width, B = _requests(row_start, lens, table, dev)
+    _check("tq_cache8_append", lib().tq_cache8_append(
+        qp, qs, kp, ks, vp, vs, _type(k, "k"), rows, Hq, None if wq is None else _dev(wq, ti, d, "wq", dev),
+        None if wk is None else _dev(wk, ti, d, "wk", dev), eps,
+        None if freq is None else _dev(freq, torch.int64, 0, "freq", dev), 0 if freq is None else 2 * freq.numel(), style,
+        _dev(pos, i32, rows, "pos", dev), start, ln, tab, width, B, _cache8(cache, dev), qo, qos, _raw_stream(stream, dev)))
+
+
+def tq_cache8_attention_workspace_size(cache, B, Hq, rows):
+    n = ctypes.c_size_t()
+    _check("tq_cache8_attention_workspace_size",
+           lib().tq_cache8_attention_workspace_size(ctypes.byref(cache.desc), B, Hq, rows, ctypes.byref(n)))
+    return n.value
+
+
+def tq_cache8_attention(q, row_start, lens, table, cache, scale, out, ws, window=0, sinks=0, stream=None):
+    """Attention of q [rows, Hq, d] over an 8-bit paged cache, each row up to and with its own token, with a sliding
+    window and first tokens that stay visible where window > 0 (include/tq.h)."""
+    _, _, _, cur = _types()
+    dev = cur()
+    rows, Hq, d = q.shape
+    if d != cache.d:
+        raise ValueError(f"q: rows of {cache.d} elements are wanted")
+    ti = q.dtype
+    qp, qs = _heads(q, rows, Hq, d, "q", dev)
+    start, ln, tab, width, B = _requests(row_start, lens, table, dev)
+    _check("tq_cache8_attention", lib().tq_cache8_attention(
+        qp, qs, _type(q, "q"), rows, start, ln, tab, width, B, Hq, _cache8(cache, dev), scale, window, sinks,
         _dev(out, ti, rows * Hq * d, "out", dev), _dev(ws, ws.dtype, 0, "ws", dev), ws.numel() * ws.element_size(),
         _raw_stream(stream, dev)))
 

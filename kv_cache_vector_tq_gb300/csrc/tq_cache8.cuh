@@ -1,0 +1,239 @@
+// A paged cache held in 8 bits: what its kernels share.
+//
+// Codes are e4m3 numbers (four significant bits, 2^-9 to 448), one scale for
+// every page, KV head and side; a token at position p of a request stands at
+// place p % block of page table[p / block].  The scales are powers of two, so
+// that dividing by one is exact and a block whose scale grows is rounded again
+// only where codes fall below 2^-6.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "tq_device.cuh"
+#include "tq_internal.h"
+
+namespace tq {
+
+constexpr float kC8Lo = 8.673617379884035e-19f;  // 2^-60: the least scale
+constexpr float kC8Hi = 1099511627776.f;         // 2^40: the largest
+
+// A request's rows and length, cut to what the buffers hold.
+struct C8Seq {
+  int start, T, len;
+};
+__device__ __forceinline__ int c8_row(const int32_t* row_start, int b, int rows) {
+  return min(max(row_start[b], 0), rows);
+}
+__device__ __forceinline__ C8Seq c8_seq(const int32_t* row_start, const int32_t* len, int b, int rows) {
+  C8Seq s;
+  s.start = c8_row(row_start, b, rows);
+  s.T = max(c8_row(row_start, b + 1, rows) - s.start, 0);
+  s.len = max(len[b], 0);
+  return s;
+}
+
+// The request of slot x, where request b has the slots from key(b) =
+// row_start[b]·num / den + 2b or b (`each`) on: enough for its blocks or row tiles,
+// since floor(x) + floor(y) <= floor(x + y), and found without a sum over the
+// requests.  Whole warps call it with one x.
+__device__ __forceinline__ int c8_key(const int32_t* row_start, int b, int rows, int num, int den, int each) {
+  return (int)((int64_t)c8_row(row_start, b, rows) * num / den) + each * b;
+}
+__device__ __forceinline__ int c8_find(const int32_t* row_start, int B, int rows, int num, int den, int each, int x) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B;
+  while (n > 1) {
+    const int step = (n + 31) / 32, at = lane * step;
+    const bool below = at < n && c8_key(row_start, lo + at, rows, num, den, each) <= x;
+    const uint32_t m = __ballot_sync(kFull, below);
+    const int i = m ? 31 - __clz(m) : 0;
+    lo += i * step;
+    n = min(step, n - i * step);
+  }
+  return lo;
+}
+
+// ------------------------------------------------------------------ attention
+//   out_r = Σ_t w_rt v̂_t / Σ_t w_rt / s_t',  w_rt = 2^(z_rt + log2 s_t' - M_r),
+//   z_rt = scale·log2(e)·s_t·⟨q_r, code_t⟩,  s, s' the scales of t's block (K, V)
+// over the tokens t that row r sees: t <= p_r, and with a window W: t > p_r - W or
+// t < sinks.  The V scale stands inside the exponent, so that weights meet the codes
+// themselves and stay within fp16 for any scale; the sum of weights takes it out
+// again, one factor for the tokens of a block.
+//
+// Work: a tile is up to `tile` rows of a request and KV head, a row being one
+// (token, query head of the KV head) pair; its units are the 128-token pieces of
+// the cache that some row of it sees.  The units of all tiles, laid end to end, are
+// shared evenly among the CTAs of a grid that fits the GPU once, whatever the
+// lengths are: lengths live on the device, so a captured call serves later ones.  A
+// tile that one CTA has all of is written out by it; parts go to the CTAs' records,
+// and a second kernel joins them.
+constexpr int kC8Unit = 128;
+constexpr float kC8Log2e = 1.4426950408889634f;
+
+// A part of a tile that was begun by a CTA and not ended: where the rest is.
+struct C8Split {
+  int b, rt, h, pad;      // h < 0: none
+  int64_t u0, u1, units;  // its units among all
+};
+
+struct C8Params {
+  const void* q;
+  int64_t qs;  // stride between tokens in elements
+  int dtype;
+  const int32_t *row_start, *len, *table;
+  int rows, B, Hq, Hkv, G, max_blocks, block, d, window, sinks;
+  int64_t pages;
+  const uint8_t *k8, *v8;
+  const float *kscale, *vscale;
+  float zscale;  // scale·log2(e)
+  void* out;
+  int32_t* status;
+  C8Split* split;  // [ctas]
+  float* rec;      // [ctas][2][tile][d + 4]: m, l, 2 pad, sums; a tile that goes on from the CTA before, one that begins here
+  int ctas, tile, slots;
+};
+
+// The rows and the tokens of a tile.
+struct C8Tile {
+  int b, rt, row0, nrow;  // of the request's T·G rows
+  int start, len;
+  int i0, il;             // first and last token of the rows
+  int lo, hi;             // tokens seen by some row: [lo, hi), and [0, sinks) with a window
+  int su, lou, n;         // units of the first tokens, first unit of lo (0 where both are one run), units
+};
+__device__ __forceinline__ C8Tile c8_tile(const C8Params& p, int b, int rt) {
+  C8Tile t;
+  const C8Seq s = c8_seq(p.row_start, p.len, b, p.rows);
+  t.b = b;
+  t.rt = rt;
+  t.start = s.start;
+  t.len = s.len;
+  const int64_t row0 = (int64_t)rt * p.tile, all = (int64_t)s.T * p.G;
+  t.n = 0;
+  t.nrow = (int)(all - row0 < p.tile ? all - row0 : p.tile);
+  if (rt < 0 || t.nrow <= 0) {
+    t.nrow = 0;
+    return t;
+  }
+  t.row0 = (int)row0;
+  t.i0 = t.row0 / p.G;
+  t.il = (t.row0 + t.nrow - 1) / p.G;
+  const int64_t cap = (int64_t)p.max_blocks * p.block;
+  t.hi = (int)min((int64_t)s.len + t.il + 1, cap);
+  t.lo = 0;
+  t.su = t.lou = 0;
+  const int hiu = (t.hi + kC8Unit - 1) / kC8Unit;
+  t.n = hiu;
+  if (p.window > 0) {
+    t.lo = (int)min(max((int64_t)s.len + t.i0 - p.window + 1, (int64_t)0), cap);
+    t.su = (min(p.sinks, t.hi) + kC8Unit - 1) / kC8Unit;
+    t.lou = t.lo / kC8Unit;
+    if (t.lou <= t.su)
+      t.lou = t.su = 0;
+    else
+      t.n = t.su + max(hiu - t.lou, 0);
+  }
+  if (t.n < 1) t.n = 1;  // rows past the capacity see nothing: the unit is empty, the rows zero
+  return t;
+}
+// First token of unit u of a tile.
+__device__ __forceinline__ int c8_unit(const C8Tile& t, int u) {
+  return (u < t.su ? u : t.lou + (u - t.su)) * kC8Unit;
+}
+// The tile of slot x, the units of which stand in t.n (0: none).
+__device__ __forceinline__ int c8_slot_b(const C8Params& p, int x) {
+  int lo = 0, n = p.B;  // as c8_find, by one thread
+  while (n > 1) {
+    const int half = n >> 1;
+    if (c8_key(p.row_start, lo + half, p.rows, p.G, p.tile, 1) <= x) {
+      lo += half;
+      n -= half;
+    } else {
+      n = half;
+    }
+  }
+  return lo;
+}
+__device__ __forceinline__ int64_t c8_cut(int64_t c, int64_t units, int64_t n) { return c * units / n; }
+
+// What a CTA begins with: its units, and the slot (and units before the slot) of
+// the first.  Called by all threads of a CTA of NT threads.
+struct C8Share {
+  int64_t u0, u1, units, before;
+  int slot;
+};
+template <int NT>
+__device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[NT / 32 + 1], int64_t* found) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  C8Share s;
+  int64_t total = 0, mine = 0, before = 0;
+  // all slots are summed; where they are more threads than one pass has, they are
+  // counted again for the place of the first unit
+  for (int again = 0; again < 2; ++again) {
+    int64_t carry = 0;
+    for (int x0 = 0; x0 < p.slots; x0 += NT) {
+      const int x = x0 + tid;
+      if (again == 0 || p.slots > NT) {
+        mine = 0;
+        if (x < p.slots) {
+          const int b = c8_slot_b(p, x);
+          mine = (int64_t)c8_tile(p, b, x - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1)).n * p.Hkv;
+        }
+        int64_t in = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t a = __shfl_up_sync(kFull, in, o);
+          if (lane >= o) in += a;
+        }
+        __syncthreads();
+        if (lane == 31) sums[0][warp] = in;
+        __syncthreads();
+        int64_t base = 0, all = 0;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+          if (w < warp) base += sums[0][w];
+          all += sums[0][w];
+        }
+        before = carry + base + in - mine;
+        carry += all;
+      }
+      if (again == 1) {
+        if (x < p.slots && mine > 0 && before <= s.u0 && s.u0 < before + mine) {
+          found[0] = x;
+          found[1] = before;
+        }
+      }
+    }
+    if (again == 0) {
+      total = carry;
+      s.units = total;
+      s.u0 = c8_cut(blockIdx.x, total, p.ctas);
+      s.u1 = c8_cut(blockIdx.x + 1, total, p.ctas);
+    }
+  }
+  __syncthreads();
+  s.slot = (int)found[0];
+  s.before = found[1];
+  return s;
+}
+
+template <typename... P, typename... A>
+inline cudaError_t c8_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
+cudaError_t c8_attend(const C8Params& p, cudaStream_t st);
+
+}  // namespace tq

@@ -1,0 +1,584 @@
+// Attention over the 8-bit paged cache (tq_cache8_attention) for few rows a request:
+// single tokens, drafted chains, and every fp32 call.  tq_cache8.cuh has the
+// mathematics and the division of the work.
+//
+// A warp takes 16 tokens of a unit at a time, tokens on the 16 rows of
+// mma.m16n8k16 and up to 8·NT rows (token x query head) on its columns:
+//     Sᵀ[token][row] = K·Q̂ᵀ,   Oᵀ[coord][row] += Vᵀ·P
+// Codes become fp16 exactly (every e4m3 number is one) on the way from shared
+// memory to the operands.  The order of the coordinates along a contraction, and of
+// the coordinates in Oᵀ, is free, so that a lane's bytes are 16 in a row: of K's
+// coordinates 16c..16c+15 (and 64 more on), of V's D/8·g.. .  P's transposition from
+// the layout of a result to that of an operand is one movmatrix for 8 tokens.
+// Bytes come by asynchronous copies into slots that are each lane's own, kStages
+// groups of tokens ahead, so that no warp waits for another inside a tile; the
+// warps' states are joined at its end.
+// Rounding: q is scaled by a power of two into fp16's range, which holds fp16 and
+// bf16 numbers whole; fp32 rows are two fp16 terms (2^-22).  Weights are one fp16
+// term for bf16 outputs (2^-12 against the output's 2^-9), two for fp16 and fp32,
+// where one would cost as much as the output's own rounding or more.
+#include "tq_cache8.cuh"
+
+namespace tq {
+
+namespace {
+
+constexpr int kAtThreads = 256, kAtWarps = 8;
+constexpr float kRaise = 14.f, kFresh = 6.f;  // raise M before a weight passes 2^14; a fresh maximum sits at 2^6
+
+template <int D, int NT>
+constexpr int kStages = D == 64 ? 6 : NT == 1 ? 3 : 5;  // (two CTAs an SM with 8 rows, one with more)
+template <int D>
+constexpr int kSlot = 32 * D + 16;  // 16 tokens' K and V codes, two scales
+template <int D, int NT>
+constexpr int kRing = kAtWarps * kStages<D, NT> * kSlot<D>;
+template <int D, int NT>
+constexpr int kMerge = kAtWarps * 8 * NT * (D + 4) * 4;
+template <int D, int NT>
+constexpr int kAtSmem = kRing<D, NT> > kMerge<D, NT> ? kRing<D, NT> : kMerge<D, NT>;
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+// Two codes (the low 16 bits) as fp16.
+__device__ __forceinline__ uint32_t wide8(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t wide8_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p) {
+  if constexpr (sizeof(T) == 4) {
+    return *reinterpret_cast<const float4*>(p);
+  } else {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    float2 a, b;
+    if constexpr (std::is_same<T, __half>::value) {
+      a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
+      b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
+    } else {
+      a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.x));
+      b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u.y));
+    }
+    return make_float4(a.x, a.y, b.x, b.y);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store1(T* p, float x) {
+  if constexpr (sizeof(T) == 4)
+    *p = x;
+  else if constexpr (std::is_same<T, __half>::value)
+    *p = __float2half_rn(x);
+  else
+    *p = __float2bfloat16_rn(x);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1) c8_attend_kernel(const C8Params p) {
+  constexpr int QT = sizeof(T) == 4 ? 2 : 1;                                 // fp16 terms of q
+  constexpr int PT = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;          // of the weights
+  constexpr int TILE = 8 * NT, KP = D / 64, KS = D / 16, ST = kStages<D, NT>, SLOT = kSlot<D>, REC = D + 4;
+  constexpr bool QREG = NT * QT <= 2;  // q's operands stay in registers
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(8) uint2 qf[NT][QT][KS][32];
+  __shared__ float s_c[TILE];
+  __shared__ int s_pos[TILE];
+  __shared__ int64_t s_sums[1][kAtThreads / 32 + 1], s_found[2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  griddep_wait();
+  griddep_launch();
+  const C8Share sh = c8_share<kAtThreads>(p, s_sums, s_found);
+  C8Split split;
+  split.h = -1;
+  const uint32_t ring = smem_u32(smem) + warp * (ST * SLOT);
+  const unsigned char* ringp = smem + warp * (ST * SLOT);
+  int64_t u = sh.u0, before = sh.before;
+  int slot = sh.slot, b = u < sh.u1 ? c8_slot_b(p, slot) : 0;
+  while (u < sh.u1 && slot < p.slots) {
+    const C8Tile t = c8_tile(p, b, slot - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1));
+    const int64_t all = (int64_t)t.n * p.Hkv;
+    if (u >= before + all) {
+      before += all;
+      ++slot;
+      while (b + 1 < p.B && c8_key(p.row_start, b + 1, p.rows, p.G, p.tile, 1) <= slot) ++b;
+      continue;
+    }
+    const int h = (int)(u - before) / t.n, first = (int)(u - before) - h * t.n;
+    const int n = (int)min((int64_t)(t.n - first), sh.u1 - u);  // units here
+    __syncthreads();  // the tile before has been read
+    // ---- the rows of q, as operands
+#pragma unroll 1
+    for (int r = warp; r < TILE; r += kAtWarps) {
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int rho = t.row0 + r, i = rho / p.G;
+      if (r < t.nrow && 4 * lane < D)
+        x = load4(static_cast<const T*>(p.q) + (int64_t)(t.start + i) * p.qs + (int64_t)(h * p.G + rho - i * p.G) * D + 4 * lane);
+      float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+      // the largest to [2^10, 2^11)
+      const int ex = top > 0.f && top < INFINITY ? max((__float_as_int(top) >> 23) - 127 - 10, -100) : 0;
+      const float f = __int_as_float((127 - ex) << 23);
+      x.x *= f;
+      x.y *= f;
+      x.z *= f;
+      x.w *= f;
+      if (4 * lane < D) {
+        // coordinates 4·lane..: operand word (k-step) 4·(lane/16) + lane % 4 of lane 4r + (lane/4) % 4
+        uint2 hi, lo;
+        split2(x.x, x.y, hi.x, lo.x);
+        split2(x.z, x.w, hi.y, lo.y);
+        const int ks = 4 * (lane >> 4) + (lane & 3), to = 4 * (r & 7) + ((lane >> 2) & 3);
+        qf[r >> 3][0][ks][to] = hi;
+        if (QT == 2) qf[r >> 3][QT - 1][ks][to] = lo;
+      }
+      if (lane == 0) {
+        s_c[r] = p.zscale * __int_as_float((127 + ex) << 23);
+        s_pos[r] = r < t.nrow ? (int)min((int64_t)t.len + i, (int64_t)INT32_MAX) : -1;
+      }
+    }
+    __syncthreads();
+    uint2 bq[QREG ? NT : 1][QREG ? QT : 1][QREG ? KS : 1];
+    if constexpr (QREG) {
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int y = 0; y < QT; ++y)
+#pragma unroll
+          for (int k = 0; k < KS; ++k) bq[x][y][k] = qf[x][y][k][lane];
+    }
+    float cf[NT][2], M[NT][2], L[NT][2], O[NT][KS][4];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        cf[x][e] = s_c[8 * x + 2 * c + e];
+        M[x][e] = -INFINITY;
+        L[x][e] = 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < KS; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) O[x][i][e] = 0.f;
+    }
+    // tokens that every row of the tile sees: up to seen, and from every on or within the first ones
+    const int64_t seen = (int64_t)t.len + t.i0;
+    const int64_t every = p.window > 0 ? (int64_t)t.len + t.il - p.window + 1 : 0;
+    const int firsts = p.window > 0 ? p.sinks : 0;
+    // pages of 32 groups of tokens, a lane each, 32 ahead
+    int pgA = -1, offA = 0, pgB, offB;
+    auto pages = [&](int i, int& pg, int& off) {
+      pg = -1;
+      off = 0;
+      if (i < n) {
+        const int t0 = c8_unit(t, first + i) + 16 * warp;
+        if (t0 < t.hi && (t0 + 16 > t.lo || t0 < firsts)) {
+          const int j = t0 / p.block;
+          off = t0 - j * p.block;
+          pg = p.table[(int64_t)t.b * p.max_blocks + j];
+          if (pg < 0 || pg >= p.pages) {
+            pg = -1;
+            if (p.status) atomicOr(p.status, 1);
+          }
+        }
+      }
+    };
+    pages(lane, pgB, offB);
+    uint32_t live = 0;  // which of the groups asked for are there, the last one in bit 0
+    auto issue = [&](int i) {
+      if ((i & 31) == 0) {
+        pgA = pgB;
+        offA = offB;
+        pages(i + 32 + lane, pgB, offB);
+      }
+      const int pg = __shfl_sync(kFull, pgA, i & 31), off = __shfl_sync(kFull, offA, i & 31);
+      live = (live << 1) | (uint32_t)(pg >= 0);
+      if (pg >= 0) {
+        const int64_t blk = (int64_t)pg * p.Hkv + h, row = blk * p.block + off;
+        const uint32_t to = ring + (uint32_t)(i % ST) * SLOT;
+        const uint8_t* k = p.k8 + row * D;
+        const uint8_t* v = p.v8 + row * D;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int x = 0; x < KP; ++x)
+            copy_async<16>(to + ((r * KP + x) * 32 + lane) * 16, k + (g + 8 * r) * D + (c + 4 * x) * 16);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          copy_async<D / 8>(to + 16 * D + (x * 32 + lane) * (D / 8), v + (2 * c + (x & 1) + 8 * (x >> 1)) * D + g * (D / 8));
+        if (lane < 2) copy_async<4>(to + 32 * D + 4 * lane, (lane ? p.vscale : p.kscale) + blk);
+      }
+      asm volatile("cp.async.commit_group;\n" ::: "memory");
+    };
+#pragma unroll 1
+    for (int i = 0; i < ST - 1; ++i) issue(i);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      asm volatile("cp.async.wait_group %0;\n" ::"n"(ST - 2) : "memory");
+      __syncwarp();
+      const bool on = (live >> (ST - 2)) & 1;
+      const unsigned char* sl = ringp + (i % ST) * SLOT;
+      if (on) {
+        // ---- scores
+        float s[NT][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < KP; ++x) {
+          const uint4 ka = *reinterpret_cast<const uint4*>(sl + (x * 32 + lane) * 16);
+          const uint4 kb = *reinterpret_cast<const uint4*>(sl + ((KP + x) * 32 + lane) * 16);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t a0 = wide8(wa[j]), a1 = wide8(wb[j]), a2 = wide8_hi(wa[j]), a3 = wide8_hi(wb[j]);
+#pragma unroll
+            for (int y = 0; y < NT; ++y)
+#pragma unroll
+              for (int q = 0; q < QT; ++q) {
+                const uint2 bb = QREG ? bq[QREG ? y : 0][QREG ? q : 0][QREG ? 4 * x + j : 0] : qf[y][q][4 * x + j][lane];
+                mma16816(s[y], a0, a1, a2, a3, bb.x, bb.y);
+              }
+          }
+        }
+        const int t0 = c8_unit(t, first + i) + 16 * warp;
+        const float ks = *reinterpret_cast<const float*>(sl + 32 * D);
+        float vs = *reinterpret_cast<const float*>(sl + 32 * D + 4);
+        vs = vs < kC8Lo ? kC8Lo : vs > kC8Hi ? kC8Hi : vs;  // a NaN stays one
+        const float lv = log2f(vs), iv = 1.f / vs;
+        float z[NT][4];
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) z[x][e] = fmaf(s[x][e], cf[x][e & 1] * ks, lv);
+        const bool masked = !(t0 + 15 <= seen && t0 + 15 < t.hi && (t0 >= every || t0 + 15 < firsts));
+        if (masked) {
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int at = t0 + g + 8 * (e >> 1), pos = s_pos[8 * x + 2 * c + (e & 1)];
+              const bool sees = at < t.hi && at <= pos && (p.window == 0 || (int64_t)at > (int64_t)pos - p.window || at < firsts);
+              if (!sees) z[x][e] = -INFINITY;
+            }
+        }
+        bool up = false;
+#pragma unroll
+        for (int x = 0; x < NT; ++x)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) up |= z[x][e] > M[x][e & 1] + kRaise;
+        if (__any_sync(kFull, up)) {
+#pragma unroll
+          for (int x = 0; x < NT; ++x)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(z[x][e], z[x][e + 2]);
+#pragma unroll
+              for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+              if (top > M[x][e] + kRaise) {
+                const float m = top - kFresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
+                M[x][e] = m;
+                L[x][e] *= f;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                  O[x][k][e] *= f;
+                  O[x][k][e + 2] *= f;
+                }
+              }
+            }
+        }
+        // ---- weights, transposed
+        uint32_t bp[NT][PT][2];
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float m = M[x][e & 1];
+            w[e] = ex2(z[x][e] - (m == -INFINITY ? 0.f : m));
+          }
+          L[x][0] = fmaf(w[0] + w[2], iv, L[x][0]);
+          L[x][1] = fmaf(w[1] + w[3], iv, L[x][1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t hi, lo;
+            split2(w[2 * e], w[2 * e + 1], hi, lo);
+            bp[x][0][e] = transpose8(hi);
+            if (PT == 2) bp[x][PT - 1][e] = transpose8(lo);
+          }
+        }
+        // ---- values
+        uint32_t wv[4][D / 32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const unsigned char* vp = sl + 16 * D + (x * 32 + lane) * (D / 8);
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vp);
+            wv[x][0] = v.x;
+            wv[x][1] = v.y;
+            wv[x][D / 32 - 2] = v.z;
+            wv[x][D / 32 - 1] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(vp);
+            wv[x][0] = v.x;
+            wv[x][1] = v.y;
+          }
+        }
+        if (masked) {  // what no row sees may be anything, and 0 times it a NaN
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int at = t0 + 2 * c + (x & 1) + 8 * (x >> 1);
+            if (!(at < t.hi && (at >= t.lo || at < firsts)))
+#pragma unroll
+              for (int k = 0; k < D / 32; ++k) wv[x][k] = 0;
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+#pragma unroll
+          for (int o = 0; o < 2; ++o) {
+            const uint32_t lo = __byte_perm(wv[0][k], wv[1][k], o ? 0x7362 : 0x5140);
+            const uint32_t hi = __byte_perm(wv[2][k], wv[3][k], o ? 0x7362 : 0x5140);
+            const uint32_t a0 = wide8(lo), a1 = wide8_hi(lo), a2 = wide8(hi), a3 = wide8_hi(hi);
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+              for (int q = 0; q < PT; ++q) mma16816(O[x][2 * k + o], a0, a1, a2, a3, bp[x][q][0], bp[x][q][1]);
+          }
+        }
+      }
+      __syncwarp();  // the slot's scales have been read
+      issue(i + ST - 1);
+    }
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    __syncthreads();  // the ring is free: the warps' states go there
+    float* mg = reinterpret_cast<float*>(smem) + warp * (TILE * REC);
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = L[x][e];
+#pragma unroll
+        for (int o = 4; o <= 16; o <<= 1) l += __shfl_xor_sync(kFull, l, o);
+        float* to = mg + (8 * x + 2 * c + e) * REC;
+        // (a row all of whose scores are no numbers has no maximum: its NaN goes on)
+        if (g == 0) *reinterpret_cast<float2*>(to) = make_float2(M[x][e] == -INFINITY && l != l ? 0.f : M[x][e], l);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+          *reinterpret_cast<float2*>(to + 4 + g * (D / 8) + 2 * k) = make_float2(O[x][k][e], O[x][k][e + 2]);
+      }
+    }
+    __syncthreads();
+    const bool whole = first == 0 && n == t.n;
+#pragma unroll 1
+    for (int r = warp; r < t.nrow; r += kAtWarps) {
+      constexpr int E = D / 32;  // coordinates of a lane
+      const float* from = reinterpret_cast<const float*>(smem) + r * REC;
+      float m[kAtWarps], top = -INFINITY, l = 0.f, o[E];
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) {
+        m[w] = from[w * (TILE * REC)];
+        top = fmaxf(top, m[w]);
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAtWarps; ++w) {
+        const float f = m[w] == -INFINITY ? 0.f : ex2(m[w] - top);
+        if (f != 0.f) {
+          l = fmaf(from[w * (TILE * REC) + 1], f, l);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(from[w * (TILE * REC) + 4 + E * lane + e], f, o[e]);
+        }
+      }
+      if (whole) {
+        const int rho = t.row0 + r, i = rho / p.G;
+        T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + h * p.G + rho - i * p.G) * D + E * lane;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+        for (int e = 0; e < E; ++e) store1(to + e, o[e] * inv);
+      } else {
+        float* to = p.rec + (((int64_t)blockIdx.x * 2 + (first == 0)) * TILE + r) * REC;
+        if (lane == 0) *reinterpret_cast<float2*>(to) = make_float2(top, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) to[4 + E * lane + e] = o[e];
+      }
+    }
+    if (first == 0 && !whole) {
+      split.b = b;
+      split.rt = t.rt;
+      split.h = h;
+      split.u0 = before + (int64_t)h * t.n;
+      split.u1 = split.u0 + t.n;
+    }
+    u += n;
+  }
+  split.units = sh.units;
+  if (tid == 0) p.split[blockIdx.x] = split;
+}
+
+// The parts of the tiles that several CTAs worked on.  A CTA joins eight rows of
+// the tile that CTA blockIdx.x began and did not end, a warp a row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) c8_join_kernel(const C8Params p) {
+  constexpr int REC = D + 4, E = D / 32;
+  griddep_wait();
+  griddep_launch();
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const C8Split s = p.split[c0];
+  if (s.h < 0) return;
+  const C8Tile t = c8_tile(p, s.b, s.rt);
+  if (r >= t.nrow) return;
+  const int parts = (int)((s.u1 * p.ctas - 1) / s.units) - c0 + 1;
+  const int64_t step = 2 * (int64_t)p.tile * REC;
+  const float* own = p.rec + (((int64_t)c0 * 2 + 1) * p.tile + r) * REC;
+  const float* more = p.rec + (int64_t)r * REC;  // of CTA k: + k·step
+  float M = -INFINITY, L = 0.f, o[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) o[e] = 0.f;
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const int k = k0 + lane;
+    bool on = k < parts;
+    if (on && k > 0 && s.units < p.ctas) on = c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas);
+    float m = -INFINITY, l = 0.f;
+    if (on) {
+      const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
+      m = ml.x;
+      l = ml.y;
+    }
+    on = on && l != 0.f;  // saw nothing (a NaN goes on)
+    float top = on ? m : -INFINITY;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+    const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
+    const float fa = M == -INFINITY ? 0.f : ex2(M - use);
+    const float f = on ? ex2(m - use) : 0.f;
+    float ls = on ? l * f : 0.f;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
+    L = L * fa + ls;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= fa;
+    uint32_t todo = __ballot_sync(kFull, on);
+    while (todo) {  // eight records at a time, all their loads in flight
+      float a[8][E], fk[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        fk[q] = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) a[q][e] = 0.f;
+        if (todo) {
+          const int kk = __ffs(todo) - 1;
+          todo &= todo - 1;
+          fk[q] = __shfl_sync(kFull, f, kk);
+          const float* from = (k0 + kk == 0 ? own : more + (c0 + k0 + kk) * step) + 4 + E * lane;
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[q][e] = from[e];
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(a[q][e], fk[q], o[e]);
+    }
+    M = nm;
+  }
+  const int rho = t.row0 + r, i = rho / p.G;
+  T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+  for (int e = 0; e < E; ++e) store1(to + e, o[e] * inv);
+}
+
+template <typename T, int D, int NT>
+cudaError_t run_attend(const C8Params& p, cudaStream_t st) {
+  static PerDeviceValue attr;
+  cudaError_t e = smem_attr_once(attr, (const void*)c8_attend_kernel<T, D, NT>, kAtSmem<D, NT>);
+  if (e == cudaSuccess) e = c8_launch(c8_attend_kernel<T, D, NT>, dim3(p.ctas), kAtThreads, kAtSmem<D, NT>, st, p);
+  if (e == cudaSuccess) e = c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, NT), 256, 0, st, p);
+  return e;
+}
+template <typename T, int D>
+cudaError_t run_attend_n(const C8Params& p, cudaStream_t st) {
+  return p.tile == 8 ? run_attend<T, D, 1>(p, st) : p.tile == 16 ? run_attend<T, D, 2>(p, st) : run_attend<T, D, 4>(p, st);
+}
+template <typename T>
+cudaError_t run_attend_d(const C8Params& p, cudaStream_t st) {
+  return p.d == 64 ? run_attend_n<T, 64>(p, st) : run_attend_n<T, 128>(p, st);
+}
+
+size_t al256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Rows of a tile: the smallest that hold a mean request's.
+int tile_rows(int64_t rows, int B, int G) {
+  const int64_t mean = (rows * G + B - 1) / B;
+  return mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+}
+int grid_ctas(int tile, int dtype) { return num_sms() * (tile == 8 && dtype != TQ_F32 ? 2 : 1); }
+
+}  // namespace
+
+size_t cache8_ws_bytes(int d, int B, int Hq, int Hkv, int64_t rows) {
+  const int tile = tile_rows(rows, B, Hq / Hkv);
+  const size_t ctas = (size_t)num_sms() * 2;
+  return al256(ctas * sizeof(C8Split)) + ctas * 2 * tile * (d + 4) * 4;
+}
+
+tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream) {
+  const tq_cache8& c = *a.cache;
+  C8Params p{};
+  p.q = a.q;
+  p.qs = a.q_stride;
+  p.dtype = a.dtype;
+  p.row_start = a.row_start;
+  p.len = a.len;
+  p.table = a.table;
+  p.rows = (int)a.rows;
+  p.B = a.B;
+  p.Hq = a.Hq;
+  p.Hkv = c.Hkv;
+  p.G = a.Hq / c.Hkv;
+  p.max_blocks = a.max_blocks;
+  p.block = c.block;
+  p.d = c.d;
+  p.window = a.window;
+  p.sinks = a.window > 0 ? a.sinks : 0;
+  p.pages = c.pages;
+  p.k8 = c.d_k;
+  p.v8 = c.d_v;
+  p.kscale = c.d_kscale;
+  p.vscale = c.d_vscale;
+  p.zscale = a.scale * kC8Log2e;
+  p.out = a.out;
+  p.status = c.d_status;
+  p.tile = tile_rows(a.rows, a.B, p.G);
+  p.ctas = grid_ctas(p.tile, a.dtype);
+  p.split = static_cast<C8Split*>(a.ws);
+  p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + al256((size_t)num_sms() * 2 * sizeof(C8Split)));
+  const int64_t slots = a.rows * p.G / p.tile + a.B;
+  const int64_t most = (int64_t)a.max_blocks * c.block / kC8Unit + 2;  // units of a tile
+  if (slots > INT32_MAX || most * p.Hkv > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+  p.slots = (int)slots;
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (a.dtype) {
+    case TQ_F32: e = run_attend_d<float>(p, stream); break;
+    case TQ_F16: e = run_attend_d<__half>(p, stream); break;
+    case TQ_BF16: e = run_attend_d<__nv_bfloat16>(p, stream); break;
+  }
+  return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
+}
+
+}  // namespace tq

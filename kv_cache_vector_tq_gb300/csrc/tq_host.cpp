@@ -1097,4 +1097,112 @@ tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* 
   return launch_tree(kc, vc, a, (cudaStream_t)stream);
 }
 
+// What every call on an 8-bit cache checks of it.
+static tq_status check_cache8(const tq_cache8* c) {
+  if (!c || c->pages <= 0 || c->Hkv <= 0 || c->block <= 0 || c->d <= 0) return TQ_ERR_INVALID_ARG;
+  if (!c->d_k || !c->d_v || !c->d_kscale || !c->d_vscale || !al16(c->d_k) || !al16(c->d_v)) return TQ_ERR_INVALID_ARG;
+  if (((uintptr_t)c->d_kscale | (uintptr_t)c->d_vscale | (uintptr_t)c->d_status) & 3u) return TQ_ERR_INVALID_ARG;
+  if ((c->d != 64 && c->d != 128) || c->block % 16 != 0 || c->block > 1024) return TQ_ERR_UNSUPPORTED;
+  return TQ_OK;
+}
+
+tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride, const void* d_v,
+                           int64_t v_stride, int dtype, int64_t rows, int Hq, const void* d_wq, const void* d_wk,
+                           float eps, const uint64_t* d_freq, int rot, int style, const int32_t* d_pos,
+                           const int32_t* d_row_start, const int32_t* d_len, const int32_t* d_table, int max_blocks,
+                           int B, const tq_cache8* cache, void* d_q_out, int64_t q_out_stride, tq_stream stream) {
+  tq_status st = check_cache8(cache);
+  if (st != TQ_OK) return st;
+  const int sz = dtype_size(dtype), d = cache->d, Hkv = cache->Hkv;
+  if (!sz || rows < 0 || Hq < 0 || B <= 0 || max_blocks <= 0 || rot < 0 || rot > d) return TQ_ERR_INVALID_ARG;
+  if (style != TQ_ROPE_HALF && style != TQ_ROPE_INTERLEAVED) return TQ_ERR_INVALID_ARG;
+  if (!(eps >= 0.f) || !std::isfinite(eps) || (eps == 0.f && (d_wq || d_wk))) return TQ_ERR_INVALID_ARG;
+  if ((Hq > 0 && (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d)) || k_stride < (int64_t)Hkv * d ||
+      v_stride < (int64_t)Hkv * d)
+    return TQ_ERR_INVALID_ARG;
+  if (rot % 16 != 0 || rows > INT32_MAX - 255 || (int64_t)max_blocks * cache->block > INT32_MAX - 255)
+    return TQ_ERR_UNSUPPORTED;
+  if (rows == 0) return TQ_OK;
+  if ((Hq > 0 && (!d_q || !d_q_out)) || !d_k || !d_v || !d_pos || !d_row_start || !d_len || !d_table ||
+      (rot > 0 && !d_freq))
+    return TQ_ERR_INVALID_ARG;
+  if (!al16(d_q) || !al16(d_k) || !al16(d_v) || !al16(d_q_out) || !al16(d_wq) || !al16(d_wk) || ((uintptr_t)d_freq & 7u))
+    return TQ_ERR_INVALID_ARG;
+  if (((uintptr_t)d_pos | (uintptr_t)d_row_start | (uintptr_t)d_len | (uintptr_t)d_table) & 3u) return TQ_ERR_INVALID_ARG;
+  if ((Hq > 0 && (q_stride * sz % 16 || q_out_stride * sz % 16)) || k_stride * sz % 16 || v_stride * sz % 16)
+    return TQ_ERR_INVALID_ARG;
+  Cache8AppendArgs a;
+  a.q = d_q;
+  a.k = d_k;
+  a.v = d_v;
+  a.wq = d_wq;
+  a.wk = d_wk;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rows = rows;
+  a.q_out_stride = q_out_stride;
+  a.dtype = dtype;
+  a.Hq = Hq;
+  a.rot = rot;
+  a.style = style;
+  a.max_blocks = max_blocks;
+  a.B = B;
+  a.eps = eps;
+  a.freq = d_freq;
+  a.pos = d_pos;
+  a.row_start = d_row_start;
+  a.len = d_len;
+  a.table = d_table;
+  a.cache = cache;
+  a.q_out = d_q_out;
+  return launch_cache8_append(a, (cudaStream_t)stream);
+}
+
+tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int Hq, int64_t rows, size_t* bytes) {
+  const tq_status st = check_cache8(cache);
+  if (st != TQ_OK) return st;
+  if (!bytes || B <= 0 || Hq <= 0 || Hq % cache->Hkv != 0 || rows < 0) return TQ_ERR_INVALID_ARG;
+  if (rows > (INT32_MAX - 255) / Hq) return TQ_ERR_UNSUPPORTED;
+  *bytes = cache8_ws_bytes(cache->d, B, Hq, cache->Hkv, rows);
+  return TQ_OK;
+}
+
+tq_status tq_cache8_attention(const void* d_q, int64_t q_stride, int dtype, int64_t rows, const int32_t* d_row_start,
+                              const int32_t* d_len, const int32_t* d_table, int max_blocks, int B, int Hq,
+                              const tq_cache8* cache, float scale, int window, int sinks, void* d_out, void* d_ws,
+                              size_t ws_bytes, tq_stream stream) {
+  const tq_status st = check_cache8(cache);
+  if (st != TQ_OK) return st;
+  const int sz = dtype_size(dtype);
+  if (!sz || rows < 0 || B <= 0 || Hq <= 0 || Hq % cache->Hkv != 0 || max_blocks <= 0 || window < 0 || sinks < 0)
+    return TQ_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale) || q_stride < (int64_t)Hq * cache->d || q_stride * sz % 16)
+    return TQ_ERR_INVALID_ARG;
+  if (rows > (INT32_MAX - 255) / Hq || (int64_t)max_blocks * cache->block > INT32_MAX - 255) return TQ_ERR_UNSUPPORTED;
+  if (rows == 0) return TQ_OK;
+  if (!d_q || !d_out || !d_ws || !d_row_start || !d_len || !d_table) return TQ_ERR_INVALID_ARG;
+  if (!al16(d_q) || !al16(d_out) || !al16(d_ws)) return TQ_ERR_INVALID_ARG;
+  if (((uintptr_t)d_row_start | (uintptr_t)d_len | (uintptr_t)d_table) & 3u) return TQ_ERR_INVALID_ARG;
+  if (ws_bytes < cache8_ws_bytes(cache->d, B, Hq, cache->Hkv, rows)) return TQ_ERR_INVALID_ARG;
+  Cache8AttendArgs a;
+  a.q = d_q;
+  a.q_stride = q_stride;
+  a.rows = rows;
+  a.dtype = dtype;
+  a.max_blocks = max_blocks;
+  a.B = B;
+  a.Hq = Hq;
+  a.window = window;
+  a.sinks = sinks;
+  a.row_start = d_row_start;
+  a.len = d_len;
+  a.table = d_table;
+  a.cache = cache;
+  a.scale = scale;
+  a.out = d_out;
+  a.ws = d_ws;
+  return launch_cache8_attention(a, (cudaStream_t)stream);
+}
+
 }  // extern "C"

@@ -139,6 +139,28 @@ struct TreeArgs {
 };
 size_t tree_ws_bytes(int B, int Hq, int Hkv, int64_t R);
 tq_status launch_tree(const DevCtx& kc, const DevCtx& vc, const TreeArgs& a, cudaStream_t stream);
+struct Cache8AppendArgs {
+  const void *q, *k, *v, *wq, *wk;
+  int64_t q_stride, k_stride, v_stride, rows, q_out_stride;
+  int dtype, Hq, rot, style, max_blocks, B;
+  float eps;
+  const uint64_t* freq;
+  const int32_t *pos, *row_start, *len, *table;
+  const tq_cache8* cache;
+  void* q_out;
+};
+tq_status launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t stream);
+struct Cache8AttendArgs {
+  const void* q;
+  int64_t q_stride, rows;
+  int dtype, max_blocks, B, Hq, window, sinks;
+  const int32_t *row_start, *len, *table;
+  const tq_cache8* cache;
+  float scale;
+  void *out, *ws;
+};
+size_t cache8_ws_bytes(int d, int B, int Hq, int Hkv, int64_t rows);
+tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream);
 // SM count of the current device (cached per device).
 int num_sms();
 // Current device, or -1 if the runtime cannot tell.
