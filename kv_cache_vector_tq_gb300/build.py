@@ -22,7 +22,7 @@ SOURCES = ["tq_host.cpp", "tq_encode.cu", "tq_encode_wht.cu", "tq_encode_umma.cu
            "tq_scores.cu",
            "tq_decode.cu", "tq_decode_k1.cu", "tq_decode_k2.cu", "tq_decode_k3.cu", "tq_decode_k4.cu",
            "tq_decode_prod.cu", "tq_decode_mixed.cu", "tq_serve.cu", "tq_tree.cu", "tq_tree_umma.cu",
-           "tq_cache8_append.cu", "tq_cache8_attend.cu"]
+           "tq_cache8_append.cu", "tq_cache8_attend.cu", "tq_cache8_umma.cu"]
 
 
 def _nvcc():

@@ -10,6 +10,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "tq_device.cuh"
 #include "tq_internal.h"
 
@@ -219,6 +221,68 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
   return s;
 }
 
+// A run of units of one tile and KV head: units [first, first + n) of it.
+struct C8Seg {
+  C8Tile t;
+  int h, first, n;
+  int64_t u0;  // the tile's first unit among all
+};
+struct C8Walk {
+  int64_t u, u1, before;
+  int slot, b;
+};
+__device__ __forceinline__ C8Walk c8_walk(const C8Params& p, const C8Share& s) {
+  return C8Walk{s.u0, s.u1, s.before, s.slot, s.u0 < s.u1 ? c8_slot_b(p, s.slot) : 0};
+}
+__device__ __forceinline__ bool c8_next(const C8Params& p, C8Walk& w, C8Seg& g) {
+  while (w.u < w.u1 && w.slot < p.slots) {
+    g.t = c8_tile(p, w.b, w.slot - c8_key(p.row_start, w.b, p.rows, p.G, p.tile, 1));
+    const int64_t all = (int64_t)g.t.n * p.Hkv;
+    if (w.u < w.before + all) {
+      const int at = (int)(w.u - w.before);
+      g.h = at / g.t.n;
+      g.first = at - g.h * g.t.n;
+      g.n = (int)min((int64_t)(g.t.n - g.first), w.u1 - w.u);
+      g.u0 = w.before + (int64_t)g.h * g.t.n;
+      w.u += g.n;
+      return true;
+    }
+    w.before += all;
+    ++w.slot;
+    while (w.b + 1 < p.B && c8_key(p.row_start, w.b + 1, p.rows, p.G, p.tile, 1) <= w.slot) ++w.b;
+  }
+  return false;
+}
+
+template <typename T>
+__device__ __forceinline__ void c8_store1(T* p, float x) {
+  if constexpr (sizeof(T) == 4)
+    *p = x;
+  else if constexpr (std::is_same<T, __half>::value)
+    *p = __float2half_rn(x);
+  else
+    *p = __float2bfloat16_rn(x);
+}
+// Two codes as fp16: the low 16 bits of w, or the high ones.
+__device__ __forceinline__ uint32_t c8_wide(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+__device__ __forceinline__ uint32_t c8_wide_hi(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+// The power of two that takes a row's largest magnitude to [2^10, 2^11): its exponent.
+__device__ __forceinline__ int c8_row_exp(float top) {
+  return top > 0.f && top < INFINITY ? max((__float_as_int(top) >> 23) - 127 - 10, -100) : 0;
+}
+__device__ __forceinline__ float c8_pow2(int e) { return __int_as_float((127 + e) << 23); }
+// A V scale as the exponents take it (a NaN stays one).
+__device__ __forceinline__ float c8_vscale(float s) { return s < kC8Lo ? kC8Lo : s > kC8Hi ? kC8Hi : s; }
+constexpr float kC8Raise = 14.f, kC8Fresh = 6.f;  // raise M before a weight passes 2^14; a fresh maximum sits at 2^6
+
 template <typename... P, typename... A>
 inline cudaError_t c8_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
@@ -234,6 +298,6 @@ inline cudaError_t c8_launch(void (*kernel)(P...), dim3 grid, int threads, size_
   return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
-cudaError_t c8_attend(const C8Params& p, cudaStream_t st);
+cudaError_t c8_attend_umma(const C8Params& p, cudaStream_t st);
 
 }  // namespace tq

@@ -24,7 +24,6 @@ namespace tq {
 namespace {
 
 constexpr int kAtThreads = 256, kAtWarps = 8;
-constexpr float kRaise = 14.f, kFresh = 6.f;  // raise M before a weight passes 2^14; a fresh maximum sits at 2^6
 
 template <int D, int NT>
 constexpr int kStages = D == 64 ? 6 : NT == 1 ? 3 : 5;  // (two CTAs an SM with 8 rows, one with more)
@@ -43,17 +42,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
-// Two codes (the low 16 bits) as fp16.
-__device__ __forceinline__ uint32_t wide8(uint32_t w) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
-  return r;
-}
-__device__ __forceinline__ uint32_t wide8_hi(uint32_t w) {
-  uint32_t r;
-  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, h;\n}\n" : "=r"(r) : "r"(w));
-  return r;
 }
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -77,16 +65,6 @@ __device__ __forceinline__ float4 load4(const T* p) {
     return make_float4(a.x, a.y, b.x, b.y);
   }
 }
-template <typename T>
-__device__ __forceinline__ void store1(T* p, float x) {
-  if constexpr (sizeof(T) == 4)
-    *p = x;
-  else if constexpr (std::is_same<T, __half>::value)
-    *p = __float2half_rn(x);
-  else
-    *p = __float2bfloat16_rn(x);
-}
-
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1) c8_attend_kernel(const C8Params p) {
   constexpr int QT = sizeof(T) == 4 ? 2 : 1;                                 // fp16 terms of q
@@ -106,19 +84,11 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
   split.h = -1;
   const uint32_t ring = smem_u32(smem) + warp * (ST * SLOT);
   const unsigned char* ringp = smem + warp * (ST * SLOT);
-  int64_t u = sh.u0, before = sh.before;
-  int slot = sh.slot, b = u < sh.u1 ? c8_slot_b(p, slot) : 0;
-  while (u < sh.u1 && slot < p.slots) {
-    const C8Tile t = c8_tile(p, b, slot - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1));
-    const int64_t all = (int64_t)t.n * p.Hkv;
-    if (u >= before + all) {
-      before += all;
-      ++slot;
-      while (b + 1 < p.B && c8_key(p.row_start, b + 1, p.rows, p.G, p.tile, 1) <= slot) ++b;
-      continue;
-    }
-    const int h = (int)(u - before) / t.n, first = (int)(u - before) - h * t.n;
-    const int n = (int)min((int64_t)(t.n - first), sh.u1 - u);  // units here
+  C8Walk walk = c8_walk(p, sh);
+  C8Seg seg;
+  while (c8_next(p, walk, seg)) {
+    const C8Tile& t = seg.t;
+    const int h = seg.h, first = seg.first, n = seg.n;  // units here
     __syncthreads();  // the tile before has been read
     // ---- the rows of q, as operands
 #pragma unroll 1
@@ -130,9 +100,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       float top = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-      // the largest to [2^10, 2^11)
-      const int ex = top > 0.f && top < INFINITY ? max((__float_as_int(top) >> 23) - 127 - 10, -100) : 0;
-      const float f = __int_as_float((127 - ex) << 23);
+      const int ex = c8_row_exp(top);
+      const float f = c8_pow2(-ex);
       x.x *= f;
       x.y *= f;
       x.z *= f;
@@ -147,7 +116,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         if (QT == 2) qf[r >> 3][QT - 1][ks][to] = lo;
       }
       if (lane == 0) {
-        s_c[r] = p.zscale * __int_as_float((127 + ex) << 23);
+        s_c[r] = p.zscale * c8_pow2(ex);
         s_pos[r] = r < t.nrow ? (int)min((int64_t)t.len + i, (int64_t)INT32_MAX) : -1;
       }
     }
@@ -244,7 +213,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = wide8(wa[j]), a1 = wide8(wb[j]), a2 = wide8_hi(wa[j]), a3 = wide8_hi(wb[j]);
+            const uint32_t a0 = c8_wide(wa[j]), a1 = c8_wide(wb[j]), a2 = c8_wide_hi(wa[j]), a3 = c8_wide_hi(wb[j]);
 #pragma unroll
             for (int y = 0; y < NT; ++y)
 #pragma unroll
@@ -256,8 +225,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         }
         const int t0 = c8_unit(t, first + i) + 16 * warp;
         const float ks = *reinterpret_cast<const float*>(sl + 32 * D);
-        float vs = *reinterpret_cast<const float*>(sl + 32 * D + 4);
-        vs = vs < kC8Lo ? kC8Lo : vs > kC8Hi ? kC8Hi : vs;  // a NaN stays one
+        const float vs = c8_vscale(*reinterpret_cast<const float*>(sl + 32 * D + 4));
         const float lv = log2f(vs), iv = 1.f / vs;
         float z[NT][4];
 #pragma unroll
@@ -279,7 +247,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up |= z[x][e] > M[x][e & 1] + kRaise;
+          for (int e = 0; e < 4; ++e) up |= z[x][e] > M[x][e & 1] + kC8Raise;
         if (__any_sync(kFull, up)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
@@ -288,8 +256,8 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
               float top = fmaxf(z[x][e], z[x][e + 2]);
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-              if (top > M[x][e] + kRaise) {
-                const float m = top - kFresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
+              if (top > M[x][e] + kC8Raise) {
+                const float m = top - kC8Fresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
                 M[x][e] = m;
                 L[x][e] *= f;
 #pragma unroll
@@ -352,7 +320,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
           for (int o = 0; o < 2; ++o) {
             const uint32_t lo = __byte_perm(wv[0][k], wv[1][k], o ? 0x7362 : 0x5140);
             const uint32_t hi = __byte_perm(wv[2][k], wv[3][k], o ? 0x7362 : 0x5140);
-            const uint32_t a0 = wide8(lo), a1 = wide8_hi(lo), a2 = wide8(hi), a3 = wide8_hi(hi);
+            const uint32_t a0 = c8_wide(lo), a1 = c8_wide_hi(lo), a2 = c8_wide(hi), a3 = c8_wide_hi(hi);
 #pragma unroll
             for (int x = 0; x < NT; ++x)
 #pragma unroll
@@ -409,7 +377,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + h * p.G + rho - i * p.G) * D + E * lane;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int e = 0; e < E; ++e) store1(to + e, o[e] * inv);
+        for (int e = 0; e < E; ++e) c8_store1(to + e, o[e] * inv);
       } else {
         float* to = p.rec + (((int64_t)blockIdx.x * 2 + (first == 0)) * TILE + r) * REC;
         if (lane == 0) *reinterpret_cast<float2*>(to) = make_float2(top, l);
@@ -418,123 +386,130 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       }
     }
     if (first == 0 && !whole) {
-      split.b = b;
+      split.b = t.b;
       split.rt = t.rt;
       split.h = h;
-      split.u0 = before + (int64_t)h * t.n;
-      split.u1 = split.u0 + t.n;
+      split.u0 = seg.u0;
+      split.u1 = seg.u0 + t.n;
     }
-    u += n;
   }
   split.units = sh.units;
   if (tid == 0) p.split[blockIdx.x] = split;
 }
 
-// The parts of the tiles that several CTAs worked on.  A CTA joins eight rows of
-// the tile that CTA blockIdx.x began and did not end, a warp a row.
+// The parts of the tiles that several CTAs worked on.  The CTAs of blockIdx.x
+// join the rows of the tile that CTA blockIdx.x there began and did not end, a warp
+// a row.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) c8_join_kernel(const C8Params p) {
   constexpr int REC = D + 4, E = D / 32;
   griddep_wait();
   griddep_launch();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31, r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
   const C8Split s = p.split[c0];
   if (s.h < 0) return;
   const C8Tile t = c8_tile(p, s.b, s.rt);
-  if (r >= t.nrow) return;
   const int parts = (int)((s.u1 * p.ctas - 1) / s.units) - c0 + 1;
   const int64_t step = 2 * (int64_t)p.tile * REC;
-  const float* own = p.rec + (((int64_t)c0 * 2 + 1) * p.tile + r) * REC;
-  const float* more = p.rec + (int64_t)r * REC;  // of CTA k: + k·step
-  float M = -INFINITY, L = 0.f, o[E];
+#pragma unroll 1
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < t.nrow; r += 8 * gridDim.y) {
+    const float* own = p.rec + (((int64_t)c0 * 2 + 1) * p.tile + r) * REC;
+    const float* more = p.rec + (int64_t)r * REC;  // of CTA k: + k·step
+    float M = -INFINITY, L = 0.f, o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += 32) {
-    const int k = k0 + lane;
-    bool on = k < parts;
-    if (on && k > 0 && s.units < p.ctas) on = c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas);
-    float m = -INFINITY, l = 0.f;
-    if (on) {
-      const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
-      m = ml.x;
-      l = ml.y;
-    }
-    on = on && l != 0.f;  // saw nothing (a NaN goes on)
-    float top = on ? m : -INFINITY;
-#pragma unroll
-    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
-    const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
-    const float fa = M == -INFINITY ? 0.f : ex2(M - use);
-    const float f = on ? ex2(m - use) : 0.f;
-    float ls = on ? l * f : 0.f;
-#pragma unroll
-    for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
-    L = L * fa + ls;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= fa;
-    uint32_t todo = __ballot_sync(kFull, on);
-    while (todo) {  // eight records at a time, all their loads in flight
-      float a[8][E], fk[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        fk[q] = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) a[q][e] = 0.f;
-        if (todo) {
-          const int kk = __ffs(todo) - 1;
-          todo &= todo - 1;
-          fk[q] = __shfl_sync(kFull, f, kk);
-          const float* from = (k0 + kk == 0 ? own : more + (c0 + k0 + kk) * step) + 4 + E * lane;
-#pragma unroll
-          for (int e = 0; e < E; ++e) a[q][e] = from[e];
-        }
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int k0 = 0; k0 < parts; k0 += 32) {
+      const int k = k0 + lane;
+      bool on = k < parts;
+      if (on && k > 0 && s.units < p.ctas) on = c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas);
+      float m = -INFINITY, l = 0.f;
+      if (on) {
+        const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
+        m = ml.x;
+        l = ml.y;
       }
+      on = on && l != 0.f;  // saw nothing (a NaN goes on)
+      float top = on ? m : -INFINITY;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
+      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+      const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
+      const float fa = M == -INFINITY ? 0.f : ex2(M - use);
+      const float f = on ? ex2(m - use) : 0.f;
+      float ls = on ? l * f : 0.f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(a[q][e], fk[q], o[e]);
+      for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
+      L = L * fa + ls;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= fa;
+      uint32_t todo = __ballot_sync(kFull, on);
+      while (todo) {  // eight records at a time, all their loads in flight
+        float a[8][E], fk[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          fk[q] = 0.f;
+#pragma unroll
+          for (int e = 0; e < E; ++e) a[q][e] = 0.f;
+          if (todo) {
+            const int kk = __ffs(todo) - 1;
+            todo &= todo - 1;
+            fk[q] = __shfl_sync(kFull, f, kk);
+            const float* from = (k0 + kk == 0 ? own : more + (c0 + k0 + kk) * step) + 4 + E * lane;
+#pragma unroll
+            for (int e = 0; e < E; ++e) a[q][e] = from[e];
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(a[q][e], fk[q], o[e]);
+      }
+      M = nm;
     }
-    M = nm;
-  }
-  const int rho = t.row0 + r, i = rho / p.G;
-  T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
-  const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int rho = t.row0 + r, i = rho / p.G;
+    T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
+    const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-  for (int e = 0; e < E; ++e) store1(to + e, o[e] * inv);
+    for (int e = 0; e < E; ++e) c8_store1(to + e, o[e] * inv);
+  }
 }
 
 template <typename T, int D, int NT>
 cudaError_t run_attend(const C8Params& p, cudaStream_t st) {
   static PerDeviceValue attr;
-  cudaError_t e = smem_attr_once(attr, (const void*)c8_attend_kernel<T, D, NT>, kAtSmem<D, NT>);
-  if (e == cudaSuccess) e = c8_launch(c8_attend_kernel<T, D, NT>, dim3(p.ctas), kAtThreads, kAtSmem<D, NT>, st, p);
-  if (e == cudaSuccess) e = c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, NT), 256, 0, st, p);
-  return e;
+  const cudaError_t e = smem_attr_once(attr, (const void*)c8_attend_kernel<T, D, NT>, kAtSmem<D, NT>);
+  return e != cudaSuccess ? e : c8_launch(c8_attend_kernel<T, D, NT>, dim3(p.ctas), kAtThreads, kAtSmem<D, NT>, st, p);
 }
 template <typename T, int D>
-cudaError_t run_attend_n(const C8Params& p, cudaStream_t st) {
-  return p.tile == 8 ? run_attend<T, D, 1>(p, st) : p.tile == 16 ? run_attend<T, D, 2>(p, st) : run_attend<T, D, 4>(p, st);
+cudaError_t run_attend_d(const C8Params& p, cudaStream_t st) {
+  cudaError_t e = p.tile == 8    ? run_attend<T, D, 1>(p, st)
+                  : p.tile == 16 ? run_attend<T, D, 2>(p, st)
+                  : p.tile == 32 ? run_attend<T, D, 4>(p, st)
+                                 : c8_attend_umma(p, st);
+  if (e == cudaSuccess) e = c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, p.tile < 64 ? p.tile / 8 : 8), 256, 0, st, p);
+  return e;
 }
 template <typename T>
-cudaError_t run_attend_d(const C8Params& p, cudaStream_t st) {
-  return p.d == 64 ? run_attend_n<T, 64>(p, st) : run_attend_n<T, 128>(p, st);
+cudaError_t run_attend_t(const C8Params& p, cudaStream_t st) {
+  return p.d == 64 ? run_attend_d<T, 64>(p, st) : run_attend_d<T, 128>(p, st);
 }
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Rows of a tile: the smallest that hold a mean request's.
-int tile_rows(int64_t rows, int B, int G) {
+// Rows of a tile, by a mean request's rows: the smallest that hold them.  From 33 on
+// fp16 and bf16 rows go to the fifth-generation tensor cores.
+int tile_rows(int64_t rows, int B, int G, bool umma) {
   const int64_t mean = (rows * G + B - 1) / B;
-  return mean <= 8 ? 8 : mean <= 16 ? 16 : 32;
+  return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 || !umma ? 32 : mean <= 128 ? 128 : 256;
 }
+// CTAs of the grid: as many as fit at once.
 int grid_ctas(int tile, int dtype) { return num_sms() * (tile == 8 && dtype != TQ_F32 ? 2 : 1); }
 
 }  // namespace
 
 size_t cache8_ws_bytes(int d, int B, int Hq, int Hkv, int64_t rows) {
-  const int tile = tile_rows(rows, B, Hq / Hkv);
-  const size_t ctas = (size_t)num_sms() * 2;
-  return al256(ctas * sizeof(C8Split)) + ctas * 2 * tile * (d + 4) * 4;
+  const int tile = tile_rows(rows, B, Hq / Hkv, true);  // (no fewer than the other kernel's)
+  const size_t ctas = (size_t)num_sms() * 2, parts = (size_t)num_sms() * (tile == 8 ? 2 : 1) * 2;
+  return al256(ctas * sizeof(C8Split)) + parts * tile * (d + 4) * 4;
 }
 
 tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream) {
@@ -564,7 +539,7 @@ tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream
   p.zscale = a.scale * kC8Log2e;
   p.out = a.out;
   p.status = c.d_status;
-  p.tile = tile_rows(a.rows, a.B, p.G);
+  p.tile = tile_rows(a.rows, a.B, p.G, a.dtype != TQ_F32);
   p.ctas = grid_ctas(p.tile, a.dtype);
   p.split = static_cast<C8Split*>(a.ws);
   p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + al256((size_t)num_sms() * 2 * sizeof(C8Split)));
@@ -574,9 +549,9 @@ tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream
   p.slots = (int)slots;
   cudaError_t e = cudaErrorInvalidValue;
   switch (a.dtype) {
-    case TQ_F32: e = run_attend_d<float>(p, stream); break;
-    case TQ_F16: e = run_attend_d<__half>(p, stream); break;
-    case TQ_BF16: e = run_attend_d<__nv_bfloat16>(p, stream); break;
+    case TQ_F32: e = run_attend_t<float>(p, stream); break;
+    case TQ_F16: e = run_attend_t<__half>(p, stream); break;
+    case TQ_BF16: e = run_attend_t<__nv_bfloat16>(p, stream); break;
   }
   return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
 }

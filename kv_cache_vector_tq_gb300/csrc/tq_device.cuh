@@ -303,6 +303,36 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&v)[8])
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
 
+// Tensor-memory loads complete; the loaded registers pass through, so that
+// nothing that uses them moves ahead of the wait.
+template <int N>
+__device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+// One poll of a phase, suspended for up to a few microseconds: many warps that
+// poll as fast as they can take issue slots from those that work.
+__device__ __forceinline__ bool poll_rest(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
+      : "memory");
+  return ok != 0;
+}
+// One lane of a converged warp, by the instruction made for it: the products
+// inside a branch on it issue every 31 clocks (N = 64, the tensor cores' rate),
+// on `lane == 0` every 54, predicated every 70 (descriptors are then moved to
+// uniform registers for each of them).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
+
 // programmatic dependent launch: wait for the preceding grid / let the next one start
 __device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void griddep_launch() {

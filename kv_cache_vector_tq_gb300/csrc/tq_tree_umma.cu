@@ -104,14 +104,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// Tensor-memory loads complete; the loaded registers pass through, so that
-// nothing that uses them moves ahead of the wait.
-template <int N>
-__device__ __forceinline__ void wait_ld(uint32_t (&r)[N]) {
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
-}
 __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[32]) {
   uint32_t a[16], b[16];
 #pragma unroll
@@ -127,18 +119,6 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[16]) { tmem
 __device__ __forceinline__ void tmem_ld_n(uint32_t at, uint32_t (&v)[8]) { tmem_ld8_nw(at, v); }
 __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[16]) { tmem_st16(at, v); }
 __device__ __forceinline__ void tmem_st_n(uint32_t at, const uint32_t (&v)[8]) { tmem_st8(at, v); }
-// One poll of a phase, suspended for up to a few microseconds: 25 warps that poll
-// as fast as they can take issue slots from those that work.
-__device__ __forceinline__ bool poll_rest(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(4000u)
-      : "memory");
-  return ok != 0;
-}
 // bar_wait with such polls; the first one, which mostly does, takes five
 // instructions (a third of all instructions here once were waits).
 __device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* status,
@@ -154,15 +134,6 @@ __device__ __forceinline__ bool bar_rest(uint64_t* bar, uint32_t parity, volatil
     if (poll_rest(bar, parity)) return true;
     if ((n & 15u) == 15u && *abort_flag) return false;
   }
-}
-// One lane of a converged warp, by the instruction made for it: the products
-// inside a branch on it issue every 31 clocks (N = 64, the tensor cores' rate),
-// on `lane == 0` every 54, predicated every 70 (descriptors are then moved to
-// uniform registers for each of them).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t r;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
-  return r != 0;
 }
 __device__ __forceinline__ void bar_softmax() { asm volatile("bar.sync 1, 256;\n" ::: "memory"); }
 // Barrier of the softmax warps that tells whether any thread asked.

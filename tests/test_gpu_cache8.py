@@ -330,6 +330,16 @@ ATTEND = [
     ([100], [1], 8, 2, 128, 16, 1000, 2),                    # a window longer than the cache
     ([4095], [1], 12, 1, 128, 1024, 0, 0),
     ([37, 90], [130, 64], 24, 2, 128, 16, 0, 0),             # 12 heads a KV head, many tiles
+    ([2000, 1000, 1500], [15, 11, 8], 16, 4, 128, 48, 0, 0), # 60 rows at most
+    ([300, 0, 127], [16, 128, 1], 2, 2, 64, 16, 0, 0),
+    ([1000], [64], 8, 4, 64, 128, 0, 0),                     # 128 rows
+    ([5000, 20], [33, 40], 6, 2, 128, 64, 700, 5),
+    ([3000, 10, 0], [1, 1, 600], 8, 2, 128, 16, 0, 0),       # a prompt beside single tokens
+    ([0], [1500], 4, 1, 128, 32, 256, 4),
+    ([129], [777], 3, 1, 64, 48, 100, 0),
+    ([0, 0], [256, 257], 1, 1, 128, 64, 0, 0),
+    ([20000], [300], 2, 1, 128, 64, 0, 0),
+    ([4000], [200], 2, 2, 64, 16, 4100, 200),
 ]
 
 
