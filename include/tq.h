@@ -483,7 +483,8 @@ tq_status tq_tree_attention(const tq_ctx* kctx, const tq_ctx* vctx, const void* 
  *   d_k, d_v  [pages, Hkv, block, d] codes, e4m3 numbers (16-byte aligned).
  *   d_kscale, d_vscale [pages, Hkv] fp32: a code stands for code · scale.
  *   d_status  one word, or NULL: a call that meets a page outside the cache sets
- *             bit 0 of it.  The caller clears and reads it.
+ *             bit 0 of it, one whose bounded device wait ran out (its outputs are
+ *             then unspecified) bit 1.  The caller clears and reads it.
  * d = 64 or 128, block a multiple of 16 up to 1024 (TQ_ERR_UNSUPPORTED otherwise).
  * Codes need no initial values; scales are written with the first token of a
  * block.  The calls keep nothing else anywhere.
@@ -546,7 +547,7 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  *           its contents do not matter).  Calls that share one must be ordered on
  *           one stream; captured graphs that may run at the same time need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
- * UNSUPPORTED for rows * Hq or max_blocks * block past 2^31 - 256, or
+ * UNSUPPORTED for rows * Hq or max_blocks * block past 2^31 - 256, or pages * Hkv or
  * (max_blocks * block / 128 + 2) * Hkv past 2^31 - 1.
  */
 tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int Hq, int64_t rows, size_t* bytes);

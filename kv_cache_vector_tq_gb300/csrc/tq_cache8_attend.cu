@@ -2,16 +2,17 @@
 // single tokens, drafted chains, and every fp32 call.  tq_cache8.cuh has the
 // mathematics and the division of the work.
 //
-// A warp takes 16 tokens of a unit at a time, tokens on the 16 rows of
-// mma.m16n8k16 and up to 8·NT rows (token x query head) on its columns:
+// A warp takes 32 tokens of a unit, 16 at a time on the rows of mma.m16n8k16 and up
+// to 8·NT rows (token x query head) on its columns:
 //     Sᵀ[token][row] = K·Q̂ᵀ,   Oᵀ[coord][row] += Vᵀ·P
 // Codes become fp16 exactly (every e4m3 number is one) on the way from shared
-// memory to the operands.  The order of the coordinates along a contraction, and of
-// the coordinates in Oᵀ, is free, so that a lane's bytes are 16 in a row: of K's
-// coordinates 16c..16c+15 (and 64 more on), of V's D/8·g.. .  P's transposition from
-// the layout of a result to that of an operand is one movmatrix for 8 tokens.
-// Bytes come by asynchronous copies into slots that are each lane's own, kStages
-// groups of tokens ahead, so that no warp waits for another inside a tile; the
+// memory to the operands.  The order of the coordinates along a contraction, of the
+// coordinates in Oᵀ and of the 16 tokens is free: a lane's bytes are 16 in a row (of
+// K's coordinates 16c.. and 64 on, of V's 16 of a row's), and rows of 128 bytes in
+// TMA's swizzle meet no bank twice (kTok, kPart).  P's transposition from the layout
+// of a result to that of an operand is one movmatrix for 8 tokens.
+// Bytes come by TMA, a box for 16 tokens of K or V, kStages groups of tokens ahead in
+// a ring of each warp's own, so that no warp waits for another inside a tile; the
 // warps' states are joined at its end.
 // Rounding: q is scaled by a power of two into fp16's range, which holds fp16 and
 // bf16 numbers whole; fp32 rows are two fp16 terms (2^-22).  Weights are one fp16
@@ -23,26 +24,23 @@ namespace tq {
 
 namespace {
 
-constexpr int kAtThreads = 256, kAtWarps = 8;
+constexpr int kAtThreads = 128, kAtWarps = 4;  // two CTAs an SM
+constexpr uint32_t kAtPolls = 1u << 20;          // polls of a wait
 
-template <int D, int NT>
-constexpr int kStages = D == 64 ? 6 : NT == 1 ? 3 : 5;  // (two CTAs an SM with 8 rows, one with more)
+template <typename T>
+constexpr int kQTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of q
+template <typename T>
+constexpr int kPTerms = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;  // of the weights
+template <typename T, int D, int NT>
+constexpr int kStages = (D == 64 ? 6 : 3) - (kQTerms<T> == 2 && NT == 4 ? 1 : 0);
 template <int D>
-constexpr int kSlot = 32 * D + 16;  // 16 tokens' K and V codes, two scales
-template <int D, int NT>
-constexpr int kRing = kAtWarps * kStages<D, NT> * kSlot<D>;
-template <int D, int NT>
-constexpr int kMerge = kAtWarps * 8 * NT * (D + 4) * 4;
-template <int D, int NT>
-constexpr int kAtSmem = kRing<D, NT> > kMerge<D, NT> ? kRing<D, NT> : kMerge<D, NT>;
+constexpr int kSlot = 64 * D;  // 32 tokens' K and V codes
+template <typename T, int D, int NT>  // the rings, and in their place the warps' states; aligned in the kernel
+constexpr int kAtSmem = kAtWarps * (kStages<T, D, NT> * kSlot<D> > 8 * NT * (D + 4) * 4 ? kStages<T, D, NT> * kSlot<D> : 8 * NT * (D + 4) * 4) + 1024;
+// Token of row g of an operand's 8, and place of lane g's part of a V row.
+template <int D>
+__device__ __forceinline__ int kTok(int g) { return D == 128 ? (g >> 1) | ((g & 1) << 2) : g; }
 
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (BYTES == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(r) : "r"(x));
@@ -66,30 +64,96 @@ __device__ __forceinline__ float4 load4(const T* p) {
   }
 }
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1) c8_attend_kernel(const C8Params p) {
-  constexpr int QT = sizeof(T) == 4 ? 2 : 1;                                 // fp16 terms of q
-  constexpr int PT = std::is_same<T, __nv_bfloat16>::value ? 1 : 2;          // of the weights
-  constexpr int TILE = 8 * NT, KP = D / 64, KS = D / 16, ST = kStages<D, NT>, SLOT = kSlot<D>, REC = D + 4;
+__global__ void __launch_bounds__(kAtThreads, 2)
+    c8_attend_kernel(const C8Params p, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr int QT = kQTerms<T>, PT = kPTerms<T>, ST = kStages<T, D, NT>;
+  constexpr int TILE = 8 * NT, KP = D / 64, KS = D / 16, SLOT = kSlot<D>, REC = D + 4;
   constexpr bool QREG = NT * QT <= 2;  // q's operands stay in registers
-  extern __shared__ __align__(16) unsigned char smem[];
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
   __shared__ __align__(8) uint2 qf[NT][QT][KS][32];
+  __shared__ float4 s_scale[kAtWarps][ST][2];  // of 16 tokens: K scale, log2 and inverse of the V scale
+  __shared__ __align__(8) uint64_t s_full[kAtWarps][ST];
   __shared__ float s_c[TILE];
   __shared__ int s_pos[TILE];
   __shared__ int64_t s_sums[1][kAtThreads / 32 + 1], s_found[2];
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, c = lane & 3;
+  if (tid < kAtWarps * ST) mbar_init(&s_full[0][0] + tid, 1);
+  fence_mbar_init();
   griddep_wait();
   griddep_launch();
-  const C8Share sh = c8_share<kAtThreads>(p, s_sums, s_found);
+  const C8Share sh = c8_share<kAtThreads>(p, s_sums, s_found);  // (its barriers are the mbarriers' too)
   C8Split split;
   split.h = -1;
-  const uint32_t ring = smem_u32(smem) + warp * (ST * SLOT);
-  const unsigned char* ringp = smem + warp * (ST * SLOT);
+  unsigned char* ring = smem + warp * (ST * SLOT);
+  uint32_t cs = 0, cph = 0, ps = 0;  // slot and phase of the next group to be read, slot of the next one to be asked for
+  uint32_t under_way = 0;            // groups asked for and not read
+  bool dead = false;
   C8Walk walk = c8_walk(p, sh);
   C8Seg seg;
   while (c8_next(p, walk, seg)) {
     const C8Tile& t = seg.t;
     const int h = seg.h, first = seg.first, n = seg.n;  // units here
-    __syncthreads();  // the tile before has been read
+    const int firsts = p.window > 0 ? p.sinks : 0;
+    // pages of 16 groups of tokens, a lane for 16 tokens, 16 groups ahead
+    int pgA = -1, offA = 0, pgB, offB;
+    auto pages = [&](int i, int& pg, int& off) {
+      pg = -1;
+      off = 0;
+      if (i < n) {
+        const int t0 = c8_unit(t, first + i) + 32 * warp + 16 * (lane & 1);
+        if (t0 < t.hi && (t0 + 16 > t.lo || t0 < firsts)) {
+          const int j = t0 / p.block;
+          off = t0 - j * p.block;
+          pg = p.table[(int64_t)t.b * p.max_blocks + j];
+          if (pg < 0 || pg >= p.pages) {
+            pg = -1;
+            if (p.status) atomicOr(p.status, 1);
+          }
+        }
+      }
+    };
+    pages(lane >> 1, pgB, offB);
+    // lane 0, 1: K of the group's tokens, 2, 3: V; pages and scales of the next group to be asked for
+    int pg = -1, off = 0;
+    float sc = 1.f;
+    auto look = [&](int i) {
+      if ((i & 15) == 0) {
+        pgA = pgB;
+        offA = offB;
+        pages(i + 16 + (lane >> 1), pgB, offB);
+      }
+      const int from = 2 * (i & 15) + (lane & 1);
+      pg = __shfl_sync(kFull, pgA, from);
+      off = __shfl_sync(kFull, offA, from);
+      if (lane < 4 && pg >= 0) sc = __ldg((lane < 2 ? p.kscale : p.vscale) + (int64_t)pg * p.Hkv + h);
+    };
+    uint32_t live = 0;  // two bits a group asked for: which of its tokens are there, the last group's in bits 0 and 1
+    auto issue = [&](int i) {
+      const uint32_t there = __ballot_sync(kFull, pg >= 0) & 3u;
+      live = (live << 2) | there;
+      float* to = reinterpret_cast<float*>(&s_scale[warp][ps][lane & 1]);
+      if (lane < 2) {
+        to[0] = sc;
+      } else if (lane < 4) {
+        const float vs = c8_vscale(sc);
+        to[1] = log2f(vs);
+        to[2] = 1.f / vs;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][ps], (uint32_t)__popc(there) * 32 * D);
+      __syncwarp();
+      if (lane < 4 && pg >= 0)
+        tma_load_3d(ring + ps * SLOT + (lane >> 1) * (32 * D) + (lane & 1) * (16 * D), lane < 2 ? &kmap : &vmap, 0, off,
+                    pg * p.Hkv + h, &s_full[warp][ps]);
+      if (++ps == ST) ps = 0;
+      ++under_way;
+      if (i + 1 < n) look(i + 1);
+    };
+    if (!dead) {
+      look(0);
+#pragma unroll 1
+      for (int i = 0; i < ST && i < n; ++i) issue(i);
+    }
     // ---- the rows of q, as operands
 #pragma unroll 1
     for (int r = warp; r < TILE; r += kAtWarps) {
@@ -147,113 +211,80 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
     // tokens that every row of the tile sees: up to seen, and from every on or within the first ones
     const int64_t seen = (int64_t)t.len + t.i0;
     const int64_t every = p.window > 0 ? (int64_t)t.len + t.il - p.window + 1 : 0;
-    const int firsts = p.window > 0 ? p.sinks : 0;
-    // pages of 32 groups of tokens, a lane each, 32 ahead
-    int pgA = -1, offA = 0, pgB, offB;
-    auto pages = [&](int i, int& pg, int& off) {
-      pg = -1;
-      off = 0;
-      if (i < n) {
-        const int t0 = c8_unit(t, first + i) + 16 * warp;
-        if (t0 < t.hi && (t0 + 16 > t.lo || t0 < firsts)) {
-          const int j = t0 / p.block;
-          off = t0 - j * p.block;
-          pg = p.table[(int64_t)t.b * p.max_blocks + j];
-          if (pg < 0 || pg >= p.pages) {
-            pg = -1;
-            if (p.status) atomicOr(p.status, 1);
-          }
+#pragma unroll 1
+    for (int i = 0; i < n && !dead; ++i) {
+      for (uint32_t k = 0; !mbar_try_wait(&s_full[warp][cs], cph); ++k)
+        if (k >= kAtPolls) {  // (never, while copies land)
+          dead = true;
+          break;
         }
-      }
-    };
-    pages(lane, pgB, offB);
-    uint32_t live = 0;  // which of the groups asked for are there, the last one in bit 0
-    auto issue = [&](int i) {
-      if ((i & 31) == 0) {
-        pgA = pgB;
-        offA = offB;
-        pages(i + 32 + lane, pgB, offB);
-      }
-      const int pg = __shfl_sync(kFull, pgA, i & 31), off = __shfl_sync(kFull, offA, i & 31);
-      live = (live << 1) | (uint32_t)(pg >= 0);
-      if (pg >= 0) {
-        const int64_t blk = (int64_t)pg * p.Hkv + h, row = blk * p.block + off;
-        const uint32_t to = ring + (uint32_t)(i % ST) * SLOT;
-        const uint8_t* k = p.k8 + row * D;
-        const uint8_t* v = p.v8 + row * D;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-          for (int x = 0; x < KP; ++x)
-            copy_async<16>(to + ((r * KP + x) * 32 + lane) * 16, k + (g + 8 * r) * D + (c + 4 * x) * 16);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          copy_async<D / 8>(to + 16 * D + (x * 32 + lane) * (D / 8), v + (2 * c + (x & 1) + 8 * (x >> 1)) * D + g * (D / 8));
-        if (lane < 2) copy_async<4>(to + 32 * D + 4 * lane, (lane ? p.vscale : p.kscale) + blk);
-      }
-      asm volatile("cp.async.commit_group;\n" ::: "memory");
-    };
-#pragma unroll 1
-    for (int i = 0; i < ST - 1; ++i) issue(i);
-#pragma unroll 1
-    for (int i = 0; i < n; ++i) {
-      asm volatile("cp.async.wait_group %0;\n" ::"n"(ST - 2) : "memory");
-      __syncwarp();
-      const bool on = (live >> (ST - 2)) & 1;
-      const unsigned char* sl = ringp + (i % ST) * SLOT;
-      if (on) {
+      dead = __any_sync(kFull, dead);
+      if (dead) break;
+      const uint32_t there = (live >> (2 * (min(n - i, ST) - 1))) & 3u;
+      const unsigned char* sl = ring + cs * SLOT;
+      if (there) {
+        const int t0 = c8_unit(t, first + i) + 32 * warp;
+        const float4 sc0 = s_scale[warp][cs][0], sc1 = s_scale[warp][cs][1];
         // ---- scores
-        float s[NT][4];
+        float z[2][NT][4];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+        for (int hf = 0; hf < 2; ++hf) {
 #pragma unroll
-        for (int x = 0; x < KP; ++x) {
-          const uint4 ka = *reinterpret_cast<const uint4*>(sl + (x * 32 + lane) * 16);
-          const uint4 kb = *reinterpret_cast<const uint4*>(sl + ((KP + x) * 32 + lane) * 16);
-          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+          for (int x = 0; x < NT; ++x) z[hf][x][0] = z[hf][x][1] = z[hf][x][2] = z[hf][x][3] = 0.f;
+          const int r = kTok<D>(g);
+          const unsigned char* row = sl + (16 * hf + r) * D;
+          const int sw = D == 128 ? r & 7 : (r >> 1) & 3;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const uint32_t a0 = c8_wide(wa[j]), a1 = c8_wide(wb[j]), a2 = c8_wide_hi(wa[j]), a3 = c8_wide_hi(wb[j]);
+          for (int x = 0; x < KP; ++x) {
+            const uint4 ka = *reinterpret_cast<const uint4*>(row + (((c + 4 * x) ^ sw) << 4));
+            const uint4 kb = *reinterpret_cast<const uint4*>(row + 8 * D + (((c + 4 * x) ^ sw) << 4));
+            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
 #pragma unroll
-            for (int y = 0; y < NT; ++y)
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a0 = c8_wide(wa[j]), a1 = c8_wide(wb[j]), a2 = c8_wide_hi(wa[j]), a3 = c8_wide_hi(wb[j]);
 #pragma unroll
-              for (int q = 0; q < QT; ++q) {
-                const uint2 bb = QREG ? bq[QREG ? y : 0][QREG ? q : 0][QREG ? 4 * x + j : 0] : qf[y][q][4 * x + j][lane];
-                mma16816(s[y], a0, a1, a2, a3, bb.x, bb.y);
-              }
+              for (int y = 0; y < NT; ++y)
+#pragma unroll
+                for (int q = 0; q < QT; ++q) {
+                  const uint2 bb = QREG ? bq[QREG ? y : 0][QREG ? q : 0][QREG ? 4 * x + j : 0] : qf[y][q][4 * x + j][lane];
+                  mma16816(z[hf][y], a0, a1, a2, a3, bb.x, bb.y);
+                }
+            }
           }
         }
-        const int t0 = c8_unit(t, first + i) + 16 * warp;
-        const float ks = *reinterpret_cast<const float*>(sl + 32 * D);
-        const float vs = c8_vscale(*reinterpret_cast<const float*>(sl + 32 * D + 4));
-        const float lv = log2f(vs), iv = 1.f / vs;
-        float z[NT][4];
 #pragma unroll
-        for (int x = 0; x < NT; ++x)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z[x][e] = fmaf(s[x][e], cf[x][e & 1] * ks, lv);
-        const bool masked = !(t0 + 15 <= seen && t0 + 15 < t.hi && (t0 >= every || t0 + 15 < firsts));
-        if (masked) {
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int at = t0 + g + 8 * (e >> 1), pos = s_pos[8 * x + 2 * c + (e & 1)];
-              const bool sees = at < t.hi && at <= pos && (p.window == 0 || (int64_t)at > (int64_t)pos - p.window || at < firsts);
-              if (!sees) z[x][e] = -INFINITY;
-            }
+            for (int e = 0; e < 4; ++e)
+              z[hf][x][e] = fmaf(z[hf][x][e], cf[x][e & 1] * (hf ? sc1.x : sc0.x), hf ? sc1.y : sc0.y);
+        const bool masked = !(there == 3u && t0 + 31 <= seen && t0 + 31 < t.hi && (t0 >= every || t0 + 31 < firsts));
+        if (masked) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int at = t0 + 16 * hf + kTok<D>(g) + 8 * (e >> 1), pos = s_pos[8 * x + 2 * c + (e & 1)];
+                const bool sees = ((there >> hf) & 1u) && at < t.hi && at <= pos &&
+                                  (p.window == 0 || (int64_t)at > (int64_t)pos - p.window || at < firsts);
+                if (!sees) z[hf][x][e] = -INFINITY;
+              }
         }
         bool up = false;
 #pragma unroll
         for (int x = 0; x < NT; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) up |= z[x][e] > M[x][e & 1] + kC8Raise;
+          for (int e = 0; e < 2; ++e)
+            up |= fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2])) > M[x][e] + kC8Raise;
         if (__any_sync(kFull, up)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(z[x][e], z[x][e + 2]);
+              float top = fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2]));
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
               if (top > M[x][e] + kC8Raise) {
@@ -269,70 +300,82 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
             }
         }
         // ---- weights, transposed
-        uint32_t bp[NT][PT][2];
+        uint32_t bp[2][NT][PT][2];
 #pragma unroll
-        for (int x = 0; x < NT; ++x) {
-          float w[4];
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float m = M[x][e & 1];
-            w[e] = ex2(z[x][e] - (m == -INFINITY ? 0.f : m));
+          for (int x = 0; x < NT; ++x) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float m = M[x][e & 1];
+              w[e] = ex2(z[hf][x][e] - (m == -INFINITY ? 0.f : m));
+            }
+            const float iv = hf ? sc1.z : sc0.z;
+            L[x][0] = fmaf(w[0] + w[2], iv, L[x][0]);
+            L[x][1] = fmaf(w[1] + w[3], iv, L[x][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              if constexpr (PT == 2) {
+                uint32_t hi, lo;
+                split2(w[2 * e], w[2 * e + 1], hi, lo);
+                bp[hf][x][0][e] = transpose8(hi);
+                bp[hf][x][PT - 1][e] = transpose8(lo);
+              } else {
+                bp[hf][x][0][e] = transpose8(pack_f16x2(w[2 * e], w[2 * e + 1]));
+              }
+            }
           }
-          L[x][0] = fmaf(w[0] + w[2], iv, L[x][0]);
-          L[x][1] = fmaf(w[1] + w[3], iv, L[x][1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t hi, lo;
-            split2(w[2 * e], w[2 * e + 1], hi, lo);
-            bp[x][0][e] = transpose8(hi);
-            if (PT == 2) bp[x][PT - 1][e] = transpose8(lo);
-          }
-        }
         // ---- values
-        uint32_t wv[4][D / 32];
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const unsigned char* vp = sl + 16 * D + (x * 32 + lane) * (D / 8);
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(vp);
-            wv[x][0] = v.x;
-            wv[x][1] = v.y;
-            wv[x][D / 32 - 2] = v.z;
-            wv[x][D / 32 - 1] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(vp);
-            wv[x][0] = v.x;
-            wv[x][1] = v.y;
-          }
-        }
-        if (masked) {  // what no row sees may be anything, and 0 times it a NaN
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t wv[4][D / 32];
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int at = t0 + 2 * c + (x & 1) + 8 * (x >> 1);
-            if (!(at < t.hi && (at >= t.lo || at < firsts)))
+            const int r = (D == 128 ? c + 4 * (x & 1) : 2 * c + (x & 1)) + 8 * (x >> 1);  // the tokens of operand rows 2c, 2c + 1
+            const unsigned char* row = sl + 32 * D + (16 * hf + r) * D;
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(row + ((kTok<D>(g) ^ (r & 7)) << 4));
+              wv[x][0] = v.x;
+              wv[x][1] = v.y;
+              wv[x][D / 32 - 2] = v.z;
+              wv[x][D / 32 - 1] = v.w;
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(row + ((((g >> 1) ^ (r >> 1)) & 3) << 4) + ((g & 1) << 3));
+              wv[x][0] = v.x;
+              wv[x][1] = v.y;
+            }
+            if (masked) {  // what no row sees may be anything, and 0 times it a NaN
+              const int at = t0 + 16 * hf + r;
+              if (!(((there >> hf) & 1u) && at < t.hi && (at >= t.lo || at < firsts)))
 #pragma unroll
-              for (int k = 0; k < D / 32; ++k) wv[x][k] = 0;
+                for (int k = 0; k < D / 32; ++k) wv[x][k] = 0;
+            }
           }
-        }
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
+          for (int k = 0; k < D / 32; ++k) {
 #pragma unroll
-          for (int o = 0; o < 2; ++o) {
-            const uint32_t lo = __byte_perm(wv[0][k], wv[1][k], o ? 0x7362 : 0x5140);
-            const uint32_t hi = __byte_perm(wv[2][k], wv[3][k], o ? 0x7362 : 0x5140);
-            const uint32_t a0 = c8_wide(lo), a1 = c8_wide_hi(lo), a2 = c8_wide(hi), a3 = c8_wide_hi(hi);
+            for (int o = 0; o < 2; ++o) {
+              const uint32_t lo = __byte_perm(wv[0][k], wv[1][k], o ? 0x7362 : 0x5140);
+              const uint32_t hi = __byte_perm(wv[2][k], wv[3][k], o ? 0x7362 : 0x5140);
+              const uint32_t a0 = c8_wide(lo), a1 = c8_wide_hi(lo), a2 = c8_wide(hi), a3 = c8_wide_hi(hi);
 #pragma unroll
-            for (int x = 0; x < NT; ++x)
+              for (int x = 0; x < NT; ++x)
 #pragma unroll
-              for (int q = 0; q < PT; ++q) mma16816(O[x][2 * k + o], a0, a1, a2, a3, bp[x][q][0], bp[x][q][1]);
+                for (int q = 0; q < PT; ++q) mma16816(O[x][2 * k + o], a0, a1, a2, a3, bp[hf][x][q][0], bp[hf][x][q][1]);
+            }
           }
         }
       }
-      __syncwarp();  // the slot's scales have been read
-      issue(i + ST - 1);
+      if (++cs == ST) {
+        cs = 0;
+        cph ^= 1u;
+      }
+      --under_way;
+      __syncwarp();  // the slot has been read
+      if (i + ST < n) issue(i + ST);
     }
-    asm volatile("cp.async.wait_all;\n" ::: "memory");
-    __syncthreads();  // the ring is free: the warps' states go there
+    __syncthreads();  // the rings are free: the warps' states go there
     float* mg = reinterpret_cast<float*>(smem) + warp * (TILE * REC);
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -346,7 +389,7 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
         if (g == 0) *reinterpret_cast<float2*>(to) = make_float2(M[x][e] == -INFINITY && l != l ? 0.f : M[x][e], l);
 #pragma unroll
         for (int k = 0; k < KS; ++k)
-          *reinterpret_cast<float2*>(to + 4 + g * (D / 8) + 2 * k) = make_float2(O[x][k][e], O[x][k][e + 2]);
+          *reinterpret_cast<float2*>(to + 4 + kTok<D>(g) * (D / 8) + 2 * k) = make_float2(O[x][k][e], O[x][k][e + 2]);
       }
     }
     __syncthreads();
@@ -392,9 +435,22 @@ __global__ void __launch_bounds__(kAtThreads, NT == 1 && sizeof(T) == 2 ? 2 : 1)
       split.u0 = seg.u0;
       split.u1 = seg.u0 + t.n;
     }
+    fence_proxy_async();  // before copies take the states' place
+    __syncthreads();
   }
   split.units = sh.units;
   if (tid == 0) p.split[blockIdx.x] = split;
+  if (dead) {  // copies under way land before the CTA ends (bounded)
+    if (lane == 0 && p.status) atomicOr(p.status, 2);
+    for (; under_way; --under_way) {
+      for (uint32_t k = 0; k < kAtPolls / 64 && !mbar_try_wait(&s_full[warp][cs], cph); ++k) {
+      }
+      if (++cs == ST) {
+        cs = 0;
+        cph ^= 1u;
+      }
+    }
+  }
 }
 
 // The parts of the tiles that several CTAs worked on.  The CTAs of blockIdx.x
@@ -474,23 +530,24 @@ __global__ void __launch_bounds__(256) c8_join_kernel(const C8Params p) {
 }
 
 template <typename T, int D, int NT>
-cudaError_t run_attend(const C8Params& p, cudaStream_t st) {
+cudaError_t run_attend(const C8Params& p, const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t st) {
   static PerDeviceValue attr;
-  const cudaError_t e = smem_attr_once(attr, (const void*)c8_attend_kernel<T, D, NT>, kAtSmem<D, NT>);
-  return e != cudaSuccess ? e : c8_launch(c8_attend_kernel<T, D, NT>, dim3(p.ctas), kAtThreads, kAtSmem<D, NT>, st, p);
+  const cudaError_t e = smem_attr_once(attr, (const void*)c8_attend_kernel<T, D, NT>, kAtSmem<T, D, NT>);
+  return e != cudaSuccess ? e
+                          : c8_launch(c8_attend_kernel<T, D, NT>, dim3(p.ctas), kAtThreads, kAtSmem<T, D, NT>, st, p, kmap, vmap);
 }
 template <typename T, int D>
-cudaError_t run_attend_d(const C8Params& p, cudaStream_t st) {
-  cudaError_t e = p.tile == 8    ? run_attend<T, D, 1>(p, st)
-                  : p.tile == 16 ? run_attend<T, D, 2>(p, st)
-                  : p.tile == 32 ? run_attend<T, D, 4>(p, st)
+cudaError_t run_attend_d(const C8Params& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  cudaError_t e = p.tile == 8    ? run_attend<T, D, 1>(p, k, v, st)
+                  : p.tile == 16 ? run_attend<T, D, 2>(p, k, v, st)
+                  : p.tile == 32 ? run_attend<T, D, 4>(p, k, v, st)
                                  : c8_attend_umma(p, st);
   if (e == cudaSuccess) e = c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, p.tile < 64 ? p.tile / 8 : 8), 256, 0, st, p);
   return e;
 }
 template <typename T>
-cudaError_t run_attend_t(const C8Params& p, cudaStream_t st) {
-  return p.d == 64 ? run_attend_d<T, 64>(p, st) : run_attend_d<T, 128>(p, st);
+cudaError_t run_attend_t(const C8Params& p, const CUtensorMap& k, const CUtensorMap& v, cudaStream_t st) {
+  return p.d == 64 ? run_attend_d<T, 64>(p, k, v, st) : run_attend_d<T, 128>(p, k, v, st);
 }
 
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
@@ -502,13 +559,13 @@ int tile_rows(int64_t rows, int B, int G, bool umma) {
   return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 || !umma ? 32 : mean <= 128 ? 128 : 256;
 }
 // CTAs of the grid: as many as fit at once.
-int grid_ctas(int tile, int dtype) { return num_sms() * (tile == 8 && dtype != TQ_F32 ? 2 : 1); }
+int grid_ctas(int tile) { return num_sms() * (tile <= 32 ? 2 : 1); }
 
 }  // namespace
 
 size_t cache8_ws_bytes(int d, int B, int Hq, int Hkv, int64_t rows) {
   const int tile = tile_rows(rows, B, Hq / Hkv, true);  // (no fewer than the other kernel's)
-  const size_t ctas = (size_t)num_sms() * 2, parts = (size_t)num_sms() * (tile == 8 ? 2 : 1) * 2;
+  const size_t ctas = (size_t)num_sms() * 2, parts = (size_t)grid_ctas(tile) * 2;
   return al256(ctas * sizeof(C8Split)) + parts * tile * (d + 4) * 4;
 }
 
@@ -540,18 +597,22 @@ tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream
   p.out = a.out;
   p.status = c.d_status;
   p.tile = tile_rows(a.rows, a.B, p.G, a.dtype != TQ_F32);
-  p.ctas = grid_ctas(p.tile, a.dtype);
+  p.ctas = grid_ctas(p.tile);
   p.split = static_cast<C8Split*>(a.ws);
   p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + al256((size_t)num_sms() * 2 * sizeof(C8Split)));
   const int64_t slots = a.rows * p.G / p.tile + a.B;
   const int64_t most = (int64_t)a.max_blocks * c.block / kC8Unit + 2;  // units of a tile
-  if (slots > INT32_MAX || most * p.Hkv > INT32_MAX) return TQ_ERR_UNSUPPORTED;
+  if (slots > INT32_MAX || most * p.Hkv > INT32_MAX || c.pages > INT32_MAX / p.Hkv) return TQ_ERR_UNSUPPORTED;
   p.slots = (int)slots;
+  CUtensorMap kmap, vmap;
+  tq_status ms = pages_tensor_map(&kmap, c.d_k, c.pages * c.Hkv, c.block, c.d);
+  if (ms == TQ_OK) ms = pages_tensor_map(&vmap, c.d_v, c.pages * c.Hkv, c.block, c.d);
+  if (ms != TQ_OK) return ms;
   cudaError_t e = cudaErrorInvalidValue;
   switch (a.dtype) {
-    case TQ_F32: e = run_attend_t<float>(p, stream); break;
-    case TQ_F16: e = run_attend_t<__half>(p, stream); break;
-    case TQ_BF16: e = run_attend_t<__nv_bfloat16>(p, stream); break;
+    case TQ_F32: e = run_attend_t<float>(p, kmap, vmap, stream); break;
+    case TQ_F16: e = run_attend_t<__half>(p, kmap, vmap, stream); break;
+    case TQ_BF16: e = run_attend_t<__nv_bfloat16>(p, kmap, vmap, stream); break;
   }
   return e == cudaSuccess ? TQ_OK : set_cuda_error(e);
 }

@@ -26,7 +26,7 @@ namespace tq {
 namespace {
 
 constexpr int kUmThreads = 512;
-constexpr int kUmRegSoft = 160, kUmRegConv = 80, kUmRegRest = 112;
+constexpr int kUmRegSoft = 192, kUmRegConv = 72, kUmRegRest = 56;
 static_assert(8 * kUmRegSoft + 4 * kUmRegConv + 4 * kUmRegRest <= 16 * 128, "registers that the launch does not have would be waited for");
 constexpr int kMeta = 4;                     // units whose scales are kept
 constexpr uint32_t kUmLimit = 1u << 20;      // polls of a wait, a few microseconds each
@@ -75,6 +75,27 @@ __device__ __forceinline__ bool um_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ float um_max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// Two fp32 numbers in one register pair, and arithmetic on both.
+__device__ __forceinline__ uint64_t um_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 um_two(uint64_t x) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(r.x), "=f"(r.y) : "l"(x));
+  return r;
+}
+__device__ __forceinline__ uint64_t um_fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t um_add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 // Columns [a, b) of 32 as bits.
@@ -230,29 +251,31 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
             if (!((valid >> (2 * c + 1)) & 1u)) on &= 0x0000FFFFu;
             return on;
           };
+          uint32_t s[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32_nw(tS + 32 * c, s[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) wait_ld(s[c]);
           float top = -INFINITY;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tmem_ld32_nw(tS + 32 * c, s);
-            const float4 m[2] = {meta[2 * c], meta[2 * c + 1]};
-            wait_ld(s);
-            if (masked) {
+          if (masked) {  // the scores to their end here
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
               const uint32_t on = sees(c);
+              const float4 m[2] = {meta[2 * c], meta[2 * c + 1]};
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if ((on >> e) & 1u) top = fmaxf(top, fmaf(__uint_as_float(s[e]), cf * m[e >> 4].x, m[e >> 4].y));
-            } else {
-#pragma unroll
-              for (int g = 0; g < 2; ++g) {
-                float x[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = __uint_as_float(s[16 * g + e]);
-                const float y0 = um_max3(um_max3(x[0], x[1], x[2]), x[3], x[4]), y1 = um_max3(um_max3(x[5], x[6], x[7]), x[8], x[9]);
-                const float y2 = um_max3(um_max3(x[10], x[11], x[12]), x[13], x[14]);
-                top = fmaxf(top, fmaf(um_max3(um_max3(y0, y1, y2), x[15], x[15]), cf * m[g].x, m[g].y));
-              }
+                s[c][e] = __float_as_uint((on >> e) & 1u ? fmaf(__uint_as_float(s[c][e]), cf * m[e >> 4].x, m[e >> 4].y) : -INFINITY);
             }
+          }
+#pragma unroll
+          for (int g = 0; g < 8; ++g) {
+            const uint32_t* x = &s[g >> 1][(g & 1) * 16];
+            auto v = [&](int e) { return __uint_as_float(x[e]); };
+            const float y0 = um_max3(um_max3(v(0), v(1), v(2)), v(3), v(4)), y1 = um_max3(um_max3(v(5), v(6), v(7)), v(8), v(9));
+            const float y2 = um_max3(um_max3(v(10), v(11), v(12)), v(13), v(14));
+            const float y = fmaxf(um_max3(y0, y1, y2), v(15));
+            const float4 m = meta[g];
+            top = fmaxf(top, masked ? y : fmaf(y, cf * m.x, m.y));
           }
           const bool up = top > M + kC8Raise;
           if (__any_sync(kFull, up)) {
@@ -278,36 +301,27 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           const float use = M == -INFINITY ? 0.f : M;
           // the weights of 32 tokens in the place of their scores: 16 columns of
           // pairs, and 16 of the second terms
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < 4; ++c) {
-            uint32_t s[32];
-            tmem_ld32_nw(tS + 32 * c, s);
-            const float4 m[2] = {meta[2 * c], meta[2 * c + 1]};
-            const uint32_t on = masked ? sees(c) : 0xFFFFFFFFu;
-            wait_ld(s);
             uint32_t ph[16], pl[16];
 #pragma unroll
             for (int g = 0; g < 2; ++g) {
-              const float a = cf * m[g].x, b = m[g].y - use;
-              float v[16];
-#pragma unroll
-              for (int e = 0; e < 16; ++e) v[e] = ex2(fmaf(__uint_as_float(s[16 * g + e]), a, b));
-              if (masked) {
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if (!((on >> (16 * g + e)) & 1u)) v[e] = 0.f;
-              }
-              float s0 = 0.f, s1 = 0.f;
+              const float4 m = meta[2 * c + g];
+              const float a = masked ? 1.f : cf * m.x, b = masked ? -use : m.y - use;
+              const uint64_t aa = um_pack(a, a), bb = um_pack(b, b);
+              uint64_t sum = 0;  // of even and of odd tokens
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                s0 += v[2 * e];
-                s1 += v[2 * e + 1];
+                const float2 z = um_two(um_fma2(um_pack(__uint_as_float(s[c][16 * g + 2 * e]), __uint_as_float(s[c][16 * g + 2 * e + 1])), aa, bb));
+                const float w0 = ex2(z.x), w1 = ex2(z.y);
+                sum = um_add2(sum, um_pack(w0, w1));
                 if constexpr (TWO)
-                  split2(v[2 * e], v[2 * e + 1], ph[8 * g + e], pl[8 * g + e]);
+                  split2(w0, w1, ph[8 * g + e], pl[8 * g + e]);
                 else
-                  ph[8 * g + e] = pack_f16x2(v[2 * e], v[2 * e + 1]);
+                  ph[8 * g + e] = pack_f16x2(w0, w1);
               }
-              L = fmaf(s0 + s1, m[g].z, L);
+              const float2 both = um_two(sum);
+              L = fmaf(both.x + both.y, m.z, L);
             }
             tmem_st16(tS + 32 * c, ph);
             if constexpr (TWO) tmem_st16(tS + 32 * c + 16, pl);

@@ -578,6 +578,19 @@ tq_status rows_tensor_map(CUtensorMap* map, const void* x, int64_t N, int d, boo
   return r == CUDA_SUCCESS ? TQ_OK : TQ_ERR_INVALID_ARG;
 }
 
+tq_status pages_tensor_map(CUtensorMap* map, const uint8_t* codes, int64_t blocks, int block, int d) {
+  const cuuint64_t gdim[3] = {(cuuint64_t)d, (cuuint64_t)block, (cuuint64_t)blocks};
+  const cuuint64_t gstride[2] = {(cuuint64_t)d, (cuuint64_t)d * block};
+  const cuuint32_t box[3] = {(cuuint32_t)d, 16u, 1u};
+  const cuuint32_t estride[3] = {1u, 1u, 1u};
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (!encode) return TQ_ERR_CUDA;
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t*>(codes), gdim, gstride, box, estride,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? TQ_OK : TQ_ERR_INVALID_ARG;
+}
+
 bool umma_supported(const DevCtx& c) {
   return c.d > kChunk && c.d % kTN == 0 && c.mode == TQ_MSE && c.b_mse >= 1 && c.b_mse <= 4 && c.umma_tab != nullptr;
 }

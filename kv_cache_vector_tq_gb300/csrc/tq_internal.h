@@ -109,6 +109,9 @@ tq_status launch_encode128(const DevCtx& c, const void* x, int x_dtype, int64_t 
 // 2-D tensor map of N rows of d fp32/fp16 values for TMA loads of boxes of
 // 128 rows x 128 bytes in the 128-byte swizzle.
 tq_status rows_tensor_map(CUtensorMap* map, const void* x, int64_t N, int d, bool f16);
+// 3-D tensor map of `blocks` blocks of `block` rows of d (64 or 128) bytes for TMA
+// loads of 16 rows of one block, in the swizzle of the row's length.
+tq_status pages_tensor_map(CUtensorMap* map, const uint8_t* codes, int64_t blocks, int block, int d);
 bool umma_supported(const DevCtx& c);
 tq_status launch_encode_umma(const DevCtx& c, const void* x, int x_dtype, int64_t N, const tq_codes* out,
                              int64_t offset, int64_t group_rows, int64_t group_stride, cudaStream_t stream);
