@@ -520,8 +520,8 @@ typedef struct {
  * not stored (see d_status).  A block that is written belongs to one request; full
  * blocks may be shared.  Calls on one cache must be ordered on one stream.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
- * UNSUPPORTED for rot not a multiple of 16, rows or max_blocks * block past
- * 2^31 - 256.
+ * UNSUPPORTED for rot not a multiple of 16, B > 65536, rows or max_blocks * block
+ * past 2^31 - 256.
  */
 tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, int64_t k_stride, const void* d_v,
                            int64_t v_stride, int dtype, int64_t rows, int Hq, const void* d_wq, const void* d_wk,
@@ -547,7 +547,7 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  *           its contents do not matter).  Calls that share one must be ordered on
  *           one stream; captured graphs that may run at the same time need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
- * UNSUPPORTED for rows * Hq or max_blocks * block past 2^31 - 256, or pages * Hkv or
+ * UNSUPPORTED for B > 65536, rows * Hq or max_blocks * block past 2^31 - 256, pages * Hkv or
  * (max_blocks * block / 128 + 2) * Hkv past 2^31 - 1.
  */
 tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int Hq, int64_t rows, size_t* bytes);

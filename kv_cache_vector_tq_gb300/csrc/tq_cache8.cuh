@@ -40,7 +40,7 @@ __device__ __forceinline__ C8Seq c8_seq(const int32_t* row_start, const int32_t*
 // since floor(x) + floor(y) <= floor(x + y), and found without a sum over the
 // requests.  Whole warps call it with one x.
 __device__ __forceinline__ int c8_key(const int32_t* row_start, int b, int rows, int num, int den, int each) {
-  return (int)((int64_t)c8_row(row_start, b, rows) * num / den) + each * b;
+  return (int)((uint32_t)(c8_row(row_start, b, rows) * num) / (uint32_t)den) + each * b;  // (rows · num < 2^31)
 }
 __device__ __forceinline__ int c8_find(const int32_t* row_start, int B, int rows, int num, int den, int each, int x) {
   const int lane = threadIdx.x & 31;
@@ -112,24 +112,22 @@ __device__ __forceinline__ C8Tile c8_tile(const C8Params& p, int b, int rt) {
   t.rt = rt;
   t.start = s.start;
   t.len = s.len;
-  const int64_t row0 = (int64_t)rt * p.tile, all = (int64_t)s.T * p.G;
-  t.n = 0;
-  t.nrow = (int)(all - row0 < p.tile ? all - row0 : p.tile);
-  if (rt < 0 || t.nrow <= 0) {
-    t.nrow = 0;
-    return t;
-  }
-  t.row0 = (int)row0;
-  t.i0 = t.row0 / p.G;
-  t.il = (t.row0 + t.nrow - 1) / p.G;
-  const int64_t cap = (int64_t)p.max_blocks * p.block;
-  t.hi = (int)min((int64_t)s.len + t.il + 1, cap);
+  const int all = s.T * p.G;  // (rows · Hq < 2^31)
+  t.n = t.nrow = 0;
+  if (rt < 0 || (int64_t)rt * p.tile >= all) return t;
+  const int row0 = rt * p.tile;
+  t.nrow = min(all - row0, p.tile);
+  t.row0 = row0;
+  t.i0 = row0 / p.G;
+  t.il = (row0 + t.nrow - 1) / p.G;
+  const int cap = p.max_blocks * p.block;
+  t.hi = (int)min((int64_t)s.len + t.il + 1, (int64_t)cap);
   t.lo = 0;
   t.su = t.lou = 0;
   const int hiu = (t.hi + kC8Unit - 1) / kC8Unit;
   t.n = hiu;
   if (p.window > 0) {
-    t.lo = (int)min(max((int64_t)s.len + t.i0 - p.window + 1, (int64_t)0), cap);
+    t.lo = (int)min(max((int64_t)s.len + t.i0 - p.window + 1, (int64_t)0), (int64_t)cap);
     t.su = (min(p.sinks, t.hi) + kC8Unit - 1) / kC8Unit;
     t.lou = t.lo / kC8Unit;
     if (t.lou <= t.su)

@@ -1120,7 +1120,7 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
   if ((Hq > 0 && (q_stride < (int64_t)Hq * d || q_out_stride < (int64_t)Hq * d)) || k_stride < (int64_t)Hkv * d ||
       v_stride < (int64_t)Hkv * d)
     return TQ_ERR_INVALID_ARG;
-  if (rot % 16 != 0 || rows > INT32_MAX - 255 || (int64_t)max_blocks * cache->block > INT32_MAX - 255)
+  if (rot % 16 != 0 || B > 65536 || rows > INT32_MAX - 255 || (int64_t)max_blocks * cache->block > INT32_MAX - 255)
     return TQ_ERR_UNSUPPORTED;
   if (rows == 0) return TQ_OK;
   if ((Hq > 0 && (!d_q || !d_q_out)) || !d_k || !d_v || !d_pos || !d_row_start || !d_len || !d_table ||
@@ -1179,7 +1179,8 @@ tq_status tq_cache8_attention(const void* d_q, int64_t q_stride, int dtype, int6
     return TQ_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale) || q_stride < (int64_t)Hq * cache->d || q_stride * sz % 16)
     return TQ_ERR_INVALID_ARG;
-  if (rows > (INT32_MAX - 255) / Hq || (int64_t)max_blocks * cache->block > INT32_MAX - 255) return TQ_ERR_UNSUPPORTED;
+  if (B > 65536 || rows > (INT32_MAX - 255) / Hq || (int64_t)max_blocks * cache->block > INT32_MAX - 255)
+    return TQ_ERR_UNSUPPORTED;
   if (rows == 0) return TQ_OK;
   if (!d_q || !d_out || !d_ws || !d_row_start || !d_len || !d_table) return TQ_ERR_INVALID_ARG;
   if (!al16(d_q) || !al16(d_out) || !al16(d_ws)) return TQ_ERR_INVALID_ARG;
