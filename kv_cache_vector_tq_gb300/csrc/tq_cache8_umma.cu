@@ -18,15 +18,15 @@
 // rows); both stand in the columns of their own scores.
 //
 // Warps: 0-3 and 4-7 softmax (thread = row), 8-11 K's codes to fp16, 12-15 V's, 16
-// issues the products, 17 and 18 the copies (lane = 16 tokens, so pages may end
-// anywhere on a multiple of 16).
+// and 17 issue the products, 18 and 19 the copies (lane = 16 tokens, so pages may
+// end anywhere on a multiple of 16).
 #include "tq_cache8.cuh"
 
 namespace tq {
 
 namespace {
 
-constexpr int kUmThreads = 640, kUmMma = 16, kUmCopy = 17;
+constexpr int kUmThreads = 640, kUmMma = 16, kUmCopy = 18;
 constexpr int kUmRegSoft = 128, kUmRegConv = 64;  // the rest keep the launch's 96
 static_assert(8 * kUmRegSoft + 8 * kUmRegConv + 4 * 96 <= 20 * 96, "registers that the launch does not have would be waited for");
 constexpr int kMeta = 4;                     // units whose scales are kept
@@ -51,7 +51,7 @@ struct Misc {
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t meta_full[kMeta];
-  uint64_t s_full[3], p_full[3], pv_done[2], q_full, o_done, pair, drain;
+  uint64_t s_full[3], s_empty[3], p_full[3], pv_done[2], q_full, o_done, pair, drain;
   int64_t sums[1][kUmThreads / 32 + 1], found[2];
   float m[128], l[128];        // of the second group, where the two are joined
   uint32_t sent[2];            // tiles of codes asked for, K and V
@@ -74,6 +74,32 @@ __device__ __forceinline__ bool um_wait(uint64_t* bar, uint32_t parity, volatile
     if (poll_rest(bar, parity)) return true;
     if ((n & 15u) == 15u && *abort_flag) return false;
   }
+}
+// One look at a phase.
+__device__ __forceinline__ bool um_look(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// um_wait for a warp whose lanes wait for different barriers: looks only (a poll that
+// suspends would do so for the lanes that have theirs as well).
+__device__ __forceinline__ bool um_wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  bool got = um_look(bar, parity);
+#pragma unroll 1
+  for (uint32_t n = 1; !__all_sync(kFull, got); ++n) {
+    if (n >= (kUmLimit << 4)) {
+      *abort_flag = 1;
+      if (status) atomicOr(status, 2);
+      return false;
+    }
+    got = got || um_look(bar, parity);
+    if ((n & 255u) == 255u && __any_sync(kFull, *abort_flag != 0)) return false;
+  }
+  return true;
 }
 __device__ __forceinline__ float um_max3(float a, float b, float c) {
   float r;
@@ -141,13 +167,14 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     }
     for (int i = 0; i < 3; ++i) {
       mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.s_empty[i], 1);
       mbar_init(&ms.p_full[i], 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&ms.meta_full[i], 1);
     mbar_init(&ms.q_full, 8);
     mbar_init(&ms.o_done, 1);
     mbar_init(&ms.pair, 8);
-    mbar_init(&ms.drain, 1);
+    mbar_init(&ms.drain, 2);
     ms.abort = 0;
     ms.sent[0] = ms.sent[1] = 0;
     fence_mbar_init();
@@ -181,7 +208,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       const C8Tile& t = seg.t;
       const int rho = t.row0 + r, tok = rho / p.G;
       const bool here = r < t.nrow, any = (warp & 3) * 32 < t.nrow;  // the row, some row of the warp
+      // tokens that the row sees: from .. upto, and the first ones
       const int pos = here ? (int)min((int64_t)t.len + tok, (int64_t)INT32_MAX) : -1;
+      const int upto = min(pos, t.hi - 1), from = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
       // ---- the row of q, as an operand: this group's half of its coordinates
       float cf;
       {
@@ -233,9 +262,10 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 #pragma unroll 1
       for (int k = 0; k < seg.n; ++k) {
         const uint32_t q = gu + k, tS = tl + 64 * buf;
-        ok = um_wait(&ms.meta_full[q % kMeta], (q / kMeta) & 1u, abort_flag, p.status) &&
-             um_wait(&ms.s_full[buf], bph, abort_flag, p.status);
-        ok = __all_sync(kFull, ok);
+        // (lanes wait for one or the other: with the converting warps' reads and writes
+        // before it, a poll takes 200 clocks even where it finds its phase complete)
+        ok = um_wait_lanes(lane & 1 ? &ms.meta_full[q % kMeta] : &ms.s_full[buf], lane & 1 ? (q / kMeta) & 1u : bph, abort_flag,
+                           p.status);
         if (!ok) break;
         tc_fence_after();
         if (any) {
@@ -245,15 +275,13 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           const float4* meta = ms.meta[q % kMeta] + 4 * w;
           const uint32_t valid = (ms.valid[q % kMeta] >> (4 * w)) & 15u;
           const int base = c8_unit(t, seg.first + k) + 64 * w;
-          const bool all = valid == 15u && pos >= base + 63 && base + 63 < t.hi &&
-                           (p.window == 0 || (int64_t)base > (int64_t)pos - p.window || base + 63 < firsts);
+          const bool all = valid == 15u && base + 63 <= upto && (base >= from || base + 63 < firsts);
           const bool masked = !__all_sync(kFull, all);
           wait_ld(s[0]);
           wait_ld(s[1]);
           if (masked) {  // the scores to their end here
             // columns that the row sees: [lo, hi) and [0, first)
-            const int hi = min(min(pos, t.hi - 1) + 1 - base, 64);
-            const int lo = p.window > 0 ? (int)max(min((int64_t)pos - p.window + 1 - base, (int64_t)64), (int64_t)0) : 0;
+            const int hi = min(upto + 1 - base, 64), lo = min(max(from - base, 0), 64);
             const int first = min(firsts - base, hi);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -286,7 +314,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
             const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
             M = nm;
             L *= f;
-            if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores were)
+            if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores' place was free)
               ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (q - 1) & 1u, abort_flag, p.status));
               if (!ok) break;
               tc_fence_after();
@@ -459,7 +487,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 #pragma unroll 1
       for (int k = 0; k < seg.n; ++k, ++q) {
         const uint32_t st = q & 1u, ph = (q >> 1) & 1u;
-        ok = __all_sync(kFull, um_wait(&ms.raw_full[rs], rph, abort_flag, p.status));
+        const bool both = warp != 12 && (lane & 1);  // (warp 12 has something to do between the two)
+        ok = um_wait_lanes(both ? &empty[st] : &ms.raw_full[rs], both ? ph ^ 1u : rph, abort_flag, p.status);
         if (!ok) break;
         uint32_t valid = 0xFFu;
         bool part = false;
@@ -478,9 +507,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           if (lane == 0) ms.valid[q % kMeta] = valid;
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms.meta_full[q % kMeta]);
+          ok = __all_sync(kFull, um_wait(&empty[st], ph ^ 1u, abort_flag, p.status));
+          if (!ok) break;
         }
-        ok = __all_sync(kFull, um_wait(&empty[st], ph ^ 1u, abort_flag, p.status));
-        if (!ok) break;
         const unsigned char* raw = smem + Ly::kRaw + rs * Ly::kRawTile;
         unsigned char* dst = smem + (is_v ? Ly::kV : Ly::kK) + st * Ly::kTile;
 #pragma unroll 4
@@ -514,71 +543,78 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       }
     }
   } else if (warp == kUmMma) {
-    // ---------------- products
-    constexpr uint32_t idesc = umma_idesc_f16(128, 64), idesc_p = umma_idesc_f16(128, D) | (1u << 16);  // V contiguous along N
+    // ---------------- scores, half a unit at a time.  (Scores and sums have a warp
+    // each: one for both took twice the products' own time, its instructions fetched
+    // anew each time round between the other roles'.)
+    constexpr uint32_t idesc = umma_idesc_f16(128, 64);
     const uint64_t dk = umma_desc_sw128(smem_u32(smem + Ly::kK));
-    // V: 64 coordinates a 128-byte row, the next 64 coordinates 16384 bytes on
-    const uint64_t dv = (umma_desc_sw128(smem_u32(smem + Ly::kV)) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(16384 >> 4) << 16);
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      return __all_sync(kFull, um_wait(bar, parity, abort_flag, p.status));
-    };
-    // halves of units, from the CTA's first on: scores of the next one, products with V of the next one
-    uint32_t qs = 0, qbuf = 0, vs = 0, vbuf = 0, vph = 0, qn = 0;
-    auto scores = [&]() -> bool {
-      const uint32_t st = (qs >> 1) & 1u;
-      if (!(qs & 1u) && !wait(&ms.k_full[st], (qs >> 2) & 1u)) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t b = dk + st * (Ly::kTile / 16) + (qs & 1u) * (8192 / 16);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks)
-          umma_f16_ts(tmem + 64 * qbuf, tmem + kColQ + 8 * ks, b + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, idesc, ks ? 1u : 0u);
-        umma_commit(&ms.s_full[qbuf]);
-        if (qs & 1u) umma_commit(&ms.k_empty[st]);
-      }
-      __syncwarp();
-      ++qs;
-      if (++qbuf == 3) qbuf = 0;
-      return true;
-    };
-    auto values = [&](bool fresh, bool last) -> bool {
-      const uint32_t st = (vs >> 1) & 1u, w = vs & 1u;
-      if (!wait(&ms.p_full[vbuf], vph) || (!w && !wait(&ms.v_full[st], (vs >> 2) & 1u))) return false;
-      tc_fence_after();
-      if (elect_one()) {
-        const uint64_t b = dv + st * (Ly::kTile / 16) + w * (8192 / 16);
-        const uint32_t a = tmem + 64 * vbuf, d = tmem + kColO + 128 * w;
-        if constexpr (TWO) {  // remainders first: not truncated against a large sum
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 32 + 8 * ks, b + ks * 128, idesc_p, (ks || !fresh) ? 1u : 0u);
-        }
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 8 * ks, b + ks * 128, idesc_p, (TWO || ks || !fresh) ? 1u : 0u);
-        umma_commit(&ms.pv_done[w]);
-        if (w) umma_commit(&ms.v_empty[st]);
-        if (last) umma_commit(&ms.o_done);
-      }
-      __syncwarp();
-      ++vs;
-      if (++vbuf == 3) {
-        vbuf = 0;
-        vph ^= 1u;
-      }
-      return true;
-    };
+    uint32_t q = 0, buf = 0, bph = 1, qn = 0;  // halves so far, place of the next scores and its phase, tiles
     bool ok = true;
     while (ok && c8_next(p, walk, seg)) {
-      if (!(ok = wait(&ms.q_full, qn++ & 1u))) break;
-      const int n = 2 * seg.n;
-      ok = scores() && scores() && (n < 3 || scores());
-      for (int k = 0; ok && k < n; ++k) {
-        ok = values(k < 2, k == n - 1);
-        if (ok && k + 3 < n) ok = scores();
+      if (!(ok = __all_sync(kFull, um_wait(&ms.q_full, qn++ & 1u, abort_flag, p.status)))) break;
+#pragma unroll 1
+      for (int k = 0; k < 2 * seg.n; ++k) {
+        const uint32_t st = (q >> 1) & 1u;
+        const bool lk = (lane & 1) && !(q & 1u);  // odd lanes look for K, with the first half
+        ok = um_wait_lanes(lk ? &ms.k_full[st] : &ms.s_empty[buf], lk ? (q >> 2) & 1u : bph, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = dk + st * (Ly::kTile / 16) + (q & 1u) * (8192 / 16);
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks)
+            umma_f16_ts(tmem + 64 * buf, tmem + kColQ + 8 * ks, b + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, idesc, ks ? 1u : 0u);
+          umma_commit(&ms.s_full[buf]);
+          if (q & 1u) umma_commit(&ms.k_empty[st]);
+        }
+        __syncwarp();
+        ++q;
+        if (++buf == 3) {
+          buf = 0;
+          bph ^= 1u;
+        }
       }
     }
     if (elect_one()) umma_commit(&ms.drain);  // every product issued completes before tensor memory is released
-    for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
+  } else if (warp == kUmMma + 1) {
+    // ---------------- weights with values
+    constexpr uint32_t idesc = umma_idesc_f16(128, D) | (1u << 16);  // V contiguous along N
+    // V: 64 coordinates a 128-byte row, the next 64 coordinates 16384 bytes on
+    const uint64_t dv = (umma_desc_sw128(smem_u32(smem + Ly::kV)) & ~((uint64_t)0x3FFF << 16)) | ((uint64_t)(16384 >> 4) << 16);
+    uint32_t q = 0, buf = 0, bph = 0;
+    bool ok = true;
+    while (ok && c8_next(p, walk, seg)) {
+#pragma unroll 1
+      for (int k = 0; k < 2 * seg.n; ++k) {
+        const uint32_t st = (q >> 1) & 1u, w = q & 1u;
+        const bool lv = (lane & 1) && !w;
+        ok = um_wait_lanes(lv ? &ms.v_full[st] : &ms.p_full[buf], lv ? (q >> 2) & 1u : bph, abort_flag, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t b = dv + st * (Ly::kTile / 16) + w * (8192 / 16);
+          const uint32_t a = tmem + 64 * buf, d = tmem + kColO + 128 * w;
+          const uint32_t on = k < 2 ? 0u : 1u;
+          if constexpr (TWO) {  // remainders first: not truncated against a large sum
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 32 + 8 * ks, b + ks * 128, idesc, ks ? 1u : on);
+          }
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 8 * ks, b + ks * 128, idesc, TWO || ks ? 1u : on);
+          umma_commit(&ms.s_empty[buf]);
+          umma_commit(&ms.pv_done[w]);
+          if (w) umma_commit(&ms.v_empty[st]);
+          if (k == 2 * seg.n - 1) umma_commit(&ms.o_done);
+        }
+        __syncwarp();
+        ++q;
+        if (++buf == 3) {
+          buf = 0;
+          bph ^= 1u;
+        }
+      }
     }
+    if (elect_one()) umma_commit(&ms.drain);
   } else if (warp < kUmCopy + 2) {
     // ---------------- copies, K by one warp and V by the other: lane = 16 tokens of
     // the unit; the first lane of a run inside one page copies the run (a copy takes
@@ -651,6 +687,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     if (lane == 0) ms.sent[is_v] = sent;
   }
 
+  if (warp == kUmMma || warp == kUmMma + 1)
+    for (uint32_t k = 0; k < kSpinLimitDev && !mbar_try_wait(&ms.drain, 0u); ++k) {
+    }
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) {
