@@ -556,7 +556,7 @@ size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 // fp16 and bf16 rows go to the fifth-generation tensor cores.
 int tile_rows(int64_t rows, int B, int G, bool umma) {
   const int64_t mean = (rows * G + B - 1) / B;
-  return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 || !umma ? 32 : 128;
+  return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 || !umma ? 32 : mean <= 128 ? 128 : 256;
 }
 // CTAs of the grid: as many as fit at once.
 int grid_ctas(int tile) { return num_sms() * (tile <= 32 ? 2 : 1); }

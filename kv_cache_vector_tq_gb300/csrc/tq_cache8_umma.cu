@@ -9,10 +9,11 @@
 //     O[row][coord] += P·V         A = P (tensor memory), B = V (shared memory, row-contiguous)
 // Rows on the lanes make a softmax row one thread's: no value changes lanes.  Two
 // groups of softmax warps take a half of every unit each, with sums of their own
-// that are joined at the tile's end; scores have three places, so that a group finds
-// its next ones made when it has written its weights.  Q in tensor memory leaves
-// shared memory's reads to K and V, where the codes' way to fp16 (exact) is the
-// other reader.
+// that are joined at the tile's end, or (WIDE: more than 128 rows a request and KV
+// head) 128 rows each, so that K and V are converted once for 256.  Scores have three
+// places, so that a group finds its next ones made when it has written its weights.
+// Q in tensor memory (the second group's of a WIDE tile does not fit) leaves shared
+// memory's reads to K and V, where the codes' way to fp16 (exact) is the other reader.
 // M is raised only before a weight passes 2^14, so that O is rarely rescaled.
 // Weights are one fp16 term for bf16 outputs, two for fp16 (as in the kernel for few
 // rows); both stand in the columns of their own scores.
@@ -135,11 +136,11 @@ __device__ __forceinline__ uint32_t bits_of(int a, int b) {
   return (b == 32 ? 0xFFFFFFFFu : (1u << b) - 1u) & ~((1u << a) - 1u);
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p) {
   using Ly = Lay<D>;
   constexpr bool TWO = std::is_same<T, __half>::value;  // terms of a weight
-  constexpr int REC = D + 4, NR = Ly::kRaws, KS = D / 16;
+  constexpr int REC = D + 4, NR = Ly::kRaws, KS = D / 16, PER = WIDE ? 4 : 2;  // scores of 64 tokens and 128 rows a unit
   extern __shared__ __align__(1024) unsigned char smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + Ly::kMisc);
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;  // (the warp's number in a uniform register)
@@ -191,10 +192,10 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kUmRegSoft));
-    // ---------------- softmax: tokens 64w.. of every unit, row r of the tile
+    // ---------------- softmax: row r of the group's rows, tokens 64w.. of every unit or (WIDE) all
     const int w = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t tl = tmem + ((uint32_t)(32 * (warp & 3)) << 16), tO = tl + kColO + 128 * w;
-    uint32_t gu = 0, buf = (uint32_t)w, bph = 0, met = 0, segs = 0;  // units so far, place of the next scores and its phase, meetings, segments
+    uint32_t gu = 0, done = 0, buf = (uint32_t)w, bph = 0, met = 0, segs = 0;  // units and this group's scores so far, place of the next ones and its phase, meetings, segments
     bool ok = true;
     // both groups (bounded, as every wait here)
     auto meet = [&]() -> bool {
@@ -206,8 +207,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     split.h = -1;
     while (ok && c8_next(p, walk, seg)) {
       const C8Tile& t = seg.t;
-      const int rho = t.row0 + r, tok = rho / p.G;
-      const bool here = r < t.nrow, any = (warp & 3) * 32 < t.nrow;  // the row, some row of the warp
+      const int row = WIDE ? 128 * w + r : r, rho = t.row0 + row, tok = rho / p.G;
+      const bool here = row < t.nrow, any = row - lane < t.nrow;  // the row, some row of the warp
       // tokens that the row sees: from .. upto, and the first ones
       const int pos = here ? (int)min((int64_t)t.len + tok, (int64_t)INT32_MAX) : -1;
       const int upto = min(pos, t.hi - 1), from = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
@@ -238,20 +239,29 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         const int ex = c8_row_exp(top);
         cf = p.zscale * c8_pow2(ex);
         const float f = c8_pow2(-ex);
+        auto half8 = [&](const uint4& x8) -> uint4 {
+          const uint32_t u[4] = {x8.x, x8.y, x8.z, x8.w};
+          uint32_t h[4];
 #pragma unroll
-        for (int i = 0; i < D / 16; i += 2) {  // eight columns of pairs
-          uint32_t h[8];
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint4 a = x[i + k], b = x[D / 16 + i + k];
-            const uint32_t u[4] = {w ? b.x : a.x, w ? b.y : a.y, w ? b.z : a.z, w ? b.w : a.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 v = two(u[e]);
-              h[4 * k + e] = pack_f16x2(v.x * f, v.y * f);
-            }
+          for (int e = 0; e < 4; ++e) {
+            const float2 v = two(u[e]);
+            h[e] = pack_f16x2(v.x * f, v.y * f);
           }
-          tmem_st8(tl + kColQ + w * (D / 4) + 4 * i, h);
+          return make_uint4(h[0], h[1], h[2], h[3]);
+        };
+        if (WIDE && w) {  // these rows' Q goes to shared memory
+          unsigned char* dst = smem + Ly::kJoin + r * 128;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = half8(x[i]);
+          fence_proxy_async();
+        } else {
+          constexpr int N = WIDE ? D / 8 : D / 16;  // (a half each where the groups have the same rows)
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {  // eight columns of pairs
+            const uint4 a = half8(!WIDE && w ? x[D / 8 - N + i] : x[i]), b = half8(!WIDE && w ? x[D / 8 - N + i + 1] : x[i + 1]);
+            const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            tmem_st8(tl + kColQ + w * (D / 4) + 4 * i, h);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -260,8 +270,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       }
       float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-      for (int k = 0; k < seg.n; ++k) {
-        const uint32_t q = gu + k, tS = tl + 64 * buf;
+      for (int k = 0; k < (WIDE ? 2 : 1) * seg.n; ++k, ++done) {
+        const int unit = WIDE ? k >> 1 : k, part = WIDE ? k & 1 : w;  // of the segment; which 64 tokens
+        const uint32_t q = gu + unit, tS = tl + 64 * buf;
         // (lanes wait for one or the other: with the converting warps' reads and writes
         // before it, a poll takes 200 clocks even where it finds its phase complete)
         ok = um_wait_lanes(lane & 1 ? &ms.meta_full[q % kMeta] : &ms.s_full[buf], lane & 1 ? (q / kMeta) & 1u : bph, abort_flag,
@@ -272,9 +283,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           uint32_t s[2][32];
           tmem_ld32_nw(tS, s[0]);
           tmem_ld32_nw(tS + 32, s[1]);
-          const float4* meta = ms.meta[q % kMeta] + 4 * w;
-          const uint32_t valid = (ms.valid[q % kMeta] >> (4 * w)) & 15u;
-          const int base = c8_unit(t, seg.first + k) + 64 * w;
+          const float4* meta = ms.meta[q % kMeta] + 4 * part;
+          const uint32_t valid = (ms.valid[q % kMeta] >> (4 * part)) & 15u;
+          const int base = c8_unit(t, seg.first + unit) + 64 * part;
           const bool all = valid == 15u && base + 63 <= upto && (base >= from || base + 63 < firsts);
           const bool masked = !__all_sync(kFull, all);
           wait_ld(s[0]);
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
             M = nm;
             L *= f;
             if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores' place was free)
-              ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (q - 1) & 1u, abort_flag, p.status));
+              ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (done - 1) & 1u, abort_flag, p.status));
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -377,7 +388,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       if (M == -INFINITY && L != L) M = 0.f;  // all scores are no numbers: the NaN goes on
       const bool whole = seg.first == 0 && seg.n == t.n;
       const int64_t orow = ((int64_t)(t.start + tok) * p.Hq + seg.h * p.G + rho - tok * p.G) * D;
-      float* rec = p.rec + (((int64_t)blockIdx.x * 2 + (seg.first == 0)) * p.tile + r) * REC;
+      float* rec = p.rec + (((int64_t)blockIdx.x * 2 + (seg.first == 0)) * p.tile + row) * REC;
       auto put = [&](int col, const float (&o)[16], float inv) {  // 16 of the row's sums
         if (!here) return;
         if (whole) {
@@ -400,65 +411,82 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           for (int e = 0; e < 4; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       };
-      // the second group's sums go to the first through shared memory, half of the columns at a time
-      float* buf_join = reinterpret_cast<float*>(smem + Ly::kJoin);  // [D/2][128]
-      if (w == 1) {
-        ms.m[r] = M;
-        ms.l[r] = L;
+      if constexpr (WIDE) {
         if (any) {
+          if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(M, L);
+          const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
+            float f[16];
             tmem_ld16_nw(tO + 16 * c, o);
             wait_ld(o);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) buf_join[(16 * c + e) * 128 + r] = __uint_as_float(o[e]);
+            for (int e = 0; e < 16; ++e) f[e] = L == 0.f ? 0.f : __uint_as_float(o[e]);
+            put(16 * c, f, inv);
           }
         }
-      }
-      if (!(ok = meet())) break;
-      float f0 = 0.f, f1 = 0.f, inv = 0.f;
-      if (w == 0) {
-        const float m1 = ms.m[r], top = fmaxf(M, m1);
-        f0 = M == -INFINITY ? 0.f : ex2(M - top);
-        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
-        L = (f0 == 0.f ? 0.f : L * f0) + (f1 == 0.f ? 0.f : ms.l[r] * f1);
-        inv = L == 0.f ? 0.f : 1.f / L;
-        if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(top, L);
-      }
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part) {
-        if (w == 0 && any) {
-#pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[16];
-            float f[16];
-            tmem_ld16_nw(tO + part * (D / 2) + 16 * c, o);
-            wait_ld(o);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              f[e] = f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
-              if (f1 != 0.f) f[e] = fmaf(buf_join[(16 * c + e) * 128 + r], f1, f[e]);
-            }
-            put(part * (D / 2) + 16 * c, f, inv);
-          }
-        }
-        if (!(ok = meet())) break;
-        if (part == 0) {
-          if (w == 1 && any) {
+      } else {
+        // the second group's sums go to the first through shared memory, half of the columns at a time
+        float* buf_join = reinterpret_cast<float*>(smem + Ly::kJoin);  // [D/2][128]
+        if (w == 1) {
+          ms.m[r] = M;
+          ms.l[r] = L;
+          if (any) {
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
               uint32_t o[16];
-              tmem_ld16_nw(tO + D / 2 + 16 * c, o);
+              tmem_ld16_nw(tO + 16 * c, o);
               wait_ld(o);
 #pragma unroll
               for (int e = 0; e < 16; ++e) buf_join[(16 * c + e) * 128 + r] = __uint_as_float(o[e]);
             }
           }
-          if (!(ok = meet())) break;
         }
+        if (!(ok = meet())) break;
+        float f0 = 0.f, f1 = 0.f, inv = 0.f;
+        if (w == 0) {
+          const float m1 = ms.m[r], top = fmaxf(M, m1);
+          f0 = M == -INFINITY ? 0.f : ex2(M - top);
+          f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
+          L = (f0 == 0.f ? 0.f : L * f0) + (f1 == 0.f ? 0.f : ms.l[r] * f1);
+          inv = L == 0.f ? 0.f : 1.f / L;
+          if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(top, L);
+        }
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          if (w == 0 && any) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[16];
+              float f[16];
+              tmem_ld16_nw(tO + part * (D / 2) + 16 * c, o);
+              wait_ld(o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) {
+                f[e] = f0 == 0.f ? 0.f : __uint_as_float(o[e]) * f0;
+                if (f1 != 0.f) f[e] = fmaf(buf_join[(16 * c + e) * 128 + r], f1, f[e]);
+              }
+              put(part * (D / 2) + 16 * c, f, inv);
+            }
+          }
+          if (!(ok = meet())) break;
+          if (part == 0) {
+            if (w == 1 && any) {
+#pragma unroll 1
+              for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[16];
+                tmem_ld16_nw(tO + D / 2 + 16 * c, o);
+                wait_ld(o);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) buf_join[(16 * c + e) * 128 + r] = __uint_as_float(o[e]);
+              }
+            }
+            if (!(ok = meet())) break;
+          }
+        }
+        if (!ok) break;
       }
-      if (!ok) break;
       tc_fence_before();
       if (seg.first == 0 && !whole) {
         split.b = t.b;
@@ -478,7 +506,11 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     // ---------------- codes to fp16 operands: K by one group of warps, V by the other
     const bool is_v = warp >= 12;
     const int ct = tid & 127;
-    constexpr int CH = D / 16;  // 16-code pieces of a token
+    constexpr int CH = D / 16, STEP = 128 / CH;  // 16-code pieces of a token, tokens that the threads take at a time
+    const int tk = ct / CH, cc = ct % CH;
+    // lanes of the second 64 coordinates store their two pieces the other way round: no bank twice
+    const bool odd = (cc >> 2) & 1;
+    const int to0 = ((2 * (cc & 3) + odd) ^ (tk & 7)) << 4, to1 = ((2 * (cc & 3) + 1 - odd) ^ (tk & 7)) << 4;
     uint64_t* full = is_v ? ms.v_full : ms.k_full;
     uint64_t* empty = is_v ? ms.v_empty : ms.k_empty;
     uint32_t q = 0, rs = is_v, rph = 0;
@@ -510,24 +542,25 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           ok = __all_sync(kFull, um_wait(&empty[st], ph ^ 1u, abort_flag, p.status));
           if (!ok) break;
         }
-        const unsigned char* raw = smem + Ly::kRaw + rs * Ly::kRawTile;
-        unsigned char* dst = smem + (is_v ? Ly::kV : Ly::kK) + st * Ly::kTile;
-#pragma unroll 4
-        for (int i = 0; i < CH; ++i) {
-          const int x = ct + 128 * i, tk = x / CH, cc = x % CH;
-          uint4 c = *reinterpret_cast<const uint4*>(raw + tk * D + cc * 16);
-          if (part) {  // what no row sees may be anything, and 0 times it a NaN
-            const int at = base + tk;
-            if (!(((valid >> (tk >> 4)) & 1u) && at < seg.t.hi && (at >= seg.t.lo || at < firsts))) c = make_uint4(0u, 0u, 0u, 0u);
-          }
+        const unsigned char* raw = smem + Ly::kRaw + rs * Ly::kRawTile + ct * 16;
+        unsigned char* row = smem + (is_v ? Ly::kV : Ly::kK) + st * Ly::kTile + (cc >> 2) * 16384 + tk * 128;
+        auto one = [&](int i, bool there) {
+          uint4 c = *reinterpret_cast<const uint4*>(raw + i * 2048);
+          if (!there) c = make_uint4(0u, 0u, 0u, 0u);
           const uint4 lo = make_uint4(c8_wide(c.x), c8_wide_hi(c.x), c8_wide(c.y), c8_wide_hi(c.y));
           const uint4 hi = make_uint4(c8_wide(c.z), c8_wide_hi(c.z), c8_wide(c.w), c8_wide_hi(c.w));
-          unsigned char* row = dst + (cc >> 2) * 16384 + tk * 128;
-          const int ch = 2 * (cc & 3), sw = tk & 7;
-          // lanes of the second 64 coordinates store their pieces the other way round: no bank twice
-          const bool odd = (cc >> 2) & 1;
-          *reinterpret_cast<uint4*>(row + (((ch + odd) ^ sw) << 4)) = odd ? hi : lo;
-          *reinterpret_cast<uint4*>(row + (((ch + 1 - odd) ^ sw) << 4)) = odd ? lo : hi;
+          *reinterpret_cast<uint4*>(row + to0 + i * (STEP * 128)) = odd ? hi : lo;
+          *reinterpret_cast<uint4*>(row + to1 + i * (STEP * 128)) = odd ? lo : hi;
+        };
+        if (!part) {
+#pragma unroll
+          for (int i = 0; i < CH; ++i) one(i, true);
+        } else {  // what no row sees may be anything, and 0 times it a NaN
+#pragma unroll 1
+          for (int i = 0; i < CH; ++i) {
+            const int t = tk + STEP * i, at = base + t;
+            one(i, ((valid >> (t >> 4)) & 1u) && at < seg.t.hi && (at >= seg.t.lo || at < firsts));
+          }
         }
         fence_proxy_async();
         __syncwarp();
@@ -543,29 +576,36 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       }
     }
   } else if (warp == kUmMma) {
-    // ---------------- scores, half a unit at a time.  (Scores and sums have a warp
-    // each: one for both took twice the products' own time, its instructions fetched
-    // anew each time round between the other roles'.)
+    // ---------------- scores, of 64 tokens at a time.  (Scores and sums have a warp
+    // each: one for both took twice the products' own time.)
     constexpr uint32_t idesc = umma_idesc_f16(128, 64);
-    const uint64_t dk = umma_desc_sw128(smem_u32(smem + Ly::kK));
-    uint32_t q = 0, buf = 0, bph = 1, qn = 0;  // halves so far, place of the next scores and its phase, tiles
+    const uint64_t dk = umma_desc_sw128(smem_u32(smem + Ly::kK)), dq = umma_desc_sw128(smem_u32(smem + Ly::kJoin));
+    uint32_t q = 0, buf = 0, bph = 1, qn = 0;  // scores so far, place of the next scores and its phase, tiles
     bool ok = true;
     while (ok && c8_next(p, walk, seg)) {
       if (!(ok = __all_sync(kFull, um_wait(&ms.q_full, qn++ & 1u, abort_flag, p.status)))) break;
 #pragma unroll 1
-      for (int k = 0; k < 2 * seg.n; ++k) {
-        const uint32_t st = (q >> 1) & 1u;
-        const bool lk = (lane & 1) && !(q & 1u);  // odd lanes look for K, with the first half
-        ok = um_wait_lanes(lk ? &ms.k_full[st] : &ms.s_empty[buf], lk ? (q >> 2) & 1u : bph, abort_flag, p.status);
+      for (int k = 0; k < PER * seg.n; ++k) {
+        const uint32_t at = q % PER, u = q / PER, st = u & 1u;
+        const bool lk = (lane & 1) && at == 0;  // odd lanes look for K, with a unit's first scores
+        ok = um_wait_lanes(lk ? &ms.k_full[st] : &ms.s_empty[buf], lk ? (u >> 1) & 1u : bph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = dk + st * (Ly::kTile / 16) + (q & 1u) * (8192 / 16);
+          const uint64_t b = dk + st * (Ly::kTile / 16) + (WIDE ? at >> 1 : at) * (8192 / 16);
+          if (WIDE && (at & 1u)) {
 #pragma unroll
-          for (int ks = 0; ks < KS; ++ks)
-            umma_f16_ts(tmem + 64 * buf, tmem + kColQ + 8 * ks, b + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, idesc, ks ? 1u : 0u);
+            for (int ks = 0; ks < KS; ++ks) {
+              const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) / 16;
+              umma_f16(tmem + 64 * buf, dq + o, b + o, idesc, ks ? 1u : 0u);
+            }
+          } else {
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+              umma_f16_ts(tmem + 64 * buf, tmem + kColQ + 8 * ks, b + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, idesc, ks ? 1u : 0u);
+          }
           umma_commit(&ms.s_full[buf]);
-          if (q & 1u) umma_commit(&ms.k_empty[st]);
+          if (at == PER - 1) umma_commit(&ms.k_empty[st]);
         }
         __syncwarp();
         ++q;
@@ -585,14 +625,14 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     bool ok = true;
     while (ok && c8_next(p, walk, seg)) {
 #pragma unroll 1
-      for (int k = 0; k < 2 * seg.n; ++k) {
-        const uint32_t st = (q >> 1) & 1u, w = q & 1u;
-        const bool lv = (lane & 1) && !w;
-        ok = um_wait_lanes(lv ? &ms.v_full[st] : &ms.p_full[buf], lv ? (q >> 2) & 1u : bph, abort_flag, p.status);
+      for (int k = 0; k < PER * seg.n; ++k) {
+        const uint32_t at = q % PER, u = q / PER, st = u & 1u, w = q & 1u;
+        const bool lv = (lane & 1) && at == 0;
+        ok = um_wait_lanes(lv ? &ms.v_full[st] : &ms.p_full[buf], lv ? (u >> 1) & 1u : bph, abort_flag, p.status);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          const uint64_t b = dv + st * (Ly::kTile / 16) + w * (8192 / 16);
+          const uint64_t b = dv + st * (Ly::kTile / 16) + (WIDE ? at >> 1 : at) * (8192 / 16);
           const uint32_t a = tmem + 64 * buf, d = tmem + kColO + 128 * w;
           const uint32_t on = k < 2 ? 0u : 1u;
           if constexpr (TWO) {  // remainders first: not truncated against a large sum
@@ -603,8 +643,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           for (int ks = 0; ks < 4; ++ks) umma_f16_ts(d, a + 8 * ks, b + ks * 128, idesc, TWO || ks ? 1u : on);
           umma_commit(&ms.s_empty[buf]);
           umma_commit(&ms.pv_done[w]);
-          if (w) umma_commit(&ms.v_empty[st]);
-          if (k == 2 * seg.n - 1) umma_commit(&ms.o_done);
+          if (at == PER - 1) umma_commit(&ms.v_empty[st]);
+          if (k == PER * seg.n - 1) umma_commit(&ms.o_done);
         }
         __syncwarp();
         ++q;
@@ -709,19 +749,23 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, bool WIDE>
 cudaError_t run_umma(const C8Params& p, cudaStream_t st) {
   static PerDeviceValue attr;
-  const cudaError_t e = smem_attr_once(attr, (const void*)c8_umma_kernel<T, D>, kUmSmem<D>);
-  return e != cudaSuccess ? e : c8_launch(c8_umma_kernel<T, D>, dim3(p.ctas), kUmThreads, kUmSmem<D>, st, p);
+  const cudaError_t e = smem_attr_once(attr, (const void*)c8_umma_kernel<T, D, WIDE>, kUmSmem<D>);
+  return e != cudaSuccess ? e : c8_launch(c8_umma_kernel<T, D, WIDE>, dim3(p.ctas), kUmThreads, kUmSmem<D>, st, p);
+}
+template <typename T>
+cudaError_t run_umma_d(const C8Params& p, cudaStream_t st) {
+  if (p.tile == 256) return p.d == 64 ? run_umma<T, 64, true>(p, st) : run_umma<T, 128, true>(p, st);
+  return p.d == 64 ? run_umma<T, 64, false>(p, st) : run_umma<T, 128, false>(p, st);
 }
 
 }  // namespace
 
-// p.tile: 128
+// p.tile: 128 or 256 (WIDE)
 cudaError_t c8_attend_umma(const C8Params& p, cudaStream_t st) {
-  if (p.dtype == TQ_F16) return p.d == 64 ? run_umma<__half, 64>(p, st) : run_umma<__half, 128>(p, st);
-  return p.d == 64 ? run_umma<__nv_bfloat16, 64>(p, st) : run_umma<__nv_bfloat16, 128>(p, st);
+  return p.dtype == TQ_F16 ? run_umma_d<__half>(p, st) : run_umma_d<__nv_bfloat16>(p, st);
 }
 
 }  // namespace tq
