@@ -548,7 +548,7 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  *           one stream; captured graphs that may run at the same time need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
  * UNSUPPORTED for B > 65536, rows * Hq or max_blocks * block past 2^31 - 256, pages * Hkv or
- * (max_blocks * block / 128 + 2) * Hkv past 2^31 - 1.
+ * (max_blocks * block / 128 + 8) * Hkv past 2^31 - 1.
  */
 tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int Hq, int64_t rows, size_t* bytes);
 tq_status tq_cache8_attention(const void* d_q, int64_t q_stride, int dtype, int64_t rows, const int32_t* d_row_start,

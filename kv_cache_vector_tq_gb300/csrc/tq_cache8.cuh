@@ -66,7 +66,8 @@ __device__ __forceinline__ int c8_find(const int32_t* row_start, int B, int rows
 //
 // Work: a tile is up to `tile` rows of a request and KV head, a row being one
 // (token, query head of the KV head) pair; its units are the 128-token pieces of
-// the cache that some row of it sees.  The units of all tiles, laid end to end, are
+// the cache that some row of it sees.  The units of all tiles, laid end to end (and
+// for each tile a few more, for what its beginning and end cost), are
 // shared evenly among the CTAs of a grid that fits the GPU once, whatever the
 // lengths are: lengths live on the device, so a captured call serves later ones.  A
 // tile that one CTA has all of is written out by it; parts go to the CTAs' records,
@@ -77,7 +78,7 @@ constexpr float kC8Log2e = 1.4426950408889634f;
 // A part of a tile that was begun by a CTA and not ended: where the rest is.
 struct C8Split {
   int b, rt, h, pad;      // h < 0: none
-  int64_t u0, u1, units;  // its units among all
+  int64_t u0, u1, units;  // its counted units among all
 };
 
 struct C8Params {
@@ -95,6 +96,7 @@ struct C8Params {
   C8Split* split;  // [ctas]
   float* rec;      // [ctas][2][tile][d + 4]: m, l, 2 pad, sums; a tile that goes on from the CTA before, one that begins here
   int ctas, tile, slots;
+  int pad;         // what a tile's beginning and end cost, in units: the CTAs' shares count it
 };
 
 // The rows and the tokens of a tile.
@@ -179,7 +181,8 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
         mine = 0;
         if (x < p.slots) {
           const int b = c8_slot_b(p, x);
-          mine = (int64_t)c8_tile(p, b, x - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1)).n * p.Hkv;
+          const int n = c8_tile(p, b, x - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1)).n;
+          if (n > 0) mine = (int64_t)(n + p.pad) * p.Hkv;
         }
         int64_t in = mine;
 #pragma unroll
@@ -223,7 +226,7 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
 struct C8Seg {
   C8Tile t;
   int h, first, n;
-  int64_t u0;  // the tile's first unit among all
+  int64_t u0;  // the tile's first counted unit among all
 };
 struct C8Walk {
   int64_t u, u1, before;
@@ -235,15 +238,18 @@ __device__ __forceinline__ C8Walk c8_walk(const C8Params& p, const C8Share& s) {
 __device__ __forceinline__ bool c8_next(const C8Params& p, C8Walk& w, C8Seg& g) {
   while (w.u < w.u1 && w.slot < p.slots) {
     g.t = c8_tile(p, w.b, w.slot - c8_key(p.row_start, w.b, p.rows, p.G, p.tile, 1));
-    const int64_t all = (int64_t)g.t.n * p.Hkv;
+    const int64_t all = g.t.n > 0 ? (int64_t)(g.t.n + p.pad) * p.Hkv : 0;
     if (w.u < w.before + all) {
-      const int at = (int)(w.u - w.before);
-      g.h = at / g.t.n;
-      g.first = at - g.h * g.t.n;
-      g.n = (int)min((int64_t)(g.t.n - g.first), w.u1 - w.u);
-      g.u0 = w.before + (int64_t)g.h * g.t.n;
-      w.u += g.n;
-      return true;
+      // the first `pad` of a tile's counted units are no units
+      const int nv = g.t.n + p.pad, at = (int)(w.u - w.before);
+      g.h = at / nv;
+      const int v0 = at - g.h * nv, cnt = (int)min((int64_t)(nv - v0), w.u1 - w.u);
+      g.first = max(v0 - p.pad, 0);
+      g.n = max(v0 + cnt - p.pad, 0) - g.first;
+      g.u0 = w.before + (int64_t)g.h * nv;
+      w.u += cnt;
+      if (g.n > 0) return true;
+      continue;
     }
     w.before += all;
     ++w.slot;

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       split.rt = t.rt;
       split.h = h;
       split.u0 = seg.u0;
-      split.u1 = seg.u0 + t.n;
+      split.u1 = seg.u0 + t.n + p.pad;
     }
     fence_proxy_async();  // before copies take the states' place
     __syncthreads();
@@ -598,10 +598,11 @@ tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream
   p.status = c.d_status;
   p.tile = tile_rows(a.rows, a.B, p.G, a.dtype != TQ_F32);
   p.ctas = grid_ctas(p.tile);
+  p.pad = 2;
   p.split = static_cast<C8Split*>(a.ws);
   p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + al256((size_t)num_sms() * 2 * sizeof(C8Split)));
   const int64_t slots = a.rows * p.G / p.tile + a.B;
-  const int64_t most = (int64_t)a.max_blocks * c.block / kC8Unit + 2;  // units of a tile
+  const int64_t most = (int64_t)a.max_blocks * c.block / kC8Unit + 2 + p.pad;  // counted units of a tile
   if (slots > INT32_MAX || most * p.Hkv > INT32_MAX || c.pages > INT32_MAX / p.Hkv) return TQ_ERR_UNSUPPORTED;
   p.slots = (int)slots;
   CUtensorMap kmap, vmap;

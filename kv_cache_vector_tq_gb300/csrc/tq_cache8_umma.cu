@@ -52,7 +52,7 @@ struct Misc {
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t meta_full[kMeta];
-  uint64_t s_full[3], s_empty[3], p_full[3], pv_done[2], q_full, o_done, pair, drain;
+  uint64_t s_full[3], s_empty[3], p_full[3], pv_done[2], q_full, turned, o_done, pair, drain;
   int64_t sums[1][kUmThreads / 32 + 1], found[2];
   float m[128], l[128];        // of the second group, where the two are joined
   uint32_t sent[2];            // tiles of codes asked for, K and V
@@ -173,6 +173,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&ms.meta_full[i], 1);
     mbar_init(&ms.q_full, 8);
+    mbar_init(&ms.turned, 4);
     mbar_init(&ms.o_done, 1);
     mbar_init(&ms.pair, 8);
     mbar_init(&ms.drain, 2);
@@ -212,55 +213,95 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       // tokens that the row sees: from .. upto, and the first ones
       const int pos = here ? (int)min((int64_t)t.len + tok, (int64_t)INT32_MAX) : -1;
       const int upto = min(pos, t.hi - 1), from = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-      // ---- the row of q, as an operand: this group's half of its coordinates
-      float cf;
+      // ---- the warp's 32 rows of q, as an operand: read along rows (a thread's own
+      // row took a look-up in L1 for every lane), turned by way of shared memory
+      float cf = 0.f;
       {
-        uint4 x[D / 8];
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (int64_t)(t.start + tok) * p.qs +
-                                                          (int64_t)(seg.h * p.G + rho - tok * p.G) * D);
+        constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;  // lanes of a row, rows of an access, accesses
+        const int c8 = lane % LPR, r0 = row - lane + lane / LPR;   // piece of a row, first row
+        uint4 x[NI];
+        int at = t.row0 + r0, tk = at / p.G, gg = at - tk * p.G;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) x[i] = here ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+        for (int i = 0; i < NI; ++i) {
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r0 + RPI * i < t.nrow)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (int64_t)(t.start + tk) * p.qs +
+                                                        (int64_t)(seg.h * p.G + gg) * D) + c8);
+          gg += RPI;
+          while (gg >= p.G) {
+            gg -= p.G;
+            ++tk;
+          }
+        }
         auto two = [](uint32_t u) -> float2 {
           if constexpr (TWO)
             return __half22float2(*reinterpret_cast<const __half2*>(&u));
           else
             return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&u));
         };
-        float top = 0.f;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-          const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+        for (int i = 0; i < NI; ++i) {
+          uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          float top = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 f = two(u[e]);
             top = um_max3(top, fabsf(f.x), fabsf(f.y));
           }
-        }
-        const int ex = c8_row_exp(top);
-        cf = p.zscale * c8_pow2(ex);
-        const float f = c8_pow2(-ex);
-        auto half8 = [&](const uint4& x8) -> uint4 {
-          const uint32_t u[4] = {x8.x, x8.y, x8.z, x8.w};
-          uint32_t h[4];
+#pragma unroll
+          for (int o = LPR / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+          const int ex = c8_row_exp(top);
+          const float f = c8_pow2(-ex), mine = __shfl_sync(kFull, p.zscale * c8_pow2(ex), (lane % RPI) * LPR);
+          if (lane / RPI == i) cf = mine;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float2 v = two(u[e]);
-            h[e] = pack_f16x2(v.x * f, v.y * f);
+            u[e] = pack_f16x2(v.x * f, v.y * f);
           }
-          return make_uint4(h[0], h[1], h[2], h[3]);
-        };
-        if (WIDE && w) {  // these rows' Q goes to shared memory
-          unsigned char* dst = smem + Ly::kJoin + r * 128;
+          x[i] = make_uint4(u[0], u[1], u[2], u[3]);
+        }
+        unsigned char* join = smem + Ly::kJoin;
+        const int rr = r - lane + lane / LPR;  // of the group's 128 rows
+        if (WIDE && w) {  // these rows' Q stays in shared memory: 64 coordinates, then the others
 #pragma unroll
-          for (int i = 0; i < D / 8; ++i) *reinterpret_cast<uint4*>(dst + (i >> 3) * 16384 + (((i & 7) ^ (r & 7)) << 4)) = half8(x[i]);
+          for (int half = 0; half < D / 64; ++half) {
+            if (half == D / 64 - 1) {  // where the first group's turning was
+              ok = __all_sync(kFull, um_wait(&ms.turned, segs & 1u, abort_flag, p.status));
+              if (!ok) break;
+            }
+            if (c8 / 8 == half)
+#pragma unroll
+              for (int i = 0; i < NI; ++i)
+                *reinterpret_cast<uint4*>(join + half * 16384 + (rr + RPI * i) * 128 + (((c8 & 7) ^ ((rr + RPI * i) & 7)) << 4)) = x[i];
+          }
+          if (!ok) break;
           fence_proxy_async();
         } else {
-          constexpr int N = WIDE ? D / 8 : D / 16;  // (a half each where the groups have the same rows)
+          // PAIR: each group its half of the coordinates; WIDE: 64 at a time in the last 16 KB
+          unsigned char* mine = join + (WIDE ? (D / 64 - 1) * 16384 + (warp & 3) * 4096 : warp * (Ly::kTile / 8));
+          constexpr int PC = WIDE ? 8 : D / 16;  // 16-byte pieces of a row that are turned at a time
 #pragma unroll
-          for (int i = 0; i < N; i += 2) {  // eight columns of pairs
-            const uint4 a = half8(!WIDE && w ? x[D / 8 - N + i] : x[i]), b = half8(!WIDE && w ? x[D / 8 - N + i + 1] : x[i + 1]);
-            const uint32_t h[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            tmem_st8(tl + kColQ + w * (D / 4) + 4 * i, h);
+          for (int half = 0; half < (WIDE ? D / 64 : 1); ++half) {
+            const int h = WIDE ? half : w;
+            if (half) __syncwarp();
+            if (c8 / PC == h)
+#pragma unroll
+              for (int i = 0; i < NI; ++i) {
+                const int lr = lane / LPR + RPI * i;
+                *reinterpret_cast<uint4*>(mine + lr * (PC * 16) + (((c8 % PC) ^ (lr & (PC - 1))) << 4)) = x[i];
+              }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PC; i += 2) {  // eight columns of pairs
+              const uint4 a = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + ((i ^ (lane & (PC - 1))) << 4));
+              const uint4 b = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + (((i + 1) ^ (lane & (PC - 1))) << 4));
+              const uint32_t h8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+              tmem_st8(tl + kColQ + h * (4 * PC) + 4 * i, h8);
+            }
+          }
+          if (WIDE) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.turned);
           }
         }
         tmem_wait_st();
@@ -390,9 +431,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       const int64_t orow = ((int64_t)(t.start + tok) * p.Hq + seg.h * p.G + rho - tok * p.G) * D;
       float* rec = p.rec + (((int64_t)blockIdx.x * 2 + (seg.first == 0)) * p.tile + row) * REC;
       auto put = [&](int col, const float (&o)[16], float inv) {  // 16 of the row's sums
-        if (!here) return;
         if (whole) {
-          T* to = static_cast<T*>(p.out) + orow + col;
           uint32_t h[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -403,9 +442,11 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
               h[e] = *reinterpret_cast<const uint32_t*>(&b);
             }
           }
+          if (!here) return;
+          T* to = static_cast<T*>(p.out) + orow + col;
           reinterpret_cast<uint4*>(to)[0] = make_uint4(h[0], h[1], h[2], h[3]);
           reinterpret_cast<uint4*>(to)[1] = make_uint4(h[4], h[5], h[6], h[7]);
-        } else {
+        } else if (here) {
           float4* to = reinterpret_cast<float4*>(rec + 4 + col);
 #pragma unroll
           for (int e = 0; e < 4; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
@@ -493,7 +534,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         split.rt = t.rt;
         split.h = seg.h;
         split.u0 = seg.u0;
-        split.u1 = seg.u0 + t.n;
+        split.u1 = seg.u0 + t.n + p.pad;
       }
     }
     split.units = sh.units;
