@@ -42,7 +42,7 @@ struct Lay {
   static constexpr int kRawTile = 128 * D;    // as codes
   static constexpr int kRaws = D == 64 ? 8 : 4;  // K and V in turn
   static constexpr int kK = 0, kV = kK + 2 * kTile, kRaw = kV + 2 * kTile, kJoin = kRaw + kRaws * kRawTile;
-  static constexpr int kMisc = kJoin + 128 * (D / 2) * 4;
+  static constexpr int kMisc = kJoin + 32768;
 };
 
 struct Misc {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         if (WIDE && w) {  // these rows' Q stays in shared memory: 64 coordinates, then the others
 #pragma unroll
           for (int half = 0; half < D / 64; ++half) {
-            if (half == D / 64 - 1) {  // where the first group's turning was
+            if (half) {  // where the first group's turning was
               ok = __all_sync(kFull, um_wait(&ms.turned, segs & 1u, abort_flag, p.status));
               if (!ok) break;
             }
@@ -278,7 +278,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           fence_proxy_async();
         } else {
           // PAIR: each group its half of the coordinates; WIDE: 64 at a time in the last 16 KB
-          unsigned char* mine = join + (WIDE ? (D / 64 - 1) * 16384 + (warp & 3) * 4096 : warp * (Ly::kTile / 8));
+          unsigned char* mine = join + (WIDE ? 16384 + (warp & 3) * 4096 : warp * (Ly::kTile / 8));
           constexpr int PC = WIDE ? 8 : D / 16;  // 16-byte pieces of a row that are turned at a time
 #pragma unroll
           for (int half = 0; half < (WIDE ? D / 64 : 1); ++half) {
@@ -430,22 +430,26 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       const bool whole = seg.first == 0 && seg.n == t.n;
       const int64_t orow = ((int64_t)(t.start + tok) * p.Hq + seg.h * p.G + rho - tok * p.G) * D;
       float* rec = p.rec + (((int64_t)blockIdx.x * 2 + (seg.first == 0)) * p.tile + row) * REC;
+      auto half8 = [&](const float* o, float inv) -> uint4 {  // eight sums as outputs
+        uint32_t h[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (TWO) {
+            h[e] = pack_f16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
+          } else {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
+            h[e] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+        }
+        return make_uint4(h[0], h[1], h[2], h[3]);
+      };
       auto put = [&](int col, const float (&o)[16], float inv) {  // 16 of the row's sums
         if (whole) {
-          uint32_t h[8];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            if constexpr (TWO) {
-              h[e] = pack_f16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-            } else {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-              h[e] = *reinterpret_cast<const uint32_t*>(&b);
-            }
-          }
+          const uint4 a = half8(o, inv), b = half8(o + 8, inv);
           if (!here) return;
           T* to = static_cast<T*>(p.out) + orow + col;
-          reinterpret_cast<uint4*>(to)[0] = make_uint4(h[0], h[1], h[2], h[3]);
-          reinterpret_cast<uint4*>(to)[1] = make_uint4(h[4], h[5], h[6], h[7]);
+          reinterpret_cast<uint4*>(to)[0] = a;
+          reinterpret_cast<uint4*>(to)[1] = b;
         } else if (here) {
           float4* to = reinterpret_cast<float4*>(rec + 4 + col);
 #pragma unroll
@@ -456,6 +460,10 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         if (any) {
           if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(M, L);
           const float inv = L == 0.f ? 0.f : 1.f / L;
+          // 64 coordinates at a time; whole rows are turned in 4 KB of the warp's own (the
+          // first group's where it turns its q, the second's where its q was), so that
+          // stores go along rows
+          unsigned char* turn = smem + Ly::kJoin + (w ? 0 : 16384) + (warp & 3) * 4096;
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
@@ -464,7 +472,23 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
             wait_ld(o);
 #pragma unroll
             for (int e = 0; e < 16; ++e) f[e] = L == 0.f ? 0.f : __uint_as_float(o[e]);
-            put(16 * c, f, inv);
+            if (!whole) {
+              put(16 * c, f, inv);
+              continue;
+            }
+            const uint4 a = half8(f, inv), b = half8(f + 8, inv);
+            *reinterpret_cast<uint4*>(turn + lane * 128 + (((2 * c) & 7) ^ (lane & 7)) * 16) = a;
+            *reinterpret_cast<uint4*>(turn + lane * 128 + (((2 * c + 1) & 7) ^ (lane & 7)) * 16) = b;
+            if ((c & 3) != 3) continue;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int lr = 4 * i + (lane >> 3), c8 = lane & 7;
+              const int64_t to = __shfl_sync(kFull, orow, lr);
+              const uint4 v = *reinterpret_cast<const uint4*>(turn + lr * 128 + ((c8 ^ (lr & 7)) << 4));
+              if (row - lane + lr < t.nrow) reinterpret_cast<uint4*>(static_cast<T*>(p.out) + to + 64 * (c >> 2))[c8] = v;
+            }
+            __syncwarp();
           }
         }
       } else {
