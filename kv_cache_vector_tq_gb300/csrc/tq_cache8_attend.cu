@@ -598,7 +598,7 @@ tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream
   p.status = c.d_status;
   p.tile = tile_rows(a.rows, a.B, p.G, a.dtype != TQ_F32);
   p.ctas = grid_ctas(p.tile);
-  p.pad = 2;
+  p.pad = p.tile >= 128 ? 3 : 2;
   p.split = static_cast<C8Split*>(a.ws);
   p.rec = reinterpret_cast<float*>(static_cast<unsigned char*>(a.ws) + al256((size_t)num_sms() * 2 * sizeof(C8Split)));
   const int64_t slots = a.rows * p.G / p.tile + a.B;

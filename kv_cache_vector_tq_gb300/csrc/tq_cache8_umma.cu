@@ -4,16 +4,19 @@
 //
 // A persistent CTA per SM; per half of a unit (64 of its 128 tokens), with 128 rows
 // (token x query head) on the lanes of tensor memory:
-//     S[row][token]  = Q·Kᵀ        A = Q (tensor memory), B = K (shared memory)
+//     S[row][token]  = Q·Kᵀ        A = Q, B = K (shared memory)
 //     P[row][token]  = 2^(z - M)   in fp16, over S
 //     O[row][coord] += P·V         A = P (tensor memory), B = V (shared memory, row-contiguous)
 // Rows on the lanes make a softmax row one thread's: no value changes lanes.  Two
 // groups of softmax warps take a half of every unit each, with sums of their own
 // that are joined at the tile's end, or (WIDE: more than 128 rows a request and KV
-// head) 128 rows each, so that K and V are converted once for 256.  Scores have three
-// places, so that a group finds its next ones made when it has written its weights.
-// Q in tensor memory (the second group's of a WIDE tile does not fit) leaves shared
-// memory's reads to K and V, where the codes' way to fp16 (exact) is the other reader.
+// head) 128 rows each, so that K and V are converted once for 256.  From the weights
+// of one place of scores to the next scores in it it is some 2000 clocks (the slowest
+// warp, two products, three waits), more than a group takes for its next weights:
+// WIDE tiles have four places.  With the same rows in both groups Q is in tensor
+// memory instead (three places): its products take two thirds of the time that way
+// and leave shared memory to the codes' way to fp16 (exact), which there is made for
+// half as many rows (64 rows over 32 x 16384: 240 against 277 us).
 // M is raised only before a weight passes 2^14, so that O is rarely rescaled.
 // Weights are one fp16 term for bf16 outputs, two for fp16 (as in the kernel for few
 // rows); both stand in the columns of their own scores.
@@ -33,16 +36,17 @@ static_assert(8 * kUmRegSoft + 8 * kUmRegConv + 4 * 96 <= 20 * 96, "registers th
 constexpr int kMeta = 4;                     // units whose scales are kept
 constexpr uint32_t kUmLimit = 1u << 20;      // polls of a wait, a few microseconds each
 constexpr uint32_t kUmLand = 1u << 14;       // a millisecond or more for copies under way
-// Tensor memory columns: three halves of scores, Q, the two sums
-constexpr uint32_t kColQ = 192, kColO = 256;
+// Tensor memory columns: places of scores (and Q behind three of them), the two sums
+constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
 
-template <int D>
+template <int D, bool WIDE>
 struct Lay {
-  static constexpr int kTile = 128 * D * 2;   // 128 tokens in fp16
+  static constexpr int kTile = 128 * D * 2;   // 128 rows or tokens in fp16
   static constexpr int kRawTile = 128 * D;    // as codes
-  static constexpr int kRaws = D == 64 ? 8 : 4;  // K and V in turn
-  static constexpr int kK = 0, kV = kK + 2 * kTile, kRaw = kV + 2 * kTile, kJoin = kRaw + kRaws * kRawTile;
-  static constexpr int kMisc = kJoin + 32768;
+  static constexpr int kRaws = D == 64 ? 8 : WIDE ? 2 : 4;  // K and V in turn
+  static constexpr int kQTiles = WIDE ? 2 : 1;
+  static constexpr int kQ = 0, kK = kQ + kQTiles * kTile, kV = kK + 2 * kTile, kRaw = kV + 2 * kTile;
+  static constexpr int kMisc = kRaw + kRaws * kRawTile;
 };
 
 struct Misc {
@@ -52,16 +56,16 @@ struct Misc {
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t meta_full[kMeta];
-  uint64_t s_full[3], s_empty[3], p_full[3], pv_done[2], q_full, turned, o_done, pair, drain;
+  uint64_t s_full[kMostPlaces], s_empty[kMostPlaces], p_full[kMostPlaces], pv_done[2], q_full, o_done, pair, drain;
   int64_t sums[1][kUmThreads / 32 + 1], found[2];
   float m[128], l[128];        // of the second group, where the two are joined
   uint32_t sent[2];            // tiles of codes asked for, K and V
   uint32_t tmem;
   int abort;
 };
-template <int D>
-constexpr int kUmSmem = Lay<D>::kMisc + (int)sizeof(Misc);
-static_assert(kUmSmem<128> <= 227 * 1024, "shared memory");
+template <int D, bool WIDE>
+constexpr int kUmSmem = Lay<D, WIDE>::kMisc + (int)sizeof(Misc);
+static_assert(kUmSmem<128, true> <= 227 * 1024 && kUmSmem<128, false> <= 227 * 1024, "shared memory");
 
 __device__ __forceinline__ bool um_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   if (poll_rest(bar, parity)) return true;
@@ -138,9 +142,10 @@ __device__ __forceinline__ uint32_t bits_of(int a, int b) {
 
 template <typename T, int D, bool WIDE>
 __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p) {
-  using Ly = Lay<D>;
+  using Ly = Lay<D, WIDE>;
   constexpr bool TWO = std::is_same<T, __half>::value;  // terms of a weight
   constexpr int REC = D + 4, NR = Ly::kRaws, KS = D / 16, PER = WIDE ? 4 : 2;  // scores of 64 tokens and 128 rows a unit
+  constexpr uint32_t kPlaces = WIDE ? 4 : 3;
   extern __shared__ __align__(1024) unsigned char smem[];
   Misc& ms = *reinterpret_cast<Misc*>(smem + Ly::kMisc);
   const int tid = threadIdx.x, warp = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;  // (the warp's number in a uniform register)
@@ -166,14 +171,13 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       mbar_init(&ms.v_empty[i], 1);
       mbar_init(&ms.pv_done[i], 1);
     }
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < (int)kMostPlaces; ++i) {
       mbar_init(&ms.s_full[i], 1);
       mbar_init(&ms.s_empty[i], 1);
       mbar_init(&ms.p_full[i], 4);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&ms.meta_full[i], 1);
     mbar_init(&ms.q_full, 8);
-    mbar_init(&ms.turned, 4);
     mbar_init(&ms.o_done, 1);
     mbar_init(&ms.pair, 8);
     mbar_init(&ms.drain, 2);
@@ -213,8 +217,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       // tokens that the row sees: from .. upto, and the first ones
       const int pos = here ? (int)min((int64_t)t.len + tok, (int64_t)INT32_MAX) : -1;
       const int upto = min(pos, t.hi - 1), from = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
-      // ---- the warp's 32 rows of q, as an operand: read along rows (a thread's own
-      // row took a look-up in L1 for every lane), turned by way of shared memory
+      // ---- the warp's 32 rows of q, as an operand: read along rows (a thread's own row
+      // takes a look-up in L1 for every lane)
       float cf = 0.f;
       {
         constexpr int LPR = D / 8, RPI = 32 / LPR, NI = 32 / RPI;  // lanes of a row, rows of an access, accesses
@@ -260,52 +264,33 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           }
           x[i] = make_uint4(u[0], u[1], u[2], u[3]);
         }
-        unsigned char* join = smem + Ly::kJoin;
-        const int rr = r - lane + lane / LPR;  // of the group's 128 rows
-        if (WIDE && w) {  // these rows' Q stays in shared memory: 64 coordinates, then the others
+        if constexpr (WIDE) {  // to shared memory: 64 coordinates, then the others
+          unsigned char* to = smem + Ly::kQ + w * Ly::kTile + (c8 >> 3) * 16384;
+          const int rr = r - lane + lane / LPR;  // of the group's 128 rows
 #pragma unroll
-          for (int half = 0; half < D / 64; ++half) {
-            if (half) {  // where the first group's turning was
-              ok = __all_sync(kFull, um_wait(&ms.turned, segs & 1u, abort_flag, p.status));
-              if (!ok) break;
-            }
-            if (c8 / 8 == half)
-#pragma unroll
-              for (int i = 0; i < NI; ++i)
-                *reinterpret_cast<uint4*>(join + half * 16384 + (rr + RPI * i) * 128 + (((c8 & 7) ^ ((rr + RPI * i) & 7)) << 4)) = x[i];
-          }
-          if (!ok) break;
+          for (int i = 0; i < NI; ++i)
+            *reinterpret_cast<uint4*>(to + (rr + RPI * i) * 128 + (((c8 & 7) ^ ((rr + RPI * i) & 7)) << 4)) = x[i];
           fence_proxy_async();
-        } else {
-          // PAIR: each group its half of the coordinates; WIDE: 64 at a time in the last 16 KB
-          unsigned char* mine = join + (WIDE ? 16384 + (warp & 3) * 4096 : warp * (Ly::kTile / 8));
-          constexpr int PC = WIDE ? 8 : D / 16;  // 16-byte pieces of a row that are turned at a time
+        } else {  // to tensor memory, each group its half of the coordinates: turned in a place of the warp's own
+          constexpr int PC = D / 16;  // 16-byte pieces
+          unsigned char* mine = smem + Ly::kQ + warp * (Ly::kTile / 8);
+          if (c8 / PC == w)
 #pragma unroll
-          for (int half = 0; half < (WIDE ? D / 64 : 1); ++half) {
-            const int h = WIDE ? half : w;
-            if (half) __syncwarp();
-            if (c8 / PC == h)
-#pragma unroll
-              for (int i = 0; i < NI; ++i) {
-                const int lr = lane / LPR + RPI * i;
-                *reinterpret_cast<uint4*>(mine + lr * (PC * 16) + (((c8 % PC) ^ (lr & (PC - 1))) << 4)) = x[i];
-              }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < PC; i += 2) {  // eight columns of pairs
-              const uint4 a = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + ((i ^ (lane & (PC - 1))) << 4));
-              const uint4 b = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + (((i + 1) ^ (lane & (PC - 1))) << 4));
-              const uint32_t h8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-              tmem_st8(tl + kColQ + h * (4 * PC) + 4 * i, h8);
+            for (int i = 0; i < NI; ++i) {
+              const int lr = lane / LPR + RPI * i;
+              *reinterpret_cast<uint4*>(mine + lr * (PC * 16) + (((c8 % PC) ^ (lr & (PC - 1))) << 4)) = x[i];
             }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < PC; i += 2) {  // eight columns of pairs
+            const uint4 a = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + ((i ^ (lane & (PC - 1))) << 4));
+            const uint4 b = *reinterpret_cast<const uint4*>(mine + lane * (PC * 16) + (((i + 1) ^ (lane & (PC - 1))) << 4));
+            const uint32_t h8[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            tmem_st8(tl + kColQ + w * (4 * PC) + 4 * i, h8);
           }
-          if (WIDE) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ms.turned);
-          }
+          tmem_wait_st();
+          tc_fence_before();
         }
-        tmem_wait_st();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.q_full);
       }
@@ -413,8 +398,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.p_full[buf]);
         buf += 2;  // the next of this group's scores
-        if (buf >= 3) {
-          buf -= 3;
+        if (buf >= kPlaces) {
+          buf -= kPlaces;
           bph ^= 1u;
         }
       }
@@ -460,10 +445,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         if (any) {
           if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(M, L);
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          // 64 coordinates at a time; whole rows are turned in 4 KB of the warp's own (the
-          // first group's where it turns its q, the second's where its q was), so that
-          // stores go along rows
-          unsigned char* turn = smem + Ly::kJoin + (w ? 0 : 16384) + (warp & 3) * 4096;
+          // 64 coordinates at a time; whole rows are turned where the warp's own q was, so
+          // that stores go along rows
+          unsigned char* turn = smem + Ly::kQ + w * Ly::kTile + (warp & 3) * 4096;
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t o[16];
@@ -493,7 +477,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         }
       } else {
         // the second group's sums go to the first through shared memory, half of the columns at a time
-        float* buf_join = reinterpret_cast<float*>(smem + Ly::kJoin);  // [D/2][128]
+        float* buf_join = reinterpret_cast<float*>(smem + Ly::kQ);  // [D/2][128], where q was
         if (w == 1) {
           ms.m[r] = M;
           ms.l[r] = L;
@@ -585,7 +569,11 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       for (int k = 0; k < seg.n; ++k, ++q) {
         const uint32_t st = q & 1u, ph = (q >> 1) & 1u;
         const bool both = warp != 12 && (lane & 1);  // (warp 12 has something to do between the two)
-        ok = um_wait_lanes(both ? &empty[st] : &ms.raw_full[rs], both ? ph ^ 1u : rph, abort_flag, p.status);
+        if constexpr (WIDE)  // (these warps are ahead, and looks would take issue slots from the others: 540 -> 515 us)
+          ok = __all_sync(kFull, um_wait(&ms.raw_full[rs], rph, abort_flag, p.status) &&
+                                     (warp == 12 || um_wait(&empty[st], ph ^ 1u, abort_flag, p.status)));
+        else
+          ok = um_wait_lanes(both ? &empty[st] : &ms.raw_full[rs], both ? ph ^ 1u : rph, abort_flag, p.status);
         if (!ok) break;
         uint32_t valid = 0xFFu;
         bool part = false;
@@ -618,7 +606,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           *reinterpret_cast<uint4*>(row + to1 + i * (STEP * 128)) = odd ? lo : hi;
         };
         if (!part) {
-#pragma unroll
+#pragma unroll 4
           for (int i = 0; i < CH; ++i) one(i, true);
         } else {  // what no row sees may be anything, and 0 times it a NaN
 #pragma unroll 1
@@ -644,7 +632,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
     // ---------------- scores, of 64 tokens at a time.  (Scores and sums have a warp
     // each: one for both took twice the products' own time.)
     constexpr uint32_t idesc = umma_idesc_f16(128, 64);
-    const uint64_t dk = umma_desc_sw128(smem_u32(smem + Ly::kK)), dq = umma_desc_sw128(smem_u32(smem + Ly::kJoin));
+    const uint64_t dk = umma_desc_sw128(smem_u32(smem + Ly::kK)), dq = umma_desc_sw128(smem_u32(smem + Ly::kQ));
     uint32_t q = 0, buf = 0, bph = 1, qn = 0;  // scores so far, place of the next scores and its phase, tiles
     bool ok = true;
     while (ok && c8_next(p, walk, seg)) {
@@ -658,23 +646,21 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         tc_fence_after();
         if (elect_one()) {
           const uint64_t b = dk + st * (Ly::kTile / 16) + (WIDE ? at >> 1 : at) * (8192 / 16);
-          if (WIDE && (at & 1u)) {
+          const uint64_t a = dq + (at & 1u) * (Ly::kTile / 16);
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-              const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) / 16;
-              umma_f16(tmem + 64 * buf, dq + o, b + o, idesc, ks ? 1u : 0u);
-            }
-          } else {
-#pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-              umma_f16_ts(tmem + 64 * buf, tmem + kColQ + 8 * ks, b + ((ks >> 2) * 16384 + (ks & 3) * 32) / 16, idesc, ks ? 1u : 0u);
+          for (int ks = 0; ks < KS; ++ks) {
+            const uint32_t o = ((ks >> 2) * 16384 + (ks & 3) * 32) / 16;
+            if constexpr (WIDE)
+              umma_f16(tmem + 64 * buf, a + o, b + o, idesc, ks ? 1u : 0u);
+            else
+              umma_f16_ts(tmem + 64 * buf, tmem + kColQ + 8 * ks, b + o, idesc, ks ? 1u : 0u);
           }
           umma_commit(&ms.s_full[buf]);
           if (at == PER - 1) umma_commit(&ms.k_empty[st]);
         }
         __syncwarp();
         ++q;
-        if (++buf == 3) {
+        if (++buf == kPlaces) {
           buf = 0;
           bph ^= 1u;
         }
@@ -713,7 +699,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         }
         __syncwarp();
         ++q;
-        if (++buf == 3) {
+        if (++buf == kPlaces) {
           buf = 0;
           bph ^= 1u;
         }
@@ -817,8 +803,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 template <typename T, int D, bool WIDE>
 cudaError_t run_umma(const C8Params& p, cudaStream_t st) {
   static PerDeviceValue attr;
-  const cudaError_t e = smem_attr_once(attr, (const void*)c8_umma_kernel<T, D, WIDE>, kUmSmem<D>);
-  return e != cudaSuccess ? e : c8_launch(c8_umma_kernel<T, D, WIDE>, dim3(p.ctas), kUmThreads, kUmSmem<D>, st, p);
+  const cudaError_t e = smem_attr_once(attr, (const void*)c8_umma_kernel<T, D, WIDE>, kUmSmem<D, WIDE>);
+  return e != cudaSuccess ? e : c8_launch(c8_umma_kernel<T, D, WIDE>, dim3(p.ctas), kUmThreads, kUmSmem<D, WIDE>, st, p);
 }
 template <typename T>
 cudaError_t run_umma_d(const C8Params& p, cudaStream_t st) {
