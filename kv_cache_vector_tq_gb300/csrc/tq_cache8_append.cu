@@ -7,14 +7,15 @@
 //   where it holds earlier tokens; codes of those: e4m3(code·s / s'), new ones:
 //   e4m3(x / s').
 //
-// A job is the new rows of one block, one KV head and side.  Its rows come by
-// asynchronous copies, a slot of shared memory for every lane and pass (no
-// barrier), are normed and turned in place there as fp32, and read again once
-// the job's warps have agreed on the scale.  A job has a warp for every two rows
-// of a pass, four passes a block, so that a block of any size has as many bytes
-// in flight for each warp; more passes than kApPass slots are read twice (from
-// L2).  Jobs need no sum over the requests: request b's are numbered from
-// row_start[b] / block + 2b on.
+// A job is the new rows of one block, one side and some KV heads, one after the
+// other: angles, once for a token, stay in shared memory for all of them.  Rows come
+// by asynchronous copies, a slot of shared memory for every lane and pass (no barrier),
+// the next head's while this one's are scaled and stored; normed and turned they wait
+// in registers until the job's warps have agreed on the scale.  A job has a warp for
+// every two rows of a pass, four passes a block, so that a block of any size has as
+// many bytes in flight for each warp; further passes read their rows twice (from L2).
+// Jobs need no sum over the requests: request b's are numbered from row_start[b] /
+// block + 2b on.
 // The CTAs behind the jobs turn q as tq_qk_norm_rope does.
 #include <algorithm>
 #include <cmath>
@@ -26,7 +27,7 @@ namespace tq {
 
 namespace {
 
-constexpr int kApPass = 4;  // passes whose rows stay in shared memory
+constexpr int kApPass = 4;  // passes whose rows stay in registers
 
 struct AppendParams {
   NormRopeParams q;  // the rows of q (Hkv = 0)
@@ -38,7 +39,7 @@ struct AppendParams {
   uint8_t *k8, *v8;
   float *kscale, *vscale;
   int32_t* status;
-  int jobs, warps;  // jobs in all, warps of a job
+  int jobs, warps, heads, groups;  // jobs in all, warps of a job, its heads, jobs of a block and side
   int kv_ctas;
 };
 
@@ -67,13 +68,17 @@ __device__ __forceinline__ float scale_of(float a) {
   return __int_as_float((min(max(e - 8 + up, -60), 40) + 127) << 23);
 }
 
-template <typename TI, int LPR, bool HALF, bool NORM>
-__device__ __forceinline__ void append_job(const AppendParams& p, int job, int w, int bar, unsigned char* smem, float* red) {
+// Shared memory of a CTA: the rows as they come, the angles (float4 cosines, sines).
+template <typename TI>
+constexpr int kApRaw = kApPass * kNrThreads * (int)sizeof(NrSlot<TI>);
+constexpr int kApTrig = kApPass * kNrThreads * 32;
+
+template <typename TI, int LPR, bool HALF, bool NORM, bool V>
+__device__ __forceinline__ void append_job(const AppendParams& p, int slot, int h0, int h1, int w, int bar, unsigned char* smem,
+                                           uint32_t (*red)[kNrThreads / 32], int red0) {
   constexpr int RPW = 32 / LPR;
   using Raw = Raw4<TI>;
   const int lane = threadIdx.x & 31, sub = lane / LPR, l = lane % LPR;
-  const bool is_v = (job & 1) != 0;
-  const int slot = (job >> 1) / p.Hkv, h = (job >> 1) - slot * p.Hkv;
   const int b = c8_find(p.row_start, p.B, p.rows, 1, p.block, 2, slot);
   const int j = slot - c8_key(p.row_start, b, p.rows, 1, p.block, 2);
   const C8Seq s = c8_seq(p.row_start, p.len, b, p.rows);
@@ -89,122 +94,172 @@ __device__ __forceinline__ void append_job(const AppendParams& p, int job, int w
     if (p.status && lane == 0 && w == 0) atomicOr(p.status, 1);
     return;
   }
-  const int64_t blk = (int64_t)page * p.Hkv + h;
-  float* scale = (is_v ? p.vscale : p.kscale) + blk;
-  uint8_t* codes = (is_v ? p.v8 : p.k8) + blk * p.block * p.d;
-  const bool turns = !is_v && 8 * l < p.q.rot;
+  const bool turns = !V && 8 * l < p.q.rot;
   const int ja = HALF && turns ? 4 * l : 8 * l, jb = HALF && turns ? (p.q.rot >> 1) + 4 * l : 8 * l + 4;
-  const TI* src = static_cast<const TI*>(is_v ? p.v : p.k) + (int64_t)r0 * (is_v ? p.vs : p.ks) + (int64_t)h * p.d;
-  const int64_t step = is_v ? p.vs : p.ks;
-  const int per = p.warps * RPW, passes = (m + per - 1) / per;  // rows of a pass
-  const int first = w * RPW + sub;
-  // this lane's slots: 32 bytes a pass, the row as it comes and then as fp32
-  unsigned char* mine = smem + threadIdx.x * 16;
-  auto at = [&](int pass, int half) { return reinterpret_cast<float4*>(mine + (pass * 2 + half) * (kNrThreads * 16)); };
+  const int64_t step = V ? p.vs : p.ks;
+  const TI* src = static_cast<const TI*>(V ? p.v : p.k) + (int64_t)r0 * step;
+  const int per = p.warps * RPW, first = w * RPW + sub;  // rows of a pass, this lane's of the first
+  NrSlot<TI>* mine = reinterpret_cast<NrSlot<TI>*>(smem) + threadIdx.x;
+  float4* trig = reinterpret_cast<float4*>(smem + kApRaw<TI>) + threadIdx.x;
+  auto fetch = [&](int h) {
+    const TI* from = src + (int64_t)h * p.d;
 #pragma unroll
-  for (int i = 0; i < kApPass; ++i) {
-    const int r = i * per + first;
-    if (r < m) {
-      nr_copy<(int)sizeof(Raw)>(at(i, 0), src + r * step + ja);
-      nr_copy<(int)sizeof(Raw)>(at(i, 1), src + r * step + jb);
+    for (int i = 0; i < kApPass; ++i) {
+      const int r = i * per + first;
+      if (r < m) {
+        nr_copy<(int)sizeof(Raw)>(&mine[i * kNrThreads].a, from + r * step + ja);
+        nr_copy<(int)sizeof(Raw)>(&mine[i * kNrThreads].b, from + r * step + jb);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  fetch(h0);
+  if (!V) {
+#pragma unroll 1
+    for (int i = 0; i < kApPass && i * per < m; ++i) {
+      const int r = i * per + first;
+      float cs[4], sn[4];
+      turn_angles(r < m ? (uint64_t)(int64_t)p.q.pos[r0 + r] : 0, p.q.freq, l, turns, cs, sn);
+      trig[2 * i * kNrThreads] = make_float4(cs[0], cs[1], cs[2], cs[3]);
+      trig[(2 * i + 1) * kNrThreads] = make_float4(sn[0], sn[1], sn[2], sn[3]);
     }
   }
-  asm volatile("cp.async.commit_group;\n" ::: "memory");
-  const float old = o0 > 0 ? *scale : 0.f;
   const float inv_d = 1.f / (float)p.d;
-  auto row = [&](int i, float (&z)[8]) {  // row of pass i; zeros past the last
+  // one row: x as it came, z as it is stored but for the scale
+  auto row = [&](float (&x)[8], const float (&cs)[4], const float (&sn)[4], float (&z)[8]) {
+    const TurnFactors f = turn_factors<TI, HALF>(static_cast<const TI*>(p.wk), true, ja, jb, cs, sn);
+    turn_row<LPR, HALF, NORM>(x, f, turns, inv_d, p.q.eps, z);
+  };
+  auto far_row = [&](int h, int i, float (&z)[8]) {  // of a pass whose rows are not kept
     const int r = i * per + first;
     float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r < m) {
-      Raw a, c;
-      if (i < kApPass) {
-        a = *reinterpret_cast<const Raw*>(at(i, 0));
-        c = *reinterpret_cast<const Raw*>(at(i, 1));
-      } else {
-        a = *reinterpret_cast<const Raw*>(src + r * step + ja);
-        c = *reinterpret_cast<const Raw*>(src + r * step + jb);
-      }
-      widen4<TI>(a, x);
-      widen4<TI>(c, x + 4);
+      widen4<TI>(*reinterpret_cast<const Raw*>(src + (int64_t)h * p.d + r * step + ja), x);
+      widen4<TI>(*reinterpret_cast<const Raw*>(src + (int64_t)h * p.d + r * step + jb), x + 4);
     }
-    if (is_v) {
+    if constexpr (V) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) z[e] = x[e];
     } else {
       float cs[4], sn[4];
       turn_angles(r < m ? (uint64_t)(int64_t)p.q.pos[r0 + r] : 0, p.q.freq, l, turns, cs, sn);
-      const TurnFactors f = turn_factors<TI, HALF>(static_cast<const TI*>(p.wk), true, ja, jb, cs, sn);
-      turn_row<LPR, HALF, NORM>(x, f, turns, inv_d, p.q.eps, z);
+      row(x, cs, sn, z);
     }
   };
-  asm volatile("cp.async.wait_all;\n" ::: "memory");
-  float top = 0.f;  // infinite where a value is not finite
-#pragma unroll 1
-  for (int i = 0; i < passes; ++i) {
-    float z[8];
-    row(i, z);
-    if (i < kApPass) {
-      *at(i, 0) = make_float4(z[0], z[1], z[2], z[3]);
-      *at(i, 1) = make_float4(z[4], z[5], z[6], z[7]);
-    }
-    if (i * per + first < m) {
+  auto top_of = [](uint32_t top, const float (&z)[8]) -> uint32_t {  // magnitudes' bits in order, what is not finite above all
 #pragma unroll
-      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(z[e]) <= 3.4028234e38f ? fabsf(z[e]) : INFINITY);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-  if (p.warps > 1) {
-    if (lane == 0) red[w] = top;
-    asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "r"(32 * p.warps) : "memory");
-    for (int i = 0; i < p.warps; ++i) top = fmaxf(top, red[i]);
-  }
-  float now = scale_of(top);
-  if (o0 > 0 && old > now) now = old;
-  const bool bad = top == INFINITY || old != old;
-  if (o0 > 0 && !bad && now > old) {  // the tokens that are there, rounded again
-    uint4* held = reinterpret_cast<uint4*>(codes);
-    const float f = old / now;
-    for (int i = w * 32 + lane; i < o0 * p.d / 16; i += 32 * p.warps) {
-      uint4 c = held[i];
-      c.x = again8(c.x, f);
-      c.y = again8(c.y, f);
-      c.z = again8(c.z, f);
-      c.w = again8(c.w, f);
-      held[i] = c;
-    }
-  }
-  if (w == 0 && lane == 0) *scale = bad ? __int_as_float(0x7FC00000) : now;
-  const float inv = 1.f / now;
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(z[e]) & 0x7FFFFFFFu);
+    return top;
+  };
 #pragma unroll 1
-  for (int i = 0; i < passes; ++i) {
-    float z[8];
-    if (i < kApPass) {
-      *reinterpret_cast<float4*>(z) = *at(i, 0);
-      *reinterpret_cast<float4*>(z + 4) = *at(i, 1);
+  for (int h = h0; h < h1; ++h) {
+    const int64_t blk = (int64_t)page * p.Hkv + h;
+    float* scale = (V ? p.vscale : p.kscale) + blk;
+    uint8_t* codes = (V ? p.v8 : p.k8) + blk * p.block * p.d;
+    const float old = o0 > 0 ? *scale : 0.f;
+    asm volatile("cp.async.wait_all;\n" ::: "memory");
+    float z[kApPass][8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kApPass; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) z[i][e] = 0.f;
+      if (i * per < m) {
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (i * per + first < m) {
+          const NrSlot<TI> raw = mine[i * kNrThreads];
+          widen4<TI>(raw.a, x);
+          widen4<TI>(raw.b, x + 4);
+        }
+        if constexpr (V) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z[i][e] = x[e];
+        } else {
+          const float4 c = trig[2 * i * kNrThreads], n = trig[(2 * i + 1) * kNrThreads];
+          const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {n.x, n.y, n.z, n.w};
+          row(x, cs, sn, z[i]);
+        }
+        if (i * per + first < m) top = top_of(top, z[i]);
+      }
+    }
+#pragma unroll 1
+    for (int i = kApPass; i * per < m; ++i) {
+      float y[8];
+      far_row(h, i, y);
+      if (i * per + first < m) top = top_of(top, y);
+    }
+    if (h + 1 < h1) fetch(h + 1);  // the slots have been read
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = max(top, __shfl_xor_sync(kFull, top, o));
+    if (p.warps > 1) {
+      uint32_t* mx = red[h & 1] + red0;  // (the other half while a slow warp still reads the head before)
+      if (lane == 0) mx[w] = top;
+      asm volatile("bar.sync %0, %1;\n" ::"r"(bar), "r"(32 * p.warps) : "memory");
+      for (int i = 0; i < p.warps; ++i) top = max(top, mx[i]);
     } else {
-      row(i, z);
+      __syncwarp();  // every lane has the scale as it was
     }
-    const int r = i * per + first;
-    if (r < m) {
+    float now = scale_of(__uint_as_float(top));
+    if (o0 > 0 && old > now) now = old;
+    const bool bad = top >= 0x7F800000u || old != old;
+    if (o0 > 0 && !bad && now > old) {  // the tokens that are there, rounded again
+      uint4* held = reinterpret_cast<uint4*>(codes);
+      const float f = old / now;
+      for (int i = w * 32 + lane; i < o0 * p.d / 16; i += 32 * p.warps) {
+        uint4 c = held[i];
+        c.x = again8(c.x, f);
+        c.y = again8(c.y, f);
+        c.z = again8(c.z, f);
+        c.w = again8(c.w, f);
+        held[i] = c;
+      }
+    }
+    if (w == 0 && lane == 0) *scale = bad ? __int_as_float(0x7FC00000) : now;
+    const float inv = 1.f / now;
+    uint8_t* to = codes + (o0 + first) * p.d;
+    auto store = [&](int i, float (&y)[8]) {
+      if (bad) {  // codes are numbers whatever comes
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = z[e] == z[e] ? z[e] * inv : 0.f;  // codes are numbers whatever comes
-      uint8_t* to = codes + (int64_t)(o0 + r) * p.d;
-      *reinterpret_cast<uint32_t*>(to + ja) = pack8(z[0], z[1], z[2], z[3]);
-      *reinterpret_cast<uint32_t*>(to + jb) = pack8(z[4], z[5], z[6], z[7]);
+        for (int e = 0; e < 8; ++e) y[e] = y[e] == y[e] ? y[e] : 0.f;
+      }
+      const uint32_t ca = pack8(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+      const uint32_t cb = pack8(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv);
+      if (i * per + first < m) {
+        if (V || !HALF) {
+          *reinterpret_cast<uint2*>(to + i * per * p.d + ja) = make_uint2(ca, cb);
+        } else {
+          *reinterpret_cast<uint32_t*>(to + i * per * p.d + ja) = ca;
+          *reinterpret_cast<uint32_t*>(to + i * per * p.d + jb) = cb;
+        }
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < kApPass; ++i)
+      if (i * per < m) store(i, z[i]);
+#pragma unroll 1
+    for (int i = kApPass; i * per < m; ++i) {
+      float y[8];
+      far_row(h, i, y);
+      store(i, y);
     }
   }
 }
 
 template <typename TI, int LPR, bool HALF, bool NORM>
 __global__ void __launch_bounds__(kNrThreads, 3) append_kernel(const AppendParams p) {
-  __shared__ __align__(16) unsigned char smem[kApPass * 32 * kNrThreads];
-  __shared__ float red[kNrThreads / 32];
-  static_assert(kNrAhead<TI> * kNrThreads * sizeof(NrSlot<TI>) <= sizeof(smem), "the rows of q use the same place");
+  extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ uint32_t red[2][kNrThreads / 32];
+  static_assert(kNrAhead<TI> * kNrThreads * sizeof(NrSlot<TI>) <= kApRaw<TI> + kApTrig, "the rows of q use the same place");
   if ((int)blockIdx.x < p.kv_ctas) {
-    const int warp = threadIdx.x >> 5, group = warp / p.warps;
+    const int warp = threadIdx.x >> 5, group = warp / p.warps, w = warp - group * p.warps;
     const int job = blockIdx.x * (kNrThreads / 32 / p.warps) + group;
-    if (job < p.jobs) append_job<TI, LPR, HALF, NORM>(p, job, warp - group * p.warps, 1 + group, smem, red + group * p.warps);
+    if (job >= p.jobs) return;
+    // K and V in turn
+    const int slot = (job >> 1) / p.groups, h0 = ((job >> 1) - slot * p.groups) * p.heads, h1 = min(h0 + p.heads, p.Hkv);
+    if (job & 1)
+      append_job<TI, LPR, HALF, NORM, true>(p, slot, h0, h1, w, 1 + group, smem, red, group * p.warps);
+    else
+      append_job<TI, LPR, HALF, NORM, false>(p, slot, h0, h1, w, 1 + group, smem, red, group * p.warps);
   } else {
     const int64_t live = c8_row(p.row_start, p.B, p.rows);
     norm_rope_rows<TI, TI, LPR, HALF, NORM>(p.q, (int64_t)blockIdx.x - p.kv_ctas, live,
@@ -212,18 +267,21 @@ __global__ void __launch_bounds__(kNrThreads, 3) append_kernel(const AppendParam
   }
 }
 
+template <typename TI, int LPR, bool HALF, bool NORM>
+cudaError_t run_append_k(const AppendParams& p, int grid, cudaStream_t st) {
+  static PerDeviceValue attr;
+  constexpr int bytes = kApRaw<TI> + kApTrig;
+  const cudaError_t e = smem_attr_once(attr, (const void*)append_kernel<TI, LPR, HALF, NORM>, bytes);
+  if (e != cudaSuccess) return e;
+  append_kernel<TI, LPR, HALF, NORM><<<grid, kNrThreads, bytes, st>>>(p);
+  return cudaGetLastError();
+}
+
 template <typename TI, int LPR>
 cudaError_t run_append(const AppendParams& p, int grid, bool norm, cudaStream_t st) {
   const bool half = p.q.style == TQ_ROPE_HALF;
-  if (half && norm)
-    append_kernel<TI, LPR, true, true><<<grid, kNrThreads, 0, st>>>(p);
-  else if (half)
-    append_kernel<TI, LPR, true, false><<<grid, kNrThreads, 0, st>>>(p);
-  else if (norm)
-    append_kernel<TI, LPR, false, true><<<grid, kNrThreads, 0, st>>>(p);
-  else
-    append_kernel<TI, LPR, false, false><<<grid, kNrThreads, 0, st>>>(p);
-  return cudaGetLastError();
+  if (half) return norm ? run_append_k<TI, LPR, true, true>(p, grid, st) : run_append_k<TI, LPR, true, false>(p, grid, st);
+  return norm ? run_append_k<TI, LPR, false, true>(p, grid, st) : run_append_k<TI, LPR, false, false>(p, grid, st);
 }
 
 template <typename TI>
@@ -273,7 +331,14 @@ tq_status launch_cache8_append(const Cache8AppendArgs& a, cudaStream_t stream) {
   // four passes a block: one warp for blocks of 16 tokens of 64, eight from 64 of 128 on
   p.warps = 1;
   while (p.warps < kNrThreads / 32 && p.warps * rpw * kApPass < c.block) p.warps <<= 1;
-  const int64_t jobs = (a.rows / c.block + 2 * (int64_t)a.B) * c.Hkv * 2, per = kNrThreads / 32 / p.warps;
+  const int64_t slots = a.rows / c.block + 2 * (int64_t)a.B, per = kNrThreads / 32 / p.warps;
+  // all heads of a block to a job while there are two CTAs an SM of such jobs with work
+  // (half of the slots of many short requests have none), else fewer
+  p.heads = c.Hkv;
+  while (p.heads > 1 && (a.rows + c.block - 1) / c.block * ((c.Hkv + p.heads - 1) / p.heads) * 2 < 2 * num_sms() * per)
+    p.heads = (p.heads + 1) / 2;
+  p.groups = (c.Hkv + p.heads - 1) / p.heads;
+  const int64_t jobs = slots * p.groups * 2;
   // q: a whole token per warp once the tokens alone fill the GPU, else as many
   // warps per token as there are trips
   int64_t qctas = 0;
