@@ -77,8 +77,8 @@ constexpr float kC8Log2e = 1.4426950408889634f;
 
 // A part of a tile that was begun by a CTA and not ended: where the rest is.
 struct C8Split {
-  int b, rt, h, pad;      // h < 0: none
-  int64_t u0, u1, units;  // its counted units among all
+  int h, row0, nrow, start;  // h < 0: none; the tile's rows of the request's, the request's first token row
+  int64_t u0, u1, units;     // its counted units among all
 };
 
 struct C8Params {

@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       }
     }
     if (first == 0 && !whole) {
-      split.b = t.b;
-      split.rt = t.rt;
+      split.row0 = t.row0;
+      split.nrow = t.nrow;
+      split.start = t.start;
       split.h = h;
       split.u0 = seg.u0;
       split.u1 = seg.u0 + t.n + p.pad;
@@ -453,79 +454,131 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   }
 }
 
-// The parts of the tiles that several CTAs worked on.  The CTAs of blockIdx.x
-// join the rows of the tile that CTA blockIdx.x there began and did not end, a warp
-// a row.
-template <typename T, int D>
-__global__ void __launch_bounds__(256) c8_join_kernel(const C8Params p) {
+// The parts k0, k0 + every, .. of row r (part 0: of the CTA that began the tile), in
+// the warp's running maximum, sum and sums of values, AT of them in flight; whole warps.
+template <int D, int AT>
+__device__ __forceinline__ void join_row(const C8Params& p, const C8Split& s, int parts, int r, int k0, int every, float& M, float& L,
+                                         float (&o)[D / 32]) {
   constexpr int REC = D + 4, E = D / 32;
+  const int lane = threadIdx.x & 31, c0 = blockIdx.x;
+  const int64_t step = 2 * (int64_t)p.tile * REC;
+  const float* own = p.rec + (((int64_t)c0 * 2 + 1) * p.tile + r) * REC;
+  const float* more = p.rec + (int64_t)r * REC;  // of CTA k: + k·step
+#pragma unroll 1
+  for (; k0 < parts; k0 += every * AT) {
+    // a lane looks at the maximum and the sum of a part
+    const int k = k0 + every * lane;
+    bool on = lane < AT && k < parts;
+    if (on && k > 0 && s.units < p.ctas) on = c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas);
+    const uint32_t asked = __ballot_sync(kFull, on);
+    float m = -INFINITY, l = 0.f;
+    if (on) {
+      const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
+      m = ml.x;
+      l = ml.y;
+    }
+    float a[AT][E];
+#pragma unroll
+    for (int q = 0; q < AT; ++q) {
+      const int kq = k0 + every * q;
+      const float* at = (kq == 0 ? own : more + (c0 + kq) * step) + 4 + E * lane;
+#pragma unroll
+      for (int e = 0; e < E; ++e) a[q][e] = (asked >> q) & 1u ? at[e] : 0.f;
+    }
+    on = on && l != 0.f;  // saw nothing (a NaN goes on)
+    float top = on ? m : -INFINITY;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
+    const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
+    const float fa = M == -INFINITY ? 0.f : ex2(M - use);
+    const float f = on ? ex2(m - use) : 0.f;
+    float ls = on ? l * f : 0.f;
+#pragma unroll
+    for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
+    L = L * fa + ls;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= fa;
+#pragma unroll
+    for (int q = 0; q < AT; ++q) {
+      const float fk = __shfl_sync(kFull, f, q);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fk == 0.f ? o[e] : fmaf(a[q][e], fk, o[e]);
+    }
+    M = nm;
+  }
+}
+
+// The parts of the tiles that several CTAs worked on.  The CTAs of blockIdx.x join the
+// rows of the tile that CTA blockIdx.x there began and did not end: a warp a row.
+// Its CTAs are let in while the kernel before is under way, and wait beside its own.
+// FEW rows a tile: a long request's parts are some 40, and four warps join a row where
+// they are more than one has in flight (one token over 131072: 56 -> 53 us).  Many rows:
+// the parts are two or three, and a CTA with shared memory would find no room beside
+// the tensor-core kernel (which cost 5 to 20 us).
+constexpr int kJoinThreads = 256;
+template <typename T, int D, bool FEW>
+__global__ void __launch_bounds__(kJoinThreads) c8_join_kernel(const C8Params p) {
+  constexpr int E = D / 32, W = kJoinThreads / 32, AT = FEW ? 12 : 4;  // coordinates of a lane, warps, records in flight
   griddep_wait();
   griddep_launch();
-  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
-  const C8Split s = p.split[c0];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const C8Split s = p.split[blockIdx.x];
   if (s.h < 0) return;
-  const C8Tile t = c8_tile(p, s.b, s.rt);
-  const int parts = (int)((s.u1 * p.ctas - 1) / s.units) - c0 + 1;
-  const int64_t step = 2 * (int64_t)p.tile * REC;
-#pragma unroll 1
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < t.nrow; r += 8 * gridDim.y) {
-    const float* own = p.rec + (((int64_t)c0 * 2 + 1) * p.tile + r) * REC;
-    const float* more = p.rec + (int64_t)r * REC;  // of CTA k: + k·step
-    float M = -INFINITY, L = 0.f, o[E];
+  const int parts = (int)((s.u1 * p.ctas - 1) / s.units) - (int)blockIdx.x + 1;
+  float M, L, o[E];
+  auto begin = [&]() {
+    M = -INFINITY;
+    L = 0.f;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int k0 = 0; k0 < parts; k0 += 32) {
-      const int k = k0 + lane;
-      bool on = k < parts;
-      if (on && k > 0 && s.units < p.ctas) on = c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas);
-      float m = -INFINITY, l = 0.f;
-      if (on) {
-        const float2 ml = *reinterpret_cast<const float2*>(k == 0 ? own : more + (c0 + k) * step);
-        m = ml.x;
-        l = ml.y;
-      }
-      on = on && l != 0.f;  // saw nothing (a NaN goes on)
-      float top = on ? m : -INFINITY;
-#pragma unroll
-      for (int i = 16; i; i >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, i));
-      const float nm = fmaxf(M, top), use = nm == -INFINITY ? 0.f : nm;
-      const float fa = M == -INFINITY ? 0.f : ex2(M - use);
-      const float f = on ? ex2(m - use) : 0.f;
-      float ls = on ? l * f : 0.f;
-#pragma unroll
-      for (int i = 16; i; i >>= 1) ls += __shfl_xor_sync(kFull, ls, i);
-      L = L * fa + ls;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] *= fa;
-      uint32_t todo = __ballot_sync(kFull, on);
-      while (todo) {  // eight records at a time, all their loads in flight
-        float a[8][E], fk[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          fk[q] = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) a[q][e] = 0.f;
-          if (todo) {
-            const int kk = __ffs(todo) - 1;
-            todo &= todo - 1;
-            fk[q] = __shfl_sync(kFull, f, kk);
-            const float* from = (k0 + kk == 0 ? own : more + (c0 + k0 + kk) * step) + 4 + E * lane;
-#pragma unroll
-            for (int e = 0; e < E; ++e) a[q][e] = from[e];
-          }
-        }
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(a[q][e], fk[q], o[e]);
-      }
-      M = nm;
-    }
-    const int rho = t.row0 + r, i = rho / p.G;
-    T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
+  };
+  auto put = [&](int r) {
+    const int rho = s.row0 + r, i = rho / p.G;
+    T* to = static_cast<T*>(p.out) + ((int64_t)(s.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
     for (int e = 0; e < E; ++e) c8_store1(to + e, o[e] * inv);
+  };
+  if (!FEW || parts <= AT) {
+#pragma unroll 1
+    for (int r = W * blockIdx.y + warp; r < s.nrow; r += W * gridDim.y) {
+      begin();
+      join_row<D, AT>(p, s, parts, r, 0, 1, M, L, o);
+      put(r);
+    }
+    return;
+  }
+  if constexpr (FEW) {
+    __shared__ float s_m[W], s_l[W], s_o[W][D];
+#pragma unroll 1
+    for (int r0 = 2 * blockIdx.y; r0 < s.nrow; r0 += 2 * gridDim.y) {
+      const int r = r0 + (warp >> 2);
+      begin();
+      if (r < s.nrow) join_row<D, AT>(p, s, parts, r, warp & 3, 4, M, L, o);
+      __syncthreads();  // the rows before have been read
+      if (lane == 0) {
+        s_m[warp] = L == 0.f ? -INFINITY : M;
+        s_l[warp] = L;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = o[e];
+      __syncthreads();
+      if ((warp & 3) == 0 && r < s.nrow) {
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[warp + w]);
+        begin();
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float f = s_m[warp + w] == -INFINITY ? 0.f : ex2(s_m[warp + w] - top);
+          if (f == 0.f) continue;
+          L = fmaf(s_l[warp + w], f, L);
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[warp + w][E * lane + e], f, o[e]);
+        }
+        put(r);
+      }
+    }
   }
 }
 
@@ -542,7 +595,9 @@ cudaError_t run_attend_d(const C8Params& p, const CUtensorMap& k, const CUtensor
                   : p.tile == 16 ? run_attend<T, D, 2>(p, k, v, st)
                   : p.tile == 32 ? run_attend<T, D, 4>(p, k, v, st)
                                  : c8_attend_umma(p, st);
-  if (e == cudaSuccess) e = c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, p.tile < 64 ? p.tile / 8 : 8), 256, 0, st, p);
+  if (e != cudaSuccess) return e;
+  if (p.tile <= 32) return c8_launch(c8_join_kernel<T, D, true>, dim3(p.ctas, p.tile / 4), kJoinThreads, 0, st, p);
+  e = c8_launch(c8_join_kernel<T, D, false>, dim3(p.ctas, 16), kJoinThreads, 0, st, p);
   return e;
 }
 template <typename T>

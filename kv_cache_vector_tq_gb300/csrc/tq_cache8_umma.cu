@@ -538,8 +538,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       }
       tc_fence_before();
       if (seg.first == 0 && !whole) {
-        split.b = t.b;
-        split.rt = t.rt;
+        split.row0 = t.row0;
+        split.nrow = t.nrow;
+        split.start = t.start;
         split.h = seg.h;
         split.u0 = seg.u0;
         split.u1 = seg.u0 + t.n + p.pad;
