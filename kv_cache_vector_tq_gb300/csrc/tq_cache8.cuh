@@ -107,9 +107,9 @@ struct C8Tile {
   int lo, hi;             // tokens seen by some row: [lo, hi), and [0, sinks) with a window
   int su, lou, n;         // units of the first tokens, first unit of lo (0 where both are one run), units
 };
-__device__ __forceinline__ C8Tile c8_tile(const C8Params& p, int b, int rt) {
+__device__ __forceinline__ C8Tile c8_tile(const C8Params& p, const int32_t* row_start, const int32_t* len, int b, int rt) {
   C8Tile t;
-  const C8Seq s = c8_seq(p.row_start, p.len, b, p.rows);
+  const C8Seq s = c8_seq(row_start, len, b, p.rows);
   t.b = b;
   t.rt = rt;
   t.start = s.start;
@@ -145,11 +145,11 @@ __device__ __forceinline__ int c8_unit(const C8Tile& t, int u) {
   return (u < t.su ? u : t.lou + (u - t.su)) * kC8Unit;
 }
 // The tile of slot x, the units of which stand in t.n (0: none).
-__device__ __forceinline__ int c8_slot_b(const C8Params& p, int x) {
+__device__ __forceinline__ int c8_slot_b(const C8Params& p, const int32_t* row_start, int x) {
   int lo = 0, n = p.B;  // as c8_find, by one thread
   while (n > 1) {
     const int half = n >> 1;
-    if (c8_key(p.row_start, lo + half, p.rows, p.G, p.tile, 1) <= x) {
+    if (c8_key(row_start, lo + half, p.rows, p.G, p.tile, 1) <= x) {
       lo += half;
       n -= half;
     } else {
@@ -161,16 +161,29 @@ __device__ __forceinline__ int c8_slot_b(const C8Params& p, int x) {
 __device__ __forceinline__ int64_t c8_cut(int64_t c, int64_t units, int64_t n) { return c * units / n; }
 
 // What a CTA begins with: its units, and the slot (and units before the slot) of
-// the first.  Called by all threads of a CTA of NT threads.
+// the first.  Called by all threads of a CTA of NT threads; `copy`: shared memory for
+// `room` numbers, where offsets and lengths are brought at once if they fit (looked up
+// one after the other in memory they took 3 us).
 struct C8Share {
   int64_t u0, u1, units, before;
-  int slot;
+  int slot, b;  // the first unit's slot and request
 };
 template <int NT>
-__device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[NT / 32 + 1], int64_t* found) {
+__device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[NT / 32 + 1], int64_t* found, int32_t* copy, int room) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   C8Share s;
+  const int32_t *row_start = p.row_start, *len = p.len;
+  if (2 * p.B + 1 <= room) {
+    for (int i = tid; i <= p.B; i += NT) {
+      copy[i] = p.row_start[i];
+      if (i < p.B) copy[p.B + 1 + i] = p.len[i];
+    }
+    row_start = copy;
+    len = copy + p.B + 1;
+    __syncthreads();
+  }
   int64_t total = 0, mine = 0, before = 0;
+  int mine_b = 0;
   // all slots are summed; where they are more threads than one pass has, they are
   // counted again for the place of the first unit
   for (int again = 0; again < 2; ++again) {
@@ -180,8 +193,8 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
       if (again == 0 || p.slots > NT) {
         mine = 0;
         if (x < p.slots) {
-          const int b = c8_slot_b(p, x);
-          const int n = c8_tile(p, b, x - c8_key(p.row_start, b, p.rows, p.G, p.tile, 1)).n;
+          const int b = mine_b = c8_slot_b(p, row_start, x);
+          const int n = c8_tile(p, row_start, len, b, x - c8_key(row_start, b, p.rows, p.G, p.tile, 1)).n;
           if (n > 0) mine = (int64_t)(n + p.pad) * p.Hkv;
         }
         int64_t in = mine;
@@ -204,7 +217,7 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
       }
       if (again == 1) {
         if (x < p.slots && mine > 0 && before <= s.u0 && s.u0 < before + mine) {
-          found[0] = x;
+          found[0] = x | ((int64_t)mine_b << 32);
           found[1] = before;
         }
       }
@@ -216,8 +229,10 @@ __device__ __forceinline__ C8Share c8_share(const C8Params& p, int64_t (*sums)[N
       s.u1 = c8_cut(blockIdx.x + 1, total, p.ctas);
     }
   }
+  fence_proxy_async();  // (copies may take the place of offsets and lengths next)
   __syncthreads();
-  s.slot = (int)found[0];
+  s.slot = (int)(found[0] & 0xFFFFFFFFll);
+  s.b = (int)(found[0] >> 32);
   s.before = found[1];
   return s;
 }
@@ -233,11 +248,11 @@ struct C8Walk {
   int slot, b;
 };
 __device__ __forceinline__ C8Walk c8_walk(const C8Params& p, const C8Share& s) {
-  return C8Walk{s.u0, s.u1, s.before, s.slot, s.u0 < s.u1 ? c8_slot_b(p, s.slot) : 0};
+  return C8Walk{s.u0, s.u1, s.before, s.slot, s.u0 < s.u1 ? s.b : 0};
 }
 __device__ __forceinline__ bool c8_next(const C8Params& p, C8Walk& w, C8Seg& g) {
   while (w.u < w.u1 && w.slot < p.slots) {
-    g.t = c8_tile(p, w.b, w.slot - c8_key(p.row_start, w.b, p.rows, p.G, p.tile, 1));
+    g.t = c8_tile(p, p.row_start, p.len, w.b, w.slot - c8_key(p.row_start, w.b, p.rows, p.G, p.tile, 1));
     const int64_t all = g.t.n > 0 ? (int64_t)(g.t.n + p.pad) * p.Hkv : 0;
     if (w.u < w.before + all) {
       // the first `pad` of a tile's counted units are no units

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
   fence_mbar_init();
   griddep_wait();
   griddep_launch();
-  const C8Share sh = c8_share<kAtThreads>(p, s_sums, s_found);  // (its barriers are the mbarriers' too)
+  const C8Share sh = c8_share<kAtThreads>(p, s_sums, s_found, reinterpret_cast<int32_t*>(smem), kAtWarps * ST * SLOT / 4);  // (its barriers are the mbarriers' too)
   C8Split split;
   split.h = -1;
   unsigned char* ring = smem + warp * (ST * SLOT);

@@ -33,7 +33,7 @@ namespace {
 constexpr int kUmThreads = 640, kUmMma = 16, kUmCopy = 18;
 constexpr int kUmRegSoft = 128, kUmRegConv = 64;  // the rest keep the launch's 96
 static_assert(8 * kUmRegSoft + 8 * kUmRegConv + 4 * 96 <= 20 * 96, "registers that the launch does not have would be waited for");
-constexpr int kMeta = 4;                     // units whose scales are kept
+constexpr int kMeta = 8;                     // units whose scales are kept (copies are four units ahead of the products at most, those of what is converted)
 constexpr uint32_t kUmLimit = 1u << 20;      // polls of a wait, a few microseconds each
 constexpr uint32_t kUmLand = 1u << 14;       // a millisecond or more for copies under way
 // Tensor memory columns: places of scores (and Q behind three of them), the two sums
@@ -51,8 +51,7 @@ struct Lay {
 
 struct Misc {
   float4 meta[kMeta][8];       // K scale, log2 and inverse of the V scale of 16 tokens
-  float2 raw_meta[kMeta][8];   // K and V scale as they are in memory
-  uint32_t raw_valid[kMeta], valid[kMeta];
+  uint32_t valid[kMeta];       // which of the unit's 16 tokens are there, a bit each
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
   uint64_t meta_full[kMeta];
@@ -187,7 +186,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
   }
   if (warp == kUmMma) tmem_alloc(&ms.tmem, 512);
   tc_fence_before();
-  const C8Share sh = c8_share<kUmThreads>(p, ms.sums, ms.found);  // (its barriers are these writes' too)
+  const C8Share sh = c8_share<kUmThreads>(p, ms.sums, ms.found, reinterpret_cast<int32_t*>(smem + Ly::kQ), Ly::kTile / 4);  // (its barriers are these writes' too)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(kFull, ms.tmem, 0);
@@ -246,6 +245,10 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
           uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+          if constexpr (TWO) {  // fp16 already
+            cf = p.zscale;
+            continue;
+          }
           float top = 0.f;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -569,32 +572,18 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
 #pragma unroll 1
       for (int k = 0; k < seg.n; ++k, ++q) {
         const uint32_t st = q & 1u, ph = (q >> 1) & 1u;
-        const bool both = warp != 12 && (lane & 1);  // (warp 12 has something to do between the two)
         if constexpr (WIDE)  // (these warps are ahead, and looks would take issue slots from the others: 540 -> 515 us)
-          ok = __all_sync(kFull, um_wait(&ms.raw_full[rs], rph, abort_flag, p.status) &&
-                                     (warp == 12 || um_wait(&empty[st], ph ^ 1u, abort_flag, p.status)));
+          ok = __all_sync(kFull, um_wait(&ms.raw_full[rs], rph, abort_flag, p.status) && um_wait(&empty[st], ph ^ 1u, abort_flag, p.status));
         else
-          ok = um_wait_lanes(both ? &empty[st] : &ms.raw_full[rs], both ? ph ^ 1u : rph, abort_flag, p.status);
+          ok = um_wait_lanes(lane & 1 ? &empty[st] : &ms.raw_full[rs], lane & 1 ? ph ^ 1u : rph, abort_flag, p.status);
         if (!ok) break;
         uint32_t valid = 0xFFu;
         bool part = false;
         int base = 0;
         if (is_v) {
-          valid = ms.raw_valid[q % kMeta];
+          valid = ms.valid[q % kMeta];
           base = c8_unit(seg.t, seg.first + k);
           part = !(valid == 0xFFu && base + 127 < seg.t.hi && (base >= seg.t.lo || base + 127 < firsts));
-        }
-        if (warp == 12) {  // the unit's scales, from what V's copy brought along (those of four units ago have been used: V of three ago has)
-          if (lane < 8) {
-            const float2 sc = ms.raw_meta[q % kMeta][lane];
-            const float vs = c8_vscale(sc.y);
-            ms.meta[q % kMeta][lane] = make_float4(sc.x, log2f(vs), 1.f / vs, 0.f);
-          }
-          if (lane == 0) ms.valid[q % kMeta] = valid;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.meta_full[q % kMeta]);
-          ok = __all_sync(kFull, um_wait(&empty[st], ph ^ 1u, abort_flag, p.status));
-          if (!ok) break;
         }
         const unsigned char* raw = smem + Ly::kRaw + rs * Ly::kRawTile + ct * 16;
         unsigned char* row = smem + (is_v ? Ly::kV : Ly::kK) + st * Ly::kTile + (cc >> 2) * 16384 + tk * 128;
@@ -755,14 +744,18 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         const int64_t at = (((int64_t)pg0 * p.Hkv + seg.h) * p.block + off0) * D;
         ok = __all_sync(kFull, um_wait(&ms.raw_empty[rs], rph, abort_flag, p.status));
         if (!ok) break;
-        if (is_v) {  // (what came with the bytes that were here has been read)
-          if (lane < 8) ms.raw_meta[q % kMeta][lane] = sc0;
-          if (lane == 0) ms.raw_valid[q % kMeta] = valid;
-          __syncwarp();
-        }
+        if (is_v && lane == 0) ms.valid[q % kMeta] = valid;
         if (lane == 0) mbar_arrive_expect_tx(&ms.raw_full[rs], (uint32_t)__popc(valid) * 16 * D);
         __syncwarp();
         if (leads) bulk_g2s(smem + Ly::kRaw + rs * Ly::kRawTile + lane * 16 * D, codes + at, run * 16 * D, &ms.raw_full[rs]);
+        if (is_v) {  // the unit's scales, for the softmax
+          if (lane < 8) {
+            const float vs = c8_vscale(sc0.y);
+            ms.meta[q % kMeta][lane] = make_float4(sc0.x, log2f(vs), 1.f / vs, 0.f);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.meta_full[q % kMeta]);
+        }
         ++sent;
         rs += 2;
         if (rs >= NR) {
