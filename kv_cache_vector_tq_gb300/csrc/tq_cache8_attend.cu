@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
     const int h = seg.h, first = seg.first, n = seg.n;  // units here
     const int firsts = p.window > 0 ? p.sinks : 0;
     // pages of 16 groups of tokens, a lane for 16 tokens, 16 groups ahead
-    int pgA = -1, offA = 0, pgB, offB;
+    int pgA, offA, pgB, offB;
     auto pages = [&](int i, int& pg, int& off) {
       pg = -1;
       off = 0;
@@ -128,18 +128,21 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       off = __shfl_sync(kFull, offA, from);
       if (lane < 4 && pg >= 0) sc = __ldg((lane < 2 ? p.kscale : p.vscale) + (int64_t)pg * p.Hkv + h);
     };
-    uint32_t live = 0;  // two bits a group asked for: which of its tokens are there, the last group's in bits 0 and 1
-    auto issue = [&](int i) {
-      const uint32_t there = __ballot_sync(kFull, pg >= 0) & 3u;
-      live = (live << 2) | there;
-      float* to = reinterpret_cast<float*>(&s_scale[warp][ps][lane & 1]);
-      if (lane < 2) {
+    auto put_scale = [&](int slot, int part) {
+      float* to = reinterpret_cast<float*>(&s_scale[warp][slot][part & 1]);
+      if (part < 2) {
         to[0] = sc;
-      } else if (lane < 4) {
+      } else {
         const float vs = c8_vscale(sc);
         to[1] = log2f(vs);
         to[2] = 1.f / vs;
       }
+    };
+    uint32_t live = 0;  // two bits a group asked for: which of its tokens are there, the last group's in bits 0 and 1
+    auto issue = [&](int i) {
+      const uint32_t there = __ballot_sync(kFull, pg >= 0) & 3u;
+      live = (live << 2) | there;
+      if (lane < 4) put_scale((int)ps, lane);
       if (lane == 0) mbar_arrive_expect_tx(&s_full[warp][ps], (uint32_t)__popc(there) * 32 * D);
       __syncwarp();
       if (lane < 4 && pg >= 0)
@@ -149,10 +152,34 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       ++under_way;
       if (i + 1 < n) look(i + 1);
     };
+    // the first groups all at once, lanes 4·i.. for group i; no copy waits for a scale
     if (!dead) {
-      look(0);
-#pragma unroll 1
-      for (int i = 0; i < ST && i < n; ++i) issue(i);
+      const int count = min(ST, n), i = lane >> 2;
+      pgA = pgB;
+      offA = offB;
+      pages(16 + (lane >> 1), pgB, offB);
+      const int from = 2 * i + (lane & 1);
+      pg = __shfl_sync(kFull, pgA, from);
+      off = __shfl_sync(kFull, offA, from);
+      if (i >= count) pg = -1;
+      const uint32_t there = __ballot_sync(kFull, pg >= 0);
+#pragma unroll
+      for (int k = 0; k < ST; ++k)
+        if (k < count) live = (live << 2) | ((there >> (4 * k)) & 3u);
+      const int at = (int)ps + i < ST ? (int)ps + i : (int)ps + i - ST;
+      if (i < count && (lane & 3) == 0)
+        mbar_arrive_expect_tx(&s_full[warp][at], (uint32_t)__popc((there >> (4 * i)) & 3u) * 32 * D);
+      __syncwarp();
+      const int part = lane & 3;
+      if (pg >= 0) {
+        tma_load_3d(ring + at * SLOT + (part >> 1) * (32 * D) + (part & 1) * (16 * D), part < 2 ? &kmap : &vmap, 0, off,
+                    pg * p.Hkv + h, &s_full[warp][at]);
+        sc = __ldg((part < 2 ? p.kscale : p.vscale) + (int64_t)pg * p.Hkv + h);
+      }
+      if (i < count) put_scale(at, part);
+      ps = (int)ps + count < ST ? ps + count : ps + count - ST;
+      under_way += count;
+      if (count < n) look(count);
     }
     // ---- the rows of q, as operands
 #pragma unroll 1
