@@ -72,3 +72,9 @@ def test_nothing_to_do_is_fine(L):
     assert call(L.tq_cache8_attention, ATTEND, dict(rows=0, q=None, out=None, ws=None), {}) == tq.TQ_OK
     assert L.tq_cache8_append(*APPEND.values()) == tq.TQ_ERR_INVALID_ARG  # no cache
     assert L.tq_cache8_attention(*ATTEND.values()) == tq.TQ_ERR_INVALID_ARG
+
+
+def test_sizes_past_what_the_kernels_count(L):
+    for change, cache in ((dict(B=65537), {}), ({}, dict(pages=2 ** 30)), (dict(width=2 ** 20, qs=2 ** 12 * 128, Hq=2 ** 12), dict(Hkv=2 ** 12, block=1024, pages=1))):
+        assert call(L.tq_cache8_attention, ATTEND, change, cache) == tq.TQ_ERR_UNSUPPORTED
+    assert call(L.tq_cache8_append, APPEND, dict(B=65537), {}) == tq.TQ_ERR_UNSUPPORTED

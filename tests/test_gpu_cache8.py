@@ -505,6 +505,134 @@ def test_captured_steps_serve_later_lengths():
         at = [v + (k % 3) for v in at]
 
 
+# lens, rows a request, Hq, Hkv, d, block: calls of both kernels, with tiles that several CTAs have parts of
+MIXED = [
+    ([20000], [300], 2, 1, 128, 64),
+    ([9000, 0, 400], [1, 700, 30], 8, 2, 64, 32),
+    ([37, 90], [130, 64], 24, 2, 128, 16),
+    ([6000, 100], [3, 1], 8, 2, 128, 16),
+]
+
+
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("lens,new,Hq,Hkv,d,block", MIXED)
+def test_many_runs_agree(lens, new, Hq, Hkv, d, block, ty):
+    """The same call again and again, alone and beside itself on another stream: the same bits."""
+    g = gen(13)
+    table, total = pages_for([a + b for a, b in zip(lens, new)], block, g)
+    cache = tq.Cache8(total, Hkv, block, d)
+    filled(cache, g)
+    start = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = (2 * torch.randn(start[-1], Hq, d, device="cuda", generator=g)).to(TYPES[ty])
+    n = tq.tq_cache8_attention_workspace_size(cache, len(lens), Hq, start[-1])
+    first, at, size = i32(start), i32(lens), n // 4 + 4
+    jobs = [(torch.cuda.Stream(), torch.empty(size, device="cuda"), [torch.empty_like(q) for _ in range(12)]) for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(12):
+        for s, ws, outs in jobs:
+            tq.tq_cache8_attention(q, first, at, table, cache, 0.1, outs[i], ws, stream=s)
+    torch.cuda.synchronize()
+    want = jobs[0][2][0]
+    assert all(torch.equal(want, o) for _, _, outs in jobs for o in outs)
+    ref, off = attend_ref(q, start, lens, table, cache, 0.1, 0, 0)
+    close(want, ref, off)
+
+
+@pytest.mark.parametrize("d,window,sinks", [(128, 0, 0), (64, 0, 0), (128, 200, 7)])
+def test_captured_prompts_serve_later_lengths(d, window, sinks):
+    """One captured call of up to 700 rows: prompts, pieces of them, single tokens and nothing at all."""
+    g = gen(14)
+    B, Hq, Hkv, block, width, rows = 3, 4, 2, 32, 80, 700
+    cache = tq.Cache8(B * width, Hkv, block, d)
+    filled(cache, g)
+    table = torch.randperm(B * width, generator=g, device="cuda").int().view(B, width)
+    q, out = (torch.zeros(rows, Hq, d, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    ws = torch.empty(tq.tq_cache8_attention_workspace_size(cache, B, Hq, rows) // 4 + 4, device="cuda")
+    start, lens = i32([0] * (B + 1)), i32([0] * B)
+
+    def step():
+        tq.tq_cache8_attention(q, start, lens, table, cache, 0.1, out, ws, window=window, sinks=sinks)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for new, at in (([700, 0, 0], [0, 5, 5]), ([1, 1, 1], [2000, 3, 0]), ([0, 0, 0], [1, 2, 3]), ([128, 300, 129], [1000, 0, 2300]), ([0, 699, 1], [9, 1800, 40])):
+        first = np.concatenate([[0], np.cumsum(new)]).tolist()
+        q.copy_(torch.randn(q.shape, device="cuda", generator=g))
+        start.copy_(i32(first))
+        lens.copy_(i32(at))
+        out.fill_(7.0)
+        graph.replay()
+        got = out.clone()
+        out.fill_(7.0)
+        step()
+        assert torch.equal(got, out) and (got[first[-1]:] == 7).all()
+        ref, off = attend_ref(q, first, at, table, cache, 0.1, window, sinks)
+        close(got[:first[-1]], ref[:first[-1]], off[:first[-1]], new)
+    assert cache.status.item() == 0
+
+
+@pytest.mark.parametrize("ty", ["bf16", "fp32"])
+@pytest.mark.parametrize("lens,new,Hq,Hkv,d,block,window,sinks", [
+    ([2000, 700], [1, 3], 8, 2, 128, 16, 100, 4), ([3000, 50], [150, 20], 4, 2, 128, 16, 300, 20), ([5000], [400], 4, 1, 64, 48, 129, 0)])
+def test_pages_behind_the_window_may_be_gone(lens, new, Hq, Hkv, d, block, window, sinks, ty):
+    g = gen(15)
+    table, total = pages_for([a + b for a, b in zip(lens, new)], block, g)
+    cache = tq.Cache8(total, Hkv, block, d)
+    filled(cache, g)
+    start = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = torch.randn(start[-1], Hq, d, device="cuda", generator=g).to(TYPES[ty])
+    want = attend(q, start, lens, table, cache, 0.1, window, sinks)
+    for b, n in enumerate(lens):  # first rows see tokens from n - window + 1 on, and the first ones
+        gone = table[b, (sinks + block - 1) // block:max((n - window + 1) // block, 0)]
+        for codes, scale in ((cache.k, cache.kscale), (cache.v, cache.vscale)):
+            codes.view(torch.uint8)[gone.long()] = 0x7F
+            scale[gone.long()] = math.nan
+        gone.fill_(-1)
+    assert torch.equal(want, attend(q, start, lens, table, cache, 0.1, window, sinks)) and cache.status.item() == 0
+
+
+def test_requests_that_share_their_first_blocks():
+    """A prefix held once: full blocks in several tables, twice in one of them, and appends behind it."""
+    g = gen(16)
+    B, Hq, Hkv, d, block = 4, 8, 2, 128, 16
+    cache = tq.Cache8(60, Hkv, block, d)
+    filled(cache, g)
+    order = torch.randperm(60, generator=g, device="cuda").int()
+    table = torch.stack([torch.cat([order[:10], order[10 + 12 * b:22 + 12 * b]]) for b in range(B)]).contiguous()
+    table[3, 4] = table[3, 3]
+    lens, new = [160, 160, 165, 170], [150, 1, 0, 9]
+    start = np.concatenate([[0], np.cumsum(new)]).tolist()
+    x = torch.randn(160, Hq + 2 * Hkv, d, device="cuda", generator=g).half()
+    q, pos, k0 = torch.empty(160, Hq, d, device="cuda", dtype=torch.half), torch.arange(160, device="cuda").int(), cache.k[order[:10].long()].view(torch.uint8).clone()
+    tq.tq_cache8_append(x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:], None, None, 0.0, None, 0, pos, i32(start), i32(lens), table, cache, q)
+    assert torch.equal(q, x[:, :Hq]) and torch.equal(k0, cache.k[order[:10].long()].view(torch.uint8))
+    out, ref = attend(q, start, lens, table, cache, 0.1), attend_ref(q, start, lens, table, cache, 0.1, 0, 0)
+    close(out, *ref)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,most", [(8, 2, 128, 1), (4, 1, 64, 40), (6, 3, 128, 130)])
+def test_hundreds_of_ragged_requests(Hq, Hkv, d, most):
+    g, r = gen(17), np.random.default_rng(17)
+    B = 400
+    new = r.integers(0, most + 1, B).tolist()
+    lens = (r.integers(0, 300, B) * r.integers(0, 2, B)).tolist()
+    table, total = pages_for([a + b for a, b in zip(lens, new)], 16, g)
+    cache = tq.Cache8(total, Hkv, 16, d)
+    filled(cache, g)
+    start = np.concatenate([[0], np.cumsum(new)]).tolist()
+    q = torch.randn(start[-1] + 5, Hq, d, device="cuda", generator=g).bfloat16()
+    out = attend(q, start, lens, table, cache, 0.1)
+    ref, off = attend_ref(q, start, lens, table, cache, 0.1, 0, 0)
+    close(out[:start[-1]], ref[:start[-1]], off[:start[-1]])
+    assert (out[start[-1]:] == 7).all() and cache.status.item() == 0
+
+
 def test_two_streams_with_workspaces_of_their_own():
     g = gen(11)
     jobs = []
