@@ -213,8 +213,10 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       const C8Tile& t = seg.t;
       const int row = WIDE ? 128 * w + r : r, rho = t.row0 + row, tok = rho / p.G;
       const bool here = row < t.nrow, any = row - lane < t.nrow;  // the row, some row of the warp
-      // tokens that the row sees: from .. upto, and the first ones
-      const int pos = here ? (int)min((int64_t)t.len + tok, (int64_t)INT32_MAX) : -1;
+      // tokens that the row sees: from .. upto, and the first ones (a row that is none sees
+      // what the last one does, so that its warp masks no more than others: a prompt's last
+      // tile took a seventh longer where it saw nothing)
+      const int pos = (int)min((int64_t)t.len + min(tok, t.il), (int64_t)INT32_MAX);
       const int upto = min(pos, t.hi - 1), from = p.window > 0 ? max(pos - p.window + 1, 0) : 0;
       // ---- the warp's 32 rows of q, as an operand: read along rows (a thread's own row
       // takes a look-up in L1 for every lane)
