@@ -94,7 +94,10 @@ struct C8Params {
   void* out;
   int32_t* status;
   C8Split* split;  // [ctas]
-  float* rec;      // [ctas][2][tile][d + 4]: m, l, 2 pad, sums; a tile that goes on from the CTA before, one that begins here
+  // [ctas][2]: a tile that goes on from the CTA before, one that begins here; in each
+  // [tile][d + 4]: m, l, 2 pad, sums, or from 128 rows on (a thread of the kernel has a
+  // row) [tile] of m, l, then [d / 4][tile] of four sums
+  float* rec;
   int ctas, tile, slots;
   int pad;         // what a tile's beginning and end cost, in units: the CTAs' shares count it
 };
@@ -273,14 +276,42 @@ __device__ __forceinline__ bool c8_next(const C8Params& p, C8Walk& w, C8Seg& g) 
   return false;
 }
 
+// N (2 or 4) numbers as T, to memory in one access.
 template <typename T>
-__device__ __forceinline__ void c8_store1(T* p, float x) {
-  if constexpr (sizeof(T) == 4)
-    *p = x;
-  else if constexpr (std::is_same<T, __half>::value)
-    *p = __float2half_rn(x);
-  else
-    *p = __float2bfloat16_rn(x);
+__device__ __forceinline__ uint32_t c8_pair(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    return pack_f16x2(a, b);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+template <typename T, int N>
+__device__ __forceinline__ void c8_store(T* p, const float (&x)[N]) {
+  if constexpr (sizeof(T) == 4) {
+    if constexpr (N == 4)
+      *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    else
+      *reinterpret_cast<float2*>(p) = make_float2(x[0], x[1]);
+  } else if constexpr (N == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(c8_pair<T>(x[0], x[1]), c8_pair<T>(x[2], x[3]));
+  } else {
+    *reinterpret_cast<uint32_t*>(p) = c8_pair<T>(x[0], x[1]);
+  }
+}
+template <int N>
+__device__ __forceinline__ void c8_load(const float* p, float (&x)[N]) {
+  if constexpr (N == 4) {
+    const float4 v = *reinterpret_cast<const float4*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+    x[2] = v.z;
+    x[3] = v.w;
+  } else {
+    const float2 v = *reinterpret_cast<const float2*>(p);
+    x[0] = v.x;
+    x[1] = v.y;
+  }
 }
 // Two codes as fp16: the low 16 bits of w, or the high ones.
 __device__ __forceinline__ uint32_t c8_wide(uint32_t w) {

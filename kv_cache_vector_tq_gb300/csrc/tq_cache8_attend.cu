@@ -447,12 +447,12 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         T* to = static_cast<T*>(p.out) + ((int64_t)(t.start + i) * p.Hq + h * p.G + rho - i * p.G) * D + E * lane;
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-        for (int e = 0; e < E; ++e) c8_store1(to + e, o[e] * inv);
+        for (int e = 0; e < E; ++e) o[e] *= inv;
+        c8_store<T, E>(to, o);
       } else {
         float* to = p.rec + (((int64_t)blockIdx.x * 2 + (first == 0)) * TILE + r) * REC;
         if (lane == 0) *reinterpret_cast<float2*>(to) = make_float2(top, l);
-#pragma unroll
-        for (int e = 0; e < E; ++e) to[4 + E * lane + e] = o[e];
+        c8_store<float, E>(to + 4 + E * lane, o);
       }
     }
     if (first == 0 && !whole) {
@@ -510,7 +510,8 @@ __device__ __forceinline__ void join_row(const C8Params& p, const C8Split& s, in
       const int kq = k0 + every * q;
       const float* at = (kq == 0 ? own : more + (c0 + kq) * step) + 4 + E * lane;
 #pragma unroll
-      for (int e = 0; e < E; ++e) a[q][e] = (asked >> q) & 1u ? at[e] : 0.f;
+      for (int e = 0; e < E; ++e) a[q][e] = 0.f;
+      if ((asked >> q) & 1u) c8_load<E>(at, a[q]);
     }
     on = on && l != 0.f;  // saw nothing (a NaN goes on)
     float top = on ? m : -INFINITY;
@@ -536,16 +537,15 @@ __device__ __forceinline__ void join_row(const C8Params& p, const C8Split& s, in
 }
 
 // The parts of the tiles that several CTAs worked on.  The CTAs of blockIdx.x join the
-// rows of the tile that CTA blockIdx.x there began and did not end: a warp a row.
-// Its CTAs are let in while the kernel before is under way, and wait beside its own.
-// FEW rows a tile: a long request's parts are some 40, and four warps join a row where
-// they are more than one has in flight (one token over 131072: 56 -> 53 us).  Many rows:
-// the parts are two or three, and a CTA with shared memory would find no room beside
-// the tensor-core kernel (which cost 5 to 20 us).
+// rows of the tile that CTA blockIdx.x there began and did not end.  They are let in
+// while the kernel before is under way, and wait beside its own.
+// Few rows a tile: a warp a row.  A long request's parts are some 40, and four warps
+// join a row where they are more than one has in flight (one token over 131072: 56 ->
+// 53 us).
 constexpr int kJoinThreads = 256;
-template <typename T, int D, bool FEW>
+template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads) c8_join_kernel(const C8Params p) {
-  constexpr int E = D / 32, W = kJoinThreads / 32, AT = FEW ? 12 : 4;  // coordinates of a lane, warps, records in flight
+  constexpr int E = D / 32, W = kJoinThreads / 32, AT = 12;  // coordinates of a lane, warps, records in flight
   griddep_wait();
   griddep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -564,9 +564,10 @@ __global__ void __launch_bounds__(kJoinThreads) c8_join_kernel(const C8Params p)
     T* to = static_cast<T*>(p.out) + ((int64_t)(s.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + E * lane;
     const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int e = 0; e < E; ++e) c8_store1(to + e, o[e] * inv);
+    for (int e = 0; e < E; ++e) o[e] *= inv;
+    c8_store<T, E>(to, o);
   };
-  if (!FEW || parts <= AT) {
+  if (parts <= AT) {
 #pragma unroll 1
     for (int r = W * blockIdx.y + warp; r < s.nrow; r += W * gridDim.y) {
       begin();
@@ -575,36 +576,108 @@ __global__ void __launch_bounds__(kJoinThreads) c8_join_kernel(const C8Params p)
     }
     return;
   }
-  if constexpr (FEW) {
-    __shared__ float s_m[W], s_l[W], s_o[W][D];
+  __shared__ float s_m[W], s_l[W], s_o[W][D];
 #pragma unroll 1
-    for (int r0 = 2 * blockIdx.y; r0 < s.nrow; r0 += 2 * gridDim.y) {
-      const int r = r0 + (warp >> 2);
+  for (int r0 = 2 * blockIdx.y; r0 < s.nrow; r0 += 2 * gridDim.y) {
+    const int r = r0 + (warp >> 2);
+    begin();
+    if (r < s.nrow) join_row<D, AT>(p, s, parts, r, warp & 3, 4, M, L, o);
+    __syncthreads();  // the rows before have been read
+    if (lane == 0) {
+      s_m[warp] = L == 0.f ? -INFINITY : M;
+      s_l[warp] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = o[e];
+    __syncthreads();
+    if ((warp & 3) == 0 && r < s.nrow) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[warp + w]);
       begin();
-      if (r < s.nrow) join_row<D, AT>(p, s, parts, r, warp & 3, 4, M, L, o);
-      __syncthreads();  // the rows before have been read
-      if (lane == 0) {
-        s_m[warp] = L == 0.f ? -INFINITY : M;
-        s_l[warp] = L;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = s_m[warp + w] == -INFINITY ? 0.f : ex2(s_m[warp + w] - top);
+        if (f == 0.f) continue;
+        L = fmaf(s_l[warp + w], f, L);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[warp + w][E * lane + e], f, o[e]);
       }
+      put(r);
+    }
+  }
+}
+
+// From 128 rows a tile on: the parts are two or three where the tiles are many.  A warp
+// takes 8 rows and 32 coordinates, a lane 8 coordinates of a row: the records' four
+// sums of 8 rows stand together (and those of 32 where the kernel before stores them;
+// with rows of d + 4 numbers instead, a store met 32 lines: prompt of 8179 with a window
+// 130 against 122 us).  No shared memory, so that CTAs find room beside that kernel's
+// (with some, 5 to 20 us more).
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads, 3) c8_join_wide_kernel(const C8Params p) {
+  constexpr int REC = D + 4, W = kJoinThreads / 32, AT = 4, CG = D / 32;  // records in flight, column groups
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c0 = blockIdx.x;
+  const C8Split s = p.split[c0];
+  if (s.h < 0) return;
+  const int parts = (int)((s.u1 * p.ctas - 1) / s.units) - c0 + 1;
+  const int64_t size = (int64_t)p.tile * REC;
+#pragma unroll 1
+  for (int u = W * blockIdx.y + warp; u < (s.nrow + 7) / 8 * CG; u += W * gridDim.y) {
+    const int r = 8 * (u / CG) + (lane >> 2), c8 = 4 * (u % CG) + (lane & 3);  // row, eight coordinates
+    const bool here = r < s.nrow;
+    float M = -INFINITY, L = 0.f, o[8];
 #pragma unroll
-      for (int e = 0; e < E; ++e) s_o[warp][E * lane + e] = o[e];
-      __syncthreads();
-      if ((warp & 3) == 0 && r < s.nrow) {
-        float top = -INFINITY;
+    for (int e = 0; e < 8; ++e) o[e] = 0.f;
+#pragma unroll 1
+    for (int k0 = 0; k0 < parts; k0 += AT) {
+      float m[AT], l[AT], a[AT][2][4];
 #pragma unroll
-        for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[warp + w]);
-        begin();
+      for (int q = 0; q < AT; ++q) {
+        const int k = k0 + q;
+        const bool on = here && k < parts &&
+                        (k == 0 || s.units >= p.ctas || c8_cut(c0 + k + 1, s.units, p.ctas) != c8_cut(c0 + k, s.units, p.ctas));
+        const float* rec = p.rec + ((int64_t)(c0 + k) * 2 + (k == 0)) * size;
+        m[q] = -INFINITY;
+        l[q] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float f = s_m[warp + w] == -INFINITY ? 0.f : ex2(s_m[warp + w] - top);
-          if (f == 0.f) continue;
-          L = fmaf(s_l[warp + w], f, L);
+        for (int e = 0; e < 8; ++e) a[q][e >> 2][e & 3] = 0.f;
+        if (on) {
+          const float2 ml = *reinterpret_cast<const float2*>(rec + 2 * r);
+          m[q] = ml.x;
+          l[q] = ml.y;
 #pragma unroll
-          for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[warp + w][E * lane + e], f, o[e]);
+          for (int e = 0; e < 2; ++e) c8_load<4>(rec + 4 * ((int64_t)p.tile * (1 + 2 * c8 + e) + r), a[q][e]);
         }
-        put(r);
       }
+      float top = M;
+#pragma unroll
+      for (int q = 0; q < AT; ++q)
+        if (l[q] != 0.f) top = fmaxf(top, m[q]);  // (0: saw nothing; a NaN goes on)
+      const float use = top == -INFINITY ? 0.f : top, fa = M == -INFINITY ? 0.f : ex2(M - use);
+      M = top;
+      L *= fa;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] *= fa;
+#pragma unroll
+      for (int q = 0; q < AT; ++q) {
+        const float f = l[q] != 0.f ? ex2(m[q] - use) : 0.f;
+        if (f == 0.f) continue;
+        L = fmaf(l[q], f, L);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] = fmaf(a[q][e >> 2][e & 3], f, o[e]);
+      }
+    }
+    if (here) {
+      const int rho = s.row0 + r, i = rho / p.G;
+      const float inv = L == 0.f ? 0.f : 1.f / L;
+      uint32_t h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) h[e] = c8_pair<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
+      *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + ((int64_t)(s.start + i) * p.Hq + s.h * p.G + rho - i * p.G) * D + 8 * c8) =
+          make_uint4(h[0], h[1], h[2], h[3]);
     }
   }
 }
@@ -623,8 +696,8 @@ cudaError_t run_attend_d(const C8Params& p, const CUtensorMap& k, const CUtensor
                   : p.tile == 32 ? run_attend<T, D, 4>(p, k, v, st)
                                  : c8_attend_umma(p, st);
   if (e != cudaSuccess) return e;
-  if (p.tile <= 32) return c8_launch(c8_join_kernel<T, D, true>, dim3(p.ctas, p.tile / 4), kJoinThreads, 0, st, p);
-  e = c8_launch(c8_join_kernel<T, D, false>, dim3(p.ctas, 16), kJoinThreads, 0, st, p);
+  if (p.tile <= 32) return c8_launch(c8_join_kernel<T, D>, dim3(p.ctas, p.tile / 4), kJoinThreads, 0, st, p);
+  if constexpr (sizeof(T) == 2) e = c8_launch(c8_join_wide_kernel<T, D>, dim3(p.ctas, 16), kJoinThreads, 0, st, p);
   return e;
 }
 template <typename T>

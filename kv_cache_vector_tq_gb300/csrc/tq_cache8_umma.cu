@@ -419,18 +419,12 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       if (M == -INFINITY && L != L) M = 0.f;  // all scores are no numbers: the NaN goes on
       const bool whole = seg.first == 0 && seg.n == t.n;
       const int64_t orow = ((int64_t)(t.start + tok) * p.Hq + seg.h * p.G + rho - tok * p.G) * D;
-      float* rec = p.rec + (((int64_t)blockIdx.x * 2 + (seg.first == 0)) * p.tile + row) * REC;
+      constexpr int TILE = WIDE ? 256 : 128;
+      float* rec = p.rec + ((int64_t)blockIdx.x * 2 + (seg.first == 0)) * (TILE * REC);
       auto half8 = [&](const float* o, float inv) -> uint4 {  // eight sums as outputs
         uint32_t h[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (TWO) {
-            h[e] = pack_f16x2(o[2 * e] * inv, o[2 * e + 1] * inv);
-          } else {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * e] * inv, o[2 * e + 1] * inv);
-            h[e] = *reinterpret_cast<const uint32_t*>(&b);
-          }
-        }
+        for (int e = 0; e < 4; ++e) h[e] = c8_pair<T>(o[2 * e] * inv, o[2 * e + 1] * inv);
         return make_uint4(h[0], h[1], h[2], h[3]);
       };
       auto put = [&](int col, const float (&o)[16], float inv) {  // 16 of the row's sums
@@ -441,14 +435,14 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           reinterpret_cast<uint4*>(to)[0] = a;
           reinterpret_cast<uint4*>(to)[1] = b;
         } else if (here) {
-          float4* to = reinterpret_cast<float4*>(rec + 4 + col);
+          float4* to = reinterpret_cast<float4*>(rec) + TILE * (1 + (col >> 2)) + row;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) to[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          for (int e = 0; e < 4; ++e) to[TILE * e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
         }
       };
       if constexpr (WIDE) {
         if (any) {
-          if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(M, L);
+          if (here && !whole) *reinterpret_cast<float2*>(rec + 2 * row) = make_float2(M, L);
           const float inv = L == 0.f ? 0.f : 1.f / L;
           // 64 coordinates at a time; whole rows are turned where the warp's own q was, so
           // that stores go along rows
@@ -505,7 +499,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
           L = (f0 == 0.f ? 0.f : L * f0) + (f1 == 0.f ? 0.f : ms.l[r] * f1);
           inv = L == 0.f ? 0.f : 1.f / L;
-          if (here && !whole) *reinterpret_cast<float2*>(rec) = make_float2(top, L);
+          if (here && !whole) *reinterpret_cast<float2*>(rec + 2 * row) = make_float2(top, L);
         }
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
