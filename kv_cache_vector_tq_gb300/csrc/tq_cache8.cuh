@@ -96,7 +96,8 @@ struct C8Params {
   C8Split* split;  // [ctas]
   // [ctas][2]: a tile that goes on from the CTA before, one that begins here; in each
   // [tile][d + 4]: m, l, 2 pad, sums, or from 128 rows on (a thread of the kernel has a
-  // row) [tile] of m, l, then [d / 4][tile] of four sums
+  // row) [tile] of m, l, then [d / 4][tile] of four sums; with 128 rows [ctas] more behind
+  // them (long sums of the second softmax group)
   float* rec;
   int ctas, tile, slots;
   int pad;         // what a tile's beginning and end cost, in units: the CTAs' shares count it

@@ -391,9 +391,21 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               const uint32_t hi = __byte_perm(wv[2][k], wv[3][k], o ? 0x7362 : 0x5140);
               const uint32_t a0 = c8_wide(lo), a1 = c8_wide_hi(lo), a2 = c8_wide(hi), a3 = c8_wide_hi(hi);
 #pragma unroll
-              for (int x = 0; x < NT; ++x)
+              for (int x = 0; x < NT; ++x) {
+                if constexpr (QT == 2) {
+                  // fp32: 16 tokens by themselves, since the matrix units cut what a long sum
+                  // has no bits for (64 requests over 65536: 2e-5 to 6e-5 off, 6e-7 this way, for
+                  // 140 -> 145 us of 32 single tokens over up to 16384)
+                  float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int q = 0; q < PT; ++q) mma16816(O[x][2 * k + o], a0, a1, a2, a3, bp[hf][x][q][0], bp[hf][x][q][1]);
+                  for (int q = 0; q < PT; ++q) mma16816(part, a0, a1, a2, a3, bp[hf][x][q][0], bp[hf][x][q][1]);
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) O[x][2 * k + o][e] += part[e];
+                } else {
+#pragma unroll
+                  for (int q = 0; q < PT; ++q) mma16816(O[x][2 * k + o], a0, a1, a2, a3, bp[hf][x][q][0], bp[hf][x][q][1]);
+                }
+              }
             }
           }
         }
@@ -725,7 +737,7 @@ int grid_ctas(int tile) { return num_sms() * (tile <= 32 ? 2 : 1); }
 size_t cache8_ws_bytes(int d, int B, int Hq, int Hkv, int64_t rows) {
   const int tile = tile_rows(rows, B, Hq / Hkv, true);  // (no fewer than the other kernel's)
   const size_t ctas = (size_t)num_sms() * 2, parts = (size_t)grid_ctas(tile) * 2;
-  return al256(ctas * sizeof(C8Split)) + parts * tile * (d + 4) * 4;
+  return al256(ctas * sizeof(C8Split)) + (parts + (tile == 128 ? parts / 2 : 0)) * tile * (d + 4) * 4;
 }
 
 tq_status launch_cache8_attention(const Cache8AttendArgs& a, cudaStream_t stream) {

@@ -25,12 +25,12 @@
 // and 17 issue the products, 18 and 19 the copies (lane = 16 tokens, so pages may
 // end anywhere on a multiple of 16).
 //
-// Measured (bf16, d = 128, 32/8 heads): a prompt's piece of 2039 tokens behind 16384 443 us,
-// 1311 TFLOP/s of the 1882 that a plain matrix product gets; tensor pipe 58 % active,
+// Measured (bf16, d = 128, 32/8 heads): a prompt's piece of 2039 tokens behind 16384 446 us,
+// 1302 TFLOP/s of the 1882 that a plain matrix product gets; tensor pipe 58 % active,
 // issue slots 65 %.  A unit of 256 rows takes 3500 clocks, its products 2560 (1536 the
 // scores, whose operands are both in shared memory, 64 columns at a time; 128 at a time
 // would take 1024 and slow the codes' way to fp16 by half).  Prompt of 8179 with a window
-// of 1024, 16/4 heads: 122 us (529 TFLOP/s; nine units a tile, its ends cost four more).
+// of 1024, 16/4 heads: 119 us (542 TFLOP/s; nine units a tile, its ends cost four more).
 #include "tq_cache8.cuh"
 
 namespace tq {
@@ -44,6 +44,12 @@ constexpr int kMeta = 8;                     // units whose scales are kept (cop
 constexpr uint32_t kUmLimit = 1u << 20;      // polls of a wait, a few microseconds each
 constexpr uint32_t kUmLand = 1u << 14;       // a millisecond or more for copies under way
 // Tensor memory columns: places of scores (and Q behind three of them), the two sums
+// Tensor memory's sums are cut, not rounded, where they are longer than the products added
+// to them: after so many products of 64 tokens they go to fp32 sums in the CTA's record, and
+// begin anew (fp16 over 65536 tokens, 2048 rows: 1e-4 to 3e-4 short without, half of its
+// rounding or more; bf16 has a quarter of the products for its rounding).
+template <bool TWO>
+constexpr int kChain = TWO ? 256 : 1024;
 constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
 
 template <int D, bool WIDE>
@@ -306,113 +312,160 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.q_full);
       }
+      constexpr int TILE = WIDE ? 256 : 128;
+      auto record = [&]() -> float* { return p.rec + ((int64_t)blockIdx.x * 2 + (seg.first == 0)) * (TILE * REC); };
+      // a long sum of the row so far stands there too (of the second group with the same
+      // rows behind the records), its maximum behind the records' own; with what tensor
+      // memory holds it goes there (`away`) or to tensor memory
+      auto long_sum = [&](bool first, bool away, float m) {
+        float* base = WIDE || w == 0 ? record() : p.rec + ((int64_t)p.ctas * 2 + blockIdx.x) * (TILE * REC);
+        float* top = base + 2 * TILE + row;
+        const float hm = here && !first ? *top : -INFINITY, scale = hm == -INFINITY ? 0.f : ex2(hm - m);
+        if (here && away) *top = m;
+#pragma unroll 1
+        for (int c = 0; c < D / 16; ++c) {
+          float4* at = reinterpret_cast<float4*>(base) + TILE * (1 + 4 * c) + row;
+          uint32_t o[16];
+          tmem_ld16_nw(tO + 16 * c, o);
+          wait_ld(o);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float f[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(o[4 * e + i]);
+            if (scale != 0.f) {
+              const float4 v = at[TILE * e];
+              f[0] = fmaf(v.x, scale, f[0]);
+              f[1] = fmaf(v.y, scale, f[1]);
+              f[2] = fmaf(v.z, scale, f[2]);
+              f[3] = fmaf(v.w, scale, f[3]);
+            }
+            if (here && away) at[TILE * e] = make_float4(f[0], f[1], f[2], f[3]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[4 * e + i] = away ? 0u : __float_as_uint(f[i]);
+          }
+          tmem_st16(tO + 16 * c, o);
+        }
+        tmem_wait_st();
+      };
+      const int halves = (WIDE ? 2 : 1) * seg.n;  // of units, this group's
       float M = -INFINITY, L = 0.f;
 #pragma unroll 1
-      for (int k = 0; k < (WIDE ? 2 : 1) * seg.n; ++k, ++done) {
-        const int unit = WIDE ? k >> 1 : k, part = WIDE ? k & 1 : w;  // of the segment; which 64 tokens
-        const uint32_t q = gu + unit, tS = tl + 64 * buf;
-        // (lanes wait for one or the other: with the converting warps' reads and writes
-        // before it, a poll takes 200 clocks even where it finds its phase complete)
-        ok = um_wait_lanes(lane & 1 ? &ms.meta_full[q % kMeta] : &ms.s_full[buf], lane & 1 ? (q / kMeta) & 1u : bph, abort_flag,
-                           p.status);
-        if (!ok) break;
-        tc_fence_after();
-        if (any) {
-          uint32_t s[2][32];
-          tmem_ld32_nw(tS, s[0]);
-          tmem_ld32_nw(tS + 32, s[1]);
-          const float4* meta = ms.meta[q % kMeta] + 4 * part;
-          const uint32_t valid = (ms.valid[q % kMeta] >> (4 * part)) & 15u;
-          const int base = c8_unit(t, seg.first + unit) + 64 * part;
-          const bool all = valid == 15u && base + 63 <= upto && (base >= from || base + 63 < firsts);
-          const bool masked = !__all_sync(kFull, all);
-          wait_ld(s[0]);
-          wait_ld(s[1]);
-          if (masked) {  // the scores to their end here
-            // columns that the row sees: [lo, hi) and [0, first)
-            const int hi = min(upto + 1 - base, 64), lo = min(max(from - base, 0), 64);
-            const int first = min(firsts - base, hi);
+      for (int k = 0, rest = kChain<TWO>; ok && k < halves; rest += kChain<TWO>) {
+        if (k > 0) {  // a rest: the last product is done (the one before it is when the next scores are there)
+          ok = __all_sync(kFull, um_wait(&ms.s_full[buf], bph, abort_flag, p.status) &&
+                                     um_wait(&ms.pv_done[w], (done - 1) & 1u, abort_flag, p.status));
+          if (!ok) break;
+          tc_fence_after();
+          if (any) long_sum(k == kChain<TWO>, true, M);
+        }
+#pragma unroll 1
+        for (; k < min(halves, rest); ++k, ++done) {
+          const int unit = WIDE ? k >> 1 : k, part = WIDE ? k & 1 : w;  // of the segment; which 64 tokens
+          const uint32_t q = gu + unit, tS = tl + 64 * buf;
+          // (lanes wait for one or the other: with the converting warps' reads and writes
+          // before it, a poll takes 200 clocks even where it finds its phase complete)
+          ok = um_wait_lanes(lane & 1 ? &ms.meta_full[q % kMeta] : &ms.s_full[buf], lane & 1 ? (q / kMeta) & 1u : bph, abort_flag,
+                             p.status);
+          if (!ok) break;
+          tc_fence_after();
+          if (any) {
+            uint32_t s[2][32];
+            tmem_ld32_nw(tS, s[0]);
+            tmem_ld32_nw(tS + 32, s[1]);
+            const float4* meta = ms.meta[q % kMeta] + 4 * part;
+            const uint32_t valid = (ms.valid[q % kMeta] >> (4 * part)) & 15u;
+            const int base = c8_unit(t, seg.first + unit) + 64 * part;
+            const bool all = valid == 15u && base + 63 <= upto && (base >= from || base + 63 < firsts);
+            const bool masked = !__all_sync(kFull, all);
+            wait_ld(s[0]);
+            wait_ld(s[1]);
+            if (masked) {  // the scores to their end here
+              // columns that the row sees: [lo, hi) and [0, first)
+              const int hi = min(upto + 1 - base, 64), lo = min(max(from - base, 0), 64);
+              const int first = min(firsts - base, hi);
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                uint32_t on = bits_of(lo - 32 * c, hi - 32 * c) | bits_of(0, first - 32 * c);
+                if (!((valid >> (2 * c)) & 1u)) on &= 0xFFFF0000u;
+                if (!((valid >> (2 * c + 1)) & 1u)) on &= 0x0000FFFFu;
+                const float4 m[2] = {meta[2 * c], meta[2 * c + 1]};
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                  s[c][e] = __float_as_uint((on >> e) & 1u ? fmaf(__uint_as_float(s[c][e]), cf * m[e >> 4].x, m[e >> 4].y) : -INFINITY);
+              }
+            }
+            float a[4], b[4], iv[4], top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const uint32_t* x = &s[g >> 1][(g & 1) * 16];
+              auto v = [&](int e) { return __uint_as_float(x[e]); };
+              const float y0 = um_max3(um_max3(v(0), v(1), v(2)), v(3), v(4)), y1 = um_max3(um_max3(v(5), v(6), v(7)), v(8), v(9));
+              const float y2 = um_max3(um_max3(v(10), v(11), v(12)), v(13), v(14));
+              const float y = fmaxf(um_max3(y0, y1, y2), v(15));
+              const float4 m = meta[g];
+              a[g] = masked ? 1.f : cf * m.x;
+              b[g] = masked ? 0.f : m.y;
+              iv[g] = m.z;
+              top = fmaxf(top, fmaf(y, a[g], b[g]));
+            }
+            const bool up = top > M + kC8Raise;
+            if (__any_sync(kFull, up)) {
+              const float nm = up ? top - kC8Fresh : M;
+              const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
+              M = nm;
+              L *= f;
+              if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores' place was free)
+                ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (done - 1) & 1u, abort_flag, p.status));
+                if (!ok) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld16_nw(tO + 16 * c, o);
+                  wait_ld(o);
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(tO + 16 * c, o);
+                }
+              }
+            }
+            const float use = M == -INFINITY ? 0.f : M;
+            // the weights of 32 tokens: 16 columns of pairs, then those of the second terms
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-              uint32_t on = bits_of(lo - 32 * c, hi - 32 * c) | bits_of(0, first - 32 * c);
-              if (!((valid >> (2 * c)) & 1u)) on &= 0xFFFF0000u;
-              if (!((valid >> (2 * c + 1)) & 1u)) on &= 0x0000FFFFu;
-              const float4 m[2] = {meta[2 * c], meta[2 * c + 1]};
+              uint32_t ph[16], pl[16];
 #pragma unroll
-              for (int e = 0; e < 32; ++e)
-                s[c][e] = __float_as_uint((on >> e) & 1u ? fmaf(__uint_as_float(s[c][e]), cf * m[e >> 4].x, m[e >> 4].y) : -INFINITY);
-            }
-          }
-          float a[4], b[4], iv[4], top = -INFINITY;
+              for (int g = 0; g < 2; ++g) {
+                const float bg = b[2 * c + g] - use;
+                const uint64_t aa = um_pack(a[2 * c + g], a[2 * c + g]), bb = um_pack(bg, bg);
+                uint64_t sum = 0;  // of even and of odd tokens
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const uint32_t* x = &s[g >> 1][(g & 1) * 16];
-            auto v = [&](int e) { return __uint_as_float(x[e]); };
-            const float y0 = um_max3(um_max3(v(0), v(1), v(2)), v(3), v(4)), y1 = um_max3(um_max3(v(5), v(6), v(7)), v(8), v(9));
-            const float y2 = um_max3(um_max3(v(10), v(11), v(12)), v(13), v(14));
-            const float y = fmaxf(um_max3(y0, y1, y2), v(15));
-            const float4 m = meta[g];
-            a[g] = masked ? 1.f : cf * m.x;
-            b[g] = masked ? 0.f : m.y;
-            iv[g] = m.z;
-            top = fmaxf(top, fmaf(y, a[g], b[g]));
-          }
-          const bool up = top > M + kC8Raise;
-          if (__any_sync(kFull, up)) {
-            const float nm = up ? top - kC8Fresh : M;
-            const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
-            M = nm;
-            L *= f;
-            if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores' place was free)
-              ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (done - 1) & 1u, abort_flag, p.status));
-              if (!ok) break;
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 0; c < D / 16; ++c) {
-                uint32_t o[16];
-                tmem_ld16_nw(tO + 16 * c, o);
-                wait_ld(o);
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(tO + 16 * c, o);
+                for (int e = 0; e < 8; ++e) {
+                  const float2 z = um_two(um_fma2(um_pack(__uint_as_float(s[c][16 * g + 2 * e]), __uint_as_float(s[c][16 * g + 2 * e + 1])), aa, bb));
+                  const float w0 = ex2(z.x), w1 = ex2(z.y);
+                  sum = um_add2(sum, um_pack(w0, w1));
+                  if constexpr (TWO)
+                    split2(w0, w1, ph[8 * g + e], pl[8 * g + e]);
+                  else
+                    ph[8 * g + e] = pack_f16x2(w0, w1);
+                }
+                const float2 both = um_two(sum);
+                L = fmaf(both.x + both.y, iv[2 * c + g], L);
               }
+              tmem_st16(tS + 16 * c, ph);
+              if constexpr (TWO) tmem_st16(tS + 32 + 16 * c, pl);
             }
+            tmem_wait_st();
           }
-          const float use = M == -INFINITY ? 0.f : M;
-          // the weights of 32 tokens: 16 columns of pairs, then those of the second terms
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t ph[16], pl[16];
-#pragma unroll
-            for (int g = 0; g < 2; ++g) {
-              const float bg = b[2 * c + g] - use;
-              const uint64_t aa = um_pack(a[2 * c + g], a[2 * c + g]), bb = um_pack(bg, bg);
-              uint64_t sum = 0;  // of even and of odd tokens
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float2 z = um_two(um_fma2(um_pack(__uint_as_float(s[c][16 * g + 2 * e]), __uint_as_float(s[c][16 * g + 2 * e + 1])), aa, bb));
-                const float w0 = ex2(z.x), w1 = ex2(z.y);
-                sum = um_add2(sum, um_pack(w0, w1));
-                if constexpr (TWO)
-                  split2(w0, w1, ph[8 * g + e], pl[8 * g + e]);
-                else
-                  ph[8 * g + e] = pack_f16x2(w0, w1);
-              }
-              const float2 both = um_two(sum);
-              L = fmaf(both.x + both.y, iv[2 * c + g], L);
-            }
-            tmem_st16(tS + 16 * c, ph);
-            if constexpr (TWO) tmem_st16(tS + 32 + 16 * c, pl);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.p_full[buf]);
+          buf += 2;  // the next of this group's scores
+          if (buf >= kPlaces) {
+            buf -= kPlaces;
+            bph ^= 1u;
           }
-          tmem_wait_st();
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.p_full[buf]);
-        buf += 2;  // the next of this group's scores
-        if (buf >= kPlaces) {
-          buf -= kPlaces;
-          bph ^= 1u;
         }
       }
       if (!ok) break;
@@ -426,8 +479,8 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       if (M == -INFINITY && L != L) M = 0.f;  // all scores are no numbers: the NaN goes on
       const bool whole = seg.first == 0 && seg.n == t.n;
       const int64_t orow = ((int64_t)(t.start + tok) * p.Hq + seg.h * p.G + rho - tok * p.G) * D;
-      constexpr int TILE = WIDE ? 256 : 128;
-      float* rec = p.rec + ((int64_t)blockIdx.x * 2 + (seg.first == 0)) * (TILE * REC);
+      if (any && halves > kChain<TWO>) long_sum(false, false, M);
+      float* rec = record();
       auto half8 = [&](const float* o, float inv) -> uint4 {  // eight sums as outputs
         uint32_t h[4];
 #pragma unroll

@@ -465,6 +465,43 @@ def test_offsets_past_32_bits():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("B,new", [(152, 1), (76, 20), (38, 300)])
+def test_long_sums_are_not_cut(B, new, ty):
+    """Values of one sign over 70000 tokens, which every request shares, so that one CTA adds all of a tile up: how much
+    of the result is missing."""
+    n, Hq, Hkv, d, block, t = 70000, 4, 2, 128, 16, TYPES[ty]
+    g = gen(18)
+    width = (n + block - 1) // block
+    cache = tq.Cache8(width, Hkv, block, d)
+    filled(cache, g, 0)
+    cache.v.copy_(cache.v.float().abs().to(F8))
+    table = torch.randperm(width, generator=g, device="cuda").int()[None].repeat(B, 1)
+    q = (0.25 * torch.randn(new, Hq, d, device="cuda", generator=g)).to(t)
+    start, scale = [new * b for b in range(B + 1)], d ** -0.5
+    out = attend(q.repeat(B, 1, 1), start, [n - new] * B, table, cache, scale).view(B, new, Hq, d)
+    page, at = table[0].long()[torch.arange(n, device="cuda") // block], torch.arange(n, device="cuda") % block
+    sees = torch.arange(n, device="cuda")[None] <= n - new + torch.arange(new, device="cuda")[:, None]
+    dot, own, most = torch.zeros(B, device="cuda", dtype=torch.float64), 0, 0
+    for h in range(Hkv):
+        k, v = (c[page, h, at].double() * x[page, h].double()[:, None] for c, x in ((cache.k, cache.kscale), (cache.v, cache.vscale)))
+        for j in range(h * 2, h * 2 + 2):
+            z = q[:, j].double() @ k.T * scale
+            ref = z.masked_fill(~sees, -math.inf).softmax(-1) @ v
+            dot += ((out[:, :, j].double() - ref) * ref).sum((1, 2))
+            own += ref.square().sum()
+            most = max(most, (q[:, j].double().abs() @ k.abs().T).amax().item() * scale)
+    # an addition cuts 2^-23 of the sum at most, which on average is half of the last; additions: of 16 tokens each, all
+    # of a warp's (fp16 and bf16 rows that are few), those between two rests in fp32, or (fp32) none; scores: 16 additions
+    terms = 1 if t is torch.bfloat16 else 2
+    units = (n + 127) // 128
+    steps = 2 if t is torch.float32 else 2 * units * terms if new == 1 else 4 * terms * min(units * (2 if new > 64 else 1), 256 if t is torch.float16 else 1024)
+    # and the results' own rounding, half a step of either sign for each of as many results, four times its deviation
+    count = new * Hq * d
+    bound = steps / 2 * 2.0 ** -23 + 2.0 ** -19 * (1 + most) + 4 * torch.finfo(t).eps / 2 / math.sqrt(count)
+    assert ((dot / own).abs() <= bound).all(), (float((dot / own).abs().max()), bound)
+
+
 # ------------------------------------------------------------------ streams and graphs, and a server's steps
 def test_captured_steps_serve_later_lengths():
     g = gen(10)
