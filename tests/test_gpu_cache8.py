@@ -670,6 +670,35 @@ def test_hundreds_of_ragged_requests(Hq, Hkv, d, most):
     assert (out[start[-1]:] == 7).all() and cache.status.item() == 0
 
 
+@pytest.mark.parametrize("Hq", [2, 40])
+def test_tens_of_thousands_of_requests(Hq):
+    """More requests than a CTA keeps offsets of: a token each, appended and attended to."""
+    B, d, block, g = 40000, 64, 16, gen(19)
+    cache = tq.Cache8(B, 1, block, d)
+    filled(cache, g)
+    table = torch.randperm(B, generator=g, device="cuda").int()[:, None].contiguous()
+    lens = torch.randint(0, block, (B,), generator=g, device="cuda").int()
+    start, pos, page = torch.arange(B + 1, device="cuda").int(), torch.zeros(B, device="cuda").int(), table[:, 0].long()
+    x = torch.randn(B, Hq + 2, d, device="cuda", generator=g).half()
+    q, old = torch.empty(B, Hq, d, device="cuda", dtype=torch.half), cache.vscale.clone()
+    tq.tq_cache8_append(x[:, :Hq], x[:, Hq:Hq + 1], x[:, Hq + 1:], None, None, 0.0, None, 0, pos, start, lens, table, cache, q)
+    assert torch.equal(q, x[:, :Hq])
+    v = x[:, Hq + 1].double()
+    s = torch.maximum(least_scale(v.abs().amax(1)), torch.where(lens > 0, old[page, 0].double(), 0))
+    assert torch.equal(cache.vscale[page, 0].double(), s)
+    assert torch.equal(cache.v[page, 0, lens.long()].float(), (v / s[:, None]).float().to(F8).float())
+    ws = torch.empty(tq.tq_cache8_attention_workspace_size(cache, B, Hq, B) // 4 + 4, device="cuda")
+    out = torch.empty_like(q)
+    tq.tq_cache8_attention(q, start, lens, table, cache, 0.1, out, ws)
+    k, v = (c[page, 0].double() * f[page].double()[..., None] for c, f in ((cache.k, cache.kscale), (cache.v, cache.vscale)))
+    sees = (torch.arange(block, device="cuda")[None] <= lens[:, None])[:, None]
+    z = (torch.einsum("bhd,btd->bht", q.double(), k) * 0.1).masked_fill(~sees, -math.inf)
+    w = z.softmax(-1)
+    most = (torch.einsum("bhd,btd->bht", q.double().abs(), k.abs()) * 0.1).masked_fill(~sees, 0).amax(-1, keepdim=True)
+    close(out, w @ v, w @ v.abs() * (2.0 ** -22 + 2.0 ** -19 * (1 + most) + 2.0 ** -23) + block * 2.0 ** -30 * v.abs().amax())
+    assert cache.status.item() == 0
+
+
 def test_two_streams_with_workspaces_of_their_own():
     g = gen(11)
     jobs = []
