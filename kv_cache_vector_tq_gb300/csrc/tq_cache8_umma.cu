@@ -30,7 +30,7 @@
 // issue slots 65 %.  A unit of 256 rows takes 3500 clocks, its products 2560 (1536 the
 // scores, whose operands are both in shared memory, 64 columns at a time; 128 at a time
 // would take 1024 and slow the codes' way to fp16 by half).  Prompt of 8179 with a window
-// of 1024, 16/4 heads: 119 us (542 TFLOP/s; nine units a tile, its ends cost four more).
+// of 1024, 16/4 heads: 120 us (540 TFLOP/s; nine units a tile, its ends cost four more).
 #include "tq_cache8.cuh"
 
 namespace tq {
