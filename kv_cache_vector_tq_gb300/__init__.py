@@ -489,6 +489,8 @@ def tq_cache8_append(q, k, v, wq, wk, eps, freq, style, pos, row_start, lens, ta
     (rows, Hkv, d), ti, i32 = k.shape, k.dtype, torch.int32
     if (Hkv, d) != (cache.Hkv, cache.d):
         raise ValueError(f"k: rows of {cache.Hkv} heads of {cache.d} elements are wanted")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
     if v.dtype is not ti or (q is not None and (q.dtype is not ti or q_out.dtype is not ti)):
         raise ValueError("q, k, v and q_out are of one type")
     Hq, qp, qs, qo, qos = 0, None, 0, None, 0

@@ -781,3 +781,13 @@ def test_other_device_stream_and_shape_refused():
         append_plain(cache, torch.zeros(1, 2, 128, device="cuda"), [0, 1], [0], table)
     n = ctypes.c_size_t()
     assert tq.lib().tq_cache8_attention_workspace_size(ctypes.byref(cache.desc), 1, 3, 1, ctypes.byref(n)) == tq.TQ_ERR_INVALID_ARG
+
+
+def test_queries_and_their_output_go_together():
+    cache, x = tq.Cache8(2, 2, 16, 64), torch.zeros(1, 2, 64, device="cuda")
+    rest = (x, x, None, None, 0.0, None, 0, i32([0]), i32([0, 1]), i32([0]), i32([[0]]), cache)
+    for q, out in ((x, None), (None, x), (x, x.half()), (x, x[..., :32])):
+        with pytest.raises(ValueError):
+            tq.tq_cache8_append(q, *rest, out)
+    tq.tq_cache8_append(x, *rest, torch.empty_like(x))
+    assert cache.status.item() == 0
