@@ -121,8 +121,8 @@ def _pages(need, width, total, g):
 def _power(a):
     """The least power of two s with a <= 448 s."""
     m, e = torch.frexp(a)  # a = m 2^e, m in [1/2, 1); 448 = 0.875 * 2^9
-    e = torch.where(a > 0, e - 9 + (m > 0.875).int(), -60).clamp(-60, 40)
-    return ((e.int() + 127) << 23).view(torch.float32)  # 2^e, bit for bit
+    s = torch.ldexp(torch.ones_like(a), e - 9 + (m > 0.875).int())
+    return torch.where(a > 0, s, 2.0 ** -60).clamp(2.0 ** -60, 2.0 ** 40)
 
 
 def _fill(codes, scales, g):
