@@ -103,7 +103,9 @@ __device__ __forceinline__ bool um_look(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 // um_wait for a warp whose lanes wait for different barriers: looks only (a poll that
-// suspends would do so for the lanes that have theirs as well).
+// suspends would do so for the lanes that have theirs as well).  What one lane's barrier
+// has made visible to it is used by all: the warp's barrier at the end hands it on (a
+// vote orders no memory).
 __device__ __forceinline__ bool um_wait_lanes(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
   bool got = um_look(bar, parity);
 #pragma unroll 1
@@ -116,6 +118,7 @@ __device__ __forceinline__ bool um_wait_lanes(uint64_t* bar, uint32_t parity, vo
     got = got || um_look(bar, parity);
     if ((n & 255u) == 255u && __any_sync(kFull, *abort_flag != 0)) return false;
   }
+  __syncwarp();
   return true;
 }
 __device__ __forceinline__ float um_max3(float a, float b, float c) {
