@@ -332,6 +332,10 @@ __device__ __forceinline__ int c8_row_exp(float top) {
 __device__ __forceinline__ float c8_pow2(int e) { return __int_as_float((127 + e) << 23); }
 // A V scale as the exponents take it (a NaN stays one).
 __device__ __forceinline__ float c8_vscale(float s) { return s < kC8Lo ? kC8Lo : s > kC8Hi ? kC8Hi : s; }
+// Its inverse, which the sum of a block's weights meets: 0 for a NaN.  Rows that see the
+// block have the NaN in their weights (the scale stands in their exponents too); those
+// that do not have weights of 0, and 0 times a NaN would be one.
+__device__ __forceinline__ float c8_inverse(float s) { return s == s ? 1.f / s : 0.f; }
 constexpr float kC8Raise = 14.f, kC8Fresh = 6.f;  // raise M before a weight passes 2^14; a fresh maximum sits at 2^6
 
 template <typename... P, typename... A>

@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       const int from = 2 * (i & 15) + (lane & 1);
       pg = __shfl_sync(kFull, pgA, from);
       off = __shfl_sync(kFull, offA, from);
+      sc = 1.f;
       if (lane < 4 && pg >= 0) sc = __ldg((lane < 2 ? p.kscale : p.vscale) + (int64_t)pg * p.Hkv + h);
     };
     auto put_scale = [&](int slot, int part) {
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       } else {
         const float vs = c8_vscale(sc);
         to[1] = log2f(vs);
-        to[2] = 1.f / vs;
+        to[2] = c8_inverse(vs);
       }
     };
     uint32_t live = 0;  // two bits a group asked for: which of its tokens are there, the last group's in bits 0 and 1

@@ -810,7 +810,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
         if (is_v) {  // the unit's scales, for the softmax
           if (lane < 8) {
             const float vs = c8_vscale(sc0.y);
-            ms.meta[q % kMeta][lane] = make_float4(sc0.x, log2f(vs), 1.f / vs, 0.f);
+            ms.meta[q % kMeta][lane] = make_float4(sc0.x, log2f(vs), c8_inverse(vs), 0.f);
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&ms.meta_full[q % kMeta]);
