@@ -452,9 +452,9 @@ __global__ void __launch_bounds__(kAtThreads, 2)
       for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
       for (int w = 0; w < kAtWarps; ++w) {
-        const float f = m[w] == -INFINITY ? 0.f : ex2(m[w] - top);
-        if (f != 0.f) {
-          l = fmaf(from[w * (TILE * REC) + 1], f, l);
+        const float f = m[w] == -INFINITY ? 0.f : ex2(m[w] - top), lw = from[w * (TILE * REC) + 1];
+        if (f != 0.f || lw != lw) {  // (a NaN goes on, whatever outweighs it)
+          l = fmaf(lw, f, l);
 #pragma unroll
           for (int e = 0; e < E; ++e) o[e] = fmaf(from[w * (TILE * REC) + 4 + E * lane + e], f, o[e]);
         }
@@ -615,7 +615,7 @@ __global__ void __launch_bounds__(kJoinThreads) c8_join_kernel(const C8Params p)
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         const float f = s_m[warp + w] == -INFINITY ? 0.f : ex2(s_m[warp + w] - top);
-        if (f == 0.f) continue;
+        if (f == 0.f && s_l[warp + w] == s_l[warp + w]) continue;  // (a NaN goes on)
         L = fmaf(s_l[warp + w], f, L);
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(s_o[warp + w][E * lane + e], f, o[e]);
@@ -681,7 +681,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) c8_join_wide_kernel(const C8P
 #pragma unroll
       for (int q = 0; q < AT; ++q) {
         const float f = l[q] != 0.f ? ex2(m[q] - use) : 0.f;
-        if (f == 0.f) continue;
+        if (f == 0.f && l[q] == l[q]) continue;  // (a NaN goes on)
         L = fmaf(l[q], f, L);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] = fmaf(a[q][e >> 2][e & 3], f, o[e]);

@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
           const float m1 = ms.m[r], top = fmaxf(M, m1);
           f0 = M == -INFINITY ? 0.f : ex2(M - top);
           f1 = m1 == -INFINITY ? 0.f : ex2(m1 - top);
-          L = (f0 == 0.f ? 0.f : L * f0) + (f1 == 0.f ? 0.f : ms.l[r] * f1);
+          L = L * f0 + ms.l[r] * f1;  // (a NaN goes on with a factor of 0)
           inv = L == 0.f ? 0.f : 1.f / L;
           if (here && !whole) *reinterpret_cast<float2*>(rec + 2 * row) = make_float2(top, L);
         }

@@ -81,3 +81,39 @@ def test_an_infinity_in_a_late_draft(ty):
         tq.tq_cache8_append(None, x[14:], y, None, None, 0.0, None, 0, i32([14, 15, 16, 17]), i32([0, 4]), i32([14]), table, cache, None)
         outs.append(attend(q, [0, 4], [14], table, cache, 0.1))
     assert torch.equal(outs[0][:2], outs[1][:2]) and torch.isfinite(outs[0]).all() and outs[1][2:].isnan().all()
+
+
+# Hq, Hkv, d, rows, tokens before them, marked blocks: what a warp, a group or a CTA has is marked, and the first token,
+# which another one has, weighs 2^200 and more times as much as what is not
+JOINS = [
+    (1, 1, 128, 1, 127, [2, 3]),                  # a warp of four
+    (4, 2, 64, 2, 126, [2]),                      # half of what the warp has
+    (8, 1, 128, 1, 999, list(range(8, 63))),      # parts of several CTAs, a warp joins them
+    (8, 1, 64, 2, 3998, list(range(8, 250))),     # four warps do
+    (8, 1, 128, 2, 3998, [200]),
+    (2, 2, 128, 40, 88, [4, 5, 6, 7]),            # a group of softmax warps of two
+    (2, 2, 64, 40, 88, [4]),
+    (2, 2, 128, 40, 2960, list(range(8, 188))),   # parts of 128 rows
+    (4, 2, 64, 200, 2800, list(range(8, 188))),   # parts of 256 rows
+    (4, 2, 128, 200, 2800, [100]),
+]
+
+
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("Hq,Hkv,d,new,n,blocks", JOINS)
+def test_nothing_outweighs_a_marked_block(Hq, Hkv, d, new, n, blocks, ty):
+    g = gen(n)
+    table, total = pages_for([n + new], BLOCK, g)
+    cache = tq.Cache8(total, Hkv, BLOCK, d)
+    filled(cache, g)
+    for scale in (cache.kscale, cache.vscale):
+        scale.fill_(2.0 ** -6)
+    cache.k.view(torch.uint8)[table[0, 0], :, 0] = 0x7E  # 448: a score of 4 · 7 · d / 10 against some ten at most
+    q = (4 + 0.1 * torch.randn(new, Hq, d, device="cuda", generator=g)).to(TYPES[ty])
+    pages = table[0, blocks].long()
+    assert torch.isfinite(attend(q, [0, new], [n], table, cache, 0.1)).all()
+    for scale in (cache.kscale, cache.vscale):
+        kept = scale[pages].clone()
+        scale[pages] = math.nan
+        assert attend(q, [0, new], [n], table, cache, 0.1).isnan().all()
+        scale[pages] = kept
