@@ -541,10 +541,15 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  * past the table's capacity.  Hq / Hkv any whole number.
  * Accuracy: codes enter the products whole, scores and sums are fp32.  q enters
  * whole for F16 and BF16 (numbers 2^-24 and less of a row's largest may lose bits),
- * as two fp16 terms for F32; weights as one fp16 term for BF16, two otherwise.
+ * as two fp16 terms for F32.  Weights are one fp16 term for BF16 (2^-12 of a weight),
+ * two otherwise (2^-23), and no finer than 2^-32 of the row's largest weight (2^-35
+ * for a mean of up to 32 rows a request and KV head, 2^-47 for F32), both times their
+ * blocks' V scales: tokens so far below another one that has next to no value of its
+ * own are less precise.
  * The tensor cores cut their sums where others round; long ones go to rounded fp32
- * sums.  Of 65536 values of one sign no more than 1e-6 (F32), 1e-4 (F16) or 3e-4
- * (BF16) is missing, of values of either sign less.
+ * sums.  Of 65536 values of one sign and of like weight no more than 1e-6 (F32), 1e-4
+ * (F16) or 3e-4 (BF16) is missing, of any weights 2e-4 (F32), 4e-4 (F16) or 6e-4
+ * (BF16), of values of either sign less.
  * V scales outside [2^-60, 2^40] count as the nearer end.
  * d_ws      workspace of tq_cache8_attention_workspace_size bytes (16-byte aligned;
  *           its contents do not matter).  Calls that share one must be ordered on

@@ -336,7 +336,6 @@ __device__ __forceinline__ float c8_vscale(float s) { return s < kC8Lo ? kC8Lo :
 // block have the NaN in their weights (the scale stands in their exponents too); those
 // that do not have weights of 0, and 0 times a NaN would be one.
 __device__ __forceinline__ float c8_inverse(float s) { return s == s ? 1.f / s : 0.f; }
-constexpr float kC8Raise = 14.f, kC8Fresh = 6.f;  // raise M before a weight passes 2^14; a fresh maximum sits at 2^6
 
 template <typename... P, typename... A>
 inline cudaError_t c8_launch(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, const A&... args) {

@@ -17,7 +17,9 @@
 // Rounding: q is scaled by a power of two into fp16's range, which holds fp16 and
 // bf16 numbers whole; fp32 rows are two fp16 terms (2^-22).  Weights are one fp16
 // term for bf16 outputs (2^-12 against the output's 2^-9), two for fp16 and fp32,
-// where one would cost as much as the output's own rounding or more.
+// where one would cost as much as the output's own rounding or more; the second one of
+// fp32 calls is 2^12 times as large and has sums of its own, so that it keeps its bits
+// for weights far below the row's largest too.
 // Measured (bf16, d = 128): 32 single tokens over up to 16384, 32/8 heads: 133 us, 6.1
 // TB/s of the 6.8 that a copy gets, issue slots 37 % used; one over 131072, 64/8 heads:
 // 54 us, of which 40 are its bytes and the rest a share's start, the states' and the
@@ -30,6 +32,11 @@ namespace {
 
 constexpr int kAtThreads = 128, kAtWarps = 4;  // two CTAs an SM
 constexpr uint32_t kAtPolls = 1u << 20;          // polls of a wait
+// M is raised before a weight passes 2^14, and then so that the row's largest is 2^10: a
+// fresh maximum that high leaves 34 binary orders to fp16's least step (weights 24 orders
+// below one other's were 0.2 % off with 2^6), and four to the next raise, which costs
+// nothing here (2^6, 2^8, 2^10, 2^11: 32 long single tokens 133 us each time).
+constexpr float kAtRaise = 14.f, kAtFresh = 10.f;
 
 template <typename T>
 constexpr int kQTerms = sizeof(T) == 4 ? 2 : 1;  // fp16 terms of q
@@ -66,6 +73,17 @@ __device__ __forceinline__ float4 load4(const T* p) {
     }
     return make_float4(a.x, a.y, b.x, b.y);
   }
+}
+// Weights as two fp16 terms, the second kLow times as large: weights far below the largest
+// keep their bits (in fp16's own range a second term is no finer than 2^-24).  A weight is
+// 2^14 at most, what its first term leaves 2^2: within the range.  (32 single tokens over up
+// to 16384 147 -> 152 us, a prompt of 512 over 4096 269 -> 300 us; a token of its weight 2^-24
+// times another's is 2^-19 off, with the second term in fp16's own range 2^-11.)
+constexpr float kLow = 4096.f;
+__device__ __forceinline__ void split2_low(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  hi = h2_bits(h);
+  lo = pack_f16x2((x0 - __low2float(h)) * kLow, (x1 - __high2float(h)) * kLow);
 }
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kAtThreads, 2)
@@ -310,7 +328,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            up |= fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2])) > M[x][e] + kC8Raise;
+            up |= fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2])) > M[x][e] + kAtRaise;
         if (__any_sync(kFull, up)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
@@ -319,8 +337,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               float top = fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2]));
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-              if (top > M[x][e] + kC8Raise) {
-                const float m = top - kC8Fresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
+              if (top > M[x][e] + kAtRaise) {
+                const float m = top - kAtFresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
                 M[x][e] = m;
                 L[x][e] *= f;
 #pragma unroll
@@ -333,6 +351,7 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         }
         // ---- weights, transposed
         uint32_t bp[2][NT][PT][2];
+        float sum[NT][2];  // of the weights: one rounding into the row's for both halves
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
@@ -344,13 +363,19 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               w[e] = ex2(z[hf][x][e] - (m == -INFINITY ? 0.f : m));
             }
             const float iv = hf ? sc1.z : sc0.z;
-            L[x][0] = fmaf(w[0] + w[2], iv, L[x][0]);
-            L[x][1] = fmaf(w[1] + w[3], iv, L[x][1]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              sum[x][e] = fmaf(w[e] + w[e + 2], iv, hf ? sum[x][e] : 0.f);
+              if (hf) L[x][e] += sum[x][e];
+            }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               if constexpr (PT == 2) {
                 uint32_t hi, lo;
-                split2(w[2 * e], w[2 * e + 1], hi, lo);
+                if constexpr (QT == 2)
+                  split2_low(w[2 * e], w[2 * e + 1], hi, lo);
+                else
+                  split2(w[2 * e], w[2 * e + 1], hi, lo);
                 bp[hf][x][0][e] = transpose8(hi);
                 bp[hf][x][PT - 1][e] = transpose8(lo);
               } else {
@@ -396,10 +421,12 @@ __global__ void __launch_bounds__(kAtThreads, 2)
                 if constexpr (QT == 2) {
                   // fp32: 16 tokens by themselves, since the matrix units cut what a long sum
                   // has no bits for (64 requests over 65536: 2e-5 to 6e-5 off, 6e-7 this way, for
-                  // 140 -> 145 us of 32 single tokens over up to 16384)
+                  // 140 -> 145 us of 32 single tokens over up to 16384); their second terms first
                   float part[4] = {0.f, 0.f, 0.f, 0.f};
+                  mma16816(part, a0, a1, a2, a3, bp[hf][x][PT - 1][0], bp[hf][x][PT - 1][1]);
 #pragma unroll
-                  for (int q = 0; q < PT; ++q) mma16816(part, a0, a1, a2, a3, bp[hf][x][q][0], bp[hf][x][q][1]);
+                  for (int e = 0; e < 4; ++e) part[e] *= 1.f / kLow;
+                  mma16816(part, a0, a1, a2, a3, bp[hf][x][0][0], bp[hf][x][0][1]);
 #pragma unroll
                   for (int e = 0; e < 4; ++e) O[x][2 * k + o][e] += part[e];
                 } else {

@@ -17,7 +17,7 @@
 // memory instead (three places): its products take two thirds of the time that way
 // and leave shared memory to the codes' way to fp16 (exact), which there is made for
 // half as many rows (64 rows over 32 x 16384: 240 against 277 us when it was measured, 203 now).
-// M is raised only before a weight passes 2^14, so that O is rarely rescaled.
+// M is raised only before a weight passes 2^15, so that O is rarely rescaled (kUmRaise).
 // Weights are one fp16 term for bf16 outputs, two for fp16 (as in the kernel for few
 // rows); both stand in the columns of their own scores.
 //
@@ -50,6 +50,11 @@ constexpr uint32_t kUmLand = 1u << 14;       // a millisecond or more for copies
 // rounding or more; bf16 has a quarter of the products for its rounding).
 template <bool TWO>
 constexpr int kChain = TWO ? 256 : 1024;
+// M is raised before a weight passes 2^15, and then so that the row's largest is 2^7.  A
+// higher fresh maximum leaves more binary orders to fp16's least step, a lower one fewer
+// raises, for each of which a whole warp rescales its sums (a prompt's piece of 2039 behind
+// 16384: eight orders between the two 453 us, six 468, four 486, three 491).
+constexpr float kUmRaise = 15.f, kUmFresh = 7.f;
 constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
 
 template <int D, bool WIDE>
@@ -412,9 +417,9 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
               iv[g] = m.z;
               top = fmaxf(top, fmaf(y, a[g], b[g]));
             }
-            const bool up = top > M + kC8Raise;
+            const bool up = top > M + kUmRaise;
             if (__any_sync(kFull, up)) {
-              const float nm = up ? top - kC8Fresh : M;
+              const float nm = up ? top - kUmFresh : M;
               const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
               M = nm;
               L *= f;
@@ -434,6 +439,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
               }
             }
             const float use = M == -INFINITY ? 0.f : M;
+            float sum64 = 0.f;  // of the weights: one rounding into the row's for 64
             // the weights of 32 tokens: 16 columns of pairs, then those of the second terms
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -454,11 +460,12 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
                     ph[8 * g + e] = pack_f16x2(w0, w1);
                 }
                 const float2 both = um_two(sum);
-                L = fmaf(both.x + both.y, iv[2 * c + g], L);
+                sum64 = fmaf(both.x + both.y, iv[2 * c + g], sum64);
               }
               tmem_st16(tS + 16 * c, ph);
               if constexpr (TWO) tmem_st16(tS + 32 + 16 * c, pl);
             }
+            L += sum64;
             tmem_wait_st();
           }
           tc_fence_before();
