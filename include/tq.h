@@ -552,8 +552,10 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  * (BF16), of values of either sign less.
  * V scales outside [2^-60, 2^40] count as the nearer end.
  * d_ws      workspace of tq_cache8_attention_workspace_size bytes (16-byte aligned;
- *           its contents do not matter).  Calls that share one must be ordered on
- *           one stream; captured graphs that may run at the same time need one each.
+ *           its contents do not matter), which also do for calls with fewer requests
+ *           or rows, whatever the two are (42 MB at most, on 152 SMs).  Calls that
+ *           share one must be ordered on one stream; captured graphs that may run at
+ *           the same time need one each.
  * Pointers and strides in bytes must be multiples of 16.  Errors: INVALID_ARG;
  * UNSUPPORTED for B > 65536, rows * Hq or max_blocks * block past 2^31 - 256, pages * Hkv or
  * (max_blocks * block / 128 + 8) * Hkv past 2^31 - 1.

@@ -1164,7 +1164,9 @@ tq_status tq_cache8_attention_workspace_size(const tq_cache8* cache, int B, int 
   if (st != TQ_OK) return st;
   if (!bytes || B <= 0 || Hq <= 0 || Hq % cache->Hkv != 0 || rows < 0) return TQ_ERR_INVALID_ARG;
   if (rows > (INT32_MAX - 255) / Hq) return TQ_ERR_UNSUPPORTED;
-  *bytes = cache8_ws_bytes(cache->d, B, Hq, cache->Hkv, rows);
+  // fewer requests with as many rows take larger tiles, and what those need: the most
+  // that any number of requests up to this one asks for
+  *bytes = cache8_ws_bytes(cache->d, 1, Hq, cache->Hkv, rows);
   return TQ_OK;
 }
 
