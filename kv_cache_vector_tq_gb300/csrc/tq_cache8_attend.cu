@@ -328,7 +328,8 @@ __global__ void __launch_bounds__(kAtThreads, 2)
         for (int x = 0; x < NT; ++x)
 #pragma unroll
           for (int e = 0; e < 2; ++e)
-            up |= fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2])) > M[x][e] + kAtRaise;
+            // (the difference: of large scores M + 14 may round to M + 16, past fp16's range)
+            up |= fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2])) - M[x][e] > kAtRaise;
         if (__any_sync(kFull, up)) {
 #pragma unroll
           for (int x = 0; x < NT; ++x)
@@ -337,8 +338,10 @@ __global__ void __launch_bounds__(kAtThreads, 2)
               float top = fmaxf(fmaxf(z[0][x][e], z[0][x][e + 2]), fmaxf(z[1][x][e], z[1][x][e + 2]));
 #pragma unroll
               for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-              if (top > M[x][e] + kAtRaise) {
-                const float m = top - kAtFresh, f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
+              if (top - M[x][e] > kAtRaise) {
+                float m = top - kAtFresh;
+                if (top - m > kAtRaise) m = top;  // (rounded, of a large score)
+                const float f = M[x][e] == -INFINITY ? 0.f : ex2(M[x][e] - m);
                 M[x][e] = m;
                 L[x][e] *= f;
 #pragma unroll

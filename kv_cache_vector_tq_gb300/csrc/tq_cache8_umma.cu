@@ -55,6 +55,10 @@ constexpr int kChain = TWO ? 256 : 1024;
 // raises, for each of which a whole warp rescales its sums (a prompt's piece of 2039 behind
 // 16384: eight orders between the two 453 us, six 468, four 486, three 491).
 constexpr float kUmRaise = 15.f, kUmFresh = 7.f;
+// A weight's exponent comes of the product in one rounding, with the maximum that was
+// rounded by itself; for maxima past this the two could differ by what takes a weight out
+// of fp16's range.
+constexpr float kUmFar = 1048576.f;
 constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
 
 template <int D, bool WIDE>
@@ -358,6 +362,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
       };
       const int halves = (WIDE ? 2 : 1) * seg.n;  // of units, this group's
       float M = -INFINITY, L = 0.f;
+      bool far = false;  // some row's maximum is past kUmFar: scores to their end first, then the differences
 #pragma unroll 1
       for (int k = 0, rest = kChain<TWO>; ok && k < halves; rest += kChain<TWO>) {
         if (k > 0) {  // a rest: the last product is done (the one before it is when the next scores are there)
@@ -385,7 +390,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
             const uint32_t valid = (ms.valid[q % kMeta] >> (4 * part)) & 15u;
             const int base = c8_unit(t, seg.first + unit) + 64 * part;
             const bool all = valid == 15u && base + 63 <= upto && (base >= from || base + 63 < firsts);
-            const bool masked = !__all_sync(kFull, all);
+            const bool masked = far || !__all_sync(kFull, all);
             wait_ld(s[0]);
             wait_ld(s[1]);
             if (masked) {  // the scores to their end here
@@ -417,12 +422,23 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
               iv[g] = m.z;
               top = fmaxf(top, fmaf(y, a[g], b[g]));
             }
-            const bool up = top > M + kUmRaise;
+            const bool up = top - M > kUmRaise;
             if (__any_sync(kFull, up)) {
               const float nm = up ? top - kUmFresh : M;
               const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
               M = nm;
               L *= f;
+              far = __any_sync(kFull, fabsf(M) > kUmFar && M != -INFINITY);
+              if (far && !masked) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                  s[e >> 5][e & 31] = __float_as_uint(fmaf(__uint_as_float(s[e >> 5][e & 31]), a[e >> 4], b[e >> 4]));
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                  a[g] = 1.f;
+                  b[g] = 0.f;
+                }
+              }
               if (k > 0) {  // the sums so far, once the last product into them is done (the one before it was when these scores' place was free)
                 ok = __all_sync(kFull, um_wait(&ms.pv_done[w], (done - 1) & 1u, abort_flag, p.status));
                 if (!ok) break;
