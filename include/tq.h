@@ -550,7 +550,10 @@ tq_status tq_cache8_append(const void* d_q, int64_t q_stride, const void* d_k, i
  * sums.  Of 65536 values of one sign and of like weight no more than 1e-6 (F32), 1e-4
  * (F16) or 3e-4 (BF16) is missing, of any weights 2e-4 (F32), 4e-4 (F16) or 6e-4
  * (BF16), of values of either sign less.
- * V scales outside [2^-60, 2^40] count as the nearer end.
+ * V scales outside [2^-60, 2^40] count as the nearer end.  A block whose scale is a NaN
+ * makes the rows that see one of its tokens NaN, and no others.
+ * One call takes tiles of one size, by the mean request's rows: pieces of prompts and
+ * single tokens take less time in calls of their own.
  * d_ws      workspace of tq_cache8_attention_workspace_size bytes (16-byte aligned;
  *           its contents do not matter), which also do for calls with fewer requests
  *           or rows, whatever the two are (42 MB at most, on 152 SMs).  Calls that

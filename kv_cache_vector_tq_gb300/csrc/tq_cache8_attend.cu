@@ -16,14 +16,17 @@
 // warps' states are joined at its end.
 // Rounding: q is scaled by a power of two into fp16's range, which holds fp16 and
 // bf16 numbers whole; fp32 rows are two fp16 terms (2^-22).  Weights are one fp16
-// term for bf16 outputs (2^-12 against the output's 2^-9), two for fp16 and fp32,
-// where one would cost as much as the output's own rounding or more; the second one of
+// term for bf16 outputs (2^-12 against the output's 2^-9; two take 137 us for the 32 single
+// tokens below and 164 for 140 with rows for a tile of 32), two for fp16 and fp32, where
+// one would cost as much as the output's own rounding or more; the second one of
 // fp32 calls is 2^12 times as large and has sums of its own, so that it keeps its bits
 // for weights far below the row's largest too.
 // Measured (bf16, d = 128): 32 single tokens over up to 16384, 32/8 heads: 133 us, 6.1
 // TB/s of the 6.8 that a copy gets, issue slots 37 % used; one over 131072, 64/8 heads:
 // 54 us, of which 40 are its bytes and the rest a share's start, the states' and the
 // parts' joins; 64 with a window of 1024, 64/8 heads: 45 us for 137 MB, the same.
+// Spills: <fp32, 128, 4> 240 bytes a thread, the other fp32 ones and the 16-bit <128, 4> 52
+// at most, the rest none.
 #include "tq_cache8.cuh"
 
 namespace tq {
@@ -77,8 +80,8 @@ __device__ __forceinline__ float4 load4(const T* p) {
 // Weights as two fp16 terms, the second kLow times as large: weights far below the largest
 // keep their bits (in fp16's own range a second term is no finer than 2^-24).  A weight is
 // 2^14 at most, what its first term leaves 2^2: within the range.  (32 single tokens over up
-// to 16384 147 -> 152 us, a prompt of 512 over 4096 269 -> 300 us; a token of its weight 2^-24
-// times another's is 2^-19 off, with the second term in fp16's own range 2^-11.)
+// to 16384 147 -> 152 us, a prompt of 512 over 4096 269 -> 300 us; a weight 2^-24 times
+// another's is 2^-23 off, with the second term in fp16's own range 2^-11.)
 constexpr float kLow = 4096.f;
 __device__ __forceinline__ void split2_low(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x0, x1);
@@ -755,7 +758,11 @@ cudaError_t run_attend_t(const C8Params& p, const CUtensorMap& k, const CUtensor
 size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Rows of a tile, by a mean request's rows: the smallest that hold them.  From 33 on
-// fp16 and bf16 rows go to the fifth-generation tensor cores.
+// fp16 and bf16 rows go to the fifth-generation tensor cores (8 requests over 8191, 32/8
+// heads of 128, up to 12 and 15 tokens: 47 us, with two 32-row tiles each 71 to 90; of up
+// to 6 and 8, where these take 51 to 59, the tensor cores' tile would take 45; 32 requests
+// over 2048 with heads of 64: 46 to 52 and 43 to 50).  One size for a whole call: a piece of
+// 512 beside 255 single tokens takes 1114 us, the two in calls of their own 847.
 int tile_rows(int64_t rows, int B, int G, bool umma) {
   const int64_t mean = (rows * G + B - 1) / B;
   return mean <= 8 ? 8 : mean <= 16 ? 16 : mean <= 32 || !umma ? 32 : mean <= 128 ? 128 : 256;

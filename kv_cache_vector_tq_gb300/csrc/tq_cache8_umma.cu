@@ -25,12 +25,13 @@
 // and 17 issue the products, 18 and 19 the copies (lane = 16 tokens, so pages may
 // end anywhere on a multiple of 16).
 //
-// Measured (bf16, d = 128, 32/8 heads): a prompt's piece of 2039 tokens behind 16384 446 us,
-// 1302 TFLOP/s of the 1882 that a plain matrix product gets; tensor pipe 58 % active,
-// issue slots 65 %.  A unit of 256 rows takes 3500 clocks, its products 2560 (1536 the
+// Measured (bf16, d = 128, 32/8 heads): a prompt's piece of 2039 tokens behind 16384 450 us,
+// 1293 TFLOP/s of the 1882 that a plain matrix product gets; tensor pipe 57 % active,
+// issue slots 65 % (fp16, with its second terms: 558 us).  A unit of 256 rows takes 3500 clocks, its products 2560 (1536 the
 // scores, whose operands are both in shared memory, 64 columns at a time; 128 at a time
 // would take 1024 and slow the codes' way to fp16 by half).  Prompt of 8179 with a window
-// of 1024, 16/4 heads: 120 us (540 TFLOP/s; nine units a tile, its ends cost four more).
+// of 1024, 16/4 heads: 122 us (528 TFLOP/s; nine units a tile, its ends cost four more).
+// Spills: <bf16, 128, false> 140 bytes a thread, the others none or 16.
 #include "tq_cache8.cuh"
 
 namespace tq {
@@ -43,7 +44,6 @@ static_assert(8 * kUmRegSoft + 8 * kUmRegConv + 4 * 96 <= 20 * 96, "registers th
 constexpr int kMeta = 8;                     // units whose scales are kept (copies are four units ahead of the products at most, those of what is converted)
 constexpr uint32_t kUmLimit = 1u << 20;      // polls of a wait, a few microseconds each
 constexpr uint32_t kUmLand = 1u << 14;       // a millisecond or more for copies under way
-// Tensor memory columns: places of scores (and Q behind three of them), the two sums
 // Tensor memory's sums are cut, not rounded, where they are longer than the products added
 // to them: after so many products of 64 tokens they go to fp32 sums in the CTA's record, and
 // begin anew (fp16 over 65536 tokens, 2048 rows: 1e-4 to 3e-4 short without, half of its
@@ -59,6 +59,7 @@ constexpr float kUmRaise = 15.f, kUmFresh = 7.f;
 // rounded by itself; for maxima past this the two could differ by what takes a weight out
 // of fp16's range.
 constexpr float kUmFar = 1048576.f;
+// Tensor memory columns: places of scores (and Q behind three of them), the two sums
 constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
 
 template <int D, bool WIDE>
