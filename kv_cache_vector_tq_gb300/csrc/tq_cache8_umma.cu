@@ -57,7 +57,8 @@ constexpr int kChain = TWO ? 256 : 1024;
 constexpr float kUmRaise = 15.f, kUmFresh = 7.f;
 // A weight's exponent comes of the product in one rounding, with the maximum that was
 // rounded by itself; for maxima past this the two could differ by what takes a weight out
-// of fp16's range.
+// of fp16's range.  (All rows of a warp then: a choice by the row costs 2 % everywhere.  A
+// row whose maximum is an infinity is a NaN either way, and asks for nothing.)
 constexpr float kUmFar = 1048576.f;
 // Tensor memory columns: places of scores (and Q behind three of them), the two sums
 constexpr uint32_t kMostPlaces = 4, kColQ = 192, kColO = 256;
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(kUmThreads, 1) c8_umma_kernel(const C8Params p
               const float f = !up ? 1.f : M == -INFINITY ? 0.f : ex2(M - nm);
               M = nm;
               L *= f;
-              far = __any_sync(kFull, fabsf(M) > kUmFar && M != -INFINITY);
+              far = __any_sync(kFull, fabsf(M) > kUmFar && fabsf(M) < INFINITY);
               if (far && !masked) {
 #pragma unroll
                 for (int e = 0; e < 64; ++e)

@@ -6,7 +6,7 @@ import pytest
 
 torch = pytest.importorskip("torch")
 import kv_cache_vector_tq_gb300 as tq  # noqa: E402
-from test_gpu_cache8 import TYPES, attend, filled, gen, pages_for  # noqa: E402
+from test_gpu_cache8 import TYPES, attend, attend_ref, close, filled, gen, pages_for  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,27 @@ def test_the_heaviest_token(n, new, Hq, Hkv, d, window, ty):
         # one weight is left: half a step of the output and of the weight's and the sum's fp32
         off = (out.double() - ref).abs() - ref.abs() * (torch.finfo(t).eps / 2 + 2.0 ** -20)
         assert (off[clear] <= 0).all(), (power, float(off[clear].max()))
+
+
+@pytest.mark.parametrize("ty", list(TYPES))
+@pytest.mark.parametrize("n,new,Hq,Hkv,d", [(700, 5, 8, 2, 64), (700, 40, 4, 2, 128), (900, 200, 4, 2, 128), (900, 200, 4, 2, 64)])
+def test_rows_of_large_scores_beside_others(n, new, Hq, Hkv, d, ty):
+    """Scores of 2^21, or infinities, in one row of a tile: the others are right all the same, with infinities bit for bit."""
+    g, t, scale = gen(new + d), TYPES[ty], 0.1 * 2.0 ** 8
+    table, total = pages_for([n + new], 16, g)
+    cache = tq.Cache8(total, Hkv, 16, d)
+    filled(cache, g)
+    q = (torch.randn(new, Hq, d, device="cuda", generator=g) * 2.0 ** -8).to(t)
+    good, (ref, off) = attend(q, [0, new], [n], table, cache, scale), attend_ref(q, [0, new], [n], table, cache, scale, 0, 0)
+    rest = torch.ones(new, Hq, dtype=torch.bool, device="cuda")
+    rest[new // 2, 1] = rest[3, 0] = False
+    close(good, ref, off)
+    for factor in (2.0 ** 21, math.inf):
+        bad = q.clone()
+        bad[~rest] *= factor
+        out = attend(bad, [0, new], [n], table, cache, scale)
+        close(out[rest], ref[rest], off[rest], factor)
+        if math.isinf(factor):
+            assert torch.equal(out[rest], good[rest]) and out[~rest].isnan().all()
+        else:
+            assert torch.isfinite(out).all()
